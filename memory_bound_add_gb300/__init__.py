@@ -40,3 +40,14 @@ from .binding import (  # noqa: F401
     PATH_AUTO, PATH_WARP_VEC, PATH_CTA_TMA, PATH_CTA_VEC, PATH_SCALAR,
 )
 from .autograd import AddLayerNormFunction, FusedAddLayerNorm, add_layernorm_train  # noqa: F401
+from .block import (  # noqa: F401
+    BlockNormFunction,
+    BlockNormGrads,
+    FusedBlockNorm,
+    block_norm,
+    block_norm_backward,
+    block_norm_bwd,
+    block_norm_bwd_workspace_size,
+    block_norm_fwd,
+    block_norm_train,
+)

@@ -16,12 +16,15 @@
 
 #include <cuda_runtime.h>
 
-#include "../../include/addln.h"
+#include "../../include/addln_block.h"
+#include "abi.h"
+#include "block.h"
 #include "launch.h"
 
 using addln::DeviceInfo;
 using addln::LaunchCtx;
 using addln::RowArgs;
+using namespace addln::abi;
 
 namespace {
 
@@ -40,38 +43,6 @@ constexpr int kMaxDevices = 64;
 std::mutex g_dev_mu;
 DeviceInfo g_dev[kMaxDevices];
 bool g_dev_ok[kMaxDevices] = {};
-
-int elem_bytes(int dtype) { return dtype == ADDLN_FP32 ? 4 : 2; }
-
-bool valid_dtype(int dtype) {
-  return dtype == ADDLN_FP32 || dtype == ADDLN_FP16 || dtype == ADDLN_BF16;
-}
-
-int64_t max_hidden(int dtype) {
-  return dtype == ADDLN_FP32 ? addln::kMaxHidden32 : addln::kMaxHidden16;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-struct Range {
-  uintptr_t lo, hi;  // [lo, hi)
-  bool present;
-};
-Range range_of(const void* p, int64_t bytes) {
-  Range r;
-  r.present = p != nullptr && bytes > 0;
-  r.lo = reinterpret_cast<uintptr_t>(p);
-  r.hi = r.lo + static_cast<uintptr_t>(bytes);
-  return r;
-}
-bool overlap(const Range& a, const Range& b) {
-  return a.present && b.present && a.lo < b.hi && b.lo < a.hi;
-}
-// An output may coincide exactly with an input of the same size (in place).
-bool bad_pair(const Range& out, const Range& in, bool in_place_ok) {
-  if (!overlap(out, in)) return false;
-  return !(in_place_ok && out.lo == in.lo && out.hi == in.hi);
-}
 
 int check_rows_args(const void* x, const void* r, bool need_r, const float* gamma,
                     const float* beta, void* y, void* a, float* mean, float* rstd, int64_t rows,
@@ -421,6 +392,9 @@ const char* addln_strerror(int code) {
     case ADDLN_ERR_DEVICE_TIMEOUT: return "a kernel's bounded wait on its own copy ran out";
     case ADDLN_ERR_CUDA: return "a CUDA runtime call failed";
     case ADDLN_ERR_WORKSPACE: return "workspace missing, too small or not 16-byte aligned";
+    case ADDLN_ERR_ALIGN: return "a pointer is not a multiple of its element's size";
+    case ADDLN_ERR_KIND: return "unknown norm or gate kind, or arguments that contradict it";
+    case ADDLN_ERR_SCALE: return "a scale or limit is NaN, infinite or out of its range";
     case ADDLN_ERR_BOUNDS: return "a kernel skipped an access outside its buffer (checked build)";
     default: return "unknown error code";
   }
@@ -443,7 +417,7 @@ int addln_get_device_error(void* stream) {
   int (*const readers[])(unsigned long long*) = {
       addln::read_bounds_rows_warp, addln::read_bounds_rows_cta, addln::read_bounds_softmax,
       addln::read_bounds_bgr,       addln::read_bounds_add,      addln::read_bounds_bwd,
-      addln::read_bounds_host};
+      addln::read_bounds_host,      addln::read_bounds_block_fwd, addln::read_bounds_block_bwd};
   unsigned long long word = 0;
   for (auto f : readers) {
     unsigned long long w = 0;
@@ -514,5 +488,7 @@ int addln::fwd_rows_mapped(const void* x, const void* r, const float* gamma, con
             g_wait_limit_ns.load(std::memory_order_relaxed)};
   return run_rows(p, dtype, stream, false);
 }
+
+int addln::launch_context(void* stream, LaunchCtx* c) { return plain_ctx(stream, c); }
 
 bool addln::pdl_enabled() { return g_pdl.load(std::memory_order_relaxed) != 0; }

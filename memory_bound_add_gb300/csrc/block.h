@@ -1,0 +1,84 @@
+// Internal interface between the block-boundary entry points (block_api.cu)
+// and their kernels.
+#pragma once
+
+#include <stdint.h>
+
+#include "launch.h"
+
+namespace addln {
+
+// Arguments of one forward launch; the meaning of each is block_norm_fwd's.
+// gate_rows: rows of a per-row gate.  C, slice: CTAs of a row and the columns
+// each owns.
+struct BlockFwdArgs {
+  const void* f;
+  const void* x;
+  const float* post_gamma;
+  const float* post_beta;
+  const void* gate;
+  const float* pre_gamma;
+  const float* pre_beta;
+  void* h;
+  void* y;
+  float* post_mean;
+  float* post_rstd;
+  float* pre_mean;
+  float* pre_rstd;
+  int64_t rows;
+  int64_t gate_rows, gate_stride, rows_per_gate;
+  int H;
+  int post, pre, gate_kind;
+  float a, s, eps, inv_h;
+  int C, slice;
+};
+
+// Arguments of one backward launch (block_norm_bwd).  part: [walkers][A][Hp]
+// fp32 column partials; seg: [walkers][2][Hp] fp32 sums of a per-row gate's
+// gradient over the rows of a gate row that the walker shares with others
+// (first and last of its range).  Hp: H rounded up to 4.
+struct BlockBwdArgs {
+  const void* dy;
+  const void* dh;
+  const void* f;
+  const void* h;
+  const float* post_mean;
+  const float* post_rstd;
+  const float* pre_mean;
+  const float* pre_rstd;
+  const float* post_gamma;
+  const float* post_beta;
+  const void* gate;
+  const float* pre_gamma;
+  void* df;
+  void* dx;
+  float* dpost_gamma;
+  float* dpost_beta;
+  void* dgate;
+  float* dpre_gamma;
+  float* dpre_beta;
+  float* part;
+  float* seg;
+  int64_t rows, walkers;
+  int64_t gate_rows, gate_stride, rows_per_gate;
+  int H, Hp;
+  int post, pre, gate_kind;
+  float a, s, inv_h;
+  int C, slice;
+};
+
+// access: elements a thread moves at once, in bytes of the widest access all
+// of the call's buffers allow (16, 4 or the element).
+int launch_block_fwd(int dtype, int access, bool layer_or_bias, const BlockFwdArgs& p, const LaunchCtx& c,
+                     const char** name);
+// Bytes of workspace of a backward call, or a negative code.
+int64_t block_bwd_workspace_bytes(int dtype, int access, bool full, int64_t rows, int H, int gate_kind,
+                                  int64_t rows_per_gate, const DeviceInfo& dev);
+int launch_block_bwd(int dtype, int access, bool full, BlockBwdArgs p, void* ws, int64_t ws_bytes,
+                     const LaunchCtx& c, const char** name);
+
+int read_bounds_block_fwd(unsigned long long* word);
+int read_bounds_block_bwd(unsigned long long* word);
+
+
+}  // namespace addln

@@ -61,6 +61,10 @@ int launch_cta_row(int dtype, bool tma, const RowArgs& p, const LaunchCtx& c,
 // One CTA per row, element-wise loads, any alignment, H <= max.
 int launch_cta_scalar(int dtype, const RowArgs& p, const LaunchCtx& c, const char** path_name);
 
+// The context of a launch on the current device with no tuning but the PDL
+// knob; ADDLN_OK or ADDLN_ERR_CUDA.
+int launch_context(void* stream, LaunchCtx* c);
+
 // Whether launches use programmatic dependent launch (knob addln_set_pdl).
 bool pdl_enabled();
 
