@@ -50,6 +50,7 @@ extern "C" {
 #define ADDLN_ERR_ALIGN (-12) /* a pointer is not a multiple of its element's size */
 #define ADDLN_ERR_KIND (-13)  /* unknown norm or gate kind, or arguments that contradict the kind */
 #define ADDLN_ERR_SCALE (-14) /* a scale or limit that is NaN, infinite or out of its range */
+#define ADDLN_ERR_HOST_MEMORY (-15) /* the host's memory ran out inside the call */
 
 /*
  * Forward.

@@ -51,3 +51,4 @@ from .block import (  # noqa: F401
     block_norm_fwd,
     block_norm_train,
 )
+from .grads import clip_grad_norm_, clip_grads, grad_norm, grad_norm_workspace_size  # noqa: F401

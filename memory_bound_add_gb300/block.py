@@ -31,7 +31,7 @@ from .binding import DTYPE_CODE, AddLNError
 
 NORM_NONE, NORM_RMS, NORM_LAYER = 0, 1, 2
 GATE_NONE, GATE_CHANNEL, GATE_ROWS = 0, 1, 2
-ERR_ALIGN, ERR_KIND, ERR_SCALE = -12, -13, -14
+ERR_ALIGN, ERR_KIND, ERR_SCALE, ERR_HOST_MEMORY = -12, -13, -14, -15
 
 _NORMS = {None: NORM_NONE, "rms": NORM_RMS, "layer": NORM_LAYER}
 

@@ -16,7 +16,7 @@
 
 #include <cuda_runtime.h>
 
-#include "../../include/addln_block.h"
+#include "../../include/addln_grad.h"
 #include "abi.h"
 #include "block.h"
 #include "launch.h"
@@ -395,6 +395,7 @@ const char* addln_strerror(int code) {
     case ADDLN_ERR_ALIGN: return "a pointer is not a multiple of its element's size";
     case ADDLN_ERR_KIND: return "unknown norm or gate kind, or arguments that contradict it";
     case ADDLN_ERR_SCALE: return "a scale or limit is NaN, infinite or out of its range";
+    case ADDLN_ERR_HOST_MEMORY: return "the host's memory ran out inside the call";
     case ADDLN_ERR_BOUNDS: return "a kernel skipped an access outside its buffer (checked build)";
     default: return "unknown error code";
   }
@@ -417,7 +418,8 @@ int addln_get_device_error(void* stream) {
   int (*const readers[])(unsigned long long*) = {
       addln::read_bounds_rows_warp, addln::read_bounds_rows_cta, addln::read_bounds_softmax,
       addln::read_bounds_bgr,       addln::read_bounds_add,      addln::read_bounds_bwd,
-      addln::read_bounds_host,      addln::read_bounds_block_fwd, addln::read_bounds_block_bwd};
+      addln::read_bounds_host,      addln::read_bounds_block_fwd, addln::read_bounds_block_bwd,
+      addln::read_bounds_grad};
   unsigned long long word = 0;
   for (auto f : readers) {
     unsigned long long w = 0;

@@ -79,6 +79,6 @@ int launch_block_bwd(int dtype, int access, bool full, BlockBwdArgs p, void* ws,
 
 int read_bounds_block_fwd(unsigned long long* word);
 int read_bounds_block_bwd(unsigned long long* word);
-
+int read_bounds_grad(unsigned long long* word);
 
 }  // namespace addln

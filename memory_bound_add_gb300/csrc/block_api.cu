@@ -61,7 +61,7 @@ int block_norm_fwd(const void* f, const void* x, int post, const float* post_gam
                    float residual_scale, float block_scale, int pre, const float* pre_gamma,
                    const float* pre_beta, void* h, void* y, float* post_mean, float* post_rstd,
                    float* pre_mean, float* pre_rstd, int64_t rows, int64_t H, float eps, int dtype,
-                   void* stream) {
+                   void* stream) try {
   int64_t gate_rows;
   int rc = check_spec(post, pre, gate_kind, gate_stride, rows_per_gate, residual_scale, block_scale, rows, H,
                       dtype, &gate_rows);
@@ -112,10 +112,12 @@ int block_norm_fwd(const void* f, const void* x, int post, const float* post_gam
   const bool layer_or_bias = post == ADDLN_NORM_LAYER || pre == ADDLN_NORM_LAYER || post_beta || pre_beta;
   const char* name = "none";
   return addln::launch_block_fwd(dtype, access, layer_or_bias, p, c, &name);
+} catch (...) {
+  return ADDLN_ERR_HOST_MEMORY;
 }
 
 int64_t block_norm_bwd_workspace_size(int64_t rows, int64_t H, int dtype, int gate_kind,
-                                      int64_t rows_per_gate) {
+                                      int64_t rows_per_gate) try {
   int64_t gate_rows;
   int rc = check_spec(ADDLN_NORM_NONE, ADDLN_NORM_NONE, gate_kind, H, rows_per_gate, 1.f, 1.f, rows, H, dtype,
                       &gate_rows);
@@ -135,6 +137,8 @@ int64_t block_norm_bwd_workspace_size(int64_t rows, int64_t H, int dtype, int ga
       if (n > most) most = n;
     }
   return most;
+} catch (...) {
+  return ADDLN_ERR_HOST_MEMORY;
 }
 
 int block_norm_bwd(const void* dy, const void* dh, const void* f, const void* h, int post,
@@ -144,7 +148,7 @@ int block_norm_bwd(const void* dy, const void* dh, const void* f, const void* h,
                    const float* pre_gamma, const float* pre_mean, const float* pre_rstd, void* df, void* dx,
                    float* dpost_gamma, float* dpost_beta, void* dgate, float* dpre_gamma, float* dpre_beta,
                    int64_t rows, int64_t H, int dtype, void* workspace, int64_t workspace_bytes,
-                   void* stream) {
+                   void* stream) try {
   int64_t gate_rows;
   int rc = check_spec(post, pre, gate_kind, gate_stride, rows_per_gate, residual_scale, block_scale, rows, H,
                       dtype, &gate_rows);
@@ -215,6 +219,8 @@ int block_norm_bwd(const void* dy, const void* dh, const void* f, const void* h,
   const bool full = post == ADDLN_NORM_LAYER || pre == ADDLN_NORM_LAYER || post_beta || dpost_beta || dpre_beta;
   const char* name = "none";
   return addln::launch_block_bwd(dtype, access, full, p, workspace, workspace_bytes, c, &name);
+} catch (...) {
+  return ADDLN_ERR_HOST_MEMORY;
 }
 
 }  // extern "C"

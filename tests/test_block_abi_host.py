@@ -40,7 +40,7 @@ def test_symbols_signatures_and_codes(lib):
     for k in ("NORM_NONE", "NORM_RMS", "NORM_LAYER", "GATE_NONE", "GATE_CHANNEL", "GATE_ROWS", "ERR_ALIGN",
               "ERR_KIND", "ERR_SCALE"):
         assert getattr(block, k) == d["ADDLN_" + k]
-    for code in (block.ERR_ALIGN, block.ERR_KIND, block.ERR_SCALE):
+    for code in (block.ERR_ALIGN, block.ERR_KIND, block.ERR_SCALE, block.ERR_HOST_MEMORY):
         assert "unknown error" not in binding.strerror(code)
 
 
