@@ -1,33 +1,30 @@
 // Shared by the block-boundary kernels (block_fwd.cu, block_bwd.cu): how a
-// row is spread over threads, loads and stores of VE neighbouring elements,
-// and the row reductions over a CTA or over the CTAs of a cluster.
+// row is spread over threads, how its elements reach them, and the row
+// reductions over a warp, a CTA or the CTAs of a cluster.
 //
-// Layout.  One walker handles one row at a time: a CTA, or for rows of more
-// than kSlice columns a cluster of C CTAs that each own a slice of the
-// columns.  A thread owns E = 8 columns of its CTA's slice, as NV = E / VE
-// groups of VE neighbours: group k starts at (k T + tid) VE of T threads.
-// VE follows the alignment that all buffers of a call share: 16-byte
-// accesses, or 4-byte, or single elements.  Eight columns a thread keep the
-// thread's share of four column sums, the row's values and the parameters in
-// registers at 512 threads a CTA, so that one kernel serves every width.
+// Layout.  One walker handles one row at a time: a warp, a CTA, or for the
+// longest rows a cluster of C CTAs that each own a slice of the columns.  A
+// warp owns 32 NV groups of VE neighbouring columns, of which lane l has
+// groups l, l + 32, ...: the addresses of a thread's groups are constants
+// apart.  VE follows the alignment that all buffers of a call share: 16-byte
+// accesses, or 4-byte, or single elements.
 #pragma once
 
 #include <cooperative_groups.h>
 
 #include "../../include/addln_block.h"
+#include "block.h"
 #include "common.cuh"
 
 namespace addln {
 namespace blk {
 
-constexpr int kE = 8;             // columns a thread
 constexpr int kMaxThreads = 512;  // threads a CTA
-constexpr int kSlice = kE * kMaxThreads;
-constexpr int kMaxCluster = 8;    // the portable cluster size: 8 * 4096 columns
 constexpr int kMaxWarps = kMaxThreads / 32;
+constexpr int kMaxCluster = 8;    // the portable cluster size
 
 // VE elements of DT at p (element offset i), as 32-bit words or one 16-bit
-// value, and their fp32 values in slots [k VE, (k + 1) VE) of float2 v[E/2].
+// value, and their fp32 values in slots [k VE, (k + 1) VE) of float2 v[NV VE / 2].
 template <int DT, int VE>
 struct Grp {
   using IO = Io<DT>;
@@ -40,8 +37,7 @@ struct Grp {
 #pragma unroll
     for (int j = 0; j < W; ++j) w[j] = 0u;
   }
-  __device__ __forceinline__ void load(const void* p, int64_t i) {
-    const char* q = static_cast<const char*>(p) + i * S;
+  __device__ __forceinline__ void load(const char* q) {
     if constexpr (kBytes == 16) {
       const uint4 u = ld_stream_v4(q);
       w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
@@ -60,11 +56,11 @@ struct Grp {
   }
 };
 
-template <int DT, int VE>
-__device__ __forceinline__ void to_slots(const Grp<DT, VE> (&g)[kE / VE], float2 (&v)[kE / 2]) {
+template <int DT, int VE, int NV>
+__device__ __forceinline__ void to_slots(const Grp<DT, VE> (&g)[NV], float2 (&v)[NV * VE / 2]) {
   if constexpr (VE >= 2) {
 #pragma unroll
-    for (int k = 0; k < kE / VE; ++k)
+    for (int k = 0; k < NV; ++k)
 #pragma unroll
       for (int q = 0; q < VE / 2; ++q) {
         if constexpr (DT == kF32)
@@ -74,14 +70,13 @@ __device__ __forceinline__ void to_slots(const Grp<DT, VE> (&g)[kE / VE], float2
       }
   } else {
 #pragma unroll
-    for (int q = 0; q < kE / 2; ++q) v[q] = make_float2(g[2 * q].get(0), g[2 * q + 1].get(0));
+    for (int q = 0; q < NV / 2; ++q) v[q] = make_float2(g[2 * q].get(0), g[2 * q + 1].get(0));
   }
 }
 
-// Stores group k of the slots (rounded to DT) at element offset i.
-template <int DT, int VE>
-__device__ __forceinline__ void store_group(void* p, int64_t i, const float2 (&v)[kE / 2], int k) {
-  char* q = static_cast<char*>(p) + i * Io<DT>::kBytes;
+// Stores group k of the slots, rounded to DT, at q.
+template <int DT, int VE, int P>
+__device__ __forceinline__ void store_group(char* q, const float2 (&v)[P], int k) {
   if constexpr (VE * Io<DT>::kBytes == 16) {
     st_stream_v4(q, Io<DT>::from_pairs(&v[k * VE / 2]));
   } else if constexpr (VE == 2) {  // 16-bit pair
@@ -91,27 +86,130 @@ __device__ __forceinline__ void store_group(void* p, int64_t i, const float2 (&v
   }
 }
 
-// VE fp32 parameters at column c into the slots of group k.
-template <int VE>
-__device__ __forceinline__ void load_param(const float* p, int c, float2 (&v)[kE / 2], int k) {
+// VE fp32 parameters at byte offset `off` into the slots of group k.
+template <int VE, int P>
+__device__ __forceinline__ void load_param(const float* p, uint32_t off, float2 (&v)[P], int k) {
+  const char* q = reinterpret_cast<const char*>(p) + off;
   if constexpr (VE >= 4) {
 #pragma unroll
-    for (int q = 0; q < VE / 4; ++q) {
-      const float4 t = ld_param_f4(p + c + 4 * q);
-      v[k * VE / 2 + 2 * q] = make_float2(t.x, t.y);
-      v[k * VE / 2 + 2 * q + 1] = make_float2(t.z, t.w);
+    for (int h = 0; h < VE / 4; ++h) {
+      const float4 t = __ldg(reinterpret_cast<const float4*>(q) + h);
+      v[k * VE / 2 + 2 * h] = make_float2(t.x, t.y);
+      v[k * VE / 2 + 2 * h + 1] = make_float2(t.z, t.w);
     }
   } else if constexpr (VE == 2) {
-    v[k] = __ldg(reinterpret_cast<const float2*>(p + c));
+    v[k] = __ldg(reinterpret_cast<const float2*>(q));
   } else {
-    const float t = __ldg(p + c);
+    const float t = __ldg(reinterpret_cast<const float*>(q));
     if (k & 1) v[k >> 1].y = t; else v[k >> 1].x = t;
   }
 }
 
-__device__ __forceinline__ float get_slot(const float2 (&v)[kE / 2], int e) {
+template <int P>
+__device__ __forceinline__ float get_slot(const float2 (&v)[P], int e) {
   return (e & 1) ? v[e >> 1].y : v[e >> 1].x;
 }
+
+// Asks L2 for the 128-byte line at p (a hint).
+__device__ __forceinline__ void prefetch_line(const void* p) {
+  asm volatile("prefetch.global.L2 [%0];" ::"l"(p) : "memory");
+}
+
+// A thread's groups of a row.  A group past the end of the slice does not
+// exist: it is fetched as zeros and never stored, and reads the parameters of
+// the slice's last group.
+template <int VE, int NV>
+struct Cols {
+  static constexpr int kStep = 32 * VE;  // columns between a thread's groups
+  int c0;           // first column of group 0
+  bool ok[NV];
+  bool all;         // every group of the warp exists
+  int cnt;          // columns that exist
+  uint32_t par[NV]; // byte offset of each group in an fp32 vector of H columns
+
+  __device__ __forceinline__ void init(int warp, int col0, int cols) {
+    const int at0 = warp * NV * kStep + (threadIdx.x & 31) * VE;
+    c0 = col0 + at0;
+    cnt = 0;
+    bool full = true;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      const int at = at0 + k * kStep;
+      ok[k] = at < cols;
+      full = full && ok[k];
+      par[k] = 4u * static_cast<uint32_t>(col0 + (ok[k] ? at : cols - VE));
+      cnt += ok[k] ? VE : 0;
+    }
+    all = __all_sync(0xffffffffu, full);
+  }
+  __device__ __forceinline__ int col(int k) const { return c0 + k * kStep; }
+  // zeros in the slots of groups that do not exist
+  __device__ __forceinline__ void clear(float2 (&v)[NV * VE / 2]) const {
+    if (all) return;
+#pragma unroll
+    for (int e = 0; e < NV * VE; ++e) {
+      float& u = (e & 1) ? v[e >> 1].y : v[e >> 1].x;
+      u = ok[e / VE] ? u : 0.f;
+    }
+  }
+};
+
+// --------------------------------------------------------------- staging
+// A thread's groups of the rows ahead, in a ring of slots of its own in
+// shared memory: it copies them itself (cp.async, 16 or 4 bytes at a time,
+// zeros for a group that does not exist) and alone reads them, so no barrier
+// is needed, and no register holds them.  Slot s of tensor i, group k:
+// [(s NT + i) NV + k][T].  Two-byte groups cannot be copied that way; they
+// wait in registers (one slot).
+template <int DT, int VE, int NV, int NT>
+struct Ring {
+  static constexpr int kBytes = Grp<DT, VE>::kBytes;
+  static constexpr bool kAsync = kBytes >= 4;
+  uint32_t base;  // this thread's first group of slot 0
+  int step;       // bytes between neighbouring groups: T kBytes
+  Grp<DT, VE> held[kAsync ? 1 : NT][kAsync ? 1 : NV];
+
+  // group k of tensor i from src, if it exists
+  __device__ __forceinline__ void fetch(int slot, int i, int k, const char* src, bool ok) {
+    if constexpr (kAsync) {
+      const uint32_t dst = base + static_cast<uint32_t>((slot * NT + i) * NV + k) * step;
+      const int n = ok ? kBytes : 0;
+      if constexpr (kBytes == 16)
+        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+      else
+        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+    } else {
+      held[i][k].zero();
+      if (ok) held[i][k].load(src);
+    }
+  }
+  __device__ __forceinline__ void commit() {
+    if constexpr (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // all but the AHEAD groups of copies committed last have arrived
+  template <int AHEAD>
+  __device__ __forceinline__ void wait() {
+    if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
+  }
+  // groups k0 .. k0 + N - 1 of tensor i
+  template <int N>
+  __device__ __forceinline__ void take(int slot, int i, int k0, Grp<DT, VE> (&g)[N]) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+      if constexpr (kAsync) {
+        const uint32_t src = base + static_cast<uint32_t>((slot * NT + i) * NV + k0 + k) * step;
+        if constexpr (kBytes == 16) {
+          const uint4 u = ld_shared_v4(src);
+          g[k].w[0] = u.x, g[k].w[1] = u.y, g[k].w[2] = u.z, g[k].w[3] = u.w;
+        } else {
+          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(g[k].w[0]) : "r"(src));
+        }
+      } else {
+        g[k] = held[i][k0 + k];
+      }
+    }
+  }
+};
 
 // --------------------------------------------------------- row reductions
 // Every warp publishes one float4; after exchange() every thread of the
@@ -120,115 +218,140 @@ __device__ __forceinline__ float get_slot(const float2 (&v)[kE / 2], int e) {
 // i + 1, which every warp passes only when it has read those of exchange i.
 struct Exchange {
   float4 (*buf)[kMaxWarps * kMaxCluster];  // [2][...]
-  int n;       // warps of the walker
-  int nw;      // warps of this CTA
-  int C;       // CTAs of the walker
-  int rank;    // this CTA's place among them
+  const Walk& w;
+  int rank;  // this CTA's place among the walker's
   int par;
 
   __device__ __forceinline__ const float4* operator()(float4 v) {
     float4* b = buf[par];
     par ^= 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    if (C == 1) {
+    if (w.C == 1) {
       if (lane == 0) b[warp] = v;
       __syncthreads();
     } else {
       namespace cg = cooperative_groups;
       cg::cluster_group cl = cg::this_cluster();
-      if (lane < C) cl.map_shared_rank(b, lane)[rank * nw + warp] = v;
+      if (lane < w.C) cl.map_shared_rank(b, lane)[rank * w.cta_warps + warp] = v;
       cl.sync();
     }
     return b;
   }
 };
 
-// Sum of (a, b) over the walker, the same bits in every thread: a warp
-// butterfly, then the warps' sums in a fixed order.
+// Sums over the walker, the same bits in every thread: a warp butterfly, then
+// the warps' sums in a fixed order.
+__device__ __forceinline__ float walker_sum(Exchange& ex, float v) {
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
+  if (ex.w.warps == 1) return v;
+  const float4* b = ex(make_float4(v, 0.f, 0.f, 0.f));
+  // groups of `width` lanes (a power of two of at least n, at most 32) add
+  // the same n sums in the same order
+  const int width = ex.w.width;
+  float t = 0.f;
+  for (int i = (threadIdx.x & 31) & (width - 1); i < ex.w.warps; i += 32) t += b[i].x;
+  for (int off = 1; off < width; off <<= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
+  return t;
+}
+
 __device__ __forceinline__ float2 walker_sum2(Exchange& ex, float2 v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1)
     v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, off), __shfl_xor_sync(0xffffffffu, v.y, off)));
-  if (ex.n == 1) return v;
+  if (ex.w.warps == 1) return v;
   const float4* b = ex(make_float4(v.x, v.y, 0.f, 0.f));
-  const int lane = threadIdx.x & 31;
+  const int width = ex.w.width;
   float2 t = dup2(0.f);
-  for (int i = lane; i < ex.n; i += 32) t = add2(t, *reinterpret_cast<const float2*>(b + i));
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
+  for (int i = (threadIdx.x & 31) & (width - 1); i < ex.w.warps; i += 32)
+    t = add2(t, *reinterpret_cast<const float2*>(b + i));
+  for (int off = 1; off < width; off <<= 1)
     t = add2(t, make_float2(__shfl_xor_sync(0xffffffffu, t.x, off), __shfl_xor_sync(0xffffffffu, t.y, off)));
   return t;
 }
 
-// Mean and sum of squared deviations of the walker's row.  Each warp works
-// on values shifted by its own first value K_w (a row whose mean is large
-// against its spread then loses nothing); the warps' parts are put on the
-// first warp's shift, K_w - K_0 being a difference of two values of the row.
-// v: this thread's slots (ok: which exist; the others hold anything finite);
-// inv_cnt: 1 / cnt of this thread, 0 for none.  Returns K_0 in .n's place
-// beside the mean and M2 relative to it.
+// Mean and sum of squared deviations of the walker's row.  Each warp takes
+// its own first value K_w off its values (a row whose mean is large against
+// its spread then loses nothing), and v is left that way; the warps' parts
+// are put on the first warp's shift, K_w - K_0 being a difference of two
+// values of the row.  Returns the mean, the mean on this warp's shift, and
+// M2.
 struct RowStat {
-  float K, m, M2;
+  float mean, m, M2;
 };
 
-template <int VE>
-__device__ __forceinline__ RowStat walker_stats(Exchange& ex, const float2 (&v)[kE / 2],
-                                                const bool (&ok)[kE / VE], int cnt, float inv_cnt) {
+template <int VE, int NV>
+__device__ __forceinline__ RowStat walker_stats(Exchange& ex, float2 (&v)[NV * VE / 2], const Cols<VE, NV>& cs) {
+  constexpr int P = NV * VE / 2;
   const float K = __shfl_sync(0xffffffffu, v[0].x, 0);
-  float sum = 0.f;
+  const float2 negK = dup2(-K);
+  float2 s[2] = {dup2(0.f), dup2(0.f)}, q[2] = {dup2(0.f), dup2(0.f)};
 #pragma unroll
-  for (int e = 0; e < kE; ++e) sum += ok[e / VE] ? get_slot(v, e) - K : 0.f;
+  for (int j = 0; j < P; ++j) v[j] = add2(v[j], negK);
+  cs.clear(v);
+#pragma unroll
+  for (int j = 0; j < P; ++j) s[j & 1] = add2(s[j & 1], v[j]);
+  s[0] = add2(s[0], s[1]);
   Part p;
-  p.n = static_cast<float>(cnt);
-  p.m = sum * inv_cnt;
-  p.M2 = 0.f;
+  p.n = static_cast<float>(cs.cnt);
+  p.m = cs.all ? (s[0].x + s[0].y) * (1.0f / (NV * VE)) : cs.cnt ? __fdiv_rn(s[0].x + s[0].y, p.n) : 0.f;
+  const float2 negm = dup2(-p.m);
+  if (cs.all) {
 #pragma unroll
-  for (int e = 0; e < kE; ++e) {
-    const float d = ok[e / VE] ? (get_slot(v, e) - K) - p.m : 0.f;
-    p.M2 = fmaf(d, d, p.M2);
+    for (int j = 0; j < P; ++j) {
+      const float2 d = add2(v[j], negm);
+      q[j & 1] = fma2(d, d, q[j & 1]);
+    }
+    q[0] = add2(q[0], q[1]);
+    p.M2 = q[0].x + q[0].y;
+    p = butterfly<true, 32>(p);
+  } else {
+#pragma unroll
+    for (int e = 0; e < NV * VE; ++e) {
+      const float d = cs.ok[e / VE] ? get_slot(v, e) - p.m : 0.f;
+      q[0].x = fmaf(d, d, q[0].x);
+    }
+    p.M2 = q[0].x;
+    p = butterfly<false, 32>(p);
   }
-  p = butterfly<false, 32>(p);
-  if (ex.n == 1) return {K, p.m, p.M2};
+  if (ex.w.warps == 1) return {K + p.m, p.m, p.M2};
   const float4* b = ex(make_float4(K, p.n, p.m, p.M2));
-  const int lane = threadIdx.x & 31;
+  const int width = ex.w.width;
   const float K0 = b[0].x;
   Part t{0.f, 0.f, 0.f};
-  for (int i = lane; i < ex.n; i += 32) {
+  for (int i = (threadIdx.x & 31) & (width - 1); i < ex.w.warps; i += 32) {
     const float4 u = b[i];
     t = merge<false>(t, Part{u.y, (u.x - K0) + u.z, u.w});
   }
-  t = butterfly<false, 32>(t);
-  return {K0, t.m, t.M2};
+  for (int off = 1; off < width; off <<= 1)
+    t = merge<false>(t, Part{__shfl_xor_sync(0xffffffffu, t.n, off), __shfl_xor_sync(0xffffffffu, t.m, off),
+                             __shfl_xor_sync(0xffffffffu, t.M2, off)});
+  return {K0 + t.m, t.m - (K - K0), t.M2};
 }
 
 // ------------------------------------------------------------------ host
-// How a call's rows are spread: VE, threads, cluster and slice.
+// How a call's rows are spread over threads and CTAs.
 struct Shape {
-  int threads;
-  int C;
-  int slice;  // columns a CTA owns, a multiple of 8
+  int threads;   // threads of a CTA
+  int rows;      // rows a CTA walks side by side, a warp for each; 1: a walker is a CTA or cluster
+  int C;         // CTAs of a row
+  int slice;     // columns a CTA owns, a multiple of 16
 };
 
-inline Shape shape_of(int H) {
-  Shape s;
-  s.C = (H + kSlice - 1) / kSlice;
-  s.slice = s.C == 1 ? H : ((H + s.C - 1) / s.C + 7) / 8 * 8;
-  s.threads = ((s.slice + kE - 1) / kE + 31) / 32 * 32;
-  return s;
-}
+// Units (CTAs, or clusters of C CTAs) of kernel f that fit the device at
+// once; cached per kernel, device, threads, cluster and shared memory.
+// Negative: a CUDA error.
+int resident_units(const void* f, const Shape& sh, int smem, const DeviceInfo& dev);
 
-inline int elem_size(int dtype) { return dtype == kF32 ? 4 : 2; }
+Walk walk_of(const Shape& sh);
 
-// Walkers (CTAs or clusters) of kernel f that fit the device at once; cached
-// per kernel, device, threads and cluster.  Negative: a CUDA error.
-int resident_walkers(const void* f, int threads, int C, const DeviceInfo& dev);
-
-// Launches kernel(args...) as walkers * C CTAs.
+// Launches kernel(args...) as units * C CTAs.
 template <typename Args>
-cudaError_t launch_walkers(void (*kernel)(Args), int64_t walkers, const Shape& sh, const LaunchCtx& c,
-                           const Args& p) {
+cudaError_t launch_units(void (*kernel)(Args), int64_t units, const Shape& sh, int smem, const LaunchCtx& c,
+                         const Args& p) {
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(static_cast<unsigned>(walkers * sh.C));
+  cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+  cfg.gridDim = dim3(static_cast<unsigned>(units * sh.C));
   cfg.blockDim = dim3(static_cast<unsigned>(sh.threads));
   cfg.stream = static_cast<cudaStream_t>(c.stream);
   cudaLaunchAttribute attr[2];

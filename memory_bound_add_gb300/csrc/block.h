@@ -8,9 +8,18 @@
 
 namespace addln {
 
+// How walkers (a warp, a CTA or a cluster for each row) cover the rows.
+struct Walk {
+  int C;             // CTAs of a row
+  int slice;         // columns each of them owns
+  int rows_per_cta;  // rows a CTA walks side by side, a warp for each; else 1
+  int cta_warps;     // warps a row has in one CTA
+  int warps;         // warps a row has
+  int width;         // lanes that join the warps' sums: a power of two, at most 32
+};
+
 // Arguments of one forward launch; the meaning of each is block_norm_fwd's.
-// gate_rows: rows of a per-row gate.  C, slice: CTAs of a row and the columns
-// each owns.
+// gate_rows: rows of a per-row gate.
 struct BlockFwdArgs {
   const void* f;
   const void* x;
@@ -30,7 +39,8 @@ struct BlockFwdArgs {
   int H;
   int post, pre, gate_kind;
   float a, s, eps, inv_h;
-  int C, slice;
+  int slots;  // rows staged ahead, 1 or 2
+  Walk w;
 };
 
 // Arguments of one backward launch (block_norm_bwd).  part: [walkers][A][Hp]
@@ -64,7 +74,7 @@ struct BlockBwdArgs {
   int H, Hp;
   int post, pre, gate_kind;
   float a, s, inv_h;
-  int C, slice;
+  Walk w;
 };
 
 // access: elements a thread moves at once, in bytes of the widest access all

@@ -108,7 +108,7 @@ int block_norm_fwd(const void* f, const void* x, int post, const float* post_gam
   addln::BlockFwdArgs p{f, x, post_gamma, post_beta, gate, pre_gamma, pre_beta, h, y, post_mean, post_rstd,
                         pre_mean, pre_rstd, rows, gate_rows, gate_stride, rows_per_gate, static_cast<int>(H),
                         post, pre, gate_kind, residual_scale, block_scale, eps,
-                        static_cast<float>(1.0 / static_cast<double>(H)), 1, static_cast<int>(H)};
+                        static_cast<float>(1.0 / static_cast<double>(H))};
   const bool layer_or_bias = post == ADDLN_NORM_LAYER || pre == ADDLN_NORM_LAYER || post_beta || pre_beta;
   const char* name = "none";
   return addln::launch_block_fwd(dtype, access, layer_or_bias, p, c, &name);
@@ -215,7 +215,7 @@ int block_norm_bwd(const void* dy, const void* dh, const void* f, const void* h,
                         pre_gamma, df, dx, dpost_gamma, dpost_beta, dgate, dpre_gamma, dpre_beta, nullptr,
                         nullptr, rows, 0, gate_rows, gate_stride, rows_per_gate, static_cast<int>(H), 0, post,
                         pre, gate_kind, residual_scale, block_scale,
-                        static_cast<float>(1.0 / static_cast<double>(H)), 1, static_cast<int>(H)};
+                        static_cast<float>(1.0 / static_cast<double>(H))};
   const bool full = post == ADDLN_NORM_LAYER || pre == ADDLN_NORM_LAYER || post_beta || dpost_beta || dpre_beta;
   const char* name = "none";
   return addln::launch_block_bwd(dtype, access, full, p, workspace, workspace_bytes, c, &name);

@@ -22,6 +22,9 @@
 namespace addln {
 namespace blk {
 
+constexpr int kE = 8;  // columns a thread
+constexpr int kSlice = kE * kMaxThreads;
+
 // First row of walker w's range.
 __host__ __device__ __forceinline__ int64_t range_begin(int64_t w, int64_t rows, int64_t walkers) {
   const int64_t q = rows / walkers, r = rows - q * walkers;
@@ -47,7 +50,7 @@ __device__ __forceinline__ void load_row(const void* t, int64_t base, const int 
   for (int k = 0; k < kE / VE; ++k) {
     r[k].zero();
     if (ok[k] && ADDLN_IN(site, (base + col[k]) * Io<DT>::kBytes, VE * Io<DT>::kBytes, extent))
-      r[k].load(t, base + col[k]);
+      r[k].load(static_cast<const char*>(t) + (base + col[k]) * Io<DT>::kBytes);
   }
 }
 
@@ -59,7 +62,7 @@ __device__ __forceinline__ void load_cols(const float* t, const int (&col)[kE / 
   if (t == nullptr) return;
 #pragma unroll
   for (int k = 0; k < kE / VE; ++k)
-    if (ok[k] && ADDLN_IN(site, 4 * col[k], 4 * VE, 4 * static_cast<int64_t>(H))) load_param<VE>(t, col[k], v, k);
+    if (ok[k] && ADDLN_IN(site, 4 * col[k], 4 * VE, 4 * static_cast<int64_t>(H))) load_param<VE>(t, 4u * col[k], v, k);
 }
 
 // Stores slots as fp32 columns of an [Hp] vector.
@@ -85,17 +88,17 @@ __device__ __forceinline__ void store_cols(float* t, const int (&col)[kE / VE], 
 
 // FULL: some norm is a layer norm or has a bias.  GR: a gate with rows.
 template <int DT, int VE, bool FULL, bool GR>
-__global__ void __launch_bounds__(kMaxThreads) k_block_bwd(const BlockBwdArgs p) {
+__global__ void __launch_bounds__(kMaxThreads) k_block_bwd(const __grid_constant__ BlockBwdArgs p) {
   constexpr int NV = kE / VE;
   [[maybe_unused]] constexpr int S = Io<DT>::kBytes;
   constexpr int A = sums_of(FULL);
   __shared__ float4 parts[2][kMaxWarps * kMaxCluster];
   const int T = blockDim.x, tid = threadIdx.x;
-  const int rank = p.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.C);
-  const int64_t walker = blockIdx.x / p.C;
-  const int col0 = rank * p.slice;
-  const int cols = min(p.slice, p.H - col0);
-  Exchange ex{parts, T / 32 * p.C, T / 32, p.C, rank, 0};
+  const int rank = p.w.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.w.C);
+  const int64_t walker = blockIdx.x / p.w.C;
+  const int col0 = rank * p.w.slice;
+  const int cols = min(p.w.slice, p.H - col0);
+  Exchange ex{parts, p.w, rank, 0};
   bool ok[NV];
   int col[NV];
 #pragma unroll
@@ -129,7 +132,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_block_bwd(const BlockBwdArgs p)
     if (has_dh) {
       Grp<DT, VE> r[NV];
       load_row<DT, VE>(p.dh, base, col, ok, 721, extent, r);
-      to_slots<DT, VE>(r, D);
+      to_slots<DT, VE, NV>(r, D);
     } else {
 #pragma unroll
       for (int j = 0; j < kE / 2; ++j) D[j] = dup2(0.f);
@@ -141,9 +144,9 @@ __global__ void __launch_bounds__(kMaxThreads) k_block_bwd(const BlockBwdArgs p)
       {
         Grp<DT, VE> r[NV];
         load_row<DT, VE>(p.dy, base, col, ok, 723, extent, r);
-        to_slots<DT, VE>(r, dy);
+        to_slots<DT, VE, NV>(r, dy);
         load_row<DT, VE>(p.h, base, col, ok, 724, extent, r);
-        to_slots<DT, VE>(r, hh);
+        to_slots<DT, VE, NV>(r, hh);
       }
       float mu = 0.f, rs = 0.f;
       if (ADDLN_IN(725, 4 * row, 4, 4 * p.rows)) {
@@ -177,7 +180,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_block_bwd(const BlockBwdArgs p)
       for (int j = 0; j < kE / 2; ++j) o[j] = mul2(a2, D[j]);
 #pragma unroll
       for (int k = 0; k < NV; ++k)
-        if (ok[k] && ADDLN_IN(727, (base + col[k]) * S, VE * S, extent)) store_group<DT, VE>(p.dx, base + col[k], o, k);
+        if (ok[k] && ADDLN_IN(727, (base + col[k]) * S, VE * S, extent)) store_group<DT, VE>(static_cast<char*>(p.dx) + (base + col[k]) * S, o, k);
     }
     // D becomes s D, then dn
     const float2 sc = dup2(p.s);
@@ -186,7 +189,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_block_bwd(const BlockBwdArgs p)
     float2 fh[kE / 2], pg[kE / 2];
     float pr = 1.f;
     if (need_f) {
-      to_slots<DT, VE>(rf, fh);
+      to_slots<DT, VE, NV>(rf, fh);
       if (post) {
         float pm = 0.f;
         if (ADDLN_IN(728, 4 * row, 4, 4 * p.rows)) {
@@ -211,7 +214,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_block_bwd(const BlockBwdArgs p)
       Grp<DT, VE> rg[NV];
       load_row<DT, VE>(p.gate, g * p.gate_stride, col, ok, 731, b_gate_bytes(p, S), rg);
       float2 gt[kE / 2];
-      to_slots<DT, VE>(rg, gt);
+      to_slots<DT, VE, NV>(rg, gt);
 #pragma unroll
       for (int j = 0; j < kE / 2; ++j) D[j] = mul2(D[j], gt[j]);
       if (--left == 0 || row + 1 == r1) {
@@ -222,7 +225,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_block_bwd(const BlockBwdArgs p)
 #pragma unroll
           for (int k = 0; k < NV && p.dgate != nullptr; ++k)
             if (ok[k] && ADDLN_IN(732, (gb + col[k]) * S, VE * S, p.gate_rows * static_cast<int64_t>(p.H) * S))
-              store_group<DT, VE>(p.dgate, gb + col[k], sd, k);
+              store_group<DT, VE>(static_cast<char*>(p.dgate) + (gb + col[k]) * S, sd, k);
         } else if (p.seg != nullptr) {
           store_cols<VE>(p.seg + (2 * walker + (first ? 0 : 1)) * p.Hp, col, ok, 733, p.Hp, sd);
         }
@@ -263,7 +266,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_block_bwd(const BlockBwdArgs p)
     }
 #pragma unroll
     for (int k = 0; k < NV; ++k)
-      if (ok[k] && ADDLN_IN(735, (base + col[k]) * S, VE * S, extent)) store_group<DT, VE>(p.df, base + col[k], D, k);
+      if (ok[k] && ADDLN_IN(735, (base + col[k]) * S, VE * S, extent)) store_group<DT, VE>(static_cast<char*>(p.df) + (base + col[k]) * S, D, k);
   }
   if (p.part != nullptr) {
     float* out = p.part + walker * A * p.Hp;
@@ -274,7 +277,7 @@ __global__ void __launch_bounds__(kMaxThreads) k_block_bwd(const BlockBwdArgs p)
       store_cols<VE>(out + 3 * p.Hp, col, ok, 739, p.Hp, s0);
     }
   }
-  if (p.C > 1) cooperative_groups::this_cluster().sync();
+  if (p.w.C > 1) cooperative_groups::this_cluster().sync();
 }
 
 // ------------------------------------------------------------ joining sums
@@ -413,6 +416,15 @@ namespace {
 
 using BwdKernel = void (*)(BlockBwdArgs);
 
+Shape shape_of(int H) {
+  Shape s;
+  s.C = (H + kSlice - 1) / kSlice;
+  s.slice = s.C == 1 ? H : ((H + s.C - 1) / s.C + 15) / 16 * 16;
+  s.threads = ((s.slice + kE - 1) / kE + 31) / 32 * 32;
+  s.rows = 1;
+  return s;
+}
+
 template <int DT, int VE>
 BwdKernel pick_ve(bool full, bool gr) {
   if (full) return gr ? &k_block_bwd<DT, VE, true, true> : &k_block_bwd<DT, VE, true, false>;
@@ -428,7 +440,7 @@ BwdKernel pick(int dtype, int access, bool full, bool gr) {
 
 // Walkers of a launch: those that fit the device at once, no more than rows.
 int64_t walkers_of(BwdKernel k, int64_t rows, const Shape& sh, const DeviceInfo& dev) {
-  const int fit = resident_walkers(reinterpret_cast<const void*>(k), sh.threads, sh.C, dev);
+  const int fit = resident_units(reinterpret_cast<const void*>(k), sh, 0, dev);
   if (fit < 0) return fit;
   return rows < fit ? rows : fit;
 }
@@ -463,8 +475,7 @@ int launch_block_bwd(int dtype, int access, bool full, BlockBwdArgs p, void* ws,
   const bool gr = p.gate_kind == ADDLN_GATE_ROWS;
   const Shape sh = shape_of(p.H);
   const BwdKernel k = pick(dtype, access, full, gr);
-  p.C = sh.C;
-  p.slice = sh.slice;
+  p.w = walk_of(sh);
   p.walkers = walkers_of(k, p.rows, sh, c.dev);
   if (p.walkers < 0) return static_cast<int>(p.walkers);
   p.Hp = (p.H + 3) / 4 * 4;
@@ -481,7 +492,7 @@ int launch_block_bwd(int dtype, int access, bool full, BlockBwdArgs p, void* ws,
     if (seg) p.seg = reinterpret_cast<float*>(static_cast<char*>(ws) + pb);
   }
   *name = access == 16 ? "block_bwd_v16" : access == 4 ? "block_bwd_v4" : "block_bwd_v2";
-  cudaError_t e = launch_walkers(k, p.walkers, sh, c, p);
+  cudaError_t e = launch_units(k, p.walkers, sh, 0, c, p);
   if (e == cudaSuccess && (cols || seg)) {
     const BwdKernel ks = dtype == kF32 ? pick_sums<kF32>(full) : dtype == kF16 ? pick_sums<kF16>(full) : pick_sums<kBF16>(full);
     const int64_t ny = seg ? shared_candidates(p.rows, p.walkers, p.gate_rows, p.rows_per_gate) : 0;

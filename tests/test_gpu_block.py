@@ -499,7 +499,11 @@ def test_module():
     assert y is None and torch.equal(h, x + f)
     g = torch.randn(4, 1, 256, device="cuda")
     h, _ = plain(f, x, gate=g)
-    assert torch.equal(h, torch.addcmul(x, f, g.expand_as(f)))
+    # x + f g: at most one rounding of the product (2^-24 of it) beside the
+    # sum's own, which assert_within counts; whether the product is rounded
+    # at all is not part of the definition, so no equality with another order
+    fg = f.cpu().double() * g.cpu().double()
+    assert_within(h, x.cpu().double() + fg, 2.0 ** -24 * fg.abs(), "h")
 
 
 def test_refusals_of_the_wrapper():
