@@ -160,14 +160,14 @@ struct Cols {
 // zeros for a group that does not exist) and alone reads them, so no barrier
 // is needed, and no register holds them.  Slot s of tensor i, group k:
 // [(s NT + i) NV + k][T].  Two-byte groups cannot be copied that way; they
-// wait in registers (one slot).
+// wait in registers, two in each (one slot).
 template <int DT, int VE, int NV, int NT>
 struct Ring {
   static constexpr int kBytes = Grp<DT, VE>::kBytes;
   static constexpr bool kAsync = kBytes >= 4;
   uint32_t base;  // this thread's first group of slot 0
   int step;       // bytes between neighbouring groups: T kBytes
-  Grp<DT, VE> held[kAsync ? 1 : NT][kAsync ? 1 : NV];
+  uint32_t held[kAsync ? 1 : NT][kAsync ? 1 : NV / 2];
 
   // group k of tensor i from src, if it exists
   __device__ __forceinline__ void fetch(int slot, int i, int k, const char* src, bool ok) {
@@ -179,8 +179,24 @@ struct Ring {
       else
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
     } else {
-      held[i][k].zero();
-      if (ok) held[i][k].load(src);
+      Grp<DT, VE> g;
+      g.zero();
+      if (ok) g.load(src);
+      held[i][k >> 1] = (k & 1) ? __byte_perm(held[i][k >> 1], g.w[0], 0x5410) : g.w[0];
+    }
+  }
+  // zeros for tensor i
+  __device__ __forceinline__ void clear(int slot, int i) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if constexpr (kAsync) {
+        const uint32_t dst = base + static_cast<uint32_t>((slot * NT + i) * NV + k) * step;
+#pragma unroll
+        for (int b = 0; b < kBytes; b += 4)
+          asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + b), "r"(0) : "memory");
+      } else {
+        held[i][k >> 1] = 0u;
+      }
     }
   }
   __device__ __forceinline__ void commit() {
@@ -205,7 +221,7 @@ struct Ring {
           asm volatile("ld.shared.u32 %0, [%1];" : "=r"(g[k].w[0]) : "r"(src));
         }
       } else {
-        g[k] = held[i][k0 + k];
+        g[k].w[0] = ((k0 + k) & 1) ? held[i][(k0 + k) >> 1] >> 16 : held[i][(k0 + k) >> 1] & 0xffffu;
       }
     }
   }

@@ -43,8 +43,8 @@ struct BlockFwdArgs {
   Walk w;
 };
 
-// Arguments of one backward launch (block_norm_bwd).  part: [walkers][A][Hp]
-// fp32 column partials; seg: [walkers][2][Hp] fp32 sums of a per-row gate's
+// Arguments of one backward launch (block_norm_bwd).  part: [parts][A][Hp]
+// fp32 column partials, one for each CTA or cluster; seg: [walkers][2][Hp] fp32 sums of a per-row gate's
 // gradient over the rows of a gate row that the walker shares with others
 // (first and last of its range).  Hp: H rounded up to 4.
 struct BlockBwdArgs {
@@ -69,11 +69,13 @@ struct BlockBwdArgs {
   float* dpre_beta;
   float* part;
   float* seg;
-  int64_t rows, walkers;
+  int64_t rows, walkers, parts;
   int64_t gate_rows, gate_stride, rows_per_gate;
   int H, Hp;
   int post, pre, gate_kind;
   float a, s, inv_h;
+  int kept_at, sums_at;  // where parameters and row sums lie in shared memory
+  int slots;
   Walk w;
 };
 

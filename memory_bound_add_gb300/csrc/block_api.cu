@@ -129,13 +129,15 @@ int64_t block_norm_bwd_workspace_size(int64_t rows, int64_t H, int dtype, int ga
   // the most over the access widths and kernels that the call may turn out to take
   int64_t most = 0;
   const int widths[3] = {16, 4, elem_bytes(dtype)};
-  for (int w : widths)
+  for (int w : widths) {
+    if (H * elem_bytes(dtype) % w != 0) continue;
     for (int full = 0; full < 2; ++full) {
       const int64_t n = addln::block_bwd_workspace_bytes(dtype, w, full != 0, rows, static_cast<int>(H), gate_kind,
                                                          rows_per_gate, c.dev);
       if (n < 0) return n;
       if (n > most) most = n;
     }
+  }
   return most;
 } catch (...) {
   return ADDLN_ERR_HOST_MEMORY;
@@ -213,7 +215,7 @@ int block_norm_bwd(const void* dy, const void* dh, const void* f, const void* h,
   if (rc != ADDLN_OK) return rc;
   addln::BlockBwdArgs p{dy, dh, f, h, post_mean, post_rstd, pre_mean, pre_rstd, post_gamma, post_beta, gate,
                         pre_gamma, df, dx, dpost_gamma, dpost_beta, dgate, dpre_gamma, dpre_beta, nullptr,
-                        nullptr, rows, 0, gate_rows, gate_stride, rows_per_gate, static_cast<int>(H), 0, post,
+                        nullptr, rows, 0, 0, gate_rows, gate_stride, rows_per_gate, static_cast<int>(H), 0, post,
                         pre, gate_kind, residual_scale, block_scale,
                         static_cast<float>(1.0 / static_cast<double>(H))};
   const bool full = post == ADDLN_NORM_LAYER || pre == ADDLN_NORM_LAYER || post_beta || dpost_beta || dpre_beta;

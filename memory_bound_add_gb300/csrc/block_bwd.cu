@@ -1,29 +1,38 @@
 // Backward of the block boundary (block_fwd.cu), in one pass over the rows.
-// With hhat = (h - mean_h) r_h, u = dy g, fhat = (f - mean_f) r_f:
-//   D  = r_h (u - mean(u) - hhat mean(u hhat)) + dh     (rms: no mean(u))
-//   dx = a D,  dn = s D gate
-//   v  = dn pg,  df = r_f (v - mean(v) - fhat mean(v fhat))
-// and over the rows dg = sum dy hhat, db = sum dy, dpg = sum dn fhat,
-// dpb = sum dn, dgate = sum s D (fhat pg + pb).
+// With hhat = (h - mean_h) r_h, u = dy g, fhat = (f - mean_f) r_f and
+// c = s gate pg (s gate without a post norm; the products' column factors):
+//   t  = r_h u + dh
+//   D  = t - r_h mean(u) - r_h mean(u hhat) hhat         (rms: no mean(u))
+//   dx = a D,  v = c D,  df = r_f (v - mean(v) - fhat mean(v fhat))
+// and over the rows dg = sum dy hhat, db = sum dy, and of D: dpg =
+// s sum gate D fhat, dpb = s sum gate D, dgate = s sum D (fhat pg + pb).
+//
+// One exchange a row.  The means of v and v fhat are those of D, which needs
+// the means of u and u hhat first; written out,
+//   sum v      = sum c t      - r_h mean(u) sum c      - r_h mean(u hhat) sum c hhat
+//   sum v fhat = sum c fhat t - r_h mean(u) sum c fhat - r_h mean(u hhat) sum c fhat hhat
+// so all the sums a row needs (8, without layer norms 3) are taken together.
+// The absolute error of such a difference is that of summing D itself, whose
+// elements are the same differences.
 //
 // Column sums.  A walker takes a contiguous range of rows and a thread
 // always the same columns, so its sums stay in registers.  Where one gate
 // row serves all rows (or there is none) two sums give three gradients:
-// with S1 = sum s D fhat and S0 = sum s D, dpg = gate S1, dpb = gate S0 and
-// dgate = pg S1 + pb S0.  With gate rows the sums over a gate row's rows are
-// written as soon as the range leaves it, rounded to the gate's type, when
-// all its rows are the walker's; a gate row shared with other walkers leaves
-// an fp32 partial.  k_block_sums adds all partials in a fixed order, so the
-// result does not depend on scheduling.
+// with S1 = sum D fhat and S0 = sum D, dpg = s gate S1, dpb = s gate S0 and
+// dgate = s (pg S1 + pb S0).  With gate rows the sums over a gate row's rows
+// are written as soon as the range leaves it, rounded to the gate's type,
+// when all its rows are the walker's; a gate row shared with other walkers
+// leaves an fp32 partial.  k_block_sums adds all partials in a fixed order,
+// so the result does not depend on scheduling.
+//
+// Several walkers share a CTA where a row needs few threads; they join their
+// column sums at the end, so that there is one partial for each CTA.
 #include "block.cuh"
 
 #include "block.h"
 
 namespace addln {
 namespace blk {
-
-constexpr int kE = 8;  // columns a thread
-constexpr int kSlice = kE * kMaxThreads;
 
 // First row of walker w's range.
 __host__ __device__ __forceinline__ int64_t range_begin(int64_t w, int64_t rows, int64_t walkers) {
@@ -42,291 +51,563 @@ __device__ __forceinline__ int64_t b_gate_bytes(const BlockBwdArgs& p, int S) {
 // dbeta and sum(s D) or dpb.
 __host__ __device__ constexpr int sums_of(bool full) { return full ? 4 : 2; }
 
-template <int DT, int VE>
-__device__ __forceinline__ void load_row(const void* t, int64_t base, const int (&col)[kE / VE],
-                                         const bool (&ok)[kE / VE], int site, int64_t extent,
-                                         Grp<DT, VE> (&r)[kE / VE]) {
-#pragma unroll
-  for (int k = 0; k < kE / VE; ++k) {
-    r[k].zero();
-    if (ok[k] && ADDLN_IN(site, (base + col[k]) * Io<DT>::kBytes, VE * Io<DT>::kBytes, extent))
-      r[k].load(static_cast<const char*>(t) + (base + col[k]) * Io<DT>::kBytes);
-  }
-}
-
-template <int VE>
-__device__ __forceinline__ void load_cols(const float* t, const int (&col)[kE / VE], const bool (&ok)[kE / VE],
-                                          int site, int H, float fill, float2 (&v)[kE / 2]) {
-#pragma unroll
-  for (int j = 0; j < kE / 2; ++j) v[j] = dup2(fill);
-  if (t == nullptr) return;
-#pragma unroll
-  for (int k = 0; k < kE / VE; ++k)
-    if (ok[k] && ADDLN_IN(site, 4 * col[k], 4 * VE, 4 * static_cast<int64_t>(H))) load_param<VE>(t, 4u * col[k], v, k);
-}
-
 // Stores slots as fp32 columns of an [Hp] vector.
-template <int VE>
-__device__ __forceinline__ void store_cols(float* t, const int (&col)[kE / VE], const bool (&ok)[kE / VE],
-                                           int site, int Hp, const float2 (&v)[kE / 2]) {
+template <int VE, int NV>
+__device__ __forceinline__ void store_cols(float* t, const Cols<VE, NV>& cs, int site, int Hp,
+                                           const float2 (&v)[NV * VE / 2]) {
 #pragma unroll
-  for (int k = 0; k < kE / VE; ++k) {
-    if (!ok[k] || !ADDLN_IN(site, 4 * col[k], 4 * VE, 4 * static_cast<int64_t>(Hp))) continue;
+  for (int k = 0; k < NV; ++k) {
+    if (!cs.ok[k] || !ADDLN_IN(site, 4 * cs.col(k), 4 * VE, 4 * static_cast<int64_t>(Hp))) continue;
+    float* q = t + cs.col(k);
     if constexpr (VE >= 4) {
 #pragma unroll
-      for (int q = 0; q < VE / 4; ++q)
-        *reinterpret_cast<float4*>(t + col[k] + 4 * q) =
-            make_float4(v[k * VE / 2 + 2 * q].x, v[k * VE / 2 + 2 * q].y, v[k * VE / 2 + 2 * q + 1].x,
-                        v[k * VE / 2 + 2 * q + 1].y);
+      for (int i = 0; i < VE / 4; ++i)
+        reinterpret_cast<float4*>(q)[i] =
+            make_float4(v[k * VE / 2 + 2 * i].x, v[k * VE / 2 + 2 * i].y, v[k * VE / 2 + 2 * i + 1].x,
+                        v[k * VE / 2 + 2 * i + 1].y);
     } else if constexpr (VE == 2) {
-      *reinterpret_cast<float2*>(t + col[k]) = v[k];
+      *reinterpret_cast<float2*>(q) = v[k];
     } else {
-      t[col[k]] = get_slot(v, k);
+      *q = get_slot(v, k);
     }
   }
 }
 
-// FULL: some norm is a layer norm or has a bias.  GR: a gate with rows.
-template <int DT, int VE, bool FULL, bool GR>
-__global__ void __launch_bounds__(kMaxThreads) k_block_bwd(const __grid_constant__ BlockBwdArgs p) {
-  constexpr int NV = kE / VE;
-  [[maybe_unused]] constexpr int S = Io<DT>::kBytes;
-  constexpr int A = sums_of(FULL);
-  __shared__ float4 parts[2][kMaxWarps * kMaxCluster];
-  const int T = blockDim.x, tid = threadIdx.x;
-  const int rank = p.w.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.w.C);
-  const int64_t walker = blockIdx.x / p.w.C;
-  const int col0 = rank * p.w.slice;
-  const int cols = min(p.w.slice, p.H - col0);
-  Exchange ex{parts, p.w, rank, 0};
-  bool ok[NV];
-  int col[NV];
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    ok[k] = (k * T + tid) * VE < cols;
-    col[k] = col0 + (k * T + tid) * VE;
-  }
-  pdl_trigger();
-  pdl_wait();
+// A thread's parameters in its own places of shared memory: part q of group k
+// of vector i at [((i NV + k) Q + q)][T], so that a warp's reads are
+// contiguous.  Vector 0: gamma of the pre norm; 1: the factor c, or with gate
+// rows s pg (c is then that times the gate); 2: s pb.
+template <int VE, int NV>
+struct Kept {
+  static constexpr int kPart = VE >= 4 ? 16 : VE * 4;
+  static constexpr int Q = VE * 4 / kPart;
+  uint32_t base;
+  int step;  // bytes between parts: threads of the CTA times kPart
 
-  const int64_t r0 = range_begin(walker, p.rows, p.walkers);
-  const int64_t r1 = range_begin(walker + 1, p.rows, p.walkers);
+  __device__ __forceinline__ uint32_t at(int i, int k, int q) const {
+    return base + static_cast<uint32_t>((i * NV + k) * Q + q) * step;
+  }
+  __device__ __forceinline__ void put(int i, int k, const float (&v)[VE]) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      if constexpr (VE >= 4)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at(i, k, q)), "f"(v[4 * q]), "f"(v[4 * q + 1]),
+                     "f"(v[4 * q + 2]), "f"(v[4 * q + 3]) : "memory");
+      else if constexpr (VE == 2)
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at(i, k, q)), "f"(v[0]), "f"(v[1]) : "memory");
+      else
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at(i, k, q)), "f"(v[0]) : "memory");
+    }
+  }
+  // N groups from k0 on
+  template <int N>
+  __device__ __forceinline__ void get(int i, int k0, float2 (&v)[N * VE / 2]) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        if constexpr (VE >= 4) {
+          const uint4 u = ld_shared_v4(at(i, k0 + k, q));
+          v[k * VE / 2 + 2 * q] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+          v[k * VE / 2 + 2 * q + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+        } else if constexpr (VE == 2) {
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v[k].x), "=f"(v[k].y) : "r"(at(i, k0 + k, q)));
+        } else {
+          float f;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(at(i, k0 + k, q)));
+          if (k & 1) v[k >> 1].y = f; else v[k >> 1].x = f;
+        }
+      }
+  }
+};
+
+// K sums (4 or 8) over the walker's threads, the same bits in every thread.
+// Within a warp each step halves the sums a lane carries: 6 (9) exchanges
+// instead of 5 K.
+template <int K>
+struct Sums {
+  float* buf;  // [2][warps][K], this walker's
+  const Walk& w;
+  int rank, par, barrier;
+
+  __device__ __forceinline__ void operator()(float (&v)[K]) {
+    constexpr unsigned kAll = 0xffffffffu;
+    const int lane = threadIdx.x & 31;
+    constexpr int n = 32 / K;  // lanes that end up with the same sum
+    float x[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) x[i] = v[i];
+#pragma unroll
+    for (int off = 16, m = K; m > 1; off >>= 1, m >>= 1) {
+      const bool up = (lane & off) != 0;
+#pragma unroll
+      for (int i = 0; i < K / 2; ++i)
+        if (i < m / 2) {
+          const float mine = up ? x[i + m / 2] : x[i], other = up ? x[i] : x[i + m / 2];
+          x[i] = mine + __shfl_xor_sync(kAll, other, off);
+        }
+    }
+#pragma unroll
+    for (int off = 16 / K; off > 0; off >>= 1) x[0] += __shfl_xor_sync(kAll, x[0], off);
+    float t = x[0];
+    // the sum a lane carries: its top bits
+    const int at = lane / n;
+    if (w.warps > 1) {
+      float* b = buf + par * w.warps * K;
+      par ^= 1;
+      const int warp = (threadIdx.x >> 5) % w.cta_warps;
+      if (w.C == 1) {
+        if (lane % n == 0) b[warp * K + at] = t;
+        asm volatile("bar.sync %0, %1;" ::"r"(barrier), "r"(w.cta_warps * 32) : "memory");
+      } else {
+        namespace cg = cooperative_groups;
+        cg::cluster_group cl = cg::this_cluster();
+        if (lane % n == 0)
+          for (int c = 0; c < w.C; ++c) cl.map_shared_rank(b, c)[(rank * w.cta_warps + warp) * K + at] = t;
+        cl.sync();
+      }
+      // lane l adds sum l / n of the warps l % n, + n, ...
+      t = 0.f;
+      for (int i = lane % n; i < w.warps; i += n) t += b[i * K + at];
+#pragma unroll
+      for (int off = 16 / K; off > 0; off >>= 1) t += __shfl_xor_sync(kAll, t, off);
+    }
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = __shfl_sync(kAll, t, i * (32 / K));
+  }
+};
+
+template <int DT, int VE, int NV, bool FULL, bool GR>
+constexpr int bwd_regs() {
+  return 128;
+}
+
+// FULL: some norm is a layer norm or has a bias.  GR: a gate with rows.
+template <int DT, int VE, int NV, bool FULL, bool GR>
+__global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV, FULL, GR>()))
+    k_block_bwd(const __grid_constant__ BlockBwdArgs p) {
+  constexpr int S = Io<DT>::kBytes;
+  constexpr int GB = Grp<DT, VE>::kBytes;
+  constexpr int A = sums_of(FULL), K = FULL ? 8 : 4;
+  constexpr int NT = GR ? 5 : 4;
+  constexpr int P = NV * VE / 2;
+  constexpr int kStepBytes = Cols<VE, NV>::kStep * S;
+  // groups that share slots in pairs (single elements) go two at a time
+  constexpr int KU = VE >= 2 ? 1 : 2, N = VE >= 2 ? VE / 2 : 1;
+  using R = Ring<DT, VE, NV, NT>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  const int T = p.w.cta_warps * 32;
+  const int side = p.w.rows_per_cta > 1 ? threadIdx.x / T : 0, tid = threadIdx.x - side * T;
+  const int rank = p.w.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.w.C);
+  const int64_t cta = blockIdx.x / p.w.C;
+  const int64_t walker = cta * p.w.rows_per_cta + side;
+  const int col0 = rank * p.w.slice;
+  const int slots = R::kAsync ? p.slots : 1;
+  R ring;
+  ring.step = blockDim.x * GB;
+  ring.base = smem_addr(smem) + threadIdx.x * GB;
+  Kept<VE, NV> kept;
+  kept.step = blockDim.x * Kept<VE, NV>::kPart;
+  kept.base = smem_addr(smem) + p.kept_at + threadIdx.x * Kept<VE, NV>::kPart;
+  Sums<K> sums{reinterpret_cast<float*>(smem + p.sums_at) + side * 2 * p.w.warps * K, p.w, rank, 0, 1 + side};
+  Cols<VE, NV> cs;
+  cs.init(tid >> 5, col0, min(p.w.slice, p.H - col0));
   const bool has_dy = p.dy != nullptr, has_dh = p.dh != nullptr;
   const bool post = p.post != ADDLN_NORM_NONE;
   const bool need_f = post || p.gate_kind != ADDLN_GATE_NONE;
   const int64_t extent = b_rows_bytes(p, S);
+  // a walker past the last has no rows
+  const int64_t r0 = min(p.rows, range_begin(walker, p.rows, p.walkers));
+  const int64_t r1 = min(p.rows, range_begin(walker + 1, p.rows, p.walkers));
 
-  float2 sg[kE / 2], sb[kE / 2], s1[kE / 2], s0[kE / 2], sd[kE / 2];
-#pragma unroll
-  for (int j = 0; j < kE / 2; ++j) sg[j] = sb[j] = s1[j] = s0[j] = sd[j] = dup2(0.f);
-  int64_t g = 0, left = 0;  // gate row, rows left of it
-  bool first = true;        // the gate row began before or at the range's begin
+  const int n = static_cast<int>(r1 - r0);  // rows of the walker
+  const int row_bytes = p.H * S;
+  // With gate rows: the byte offset of the gate row of the row to fetch next,
+  // and how many rows it still serves.
+  int gate_left = 0;
+  int64_t gate_at = 0;
+  auto clip = [](int64_t v) { return static_cast<int>(min(v, static_cast<int64_t>(0x7fffffff))); };
+  auto gate_of = [&](int64_t r) {
+    return p.rows <= 0x7fffffff ? static_cast<int64_t>(static_cast<uint32_t>(r) / static_cast<uint32_t>(p.rows_per_gate))
+                                : r / p.rows_per_gate;
+  };
   if constexpr (GR) {
-    g = r0 / p.rows_per_gate;
-    left = (g + 1) * p.rows_per_gate - r0;
+    const int64_t g = gate_of(r0);
+    gate_left = clip((g + 1) * p.rows_per_gate - r0);
+    gate_at = (g * p.gate_stride + cs.c0) * S;
   }
+  // row number i of the range, whose group 0 of this thread is at byte `at`
+  auto fetch = [&](int slot, int i, int64_t at) {
+    if (i < n) {
+      auto one = [&](int i, const void* t, int64_t off, int site, int64_t ext) {
+        const char* q = static_cast<const char*>(t) + off;
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          const bool in = ADDLN_IN(site, off + k * kStepBytes, cs.ok[k] ? GB : 0, ext);
+          ring.fetch(slot, i, k, q + k * kStepBytes, cs.ok[k] && in);
+        }
+      };
+      if (has_dy) {
+        one(0, p.dy, at, 723, extent);
+        one(1, p.h, at, 724, extent);
+      }
+      if (has_dh) one(2, p.dh, at, 721, extent);
+      if (need_f) one(3, p.f, at, 722, extent);
+      if constexpr (GR) {
+        one(4, p.gate, gate_at, 731, b_gate_bytes(p, S));
+        if (--gate_left == 0) {
+          gate_left = clip(p.rows_per_gate);
+          gate_at += p.gate_stride * S;
+        }
+      }
+    }
+    ring.commit();
+  };
+  // While the previous kernel of the stream may still be finishing, ask L2
+  // for the walker's first rows (hints alone, as in the forward).
+  if (r0 < r1 && r1 - r0 <= 8) {
+    const int ln = tid & 31, chunk0 = cs.c0 * S - ln * GB;
+    const int bytes = min(NV * kStepBytes, (col0 + min(p.w.slice, p.H - col0)) * S - chunk0);
+    for (int s = 0; s < slots && r0 + s < r1; ++s) {
+      const int64_t at = (r0 + s) * p.H * S + chunk0 + ln * 128;
+      if (ln * 128 >= bytes || !ADDLN_IN(720, at, 1, extent)) break;
+      if (has_dy) prefetch_line(static_cast<const char*>(p.dy) + at), prefetch_line(static_cast<const char*>(p.h) + at);
+      if (has_dh) prefetch_line(static_cast<const char*>(p.dh) + at);
+      if (need_f) prefetch_line(static_cast<const char*>(p.f) + at);
+    }
+  }
+  pdl_trigger();
+  pdl_wait();
+  // A tensor that the call does not have is zeros, written once: the rows'
+  // arithmetic then needs no branches (u, hhat and dh are zeros, and rstd is
+  // 0 or, for fhat, 1).
+  for (int s = 0; s < slots; ++s) {
+    if (!has_dy) ring.clear(s, 0), ring.clear(s, 1);
+    if (!has_dh) ring.clear(s, 2);
+    if (!need_f) ring.clear(s, 3);
+  }
+  if constexpr (R::kAsync)
+    for (int s = 0; s < slots; ++s) fetch(s, s, (r0 + s) * row_bytes + cs.c0 * S);
 
-  for (int64_t row = r0; row < r1; ++row) {
-    const int64_t base = row * p.H;
-    float2 D[kE / 2];
-    if (has_dh) {
-      Grp<DT, VE> r[NV];
-      load_row<DT, VE>(p.dh, base, col, ok, 721, extent, r);
-      to_slots<DT, VE, NV>(r, D);
-    } else {
+  // parameters, while the first rows arrive
 #pragma unroll
-      for (int j = 0; j < kE / 2; ++j) D[j] = dup2(0.f);
+  for (int k = 0; k < NV; ++k) {
+    float g[VE], w[VE], b[VE];
+#pragma unroll
+    for (int e = 0; e < VE; ++e) {
+      const uint32_t c = cs.par[k] / 4u + e;
+      const bool in = ADDLN_IN(726, 4 * c, 4, 4 * static_cast<int64_t>(p.H));
+      g[e] = has_dy && in ? __ldg(p.pre_gamma + c) : 0.f;
+      w[e] = p.s;
+      if (!GR && p.gate_kind == ADDLN_GATE_CHANNEL && in) w[e] *= __ldg(static_cast<const float*>(p.gate) + c);
+      if (post && in) w[e] *= __ldg(p.post_gamma + c);
+      b[e] = FULL && GR && p.post_beta && in ? p.s * __ldg(p.post_beta + c) : 0.f;
+      if (!cs.ok[k]) g[e] = w[e] = b[e] = 0.f;
     }
-    Grp<DT, VE> rf[NV];
-    if (need_f) load_row<DT, VE>(p.f, base, col, ok, 722, extent, rf);
-    if (has_dy) {
-      float2 dy[kE / 2], hh[kE / 2], u[kE / 2];
-      {
-        Grp<DT, VE> r[NV];
-        load_row<DT, VE>(p.dy, base, col, ok, 723, extent, r);
-        to_slots<DT, VE, NV>(r, dy);
-        load_row<DT, VE>(p.h, base, col, ok, 724, extent, r);
-        to_slots<DT, VE, NV>(r, hh);
-      }
-      float mu = 0.f, rs = 0.f;
-      if (ADDLN_IN(725, 4 * row, 4, 4 * p.rows)) {
-        rs = __ldg(p.pre_rstd + row);
-        if (FULL && p.pre == ADDLN_NORM_LAYER) mu = __ldg(p.pre_mean + row);
-      }
-      const float2 negmu = dup2(-mu), rs2 = dup2(rs);
-      load_cols<VE>(p.pre_gamma, col, ok, 726, p.H, 0.f, u);
-      float2 t1 = dup2(0.f), t2 = dup2(0.f);
+    kept.put(0, k, g);
+    kept.put(1, k, w);
+    if constexpr (FULL && GR) kept.put(2, k, b);
+  }
+  // statistics of the next row, loaded a row ahead
+  float hm_n = 0.f, hr_n = 0.f, fm_n = 0.f, fr_n = 1.f;
+  auto stats = [&](int64_t r) {
+    if (r >= r1 || !ADDLN_IN(725, 4 * r, 4, 4 * p.rows)) return;
+    if (has_dy) hr_n = __ldg(p.pre_rstd + r);
+    if (post) fr_n = __ldg(p.post_rstd + r);
+    if constexpr (FULL) {
+      if (p.pre_mean) hm_n = __ldg(p.pre_mean + r);
+      if (p.post_mean) fm_n = __ldg(p.post_mean + r);
+    }
+  };
+  stats(r0);
+
+  // The gate's sums of single-element rows lie in shared memory (whose ring is
+  // not used): beside the waiting elements they would spill.
+  constexpr bool kSdOut = GR && FULL && !R::kAsync;
+  float* sd_at = reinterpret_cast<float*>(smem) + threadIdx.x;
+  auto get_sd = [&](int j) {
+    return make_float2(sd_at[2 * j * blockDim.x], sd_at[(2 * j + 1) * blockDim.x]);
+  };
+  auto put_sd = [&](int j, float2 v) {
+    sd_at[2 * j * blockDim.x] = v.x;
+    sd_at[(2 * j + 1) * blockDim.x] = v.y;
+  };
+  float2 sg[P], s1[P], sb[FULL ? P : 1], s0[FULL ? P : 1], sd[GR && !kSdOut ? P : 1];
 #pragma unroll
-      for (int j = 0; j < kE / 2; ++j) {
-        hh[j] = mul2(add2(hh[j], negmu), rs2);
-        u[j] = mul2(u[j], dy[j]);
-        sg[j] = fma2(dy[j], hh[j], sg[j]);
+  for (int j = 0; j < P; ++j) {
+    sg[j] = s1[j] = dup2(0.f);
+    if constexpr (FULL) sb[j] = s0[j] = dup2(0.f);
+    if constexpr (kSdOut) put_sd(j, dup2(0.f));
+    else if constexpr (GR) sd[j] = dup2(0.f);
+  }
+  // rows left of the current gate row
+  int flush = 0;
+  if constexpr (GR) flush = clip((gate_of(r0) + 1) * p.rows_per_gate - r0);
+
+  int slot = 0;
+  int64_t off = r0 * row_bytes + cs.c0 * S;
+  for (int it = 0; it < n; ++it, off += row_bytes) {
+    if constexpr (!R::kAsync) fetch(0, it, off);
+    if (slots == 1) ring.template wait<0>(); else ring.template wait<1>();
+    const float2 nhm = dup2(-hm_n), hr = dup2(hr_n), nfm = dup2(-fm_n), fr = dup2(fr_n);
+    stats(r0 + it + 1);
+    auto take = [&](int i, int k, float2 (&v)[N]) {
+      Grp<DT, VE> r[KU];
+      ring.template take<KU>(slot, i, k, r);
+      to_slots<DT, VE, KU>(r, v);
+    };
+    auto hat = [&](int i, int k, float2 negm, float2 r, float2 (&v)[N]) {
+      take(i, k, v);
+#pragma unroll
+      for (int i = 0; i < N; ++i) v[i] = mul2(FULL ? add2(v[i], negm) : v[i], r);
+    };
+
+    float2 t[P];
+    float2 q[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) q[i] = dup2(0.f);
+#pragma unroll
+    for (int k = 0; k < NV; k += KU) {
+      float2 hh[N], fh[N], c[N], dy[N], d[N], u[N];
+      const int j0 = VE >= 2 ? k * VE / 2 : k / 2;
+      hat(1, k, nhm, hr, hh);
+      hat(3, k, nfm, fr, fh);
+      take(0, k, dy);
+      take(2, k, d);
+      kept.template get<KU>(0, k, u);
+      kept.template get<KU>(1, k, c);
+      if constexpr (GR) {
+        float2 gt[N];
+        take(4, k, gt);
+#pragma unroll
+        for (int i = 0; i < N; ++i) c[i] = mul2(c[i], gt[i]);
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        u[i] = mul2(u[i], dy[i]);
+        sg[j0 + i] = fma2(dy[i], hh[i], sg[j0 + i]);
+        q[0] = fma2(u[i], hh[i], q[0]);
+        const float2 tt = fma2(hr, u[i], d[i]);
+        t[j0 + i] = tt;
+        const float2 cf = mul2(c[i], fh[i]);
+        q[1] = fma2(cf, tt, q[1]);
+        q[2] = fma2(cf, hh[i], q[2]);
         if constexpr (FULL) {
-          sb[j] = add2(sb[j], dy[j]);
-          t1 = add2(t1, u[j]);
+          sb[j0 + i] = add2(sb[j0 + i], dy[i]);
+          q[3] = add2(q[3], u[i]);
+          q[4] = fma2(c[i], tt, q[4]);
+          q[5] = fma2(c[i], hh[i], q[5]);
+          q[6] = add2(q[6], c[i]);
+          q[7] = add2(q[7], cf);
         }
-        t2 = fma2(u[j], hh[j], t2);
-      }
-      const float2 t = walker_sum2(ex, make_float2(t1.x + t1.y, t2.x + t2.y));
-      const float2 nm = dup2(FULL && p.pre == ADDLN_NORM_LAYER ? -(t.x * p.inv_h) : 0.f);
-      const float2 nmx = dup2(-(t.y * p.inv_h));
-#pragma unroll
-      for (int j = 0; j < kE / 2; ++j) D[j] = fma2(rs2, add2(u[j], fma2(hh[j], nmx, nm)), D[j]);
-    }
-    {
-      float2 o[kE / 2];
-      const float2 a2 = dup2(p.a);
-#pragma unroll
-      for (int j = 0; j < kE / 2; ++j) o[j] = mul2(a2, D[j]);
-#pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (ok[k] && ADDLN_IN(727, (base + col[k]) * S, VE * S, extent)) store_group<DT, VE>(static_cast<char*>(p.dx) + (base + col[k]) * S, o, k);
-    }
-    // D becomes s D, then dn
-    const float2 sc = dup2(p.s);
-#pragma unroll
-    for (int j = 0; j < kE / 2; ++j) D[j] = mul2(sc, D[j]);
-    float2 fh[kE / 2], pg[kE / 2];
-    float pr = 1.f;
-    if (need_f) {
-      to_slots<DT, VE, NV>(rf, fh);
-      if (post) {
-        float pm = 0.f;
-        if (ADDLN_IN(728, 4 * row, 4, 4 * p.rows)) {
-          pr = __ldg(p.post_rstd + row);
-          if (FULL && p.post == ADDLN_NORM_LAYER) pm = __ldg(p.post_mean + row);
-        }
-        const float2 npm = dup2(-pm), pr2 = dup2(pr);
-#pragma unroll
-        for (int j = 0; j < kE / 2; ++j) fh[j] = mul2(add2(fh[j], npm), pr2);
       }
     }
-    if (post) load_cols<VE>(p.post_gamma, col, ok, 729, p.H, 0.f, pg);
+    float m[K];
+#pragma unroll
+    for (int i = 0; i < K; ++i) m[i] = q[i].x + q[i].y;
+    if (has_dy || post) sums(m);
+    // r_h mean(u hhat), r_h mean(u), mean(v fhat), mean(v)
+    const float a2 = hr.x * (m[0] * p.inv_h);
+    float a1 = 0.f, v2 = m[1] - a2 * m[2], v1 = 0.f;
+    if constexpr (FULL) {
+      if (p.pre == ADDLN_NORM_LAYER) a1 = hr.x * (m[FULL ? 3 : 0] * p.inv_h);
+      v2 -= a1 * m[FULL ? 7 : 0];
+      if (p.post == ADDLN_NORM_LAYER) v1 = (m[FULL ? 4 : 0] - a2 * m[FULL ? 5 : 0] - a1 * m[FULL ? 6 : 0]) * p.inv_h;
+    }
+    v2 *= p.inv_h;
+    const float2 na2 = dup2(-a2), na1 = dup2(-a1), nv2 = dup2(-v2), nv1 = dup2(-v1), pa = dup2(p.a);
+    char* dx = static_cast<char*>(p.dx) + off;
+    char* df = static_cast<char*>(p.df) + off;
+#pragma unroll
+    for (int k = 0; k < NV; k += KU) {
+      float2 hh[N], fh[N], c[N], o[N];
+      const int j0 = VE >= 2 ? k * VE / 2 : k / 2;
+      hat(1, k, nhm, hr, hh);
+      hat(3, k, nfm, fr, fh);
+      kept.template get<KU>(1, k, c);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        t[j0 + i] = fma2(na2, hh[i], FULL ? add2(t[j0 + i], na1) : t[j0 + i]);
+        o[i] = mul2(pa, t[j0 + i]);
+      }
+#pragma unroll
+      for (int e = 0; e < KU; ++e)
+        if (cs.ok[k + e] && ADDLN_IN(727, off + (k + e) * kStepBytes, GB, extent))
+          store_group<DT, VE>(dx + (k + e) * kStepBytes, o, e);
+      if constexpr (GR) {
+        // the gate's own gradient D (fhat w + b), and D times the gate
+        float2 b[N], gt[N];
+        if constexpr (FULL) kept.template get<KU>(2, k, b);
+        take(4, k, gt);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+          const float2 D = t[j0 + i];
+          const float2 nn = FULL ? fma2(fh[i], c[i], b[i]) : mul2(fh[i], c[i]);
+          if constexpr (kSdOut) put_sd(j0 + i, fma2(D, nn, get_sd(j0 + i)));
+          else sd[j0 + i] = fma2(D, nn, sd[j0 + i]);
+          t[j0 + i] = mul2(D, gt[i]);
+        }
+      }
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        s1[j0 + i] = fma2(t[j0 + i], fh[i], s1[j0 + i]);
+        if constexpr (FULL) s0[j0 + i] = add2(s0[j0 + i], t[j0 + i]);
+        o[i] = mul2(c[i], t[j0 + i]);
+      }
+      if (post)
+#pragma unroll
+        for (int i = 0; i < N; ++i) o[i] = mul2(fr, fma2(fh[i], nv2, FULL ? add2(o[i], nv1) : o[i]));
+#pragma unroll
+      for (int e = 0; e < KU; ++e)
+        if (cs.ok[k + e] && ADDLN_IN(735, off + (k + e) * kStepBytes, GB, extent))
+          store_group<DT, VE>(df + (k + e) * kStepBytes, o, e);
+    }
+    if constexpr (R::kAsync) fetch(slot, it + slots, off + slots * row_bytes);  // the slot has been read
+    slot = slot + 1 == slots ? 0 : slot + 1;
     if constexpr (GR) {
-      // the gate's gradient s D n, then dn = s D gate
-      float2 b[kE / 2];
-      load_cols<VE>(FULL && post ? p.post_beta : nullptr, col, ok, 730, p.H, 0.f, b);
+      if (--flush == 0 || it + 1 == n) {
+        const int64_t row = r0 + it, g = gate_of(row), begin = g * p.rows_per_gate;
+        const bool whole = begin >= r0 && row + 1 == min(p.rows, begin + p.rows_per_gate);
+        float2 sv[P];
 #pragma unroll
-      for (int j = 0; j < kE / 2; ++j) {
-        const float2 n = post ? fma2(fh[j], pg[j], b[j]) : fh[j];
-        sd[j] = fma2(D[j], n, sd[j]);
-      }
-      Grp<DT, VE> rg[NV];
-      load_row<DT, VE>(p.gate, g * p.gate_stride, col, ok, 731, b_gate_bytes(p, S), rg);
-      float2 gt[kE / 2];
-      to_slots<DT, VE, NV>(rg, gt);
-#pragma unroll
-      for (int j = 0; j < kE / 2; ++j) D[j] = mul2(D[j], gt[j]);
-      if (--left == 0 || row + 1 == r1) {
-        const bool begun_here = !first || g * p.rows_per_gate >= r0;
-        const bool ends_here = left == 0 || row + 1 == p.rows;
-        if (begun_here && ends_here) {
-          const int64_t gb = g * p.H;
-#pragma unroll
-          for (int k = 0; k < NV && p.dgate != nullptr; ++k)
-            if (ok[k] && ADDLN_IN(732, (gb + col[k]) * S, VE * S, p.gate_rows * static_cast<int64_t>(p.H) * S))
-              store_group<DT, VE>(static_cast<char*>(p.dgate) + (gb + col[k]) * S, sd, k);
-        } else if (p.seg != nullptr) {
-          store_cols<VE>(p.seg + (2 * walker + (first ? 0 : 1)) * p.Hp, col, ok, 733, p.Hp, sd);
+        for (int j = 0; j < P; ++j) {
+          if constexpr (kSdOut) {
+            sv[j] = get_sd(j);
+            put_sd(j, dup2(0.f));
+          } else {
+            sv[j] = sd[j];
+            sd[j] = dup2(0.f);
+          }
         }
+        if (whole) {
+          const int64_t gb = (g * p.H + cs.c0) * S;
+          char* out = static_cast<char*>(p.dgate) + gb;
 #pragma unroll
-        for (int j = 0; j < kE / 2; ++j) sd[j] = dup2(0.f);
-        first = false;
-        left = p.rows_per_gate;
-        ++g;
+          for (int k = 0; k < NV; ++k)
+            if (p.dgate != nullptr && cs.ok[k] &&
+                ADDLN_IN(732, gb + k * kStepBytes, GB, p.gate_rows * static_cast<int64_t>(p.H) * S))
+              store_group<DT, VE>(out + k * kStepBytes, sv, k);
+        } else if (p.seg != nullptr) {
+          // the range's first gate row, or its last
+          store_cols<VE, NV>(p.seg + (2 * walker + (begin <= r0 ? 0 : 1)) * p.Hp, cs, 733, p.Hp, sv);
+        }
+        flush = clip(p.rows_per_gate);
       }
     }
-    // column sums of dn fhat and dn (GR), or of s D fhat and s D
-    if (need_f) {
-#pragma unroll
-      for (int j = 0; j < kE / 2; ++j) {
-        s1[j] = fma2(D[j], fh[j], s1[j]);
-        if constexpr (FULL) s0[j] = add2(s0[j], D[j]);
-      }
-    }
-    if (!GR && p.gate_kind == ADDLN_GATE_CHANNEL) {
-      float2 gt[kE / 2];
-      load_cols<VE>(static_cast<const float*>(p.gate), col, ok, 734, p.H, 0.f, gt);
-#pragma unroll
-      for (int j = 0; j < kE / 2; ++j) D[j] = mul2(D[j], gt[j]);
-    }
-    if (post) {
-      float2 t1 = dup2(0.f), t2 = dup2(0.f);
-#pragma unroll
-      for (int j = 0; j < kE / 2; ++j) {
-        D[j] = mul2(D[j], pg[j]);
-        if constexpr (FULL) t1 = add2(t1, D[j]);
-        t2 = fma2(D[j], fh[j], t2);
-      }
-      const float2 t = walker_sum2(ex, make_float2(t1.x + t1.y, t2.x + t2.y));
-      const float2 nm = dup2(FULL && p.post == ADDLN_NORM_LAYER ? -(t.x * p.inv_h) : 0.f);
-      const float2 nmx = dup2(-(t.y * p.inv_h)), pr2 = dup2(pr);
-#pragma unroll
-      for (int j = 0; j < kE / 2; ++j) D[j] = mul2(pr2, add2(D[j], fma2(fh[j], nmx, nm)));
-    }
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (ok[k] && ADDLN_IN(735, (base + col[k]) * S, VE * S, extent)) store_group<DT, VE>(static_cast<char*>(p.df) + (base + col[k]) * S, D, k);
   }
   if (p.part != nullptr) {
-    float* out = p.part + walker * A * p.Hp;
-    store_cols<VE>(out, col, ok, 736, p.Hp, sg);
-    store_cols<VE>(out + p.Hp, col, ok, 737, p.Hp, s1);
-    if constexpr (FULL) {
-      store_cols<VE>(out + 2 * p.Hp, col, ok, 738, p.Hp, sb);
-      store_cols<VE>(out + 3 * p.Hp, col, ok, 739, p.Hp, s0);
+    // the CTA's walkers join their sums in shared memory, halving their number
+    // (the ring is free: what is in flight arrives first)
+    int top = 1;
+    while (top < p.w.rows_per_cta) top *= 2;
+    if (top > 1) {
+      ring.template wait<0>();
+      __syncthreads();
+    }
+    for (int half = top / 2; half > 0; half /= 2) {
+      const int to = side < half ? side : side - half;
+      float* at = reinterpret_cast<float*>(smem) + static_cast<int64_t>(to) * A * 2 * P * T + tid;
+      const bool gives = side >= half && side < 2 * half, gets = side < half && side + half < p.w.rows_per_cta;
+      auto give = [&](const float2 (&v)[P], int a) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          at[(a * 2 * P + 2 * j) * T] = v[j].x;
+          at[(a * 2 * P + 2 * j + 1) * T] = v[j].y;
+        }
+      };
+      auto get = [&](float2 (&v)[P], int a) {
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+          v[j] = add2(v[j], make_float2(at[(a * 2 * P + 2 * j) * T], at[(a * 2 * P + 2 * j + 1) * T]));
+      };
+      if (gives) {
+        give(sg, 0);
+        give(s1, 1);
+        if constexpr (FULL) give(sb, 2), give(s0, 3);
+      }
+      __syncthreads();
+      if (gets) {
+        get(sg, 0);
+        get(s1, 1);
+        if constexpr (FULL) get(sb, 2), get(s0, 3);
+      }
+      __syncthreads();
+    }
+    if (side == 0) {
+      float* out = p.part + cta * A * p.Hp;
+      store_cols<VE, NV>(out, cs, 736, p.Hp, sg);
+      store_cols<VE, NV>(out + p.Hp, cs, 737, p.Hp, s1);
+      if constexpr (FULL) {
+        store_cols<VE, NV>(out + 2 * p.Hp, cs, 738, p.Hp, sb);
+        store_cols<VE, NV>(out + 3 * p.Hp, cs, 739, p.Hp, s0);
+      }
     }
   }
   if (p.w.C > 1) cooperative_groups::this_cluster().sync();
 }
 
 // ------------------------------------------------------------ joining sums
-// blockIdx.y == 0: the walkers' column sums of kQuads column quads, added in
-// a fixed order (thread t takes quad t % kQuads and the walkers t / kQuads,
-// + kSlices, ...; then a butterfly over the warp's lanes of that quad and
-// the warps in order), and from them the gradients of both norms and of a
-// per-channel gate.  blockIdx.y > 0: the gate rows that several walkers
-// share, the walkers in order.
-constexpr int kSumThreads = 256, kQuads = 4, kSlices = kSumThreads / kQuads;
+// blockIdx.y == 0: the CTAs' column sums of QUADS column quads, added in a
+// fixed order (thread t takes quad t % QUADS and the partials t / QUADS,
+// + kSumThreads / QUADS, ...; then a butterfly over the warp's lanes of that
+// quad and the warps in order), and from them the gradients of both norms
+// and of a per-channel gate.  blockIdx.y > 0: the gate rows that several
+// walkers share, the walkers in order.  The partials sit in L2 and the
+// kernel's time is its latency, so a thread's loads of all A sums are in
+// flight together.
+constexpr int kSumThreads = 256;
 
 __device__ __forceinline__ float4 add4(float4 a, float4 b) {
   return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
 }
 
-// Sum over i < n of the quad at src + i * ld (in floats); every thread of the
-// block takes part, the result is in the threads below kQuads.
-__device__ __forceinline__ float4 block_quad_sum(const float* src, int64_t n, int64_t ld, bool in,
-                                                 int64_t extent, float4 (*wsum)[kQuads]) {
-  constexpr int kU = 8;  // loads in flight a thread
+// r[a] = sum over i < n of the quad at src + i * ld + a * la (in floats);
+// every thread of the block takes part, the result is in the threads below
+// QUADS.
+template <int A, int QUADS>
+__device__ __forceinline__ void block_quad_sums(const float* src, int64_t n, int64_t ld, int64_t la, bool in,
+                                                int64_t extent, float4 (*wsum)[A][QUADS], float4 (&r)[A]) {
+  constexpr int kU = 8 / A;  // partials a thread has in flight
+  constexpr int kStep = kSumThreads / QUADS;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+  for (int a = 0; a < A; ++a) r[a] = make_float4(0.f, 0.f, 0.f, 0.f);
   if (in)
-    for (int64_t i0 = t / kQuads; i0 < n; i0 += kSlices * kU) {
-      float4 v[kU];
+    for (int64_t i0 = t / QUADS; i0 < n; i0 += kStep * kU) {
+      float4 v[kU][A];
 #pragma unroll
-      for (int u = 0; u < kU; ++u) {
-        const int64_t i = i0 + u * kSlices;
-        v[u] = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (i < n && ADDLN_IN(741, i * ld * 4, 16, extent))
-          v[u] = __ldcg(reinterpret_cast<const float4*>(src + i * ld));
-      }
+      for (int u = 0; u < kU; ++u)
 #pragma unroll
-      for (int u = 0; u < kU; ++u) acc = add4(acc, v[u]);
+        for (int a = 0; a < A; ++a) {
+          const int64_t i = i0 + u * kStep;
+          v[u][a] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < n && ADDLN_IN(741, (i * ld + a * la) * 4, 16, extent))
+            v[u][a] = __ldcg(reinterpret_cast<const float4*>(src + i * ld + a * la));
+        }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int a = 0; a < A; ++a) r[a] = add4(r[a], v[u][a]);
     }
 #pragma unroll
-  for (int off = kQuads; off < 32; off <<= 1) {
-    acc.x += __shfl_xor_sync(0xffffffffu, acc.x, off);
-    acc.y += __shfl_xor_sync(0xffffffffu, acc.y, off);
-    acc.z += __shfl_xor_sync(0xffffffffu, acc.z, off);
-    acc.w += __shfl_xor_sync(0xffffffffu, acc.w, off);
+  for (int a = 0; a < A; ++a) {
+#pragma unroll
+    for (int off = QUADS; off < 32; off <<= 1) {
+      r[a].x += __shfl_xor_sync(0xffffffffu, r[a].x, off);
+      r[a].y += __shfl_xor_sync(0xffffffffu, r[a].y, off);
+      r[a].z += __shfl_xor_sync(0xffffffffu, r[a].z, off);
+      r[a].w += __shfl_xor_sync(0xffffffffu, r[a].w, off);
+    }
+    if (lane < QUADS) wsum[warp][a][lane] = r[a];
   }
-  __syncthreads();  // the last call's sums have been read
-  if (lane < kQuads) wsum[warp][lane] = acc;
   __syncthreads();
-  float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (t < kQuads)
-    for (int w = 0; w < kSumThreads / 32; ++w) r = add4(r, wsum[w][t]);
-  return r;
+  if (t < QUADS)
+#pragma unroll
+    for (int a = 0; a < A; ++a) {
+      r[a] = wsum[0][a][t];
+#pragma unroll
+      for (int w = 1; w < kSumThreads / 32; ++w) r[a] = add4(r[a], wsum[w][a][t]);
+    }
 }
 
 // The gate rows that more than one walker shares.  Where walkers have at
@@ -338,22 +619,20 @@ __host__ __device__ __forceinline__ int64_t shared_candidates(int64_t rows, int6
   return rows / walkers >= rpg ? walkers - 1 : gate_rows;
 }
 
-template <int DT, bool FULL>
-__global__ void __launch_bounds__(kSumThreads) k_block_sums(const BlockBwdArgs p) {
+template <int DT, bool FULL, int QUADS>
+__global__ void __launch_bounds__(kSumThreads) k_block_sums(const __grid_constant__ BlockBwdArgs p) {
   constexpr int A = sums_of(FULL);
-  __shared__ float4 wsum[kSumThreads / 32][kQuads];
+  __shared__ float4 wsum[kSumThreads / 32][A][QUADS];
   pdl_trigger();
   pdl_wait();
   const int t = threadIdx.x;
-  const int j = (blockIdx.x * kQuads + t % kQuads) * 4;  // the thread's first column
+  const int j = (blockIdx.x * QUADS + t % QUADS) * 4;  // the thread's first column
   if (blockIdx.y == 0) {
     if (p.part == nullptr) return;
     float4 r[A];
-#pragma unroll
-    for (int a = 0; a < A; ++a)
-      r[a] = block_quad_sum(p.part + a * static_cast<int64_t>(p.Hp) + j, p.walkers, static_cast<int64_t>(A) * p.Hp,
-                            j < p.H, (p.walkers * A * p.Hp - a * static_cast<int64_t>(p.Hp) - j) * 4, wsum);
-    if (t >= kQuads) return;
+    block_quad_sums<A, QUADS>(p.part + j, p.parts, static_cast<int64_t>(A) * p.Hp, p.Hp, j < p.H,
+                              (p.parts * A * p.Hp - j) * 4, wsum, r);
+    if (t >= QUADS) return;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int c = j + q;
@@ -362,14 +641,14 @@ __global__ void __launch_bounds__(kSumThreads) k_block_sums(const BlockBwdArgs p
       if (p.dpre_gamma) p.dpre_gamma[c] = at(0);
       if (FULL && p.dpre_beta) p.dpre_beta[c] = at(FULL ? 2 : 0);
       const bool channel = p.gate_kind == ADDLN_GATE_CHANNEL;
-      const float gt = channel ? __ldg(static_cast<const float*>(p.gate) + c) : 1.f;
+      const float gt = channel ? p.s * __ldg(static_cast<const float*>(p.gate) + c) : p.s;
       if (p.dpost_gamma) p.dpost_gamma[c] = gt * at(1);
       if (FULL && p.dpost_beta) p.dpost_beta[c] = gt * at(FULL ? 3 : 1);
       if (channel && p.dgate) {
-        float d = at(1);
+        float d = p.s * at(1);
         if (p.post != ADDLN_NORM_NONE) {
           d *= __ldg(p.post_gamma + c);
-          if (FULL && p.post_beta) d = fmaf(__ldg(p.post_beta + c), at(FULL ? 3 : 1), d);
+          if (FULL && p.post_beta) d = fmaf(p.s * __ldg(p.post_beta + c), at(FULL ? 3 : 1), d);
         }
         static_cast<float*>(p.dgate)[c] = d;
       }
@@ -396,13 +675,14 @@ __global__ void __launch_bounds__(kSumThreads) k_block_sums(const BlockBwdArgs p
   const int64_t ex = p.walkers * 2 * p.Hp * 4;
   // walkers w0 + 1 .. w1 hold it in their first slot
   const float* src = p.seg + 2 * (w0 + 1) * p.Hp + j;
-  const float4 rest = block_quad_sum(src, w1 - w0, 2 * static_cast<int64_t>(p.Hp), j < p.H,
-                                     ex - (2 * (w0 + 1) * p.Hp + j) * 4, wsum);
-  if (t >= kQuads || j >= p.H) return;
+  float4 rest[1];
+  block_quad_sums<1, QUADS>(src, w1 - w0, 2 * static_cast<int64_t>(p.Hp), 0, j < p.H,
+                            ex - (2 * (w0 + 1) * p.Hp + j) * 4, reinterpret_cast<float4(*)[1][QUADS]>(wsum), rest);
+  if (t >= QUADS || j >= p.H) return;
   const int64_t at0 = (2 * w0 + (head ? 0 : 1)) * p.Hp + j;
   float4 r = make_float4(0.f, 0.f, 0.f, 0.f);
   if (ADDLN_IN(743, at0 * 4, 16, ex)) r = __ldcg(reinterpret_cast<const float4*>(p.seg + at0));
-  r = add4(r, rest);
+  r = add4(r, rest[0]);
   const float o[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
   for (int q = 0; q < 4; ++q)
@@ -416,43 +696,89 @@ namespace {
 
 using BwdKernel = void (*)(BlockBwdArgs);
 
-Shape shape_of(int H) {
-  Shape s;
-  s.C = (H + kSlice - 1) / kSlice;
-  s.slice = s.C == 1 ? H : ((H + s.C - 1) / s.C + 15) / 16 * 16;
-  s.threads = ((s.slice + kE - 1) / kE + 31) / 32 * 32;
-  s.rows = 1;
-  return s;
+struct Choice {
+  BwdKernel k = nullptr;
+  Shape sh{};
+  int smem = 0, kept_at = 0, sums_at = 0;
+};
+
+// NV groups of VE columns a thread; a CTA of kSideThreads threads for as many
+// rows side by side as fit it, else one CTA of up to kMaxThreads for a row,
+// else a cluster.  Shared memory: two slots of the ring (at least what the
+// walkers need to join their sums), the parameters, the row sums.
+constexpr int kSideThreads = 512;
+
+template <int DT, int VE, int NV, bool GR>
+Choice make(int H, bool full) {
+  Choice c;
+  c.k = &k_block_bwd<DT, VE, NV, false, GR>;
+  if constexpr (NV * VE <= 8)
+    if (full) c.k = &k_block_bwd<DT, VE, NV, true, GR>;
+  const int groups = H / VE;
+  c.sh.C = (groups + NV * kMaxThreads - 1) / (NV * kMaxThreads);
+  c.sh.slice = c.sh.C == 1 ? H : ((H + c.sh.C - 1) / c.sh.C + 15) / 16 * 16;
+  const int threads = ((c.sh.slice / VE + NV - 1) / NV + 31) / 32 * 32;
+  c.sh.rows = c.sh.C > 1 || threads > kSideThreads / 2 ? 1 : kSideThreads / threads;
+  c.sh.threads = threads * c.sh.rows;
+  const int nt = GR ? 5 : 4, np = full && GR ? 3 : 2, gb = Grp<DT, VE>::kBytes;
+  int ring = gb >= 4 ? 2 * nt * NV * c.sh.threads * gb : 0;
+  int half = 0;  // walkers that give their sums to another at once
+  for (int top = 1; top < c.sh.rows; top *= 2) half = top;
+  const int join = half * sums_of(full) * NV * VE * threads * 4;
+  if (ring < join) ring = join;
+  const int sd = GR && gb < 4 ? NV * VE * 4 * c.sh.threads : 0;
+  if (ring < sd) ring = sd;
+  c.kept_at = ring;
+  c.sums_at = c.kept_at + np * NV * VE * 4 * c.sh.threads;
+  c.smem = c.sums_at + c.sh.rows * 2 * (threads / 32) * c.sh.C * (full ? 8 : 4) * 4;
+  return c;
 }
 
-template <int DT, int VE>
-BwdKernel pick_ve(bool full, bool gr) {
-  if (full) return gr ? &k_block_bwd<DT, VE, true, true> : &k_block_bwd<DT, VE, true, false>;
-  return gr ? &k_block_bwd<DT, VE, false, true> : &k_block_bwd<DT, VE, false, false>;
+template <int DT, bool GR>
+Choice choose(int H, int access, bool full) {
+  constexpr int VEC = Io<DT>::kVec;
+  if constexpr (DT != kF32) {
+    // 16 columns a thread where the sums are two or three for a column, else 8
+    if (access == 16 && !full && H > 32 * VEC) return make<DT, VEC, 2, GR>(H, full);
+    if (access == 16) return make<DT, VEC, 1, GR>(H, full);
+    if (access == 4) return make<DT, 2, 4, GR>(H, full);
+    return make<DT, 1, 8, GR>(H, full);
+  } else {
+    return access == 16 ? make<DT, VEC, 2, GR>(H, full) : make<DT, 1, 8, GR>(H, full);
+  }
 }
 
-BwdKernel pick(int dtype, int access, bool full, bool gr) {
-  if (dtype == kF32) return access == 16 ? pick_ve<kF32, 4>(full, gr) : pick_ve<kF32, 1>(full, gr);
-  if (dtype == kF16)
-    return access == 16 ? pick_ve<kF16, 8>(full, gr) : access == 4 ? pick_ve<kF16, 2>(full, gr) : pick_ve<kF16, 1>(full, gr);
-  return access == 16 ? pick_ve<kBF16, 8>(full, gr) : access == 4 ? pick_ve<kBF16, 2>(full, gr) : pick_ve<kBF16, 1>(full, gr);
+Choice choose(int dtype, int H, int access, bool full, bool gr) {
+  if (dtype == kF32) return gr ? choose<kF32, true>(H, access, full) : choose<kF32, false>(H, access, full);
+  if (dtype == kF16) return gr ? choose<kF16, true>(H, access, full) : choose<kF16, false>(H, access, full);
+  return gr ? choose<kBF16, true>(H, access, full) : choose<kBF16, false>(H, access, full);
 }
 
-// Walkers of a launch: those that fit the device at once, no more than rows.
-int64_t walkers_of(BwdKernel k, int64_t rows, const Shape& sh, const DeviceInfo& dev) {
-  const int fit = resident_units(reinterpret_cast<const void*>(k), sh, 0, dev);
+// Units (CTAs or clusters) of a launch: those that fit the device at once, no
+// more than the rows need.
+int64_t units_of(const Choice& c, int64_t rows, const DeviceInfo& dev) {
+  const int fit = resident_units(reinterpret_cast<const void*>(c.k), c.sh, c.smem, dev);
   if (fit < 0) return fit;
-  return rows < fit ? rows : fit;
+  const int64_t need = (rows + c.sh.rows - 1) / c.sh.rows;
+  return need < fit ? need : fit;
 }
 
-int64_t part_bytes(int64_t walkers, bool full, int64_t Hp) { return walkers * sums_of(full) * Hp * 4; }
+int64_t part_bytes(int64_t parts, bool full, int64_t Hp) { return parts * sums_of(full) * Hp * 4; }
 int64_t seg_bytes(int64_t walkers, bool gr, int64_t rpg, int64_t Hp) {
   return gr && rpg > 1 ? walkers * 2 * Hp * 4 : 0;
 }
 
+// Quads a block: the most (of 2, 4, 8) whose partials a thread still loads in
+// one round.
+inline int sums_quads(int64_t parts, bool full) {
+  const int64_t one_round = kSumThreads * (8 / sums_of(full));
+  return 8 * parts <= one_round ? 8 : 4 * parts <= one_round ? 4 : 2;
+}
+
 template <int DT>
-BwdKernel pick_sums(bool full) {
-  return full ? &k_block_sums<DT, true> : &k_block_sums<DT, false>;
+BwdKernel pick_sums(bool full, int quads) {
+  if (full) return quads == 8 ? &k_block_sums<DT, true, 8> : quads == 4 ? &k_block_sums<DT, true, 4> : &k_block_sums<DT, true, 2>;
+  return quads == 8 ? &k_block_sums<DT, false, 8> : quads == 4 ? &k_block_sums<DT, false, 4> : &k_block_sums<DT, false, 2>;
 }
 
 }  // namespace
@@ -462,22 +788,26 @@ int64_t block_bwd_workspace_bytes(int dtype, int access, bool full, int64_t rows
                                   int64_t rows_per_gate, const DeviceInfo& dev) {
   using namespace blk;
   const bool gr = gate_kind == ADDLN_GATE_ROWS;
-  const Shape sh = shape_of(H);
-  const int64_t w = walkers_of(pick(dtype, access, full, gr), rows, sh, dev);
-  if (w < 0) return w;
+  const Choice ch = choose(dtype, H, access, full, gr);
+  const int64_t units = units_of(ch, rows, dev);
+  if (units < 0) return units;
   const int64_t Hp = (H + 3) / 4 * 4;
-  return part_bytes(w, full, Hp) + seg_bytes(w, gr, rows_per_gate, Hp);
+  return part_bytes(units, full, Hp) + seg_bytes(units * ch.sh.rows, gr, rows_per_gate, Hp);
 }
 
 int launch_block_bwd(int dtype, int access, bool full, BlockBwdArgs p, void* ws, int64_t ws_bytes,
                      const LaunchCtx& c, const char** name) {
   using namespace blk;
   const bool gr = p.gate_kind == ADDLN_GATE_ROWS;
-  const Shape sh = shape_of(p.H);
-  const BwdKernel k = pick(dtype, access, full, gr);
-  p.w = walk_of(sh);
-  p.walkers = walkers_of(k, p.rows, sh, c.dev);
-  if (p.walkers < 0) return static_cast<int>(p.walkers);
+  const Choice ch = choose(dtype, p.H, access, full, gr);
+  p.w = walk_of(ch.sh);
+  p.parts = units_of(ch, p.rows, c.dev);
+  if (p.parts < 0) return static_cast<int>(p.parts);
+  p.walkers = p.parts * ch.sh.rows;
+  if (p.walkers > p.rows) p.walkers = p.rows;
+  p.kept_at = ch.kept_at;
+  p.sums_at = ch.sums_at;
+  p.slots = 2;
   p.Hp = (p.H + 3) / 4 * 4;
   const bool cols = p.dpre_gamma || p.dpre_beta || p.dpost_gamma || p.dpost_beta ||
                     (p.dgate && p.gate_kind == ADDLN_GATE_CHANNEL);
@@ -485,18 +815,21 @@ int launch_block_bwd(int dtype, int access, bool full, BlockBwdArgs p, void* ws,
   p.part = nullptr;
   p.seg = nullptr;
   if (cols || seg) {
-    const int64_t pb = part_bytes(p.walkers, full, p.Hp);
-    const int64_t need = pb + seg_bytes(p.walkers, gr, p.rows_per_gate, p.Hp);
+    const int64_t pb = part_bytes(p.parts, full, p.Hp);
+    const int64_t need = pb + seg_bytes(p.parts * ch.sh.rows, gr, p.rows_per_gate, p.Hp);
     if (ws == nullptr || ws_bytes < need || (reinterpret_cast<uintptr_t>(ws) & 15u)) return ADDLN_ERR_WORKSPACE;
     if (cols) p.part = static_cast<float*>(ws);
     if (seg) p.seg = reinterpret_cast<float*>(static_cast<char*>(ws) + pb);
   }
   *name = access == 16 ? "block_bwd_v16" : access == 4 ? "block_bwd_v4" : "block_bwd_v2";
-  cudaError_t e = launch_units(k, p.walkers, sh, 0, c, p);
+  cudaError_t e = launch_units(ch.k, p.parts, ch.sh, ch.smem, c, p);
   if (e == cudaSuccess && (cols || seg)) {
-    const BwdKernel ks = dtype == kF32 ? pick_sums<kF32>(full) : dtype == kF16 ? pick_sums<kF16>(full) : pick_sums<kBF16>(full);
+    const int quads = sums_quads(p.parts, full);
+    const BwdKernel ks = dtype == kF32   ? pick_sums<kF32>(full, quads)
+                         : dtype == kF16 ? pick_sums<kF16>(full, quads)
+                                         : pick_sums<kBF16>(full, quads);
     const int64_t ny = seg ? shared_candidates(p.rows, p.walkers, p.gate_rows, p.rows_per_gate) : 0;
-    const dim3 grid(static_cast<unsigned>((p.Hp / 4 + kQuads - 1) / kQuads), static_cast<unsigned>(1 + ny));
+    const dim3 grid(static_cast<unsigned>((p.Hp / 4 + quads - 1) / quads), static_cast<unsigned>(1 + ny));
     e = launch_kernel(ks, grid, dim3(kSumThreads), 0, c.stream, c.pdl, p);
   }
   if (e != cudaSuccess) {
