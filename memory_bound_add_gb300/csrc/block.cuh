@@ -158,21 +158,28 @@ struct Cols {
 // A thread's groups of the rows ahead, in a ring of slots of its own in
 // shared memory: it copies them itself (cp.async, 16 or 4 bytes at a time,
 // zeros for a group that does not exist) and alone reads them, so no barrier
-// is needed, and no register holds them.  Slot s of tensor i, group k:
-// [(s NT + i) NV + k][T].  Two-byte groups cannot be copied that way; they
-// wait in registers, two in each (one slot).
+// is needed, and no register holds them.  A warp's ring is one piece,
+// [slot][tensor][group][lane], so that all its addresses are constants apart.
+// Two-byte groups cannot be copied that way; they wait in registers, two in
+// each (one slot).
+constexpr int kMaxSlots = 2;
+
 template <int DT, int VE, int NV, int NT>
 struct Ring {
   static constexpr int kBytes = Grp<DT, VE>::kBytes;
   static constexpr bool kAsync = kBytes >= 4;
+  static constexpr uint32_t kStep = 32 * kBytes;                               // between groups
+  static constexpr uint32_t kWarp = kAsync ? kMaxSlots * NT * NV * kStep : 0;  // bytes a warp needs
   uint32_t base;  // this thread's first group of slot 0
-  int step;       // bytes between neighbouring groups: T kBytes
   uint32_t held[kAsync ? 1 : NT][kAsync ? 1 : NV / 2];
 
+  __device__ __forceinline__ uint32_t at(int slot, int i, int k) const {
+    return base + static_cast<uint32_t>(slot) * (NT * NV * kStep) + static_cast<uint32_t>(i * NV + k) * kStep;
+  }
   // group k of tensor i from src, if it exists
   __device__ __forceinline__ void fetch(int slot, int i, int k, const char* src, bool ok) {
     if constexpr (kAsync) {
-      const uint32_t dst = base + static_cast<uint32_t>((slot * NT + i) * NV + k) * step;
+      const uint32_t dst = at(slot, i, k);
       const int n = ok ? kBytes : 0;
       if constexpr (kBytes == 16)
         asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
@@ -190,7 +197,7 @@ struct Ring {
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       if constexpr (kAsync) {
-        const uint32_t dst = base + static_cast<uint32_t>((slot * NT + i) * NV + k) * step;
+        const uint32_t dst = at(slot, i, k);
 #pragma unroll
         for (int b = 0; b < kBytes; b += 4)
           asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + b), "r"(0) : "memory");
@@ -213,7 +220,7 @@ struct Ring {
 #pragma unroll
     for (int k = 0; k < N; ++k) {
       if constexpr (kAsync) {
-        const uint32_t src = base + static_cast<uint32_t>((slot * NT + i) * NV + k0 + k) * step;
+        const uint32_t src = at(slot, i, k0 + k);
         if constexpr (kBytes == 16) {
           const uint4 u = ld_shared_v4(src);
           g[k].w[0] = u.x, g[k].w[1] = u.y, g[k].w[2] = u.z, g[k].w[3] = u.w;

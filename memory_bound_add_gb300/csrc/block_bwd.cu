@@ -73,19 +73,22 @@ __device__ __forceinline__ void store_cols(float* t, const Cols<VE, NV>& cs, int
   }
 }
 
-// A thread's parameters in its own places of shared memory: part q of group k
-// of vector i at [((i NV + k) Q + q)][T], so that a warp's reads are
-// contiguous.  Vector 0: gamma of the pre norm; 1: the factor c, or with gate
-// rows s pg (c is then that times the gate); 2: s pb.
+// A thread's parameters in its own places of shared memory, a warp's in one
+// piece [vector][group][part][lane].  Vector 0: gamma of the pre norm; 1: the
+// factor c, or with gate rows s pg (c is then that times the gate); 2: s pb.
 template <int VE, int NV>
 struct Kept {
   static constexpr int kPart = VE >= 4 ? 16 : VE * 4;
   static constexpr int Q = VE * 4 / kPart;
+  static constexpr uint32_t kStep = 32 * kPart;
+  template <int NP>
+  __device__ static constexpr uint32_t bytes() {
+    return NP * NV * Q * kStep;
+  }
   uint32_t base;
-  int step;  // bytes between parts: threads of the CTA times kPart
 
   __device__ __forceinline__ uint32_t at(int i, int k, int q) const {
-    return base + static_cast<uint32_t>((i * NV + k) * Q + q) * step;
+    return base + static_cast<uint32_t>((i * NV + k) * Q + q) * kStep;
   }
   __device__ __forceinline__ void put(int i, int k, const float (&v)[VE]) const {
 #pragma unroll
@@ -194,6 +197,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
   constexpr int kStepBytes = Cols<VE, NV>::kStep * S;
   // groups that share slots in pairs (single elements) go two at a time
   constexpr int KU = VE >= 2 ? 1 : 2, N = VE >= 2 ? VE / 2 : 1;
+  constexpr int NP = FULL && GR ? 3 : 2;
   using R = Ring<DT, VE, NV, NT>;
   extern __shared__ __align__(128) unsigned char smem[];
   const int T = p.w.cta_warps * 32;
@@ -204,11 +208,10 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
   const int col0 = rank * p.w.slice;
   const int slots = R::kAsync ? p.slots : 1;
   R ring;
-  ring.step = blockDim.x * GB;
-  ring.base = smem_addr(smem) + threadIdx.x * GB;
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  ring.base = smem_addr(smem) + warp * R::kWarp + lane * GB;
   Kept<VE, NV> kept;
-  kept.step = blockDim.x * Kept<VE, NV>::kPart;
-  kept.base = smem_addr(smem) + p.kept_at + threadIdx.x * Kept<VE, NV>::kPart;
+  kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<NP>() + lane * Kept<VE, NV>::kPart;
   Sums<K> sums{reinterpret_cast<float*>(smem + p.sums_at) + side * 2 * p.w.warps * K, p.w, rank, 0, 1 + side};
   Cols<VE, NV> cs;
   cs.init(tid >> 5, col0, min(p.w.slice, p.H - col0));
@@ -721,7 +724,7 @@ Choice make(int H, bool full) {
   c.sh.rows = c.sh.C > 1 || threads > kSideThreads / 2 ? 1 : kSideThreads / threads;
   c.sh.threads = threads * c.sh.rows;
   const int nt = GR ? 5 : 4, np = full && GR ? 3 : 2, gb = Grp<DT, VE>::kBytes;
-  int ring = gb >= 4 ? 2 * nt * NV * c.sh.threads * gb : 0;
+  int ring = gb >= 4 ? kMaxSlots * nt * NV * c.sh.threads * gb : 0;
   int half = 0;  // walkers that give their sums to another at once
   for (int top = 1; top < c.sh.rows; top *= 2) half = top;
   const int join = half * sums_of(full) * NV * VE * threads * 4;

@@ -139,8 +139,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, VE, NV,
   Exchange ex{parts, p.w, rank, 0};
   const bool leader = rank == 0 && lane == 0 && (row_warp || warp == 0);
   Ring<DT, VE, NV, NT> ring;
-  ring.step = p.w.cta_warps * 32 * GB;
-  ring.base = smem_addr(smem) + (row_warp ? warp * slots * NT * NV * 32 + lane : threadIdx.x) * GB;
+  ring.base = smem_addr(smem) + warp * Ring<DT, VE, NV, NT>::kWarp + lane * GB;
   Cols<VE, NV> cs;
   cs.init(row_warp ? 0 : warp, col0, min(p.w.slice, p.H - col0));
   // byte offset of this thread's group 0 in a row
@@ -328,7 +327,7 @@ Choice make(const BlockFwdArgs& p, bool ln) {
   c.sh.rows = threads == 32 ? 4 : 1;
   c.sh.threads = threads * c.sh.rows;
   const int nt = p.gate_kind == ADDLN_GATE_ROWS ? 3 : 2;
-  if (Grp<DT, VE>::kBytes >= 4) c.smem = 2 * nt * NV * c.sh.threads * Grp<DT, VE>::kBytes;
+  if (Grp<DT, VE>::kBytes >= 4) c.smem = kMaxSlots * nt * NV * c.sh.threads * Grp<DT, VE>::kBytes;
   return c;
 }
 
