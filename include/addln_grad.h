@@ -25,8 +25,8 @@
  *              bytes, 16-byte aligned, the caller's; no two calls that may
  *              overlap on the GPU share one; needs no initialisation
  * The squares are summed in a fixed order (fp32 within a thread's share of a
- * few dozen elements, fp64 beyond; elements whose squares leave fp32's range
- * are summed in fp64 throughout), so the same call gives the same bits.
+ * few dozen elements, pairs of fp32 values beyond; shares whose squares leave
+ * fp32's range are summed in fp64), so the same call gives the same bits.
  * Where nothing is to be scaled in place (factor 1), nothing is written.
  */
 #ifndef ADDLN_GRAD_H

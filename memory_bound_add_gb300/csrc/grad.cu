@@ -2,12 +2,14 @@
 //
 // The table of tensors travels in the launch's parameters (up to 1000
 // tensors a launch), so a call needs no copy to the device and can be
-// captured.  The elements of all tensors are cut into chunks, which the CTAs
-// of a persistent grid take in turn; a CTA sums squares in fp32 within a
-// thread's share of a chunk and in fp64 beyond, and leaves one fp64 partial.
-// The kernel that scales adds the partials itself, in a fixed order, in every
-// CTA, and takes the chunks from the last to the first: what the first kernel
-// read last is in L2 still.
+// captured.  The memory of all tensors is cut into chunks of 16 KB on 16-byte
+// borders, which the CTAs of a persistent grid take in turn: 4 vectors a
+// thread, the next chunk's loads issued before the current one is used.  A
+// thread adds the squares of a chunk's share (at most 32 elements) in fp32
+// and the shares as an unevaluated sum of two fp32 values; a CTA leaves one
+// partial.  The kernel that scales adds the partials itself, in a fixed
+// order, in every CTA, and takes the chunks from the last to the first: what
+// the first kernel read last is in L2 still.
 #include <math.h>
 
 #include <algorithm>
@@ -27,6 +29,8 @@ constexpr int kThreads = 256;
 constexpr int kCtasPerSm = 4;
 constexpr int kMaxCtas = 2048;  // partials a launch may leave
 constexpr int kManyTensors = 1000, kFewTensors = 120;
+constexpr int kVecs = 4;        // 16-byte vectors a thread has of a chunk
+constexpr int kChunk = kThreads * kVecs * 16;
 
 struct Entry {
   const void* g;
@@ -41,11 +45,30 @@ struct Table {
   Entry e[N];
   int count;
   uint32_t chunks;
-  int chunk;  // elements, a multiple of 8
+};
+
+// hi + lo, lo being what the roundings of hi left.  (fp64 would do, but has
+// a 64th of the rate: adding a few hundred partials in every CTA took it
+// longer than the memory traffic of a small model.)
+struct Two {
+  float hi, lo;
+  __device__ __forceinline__ void add(float s, float s_lo) {
+    const float sum = __fadd_rn(hi, s), b = __fadd_rn(sum, -hi);
+    const float err = __fadd_rn(__fadd_rn(hi, -__fadd_rn(sum, -b)), __fadd_rn(s, -b));
+    lo = __fadd_rn(lo, __fadd_rn(err, s_lo));
+    hi = sum;
+  }
+};
+
+// A CTA's sum of squares: hi + lo, and in fp64 the shares that leave fp32's
+// range.
+struct alignas(16) Partial {
+  Two s;
+  double wide;
 };
 
 struct ClipArgs {
-  const double* part;  // partials to add (nparts of them), or nullptr: *norm is there already
+  const Partial* part;  // partials to add (nparts of them), or nullptr: *norm is there already
   int nparts;
   float* norm_out;     // written from the partials by the first CTA, or nullptr
   const float* norm;
@@ -63,204 +86,310 @@ __device__ __forceinline__ int tensor_of(const Table<N>& t, uint32_t c) {
   return lo;
 }
 
-__device__ __forceinline__ double block_sum(double v, double* red) {
+// Which elements of a chunk are the tensor's: the chunk's element r (counted
+// from its 16-byte border) is element begin + r of the tensor, for r in
+// [lo, hi); `mis` of the tensor's first elements' places on that border are
+// not its own.  one: the element before the first or after the last whole
+// vector that this thread has (thread q of the first warp has r = lo + q,
+// thread q of the second r = hi / VEC VEC + q), or -1.
+template <int S>  // bytes of an element
+struct Share {
+  static constexpr int VEC = 16 / S;
+  int64_t begin;
+  int lo, hi;
+
+  __device__ __forceinline__ Share(const Entry& e, uint32_t chunk) {
+    const int mis = static_cast<int>(reinterpret_cast<uintptr_t>(e.g) & 15u) / S;
+    begin = static_cast<int64_t>(chunk) * (kChunk / S) - mis;
+    lo = chunk == 0 ? mis : 0;
+    hi = static_cast<int>(min(static_cast<int64_t>(kChunk / S), e.n - begin));
+  }
+  __device__ __forceinline__ bool whole(int r) const { return r >= lo && r + VEC <= hi; }
+  __device__ __forceinline__ int one() const {
+    const int t = threadIdx.x, q = t & 31, first = (lo + VEC - 1) / VEC * VEC, last = max(first, hi / VEC * VEC);
+    if (t < 32 && lo + q < min(first, hi)) return lo + q;
+    if (t >= 32 && t < 64 && last + q < hi) return last + q;
+    return -1;
+  }
+};
+
+struct Piece {
+  int k;           // tensor
+  uint32_t chunk;  // its chunk
+  uint4 v[kVecs];  // vector j: elements (threadIdx.x + j kThreads) VEC on, zeros if not all are the tensor's
+  uint32_t e;      // the one element, or 0
+};
+
+template <int S>
+__device__ __forceinline__ void load_share(const Entry& e, Piece& p) {
+  const Share<S> s(e, p.chunk);
+  const char* g = static_cast<const char*>(e.g) + s.begin * S;
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
-  __syncthreads();
-  if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-  __syncthreads();
-  double t = 0.0;
-#pragma unroll
-  for (int w = 0; w < kThreads / 32; ++w) t += red[w];
-  return t;
+  for (int j = 0; j < kVecs; ++j) {
+    const int r = (threadIdx.x + j * kThreads) * s.VEC;
+    p.v[j] = make_uint4(0, 0, 0, 0);
+    if (s.whole(r) && ADDLN_IN(801, (s.begin + r) * S, 16, e.n * S))
+      p.v[j] = __ldg(reinterpret_cast<const uint4*>(g + r * S));
+  }
+  p.e = 0;
+  const int r = s.one();
+  if (r >= 0 && ADDLN_IN(802, (s.begin + r) * S, S, e.n * S)) {
+    if constexpr (S == 4)
+      p.e = __ldg(reinterpret_cast<const uint32_t*>(g) + r);
+    else
+      p.e = __ldg(reinterpret_cast<const unsigned short*>(g) + r);
+  }
 }
 
-// Sum of squares of elements [0, n) at g (n at most one chunk), this
-// thread's share.  The share is at most a few dozen elements, so fp32 keeps
-// it to a few roundings; where it leaves [1e-30, 1e30], squares may have been
-// lost to fp32's range, and the share is summed again in fp64.
+template <int N>
+__device__ __forceinline__ void load_piece(const Table<N>& t, uint32_t c, Piece& p) {
+  const Entry& e = t.e[p.k];
+  p.chunk = c - e.first;
+  if (e.dtype == kF32)
+    load_share<4>(e, p);
+  else
+    load_share<2>(e, p);
+}
+
 template <int DT>
-__device__ __forceinline__ double chunk_squares(const char* g, int n, int64_t left_bytes) {
+__device__ __forceinline__ float value_of(uint32_t raw) {
+  if constexpr (DT == kF32) return __uint_as_float(raw);
+  const unsigned short b = static_cast<unsigned short>(raw);
+  return DT == kF16 ? __half2float(__ushort_as_half(b)) : __bfloat162float(__ushort_as_bfloat16(b));
+}
+
+// Sum of squares of a thread's share.  At most 33 elements, so fp32 keeps it
+// to a few roundings.  Where the sum leaves [1e-30, 1e30], squares may have
+// been lost to fp32's range: 0 is returned and *lost set, unless all elements
+// are zeros.
+template <int DT>
+__device__ __forceinline__ float squares(const Piece& p, bool* lost) {
   using IO = Io<DT>;
-  constexpr int S = IO::kBytes, VEC = IO::kVec;
-  const int tid = threadIdx.x;
-  const int head = min(n, static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(g) & 15u)) & 15u) / S));
-  const int nv = (n - head) / VEC;
-  const int tail = n - head - nv * VEC;
-  const char* body = g + head * S;
-  float2 acc[2] = {dup2(0.f), dup2(0.f)};
-  uint32_t any = 0;
-  auto vec = [&](const uint4& u) {
+  constexpr int VEC = IO::kVec;
+  const float one = value_of<DT>(p.e);
+  float2 acc[2] = {make_float2(one * one, 0.f), dup2(0.f)};
+  uint32_t any = p.e;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
     float2 f[VEC / 2];
-    IO::to_pairs(u, f);
+    IO::to_pairs(p.v[j], f);
 #pragma unroll
     for (int q = 0; q < VEC / 2; ++q) acc[q & 1] = fma2(f[q], f[q], acc[q & 1]);
-    any |= u.x | u.y | u.z | u.w;
-  };
-  constexpr int kU = 4;  // 16-byte loads in flight a thread
-  int i = tid;
-  for (; i + (kU - 1) * kThreads < nv; i += kU * kThreads) {
-    uint4 u[kU];
-#pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      u[k] = make_uint4(0, 0, 0, 0);
-      if (ADDLN_IN(801, (i + k * kThreads) * 16 + head * S, 16, left_bytes))
-        u[k] = __ldg(reinterpret_cast<const uint4*>(body) + i + k * kThreads);
-    }
-#pragma unroll
-    for (int k = 0; k < kU; ++k) vec(u[k]);
-  }
-  for (; i < nv; i += kThreads)
-    if (ADDLN_IN(802, i * 16 + head * S, 16, left_bytes)) vec(__ldg(reinterpret_cast<const uint4*>(body) + i));
-  // the elements before the first and after the last 16-byte vector
-  const int extra = tid < head ? tid : tid - head < tail ? n - tail + (tid - head) : -1;
-  if (extra >= 0 && ADDLN_IN(803, extra * S, S, left_bytes)) {
-    const float v = IO::load1(g, extra);
-    acc[0].x = fmaf(v, v, acc[0].x);
-    any |= v != 0.f;
+    any |= p.v[j].x | p.v[j].y | p.v[j].z | p.v[j].w;
   }
   const float s = (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
-  if (DT == kF16 || (s >= 1e-30f && s <= 1e30f)) return s;
-  const uint32_t mask = DT == kF32 ? 0x7fffffffu : 0x7fff7fffu;
-  if ((any & mask) == 0) return 0.0;
-  double d = 0.0;
-  for (int j = tid; j < nv; j += kThreads)
-    if (ADDLN_IN(804, j * 16 + head * S, 16, left_bytes)) {
-      float f[VEC];
-      IO::unpack(__ldg(reinterpret_cast<const uint4*>(body) + j), f);
+  if (DT == kF16 ? s <= 1e30f : s >= 1e-30f && s <= 1e30f) return s;
+  *lost = (any & (DT == kF32 ? 0x7fffffffu : 0x7fff7fffu)) != 0;
+  return 0.f;
+}
+
+template <int DT>
+__device__ __forceinline__ double squares_wide(const Piece& p) {
+  using IO = Io<DT>;
+  constexpr int VEC = IO::kVec;
+  const double one = value_of<DT>(p.e);
+  double d = one * one;
 #pragma unroll
-      for (int e = 0; e < VEC; ++e) d = fma(static_cast<double>(f[e]), static_cast<double>(f[e]), d);
-    }
-  if (extra >= 0 && ADDLN_IN(805, extra * S, S, left_bytes)) {
-    const double v = IO::load1(g, extra);
-    d = fma(v, v, d);
+  for (int j = 0; j < kVecs; ++j) {
+    float f[VEC];
+    IO::unpack(p.v[j], f);
+#pragma unroll
+    for (int e = 0; e < VEC; ++e) d = fma(static_cast<double>(f[e]), static_cast<double>(f[e]), d);
   }
   return d;
 }
 
+__device__ __forceinline__ float squares_of(int dt, const Piece& p, bool* lost) {
+  return dt == kF32 ? squares<kF32>(p, lost) : dt == kF16 ? squares<kF16>(p, lost) : squares<kBF16>(p, lost);
+}
+
 template <int N>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_grad_squares(const __grid_constant__ Table<N> t, double* part) {
-  __shared__ double red[kThreads / 32];
+__global__ void __launch_bounds__(kThreads, kCtasPerSm) k_grad_squares(const __grid_constant__ Table<N> t, Partial* part) {
+  constexpr int kWarps = kThreads / 32;
+  __shared__ Partial sums[kWarps];
   pdl_trigger();
   pdl_wait();
-  double sum = 0.0;
-  {
-    int k = tensor_of(t, blockIdx.x);
+  Two sum{0.f, 0.f};
+  Piece next;
+  next.k = tensor_of(t, blockIdx.x);
+  bool have = false, again = false;
+  for (uint32_t c = blockIdx.x;; c += gridDim.x) {
+    // the next chunk's loads, before the current one is used
+    const Piece cur = next;
+    const bool more = c < t.chunks;
+    if (more) {
+      while (next.k + 1 < t.count && t.e[next.k + 1].first <= c) ++next.k;
+      load_piece(t, c, next);
+    }
+    if (have) {
+      bool lost = false;
+      sum.add(squares_of(t.e[cur.k].dtype, cur, &lost), 0.f);
+      again |= lost;
+    }
+    if (!more) break;
+    have = true;
+  }
+  // shares that fp32 cannot hold (NaN, infinite, very large or small), again
+  double wide = 0.0;
+  const bool redo = __syncthreads_or(again);
+  if (redo) {
+    Piece p;
+    p.k = tensor_of(t, blockIdx.x);
     for (uint32_t c = blockIdx.x; c < t.chunks; c += gridDim.x) {
-      while (k + 1 < t.count && t.e[k + 1].first <= c) ++k;
-      const int64_t at = static_cast<int64_t>(c - t.e[k].first) * t.chunk;
-      const int64_t rest = t.e[k].n - at;
-      const int n = static_cast<int>(rest < t.chunk ? rest : t.chunk);
-      const int dt = t.e[k].dtype;
-      const char* g = static_cast<const char*>(t.e[k].g) + at * (dt == kF32 ? 4 : 2);
-      if (dt == kF32)
-        sum += chunk_squares<kF32>(g, n, rest * 4);
-      else if (dt == kF16)
-        sum += chunk_squares<kF16>(g, n, rest * 2);
-      else
-        sum += chunk_squares<kBF16>(g, n, rest * 2);
+      while (p.k + 1 < t.count && t.e[p.k + 1].first <= c) ++p.k;
+      load_piece(t, c, p);
+      const int dt = t.e[p.k].dtype;
+      bool lost = false;
+      squares_of(dt, p, &lost);
+      if (lost) wide += dt == kF32 ? squares_wide<kF32>(p) : dt == kF16 ? squares_wide<kF16>(p) : squares_wide<kBF16>(p);
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) wide += __shfl_down_sync(0xffffffffu, wide, off);
+  }
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const float hi = __shfl_down_sync(0xffffffffu, sum.hi, off), lo = __shfl_down_sync(0xffffffffu, sum.lo, off);
+    sum.add(hi, lo);
+  }
+  if (lane == 0) sums[warp] = Partial{sum, wide};
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    for (int w = 1; w < kWarps; ++w) {
+      sum.add(sums[w].s.hi, sums[w].s.lo);
+      if (redo) wide += sums[w].wide;
+    }
+    part[blockIdx.x] = Partial{sum, wide};
+  }
+}
+
+// norm from the partials, added in a fixed order; the same value in every
+// thread of every CTA.
+__device__ __forceinline__ float norm_of(const Partial* part, int n, float scale, Partial* shared) {
+  constexpr int kWarps = kThreads / 32;
+  Two sum{0.f, 0.f};
+  double wide = 0.0;
+  for (int i = threadIdx.x; i < n; i += kThreads * 4) {
+    uint4 v[4];
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      v[u] = make_uint4(0, 0, 0, 0);
+      if (i + u * kThreads < n) v[u] = __ldcg(reinterpret_cast<const uint4*>(part + i + u * kThreads));
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      sum.add(__uint_as_float(v[u].x), __uint_as_float(v[u].y));
+      if ((v[u].z | v[u].w) != 0) wide += __hiloint2double(static_cast<int>(v[u].w), static_cast<int>(v[u].z));
     }
   }
-  sum = block_sum(sum, red);
-  if (threadIdx.x == 0) part[blockIdx.x] = sum;
+  const bool any = __syncthreads_or(wide != 0.0);  // true for a NaN
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1) {
+    const float hi = __shfl_down_sync(0xffffffffu, sum.hi, off), lo = __shfl_down_sync(0xffffffffu, sum.lo, off);
+    sum.add(hi, lo);
+    if (any) wide += __shfl_down_sync(0xffffffffu, wide, off);
+  }
+  if ((threadIdx.x & 31) == 0) shared[threadIdx.x >> 5] = Partial{sum, wide};
+  __syncthreads();
+  // every thread joins the warps' sums itself
+  sum = shared[0].s;
+#pragma unroll
+  for (int w = 1; w < kWarps; ++w) sum.add(shared[w].s.hi, shared[w].s.lo);
+  if (!any) return scale * __fsqrt_rn(__fadd_rn(sum.hi, sum.lo));
+  wide = shared[0].wide;
+  for (int w = 1; w < kWarps; ++w) wide += shared[w].wide;
+  return static_cast<float>(static_cast<double>(scale) * sqrt((static_cast<double>(sum.hi) + sum.lo) + wide));
 }
 
-// norm from the partials: every thread of every CTA gets the same value.
-__device__ __forceinline__ float norm_of(const double* part, int n, float scale, double* red) {
-  double s = 0.0;
-  for (int i = threadIdx.x; i < n; i += kThreads) s += __ldcg(part + i);
-  s = block_sum(s, red);
-  return static_cast<float>(static_cast<double>(scale) * sqrt(s));
-}
-
-__global__ void __launch_bounds__(kThreads) k_grad_norm(const double* part, int n, float scale, float* norm) {
-  __shared__ double red[kThreads / 32];
+__global__ void __launch_bounds__(kThreads) k_grad_norm(const Partial* part, int n, float scale, float* norm) {
+  __shared__ Partial shared[kThreads / 32];
   pdl_trigger();
   pdl_wait();
-  const float v = norm_of(part, n, scale, red);
+  const float v = norm_of(part, n, scale, shared);
   if (threadIdx.x == 0) *norm = v;
 }
 
-// out = g factor for elements [0, n) of one chunk.
+// 32 bytes at q, 32-byte aligned (evict-first, as st_stream_v4).
+__device__ __forceinline__ void st_stream_v8(void* q, const uint4& a, const uint4& b) {
+  asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(q), "r"(a.x), "r"(a.y), "r"(a.z),
+               "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
+}
+
+// out = g factor for a thread's share of a chunk.
 template <int DT, int OUT>
-__device__ __forceinline__ void chunk_scale(const char* g, char* out, int n, float factor, int64_t left) {
+__device__ __forceinline__ void scale_share(const Entry& e, const Piece& p, float factor) {
   using IO = Io<DT>;
   using OO = Io<OUT>;
-  constexpr int S = IO::kBytes, VEC = IO::kVec, OV = OO::kVec, OS = OO::kBytes;
-  const int tid = threadIdx.x;
-  int head = min(n, static_cast<int>(((16u - (reinterpret_cast<uintptr_t>(g) & 15u)) & 15u) / S));
-  if ((reinterpret_cast<uintptr_t>(out + head * OS) & 15u) != 0) {
-    // no common place for 16-byte accesses: element by element
-    for (int i = tid; i < n; i += kThreads)
-      if (ADDLN_IN(811, i, 1, left)) OO::store1(out, i, IO::load1(g, i) * factor);
-    return;
-  }
-  const int nv = (n - head) / VEC;
-  const int tail = n - head - nv * VEC;
-  const char* body = g + head * S;
-  char* obody = out + head * OS;
+  constexpr int VEC = IO::kVec, OV = OO::kVec, OS = OO::kBytes;
+  const Share<IO::kBytes> s(e, p.chunk);
+  char* out = static_cast<char*>(e.out) + s.begin * OS;
   const float2 f2 = dup2(factor);
-  auto store = [&](int i, const uint4& u) {
+  // out's vectors begin where g's do on a border of their own size (16 bytes,
+  // or 32 for two of fp32)
+  const bool wide = (reinterpret_cast<uintptr_t>(out) & (VEC * OS - 1)) == 0;
+#pragma unroll
+  for (int j = 0; j < kVecs; ++j) {
+    const int r = (threadIdx.x + j * kThreads) * VEC;
+    if (!s.whole(r) || !ADDLN_IN(813, s.begin + r, VEC, e.n)) continue;
     float2 f[VEC / 2];
-    IO::to_pairs(u, f);
+    IO::to_pairs(p.v[j], f);
 #pragma unroll
     for (int q = 0; q < VEC / 2; ++q) f[q] = mul2(f[q], f2);
+    if (wide) {
+      if constexpr (VEC == OV)
+        st_stream_v4(out + r * OS, OO::from_pairs(f));
+      else
+        st_stream_v8(out + r * OS, OO::from_pairs(f), OO::from_pairs(f + OV / 2));
+    } else {
 #pragma unroll
-    for (int q = 0; q < VEC / OV; ++q)
-      st_stream_v4(obody + (static_cast<int64_t>(i) * VEC + q * OV) * OS, OO::from_pairs(f + q * OV / 2));
-  };
-  constexpr int kU = 4;
-  int i = tid;
-  for (; i + (kU - 1) * kThreads < nv; i += kU * kThreads) {
-    uint4 u[kU];
-#pragma unroll
-    for (int k = 0; k < kU; ++k) {
-      u[k] = make_uint4(0, 0, 0, 0);
-      if (ADDLN_IN(812, (i + k * kThreads) * VEC + head, VEC, left))
-        u[k] = ld_stream_v4(body + static_cast<int64_t>(i + k * kThreads) * 16);
+      for (int q = 0; q < VEC; ++q) OO::store1(out, r + q, (q & 1) ? f[q >> 1].y : f[q >> 1].x);
     }
-#pragma unroll
-    for (int k = 0; k < kU; ++k)
-      if (ADDLN_IN(813, (i + k * kThreads) * VEC + head, VEC, left)) store(i + k * kThreads, u[k]);
   }
-  for (; i < nv; i += kThreads)
-    if (ADDLN_IN(814, i * VEC + head, VEC, left)) store(i, ld_stream_v4(body + static_cast<int64_t>(i) * 16));
-  const int extra = tid < head ? tid : tid - head < tail ? n - tail + (tid - head) : -1;
-  if (extra >= 0 && ADDLN_IN(815, extra, 1, left)) OO::store1(out, extra, IO::load1(g, extra) * factor);
+  const int r = s.one();
+  if (r >= 0 && ADDLN_IN(814, s.begin + r, 1, e.n)) OO::store1(out, r, value_of<DT>(p.e) * factor);
 }
 
 template <int N>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_grad_clip(const __grid_constant__ Table<N> t, const ClipArgs a) {
-  __shared__ double red[kThreads / 32];
+  __shared__ Partial shared[kThreads / 32];
   pdl_trigger();
   pdl_wait();
   float norm;
   if (a.part != nullptr) {
-    norm = norm_of(a.part, a.nparts, a.scale, red);
+    norm = norm_of(a.part, a.nparts, a.scale, shared);
     if (a.norm_out != nullptr && blockIdx.x == 0 && threadIdx.x == 0) *a.norm_out = norm;
   } else {
     norm = __ldcg(a.norm);
   }
   const float coef = a.max_norm / (norm + 1e-6f);
   const float factor = a.scale * (coef > 1.f ? 1.f : coef);  // a NaN stays
+  // from the last chunk to the first; in place with factor 1 there is
+  // nothing to write
   if (blockIdx.x >= t.chunks) return;
-  int k = tensor_of(t, t.chunks - 1 - blockIdx.x);
-  for (int64_t left = static_cast<int64_t>(t.chunks) - 1 - blockIdx.x; left >= 0; left -= gridDim.x) {
-    const uint32_t c = static_cast<uint32_t>(left);
-    while (t.e[k].first > c) --k;
-    const int64_t at = static_cast<int64_t>(c - t.e[k].first) * t.chunk;
-    const int64_t rest = t.e[k].n - at;
-    const int n = static_cast<int>(rest < t.chunk ? rest : t.chunk);
-    const int dt = t.e[k].dtype, od = t.e[k].out_dtype;
-    const char* g = static_cast<const char*>(t.e[k].g) + at * (dt == kF32 ? 4 : 2);
-    char* out = static_cast<char*>(t.e[k].out) + at * (od == kF32 ? 4 : 2);
-    if (factor == 1.f && g == out) continue;  // in place, nothing to scale
-    if (dt == kF32)
-      chunk_scale<kF32, kF32>(g, out, n, factor, rest);
-    else if (dt == kF16)
-      od == kF32 ? chunk_scale<kF16, kF32>(g, out, n, factor, rest) : chunk_scale<kF16, kF16>(g, out, n, factor, rest);
-    else
-      od == kF32 ? chunk_scale<kBF16, kF32>(g, out, n, factor, rest) : chunk_scale<kBF16, kBF16>(g, out, n, factor, rest);
+  auto skip = [&](int k) { return factor == 1.f && t.e[k].g == t.e[k].out; };
+  Piece next;
+  next.k = tensor_of(t, t.chunks - 1 - blockIdx.x);
+  bool have = false;
+  for (int64_t left = static_cast<int64_t>(t.chunks) - 1 - blockIdx.x;; left -= gridDim.x) {
+    const Piece cur = next;
+    const bool more = left >= 0;
+    if (more) {
+      const uint32_t c = static_cast<uint32_t>(left);
+      while (t.e[next.k].first > c) --next.k;
+      if (!skip(next.k)) load_piece(t, c, next);
+    }
+    if (have && !skip(cur.k)) {
+      const Entry& e = t.e[cur.k];
+      if (e.dtype == kF32)
+        scale_share<kF32, kF32>(e, cur, factor);
+      else if (e.dtype == kF16)
+        e.out_dtype == kF32 ? scale_share<kF16, kF32>(e, cur, factor) : scale_share<kF16, kF16>(e, cur, factor);
+      else
+        e.out_dtype == kF32 ? scale_share<kBF16, kF32>(e, cur, factor) : scale_share<kBF16, kBF16>(e, cur, factor);
+    }
+    if (!more) break;
+    have = true;
   }
 }
 
@@ -281,7 +410,7 @@ struct Lists {
 };
 
 // More elements than any memory holds; chunk numbers stay within 32 bits.
-constexpr int64_t kMaxTotal = int64_t{1} << 45;
+constexpr int64_t kMaxTotal = int64_t{1} << 43;
 
 struct Span {
   uintptr_t lo, hi;
@@ -336,28 +465,19 @@ int check_overlap(const Lists& l, bool scaled, const Range& norm, bool norm_is_o
   return ADDLN_OK;
 }
 
-// Elements a chunk: about sixteen chunks a CTA of one full wave, so that the
-// CTAs come out even, between 2048 (8 elements a thread) and 16384 (64).
-int chunk_of(int64_t total, int sms) {
-  const int64_t want = total / (static_cast<int64_t>(sms) * kCtasPerSm * 16);
-  int64_t c = 2048;
-  while (c < 16384 && c < want) c *= 2;
-  return static_cast<int>(c);
-}
-
 // One launch's share of the lists, from tensor `from` on; returns the next
 // that has elements, or count.
 template <int N>
-int64_t fill(const Lists& l, int64_t from, int chunk, bool scaled, Table<N>* t) {
+int64_t fill(const Lists& l, int64_t from, bool scaled, Table<N>* t) {
   t->count = 0;
-  t->chunk = chunk;
   int64_t chunks = 0, i = from;
   for (; i < l.count; ++i) {
     if (l.sizes[i] == 0) continue;
     if (t->count == N) break;
     t->e[t->count++] = {l.grads[i], scaled ? l.out(i) : nullptr, l.sizes[i], static_cast<uint32_t>(chunks),
                         static_cast<uint8_t>(l.dtypes[i]), static_cast<uint8_t>(scaled ? l.out_dtype(i) : 0)};
-    chunks += (l.sizes[i] - 1) / chunk + 1;
+    const int64_t bytes = l.sizes[i] * elem_bytes(l.dtypes[i]) + (reinterpret_cast<uintptr_t>(l.grads[i]) & 15u);
+    chunks += (bytes - 1) / kChunk + 1;
   }
   t->chunks = static_cast<uint32_t>(chunks);
   return i;
@@ -375,16 +495,13 @@ unsigned ctas_of(uint32_t chunks, int sms) {
 }
 
 template <int N>
-int run(const Lists& l, bool want_norm, bool scaled, float scale, float max_norm, float* norm, double* part,
+int run(const Lists& l, bool want_norm, bool scaled, float scale, float max_norm, float* norm, Partial* part,
         const LaunchCtx& c) {
-  int64_t total = 0;
-  for (int64_t i = 0; i < l.count; ++i) total += l.sizes[i];
-  const int chunk = chunk_of(total, c.dev.sms);
   Table<N> t;
   int nparts = 0, launches = 0;
   if (want_norm) {
     for (int64_t i = 0; i < l.count;) {
-      i = fill(l, i, chunk, scaled, &t);
+      i = fill(l, i, scaled, &t);
       if (t.chunks == 0) continue;
       const unsigned ctas = ctas_of(t.chunks, c.dev.sms);
       const int rc = launched(launch_kernel(k_grad_squares<N>, dim3(ctas), dim3(kThreads), 0, c.stream, c.pdl, t,
@@ -396,14 +513,14 @@ int run(const Lists& l, bool want_norm, bool scaled, float scale, float max_norm
     // one launch's partials are added by the scaling kernel's CTAs themselves
     if (!scaled || launches != 1) {
       const int rc = launched(launch_kernel(k_grad_norm, dim3(1), dim3(kThreads), 0, c.stream, c.pdl,
-                                            static_cast<const double*>(part), nparts, scale, norm));
+                                            static_cast<const Partial*>(part), nparts, scale, norm));
       if (rc != ADDLN_OK) return rc;
     }
   }
   if (!scaled) return ADDLN_OK;
   const bool join = want_norm && launches == 1;
   for (int64_t i = 0; i < l.count;) {
-    if (!join) i = fill(l, i, chunk, true, &t);
+    if (!join) i = fill(l, i, true, &t);
     else i = l.count;  // the table is the one just launched
     if (t.chunks == 0) continue;
     const ClipArgs a{join ? part : nullptr, nparts, join ? norm : nullptr, norm, scale, max_norm};
@@ -417,7 +534,7 @@ int run(const Lists& l, bool want_norm, bool scaled, float scale, float max_norm
 int64_t workspace_size(int64_t count) {
   if (count < 0 || count > INT64_MAX / 64) return ADDLN_ERR_SHAPE;
   // every launch but the last takes at least kFewTensors tensors
-  return (count / kFewTensors + 1) * kMaxCtas * static_cast<int64_t>(sizeof(double));
+  return (count / kFewTensors + 1) * kMaxCtas * static_cast<int64_t>(sizeof(Partial));
 }
 
 int call(const Lists& l, bool want_norm, bool scaled, float scale, float max_norm, float* norm, void* ws,
@@ -433,7 +550,7 @@ int call(const Lists& l, bool want_norm, bool scaled, float scale, float max_nor
   LaunchCtx c;
   rc = launch_context(stream, &c);
   if (rc != ADDLN_OK) return rc;
-  double* part = static_cast<double*>(ws);
+  Partial* part = static_cast<Partial*>(ws);
   return l.count <= kFewTensors ? run<kFewTensors>(l, want_norm, scaled, scale, max_norm, norm, part, c)
                                 : run<kManyTensors>(l, want_norm, scaled, scale, max_norm, norm, part, c);
 }

@@ -146,6 +146,20 @@ def test_values_whose_squares_leave_fp32(mag, dtype):
     assert abs(float(mba.grad_norm([mixed])) - want) <= 12 * U * want
 
 
+@pytest.mark.parametrize("n", [1, 3, 8, 13, 4099])
+@pytest.mark.parametrize("off", [0, 1, 5])
+def test_bf16_of_the_largest_exponents(n, off):
+    # bit patterns that would be NaN in the other 16-bit type, also in the
+    # vectors that hold a tensor's first and last elements
+    big = torch.full((n + off,), 2.0 ** 125, dtype=BF16, device="cuda")[off:]
+    norm = mba.grad_norm([big], scale=2.0 ** -10)
+    want = 2.0 ** 115 * math.sqrt(n)
+    assert abs(float(norm) - want) <= 12 * U * want
+    out = [torch.empty(n, device="cuda")]
+    mba.clip_grads([big], math.inf, out=out, scale=2.0 ** -10)
+    assert bool((out[0] == 2.0 ** 115).all())
+
+
 def test_nan_and_infinity():
     gs = draw([1000, 70], F32, seed=5)
     gs[0][3] = float("nan")

@@ -64,7 +64,7 @@ def test_refusals(lib):
                 (dict(scale=nan), k.ERR_SCALE), (dict(scale=inf), k.ERR_SCALE), (dict(g=None), b.ERR_NULL),
                 (dict(n=None), b.ERR_NULL), (dict(d=None), b.ERR_NULL), (dict(d=(0, 3)), b.ERR_DTYPE),
                 (dict(n=(4, -1)), b.ERR_SHAPE), (dict(n=(1 << 46, 1)), b.ERR_SHAPE),
-                (dict(n=(1 << 45, 1)), b.ERR_SHAPE), (dict(g=(at(0), None)), b.ERR_NULL),
+                (dict(n=(1 << 43, 1)), b.ERR_SHAPE), (dict(g=(at(0), None)), b.ERR_NULL),
                 (dict(g=(at(0) + 2, at(1))), k.ERR_ALIGN), (dict(g=(at(0), at(1) + 1)), k.ERR_ALIGN),
                 (dict(norm=None), b.ERR_NULL), (dict(norm=at(8) + 2), k.ERR_ALIGN)]:
             assert call(lib, which, **kw) == code, (which, kw)
