@@ -64,14 +64,22 @@ def lib():
 
 
 # ------------------------------------------------------------------ helpers
+# The current device's index and a device's current stream as a raw handle,
+# without the objects that torch.cuda's functions build around them (a few
+# microseconds a call, as much as a small launch).
+_current_device = torch._C._cuda_getDevice
+_current_stream = torch._C._cuda_getCurrentRawStream
+
+
 def on_stream(device, stream, call):
     """call(raw stream handle) with `device` current; what it allocates
     belongs to the stream it launches on."""
     if stream is None:
-        if device.index == torch.cuda.current_device():
-            return call(torch.cuda.current_stream().cuda_stream)
+        index = device.index
+        if index == _current_device():
+            return call(_current_stream(index))
         with torch.cuda.device(device):
-            return call(torch.cuda.current_stream().cuda_stream)
+            return call(_current_stream(index))
     if isinstance(stream, int):
         stream = torch.cuda.ExternalStream(stream, device=device) if stream else torch.cuda.default_stream(device)
     if stream.device != device:
@@ -82,6 +90,9 @@ def on_stream(device, stream, call):
 
 def _tensor(t, name, dtype, shape, device):
     """A contiguous CUDA tensor of this dtype and shape: its address."""
+    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
+            and t.is_contiguous()):
+        return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
@@ -90,9 +101,7 @@ def _tensor(t, name, dtype, shape, device):
         raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
     if t.device != device:
         raise ValueError(f"{name} must be on {device}, got {t.device}")
-    if not t.is_contiguous():
-        raise ValueError(f"{name} must be contiguous")
-    return t.data_ptr()
+    raise ValueError(f"{name} must be contiguous")
 
 
 def _optional(t, name, dtype, shape, device):
@@ -175,6 +184,27 @@ def _check(rc, where):
 
 
 # ------------------------------------------------------------------ forward
+_NO_STATS = (None, None, None, None)
+_F32 = torch.float32
+
+
+def _forward(s, f, x, h, y, stats, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta,
+             residual_scale, block_scale, eps):
+    dt, dev, shape = f.dtype, f.device, f.shape
+    vec, st = shape[-1:], (rows,)
+    pm, pr, nm, nr = stats
+    gp, gk, gs, rpg = _gate_args(gate, f)
+    _check(lib().block_norm_fwd(
+        _tensor(f, "f", dt, shape, dev), _tensor(x, "x", dt, shape, dev), _norm_kind(post, "post"),
+        _optional(post_gamma, "post_gamma", _F32, vec, dev), _optional(post_beta, "post_beta", _F32, vec, dev),
+        gp, gk, gs, rpg, residual_scale, block_scale, _norm_kind(pre, "pre"),
+        _optional(pre_gamma, "pre_gamma", _F32, vec, dev), _optional(pre_beta, "pre_beta", _F32, vec, dev),
+        _tensor(h, "h", dt, shape, dev), _optional(y, "y", dt, shape, dev),
+        _optional(pm, "post_mean", _F32, st, dev), _optional(pr, "post_rstd", _F32, st, dev),
+        _optional(nm, "pre_mean", _F32, st, dev), _optional(nr, "pre_rstd", _F32, st, dev), rows, H, eps,
+        DTYPE_CODE[dt], s), "block_norm_fwd")
+
+
 def block_norm_fwd(f, x, h, y=None, stats=None, *, post=None, post_gamma=None, post_beta=None,
                    gate=None, pre="rms", pre_gamma=None, pre_beta=None, residual_scale: float = 1.0,
                    block_scale: float = 1.0, eps: float = 1e-5, stream=None):
@@ -182,20 +212,9 @@ def block_norm_fwd(f, x, h, y=None, stats=None, *, post=None, post_gamma=None, p
     may be f or x itself) and, with stats = (post_mean, post_rstd, pre_mean,
     pre_rstd), into [rows] fp32 tensors (None: not written)."""
     rows, H = _rows_tensor(f, "f")
-    dt, dev, shape, vec, st = f.dtype, f.device, f.shape, f.shape[-1:], (rows,)
-    post_kind, pre_kind = _norm_kind(post, "post"), _norm_kind(pre, "pre")
-    f32 = torch.float32
-    pm, pr, nm, nr = stats or (None, None, None, None)
-    gp, gk, gs, rpg = _gate_args(gate, f)
-    args = (_tensor(f, "f", dt, shape, dev), _tensor(x, "x", dt, shape, dev), post_kind,
-            _optional(post_gamma, "post_gamma", f32, vec, dev),
-            _optional(post_beta, "post_beta", f32, vec, dev), gp, gk, gs, rpg, residual_scale,
-            block_scale, pre_kind, _optional(pre_gamma, "pre_gamma", f32, vec, dev),
-            _optional(pre_beta, "pre_beta", f32, vec, dev), _tensor(h, "h", dt, shape, dev),
-            _optional(y, "y", dt, shape, dev), _optional(pm, "post_mean", f32, st, dev),
-            _optional(pr, "post_rstd", f32, st, dev), _optional(nm, "pre_mean", f32, st, dev),
-            _optional(nr, "pre_rstd", f32, st, dev), rows, H, eps, DTYPE_CODE[dt])
-    _check(on_stream(dev, stream, lambda s: lib().block_norm_fwd(*args, s)), "block_norm_fwd")
+    on_stream(f.device, stream, lambda s: _forward(
+        s, f, x, h, y, stats or _NO_STATS, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta,
+        residual_scale, block_scale, eps))
 
 
 def block_norm(f, x, *, post=None, post_gamma=None, post_beta=None, gate=None, pre="rms",
@@ -206,18 +225,17 @@ def block_norm(f, x, *, post=None, post_gamma=None, post_beta=None, gate=None, p
     Returns (h, y or None, stats or None), stats = (post_mean, post_rstd,
     pre_mean, pre_rstd), each [rows] fp32 or None where the norm has none.
     """
-    rows, _ = _rows_tensor(f, "f")
+    rows, H = _rows_tensor(f, "f")
 
     def call(s):
         h = torch.empty_like(f)
         y = torch.empty_like(f) if pre is not None else None
         stats = None
         if want_stats:
-            new = lambda w: torch.empty(rows, dtype=torch.float32, device=f.device) if w else None  # noqa: E731
+            new = lambda w: torch.empty(rows, dtype=_F32, device=f.device) if w else None  # noqa: E731
             stats = (new(post == "layer"), new(post is not None), new(pre == "layer"), new(pre is not None))
-        block_norm_fwd(f, x, h, y, stats, post=post, post_gamma=post_gamma, post_beta=post_beta, gate=gate,
-                       pre=pre, pre_gamma=pre_gamma, pre_beta=pre_beta, residual_scale=residual_scale,
-                       block_scale=block_scale, eps=eps)
+        _forward(s, f, x, h, y, stats or _NO_STATS, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma,
+                 pre_beta, residual_scale, block_scale, eps)
         return h, y, stats
 
     return on_stream(f.device, stream, call)
@@ -244,6 +262,44 @@ def block_norm_bwd_workspace_size(rows: int, H: int, dtype: int, gate_kind: int 
     return n
 
 
+def _given(dy, dh):
+    """The gradient that is given, with its rows and H."""
+    some, name = (dy, "dy") if dy is not None else (dh, "dh")
+    return (some, *_rows_tensor(some, name))
+
+
+def _backward(s, some, rows, H, dy, dh, f, h, stats, df, dx, post, post_gamma, post_beta, gate, pre, pre_gamma,
+              residual_scale, block_scale, dpost_gamma, dpost_beta, dgate, dpre_gamma, dpre_beta, workspace):
+    dt, dev, shape = some.dtype, some.device, some.shape
+    vec, st, code = shape[-1:], (rows,), DTYPE_CODE[dt]
+    pm, pr, nm, nr = stats or _NO_STATS
+    gp, gk, gs, rpg = _gate_args(gate, some)
+    dgp = None
+    if dgate is not None:
+        if gate is None:
+            raise ValueError("dgate without a gate")
+        dgp = _tensor(dgate, "dgate", _F32 if gk == GATE_CHANNEL else dt, gate.shape, dev)
+    if workspace is None:
+        size = block_norm_bwd_workspace_size(rows, H, code, gk, rpg or 1)
+        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
+    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    else:
+        size = workspace.numel() * workspace.element_size()
+    _check(lib().block_norm_bwd(
+        _optional(dy, "dy", dt, shape, dev), _optional(dh, "dh", dt, shape, dev), _optional(f, "f", dt, shape, dev),
+        _optional(h, "h", dt, shape, dev), _norm_kind(post, "post"),
+        _optional(post_gamma, "post_gamma", _F32, vec, dev), _optional(post_beta, "post_beta", _F32, vec, dev),
+        _optional(pm, "post_mean", _F32, st, dev), _optional(pr, "post_rstd", _F32, st, dev), gp, gk, gs, rpg,
+        residual_scale, block_scale, _norm_kind(pre, "pre"), _optional(pre_gamma, "pre_gamma", _F32, vec, dev),
+        _optional(nm, "pre_mean", _F32, st, dev), _optional(nr, "pre_rstd", _F32, st, dev),
+        _tensor(df, "df", dt, shape, dev), _tensor(dx, "dx", dt, shape, dev),
+        _optional(dpost_gamma, "dpost_gamma", _F32, vec, dev), _optional(dpost_beta, "dpost_beta", _F32, vec, dev),
+        dgp, _optional(dpre_gamma, "dpre_gamma", _F32, vec, dev),
+        _optional(dpre_beta, "dpre_beta", _F32, vec, dev), rows, H, code, workspace.data_ptr(), size, s),
+        "block_norm_bwd")
+
+
 def block_norm_bwd(dy, dh, f, h, stats, df, dx, *, post=None, post_gamma=None, post_beta=None,
                    gate=None, pre="rms", pre_gamma=None, residual_scale: float = 1.0,
                    block_scale: float = 1.0, dpost_gamma=None, dpost_beta=None, dgate=None,
@@ -253,41 +309,10 @@ def block_norm_bwd(dy, dh, f, h, stats, df, dx, *, post=None, post_gamma=None, p
     y, or h from elsewhere).  workspace: a CUDA tensor of at least
     block_norm_bwd_workspace_size(...) bytes, reusable call after call
     (allocated here when None)."""
-    some = dy if dy is not None else dh
-    rows, H = _rows_tensor(some, "dy" if dy is not None else "dh")
-    dt, dev, shape, vec, st = some.dtype, some.device, some.shape, some.shape[-1:], (rows,)
-    post_kind, pre_kind = _norm_kind(post, "post"), _norm_kind(pre, "pre")
-    f32 = torch.float32
-    pm, pr, nm, nr = stats or (None, None, None, None)
-    gp, gk, gs, rpg = _gate_args(gate, some)
-    if dgate is not None and gate is None:
-        raise ValueError("dgate without a gate")
-    dgp = None if dgate is None else _tensor(dgate, "dgate", f32 if gk == GATE_CHANNEL else dt, gate.shape, dev)
-    code = DTYPE_CODE[dt]
-
-    def call(s):
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(block_norm_bwd_workspace_size(rows, H, code, gk, max(rpg, 1)), dtype=torch.uint8,
-                             device=dev)
-        elif not isinstance(ws, torch.Tensor) or ws.device != dev or not ws.is_contiguous():
-            raise ValueError(f"workspace must be a contiguous tensor on {dev}")
-        return lib().block_norm_bwd(
-            _optional(dy, "dy", dt, shape, dev), _optional(dh, "dh", dt, shape, dev),
-            _optional(f, "f", dt, shape, dev), _optional(h, "h", dt, shape, dev), post_kind,
-            _optional(post_gamma, "post_gamma", f32, vec, dev),
-            _optional(post_beta, "post_beta", f32, vec, dev), _optional(pm, "post_mean", f32, st, dev),
-            _optional(pr, "post_rstd", f32, st, dev), gp, gk, gs, rpg, residual_scale, block_scale,
-            pre_kind, _optional(pre_gamma, "pre_gamma", f32, vec, dev),
-            _optional(nm, "pre_mean", f32, st, dev), _optional(nr, "pre_rstd", f32, st, dev),
-            _tensor(df, "df", dt, shape, dev), _tensor(dx, "dx", dt, shape, dev),
-            _optional(dpost_gamma, "dpost_gamma", f32, vec, dev),
-            _optional(dpost_beta, "dpost_beta", f32, vec, dev), dgp,
-            _optional(dpre_gamma, "dpre_gamma", f32, vec, dev),
-            _optional(dpre_beta, "dpre_beta", f32, vec, dev), rows, H, code, ws.data_ptr(),
-            ws.numel() * ws.element_size(), s)
-
-    _check(on_stream(dev, stream, call), "block_norm_bwd")
+    some, rows, H = _given(dy, dh)
+    on_stream(some.device, stream, lambda s: _backward(
+        s, some, rows, H, dy, dh, f, h, stats, df, dx, post, post_gamma, post_beta, gate, pre, pre_gamma,
+        residual_scale, block_scale, dpost_gamma, dpost_beta, dgate, dpre_gamma, dpre_beta, workspace))
 
 
 def block_norm_backward(dy, dh, f, h, stats, *, post=None, post_gamma=None, post_beta=None, gate=None,
@@ -295,17 +320,16 @@ def block_norm_backward(dy, dh, f, h, stats, *, post=None, post_gamma=None, post
                         block_scale: float = 1.0, stream=None) -> BlockNormGrads:
     """Allocate the gradients with PyTorch and run block_norm_bwd: the
     gradient of every input that is given (beta's gradients where a beta is)."""
-    some = dy if dy is not None else dh
-    _rows_tensor(some, "dy" if dy is not None else "dh")
+    some, rows, H = _given(dy, dh)
+
+    def like(t):
+        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
 
     def call(s):
         df, dx = torch.empty_like(some), torch.empty_like(some)
-        like = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)  # noqa: E731
         dpg, dpb, dg, dng, dnb = like(post_gamma), like(post_beta), like(gate), like(pre_gamma), like(pre_beta)
-        block_norm_bwd(dy, dh, f, h, stats, df, dx, post=post, post_gamma=post_gamma, post_beta=post_beta,
-                       gate=gate, pre=pre, pre_gamma=pre_gamma, residual_scale=residual_scale,
-                       block_scale=block_scale, dpost_gamma=dpg, dpost_beta=dpb, dgate=dg, dpre_gamma=dng,
-                       dpre_beta=dnb)
+        _backward(s, some, rows, H, dy, dh, f, h, stats, df, dx, post, post_gamma, post_beta, gate, pre, pre_gamma,
+                  residual_scale, block_scale, dpg, dpb, dg, dng, dnb, None)
         return BlockNormGrads(df, dx, dpg, dpb, dg, dng, dnb)
 
     return on_stream(some.device, stream, call)
