@@ -124,13 +124,15 @@ struct Cols {
   int c0;           // first column of group 0
   bool ok[NV];
   bool all;         // every group of the warp exists
-  int cnt;          // columns that exist
+  float n, inv_n;   // columns of the warp, 1 / n (0 for none)
   uint32_t par[NV]; // byte offset of each group in an fp32 vector of H columns
 
   __device__ __forceinline__ void init(int warp, int col0, int cols) {
     const int at0 = warp * NV * kStep + (threadIdx.x & 31) * VE;
     c0 = col0 + at0;
-    cnt = 0;
+    const int own = min(max(cols - warp * NV * kStep, 0), NV * kStep);
+    n = static_cast<float>(own);
+    inv_n = own ? __frcp_rn(n) : 0.f;
     bool full = true;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -138,7 +140,6 @@ struct Cols {
       ok[k] = at < cols;
       full = full && ok[k];
       par[k] = 4u * static_cast<uint32_t>(col0 + (ok[k] ? at : cols - VE));
-      cnt += ok[k] ? VE : 0;
     }
     all = __all_sync(0xffffffffu, full);
   }
@@ -294,11 +295,15 @@ __device__ __forceinline__ float2 walker_sum2(Exchange& ex, float2 v) {
 }
 
 // Mean and sum of squared deviations of the walker's row.  Each warp takes
-// its own first value K_w off its values (a row whose mean is large against
-// its spread then loses nothing), and v is left that way; the warps' parts
-// are put on the first warp's shift, K_w - K_0 being a difference of two
-// values of the row.  Returns the mean, the mean on this warp's shift, and
-// M2.
+// the mean of its own values, K_w, off them (a row whose mean is large
+// against its spread then loses nothing to it), and v is left that way; the
+// little that is left of the mean and the squares are summed around K_w, and
+// the warps' parts are put on the first warp's K_0.  Returns the mean, the
+// mean on this warp's shift, and M2.
+//
+// Two different fp32 values of size K differ by 2^-24 K or more, so an M2
+// below a quarter of that square is the rounding of K_w in a row of equal
+// values: such a row is made exact (all deviations and M2 zero).
 struct RowStat {
   float mean, m, M2;
 };
@@ -306,50 +311,56 @@ struct RowStat {
 template <int VE, int NV>
 __device__ __forceinline__ RowStat walker_stats(Exchange& ex, float2 (&v)[NV * VE / 2], const Cols<VE, NV>& cs) {
   constexpr int P = NV * VE / 2;
-  const float K = __shfl_sync(0xffffffffu, v[0].x, 0);
-  const float2 negK = dup2(-K);
+  constexpr unsigned kAll = 0xffffffffu;
   float2 s[2] = {dup2(0.f), dup2(0.f)}, q[2] = {dup2(0.f), dup2(0.f)};
-#pragma unroll
-  for (int j = 0; j < P; ++j) v[j] = add2(v[j], negK);
   cs.clear(v);
 #pragma unroll
   for (int j = 0; j < P; ++j) s[j & 1] = add2(s[j & 1], v[j]);
   s[0] = add2(s[0], s[1]);
-  Part p;
-  p.n = static_cast<float>(cs.cnt);
-  p.m = cs.all ? (s[0].x + s[0].y) * (1.0f / (NV * VE)) : cs.cnt ? __fdiv_rn(s[0].x + s[0].y, p.n) : 0.f;
-  const float2 negm = dup2(-p.m);
-  if (cs.all) {
+  float sum = s[0].x + s[0].y;
 #pragma unroll
-    for (int j = 0; j < P; ++j) {
-      const float2 d = add2(v[j], negm);
-      q[j & 1] = fma2(d, d, q[j & 1]);
-    }
-    q[0] = add2(q[0], q[1]);
-    p.M2 = q[0].x + q[0].y;
-    p = butterfly<true, 32>(p);
-  } else {
+  for (int off = 16; off > 0; off >>= 1) sum += __shfl_xor_sync(kAll, sum, off);
+  const float K = sum * cs.inv_n;
+  const float2 negK = dup2(-K);
 #pragma unroll
-    for (int e = 0; e < NV * VE; ++e) {
-      const float d = cs.ok[e / VE] ? get_slot(v, e) - p.m : 0.f;
-      q[0].x = fmaf(d, d, q[0].x);
+  for (int j = 0; j < P; ++j) v[j] = add2(v[j], negK);
+  cs.clear(v);
+  s[0] = s[1] = dup2(0.f);
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    s[j & 1] = add2(s[j & 1], v[j]);
+    q[j & 1] = fma2(v[j], v[j], q[j & 1]);
+  }
+  s[0] = add2(s[0], s[1]);
+  q[0] = add2(q[0], q[1]);
+  float2 w = make_float2(s[0].x + s[0].y, q[0].x + q[0].y);
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    w = add2(w, make_float2(__shfl_xor_sync(kAll, w.x, off), __shfl_xor_sync(kAll, w.y, off)));
+  const float m = w.x * cs.inv_n;
+  Part t{cs.n, m, fmaxf(fmaf(-w.x, m, w.y), 0.f) + (w.y - w.y)};  // a NaN stays
+  float K0 = K;
+  if (ex.w.warps > 1) {
+    const float4* b = ex(make_float4(K, t.n, t.m, t.M2));
+    const int width = ex.w.width;
+    K0 = b[0].x;
+    t = Part{0.f, 0.f, 0.f};
+    for (int i = (threadIdx.x & 31) & (width - 1); i < ex.w.warps; i += width) {
+      const float4 u = b[i];
+      t = merge<false>(t, Part{u.y, (u.x - K0) + u.z, u.w});
     }
-    p.M2 = q[0].x;
-    p = butterfly<false, 32>(p);
+    for (int off = 1; off < width; off <<= 1)
+      t = merge<false>(t, Part{__shfl_xor_sync(kAll, t.n, off), __shfl_xor_sync(kAll, t.m, off),
+                               __shfl_xor_sync(kAll, t.M2, off)});
   }
-  if (ex.w.warps == 1) return {K + p.m, p.m, p.M2};
-  const float4* b = ex(make_float4(K, p.n, p.m, p.M2));
-  const int width = ex.w.width;
-  const float K0 = b[0].x;
-  Part t{0.f, 0.f, 0.f};
-  for (int i = (threadIdx.x & 31) & (width - 1); i < ex.w.warps; i += 32) {
-    const float4 u = b[i];
-    t = merge<false>(t, Part{u.y, (u.x - K0) + u.z, u.w});
+  RowStat st{K0 + t.m, t.m - (K - K0), t.M2};
+  const float least = 0x1p-25f * K0;
+  if (t.M2 < least * least) {
+#pragma unroll
+    for (int j = 0; j < P; ++j) v[j] = dup2(0.f);
+    st.m = st.M2 = 0.f;
   }
-  for (int off = 1; off < width; off <<= 1)
-    t = merge<false>(t, Part{__shfl_xor_sync(0xffffffffu, t.n, off), __shfl_xor_sync(0xffffffffu, t.m, off),
-                             __shfl_xor_sync(0xffffffffu, t.M2, off)});
-  return {K0 + t.m, t.m - (K - K0), t.M2};
+  return st;
 }
 
 // ------------------------------------------------------------------ host

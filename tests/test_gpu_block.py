@@ -540,3 +540,44 @@ def test_refusals_of_the_wrapper():
         mba.block_norm_backward(y[:, :32].contiguous(), None, fc, h, st, **kw)
     with pytest.raises(TypeError):
         mba.block_norm_backward(None, None, fc, h, st, **kw)
+
+
+@pytest.mark.parametrize("H", [64, 1000, 1001, 4096, 8200])
+@pytest.mark.parametrize("c", [7.0, 0.1, -3.3e4, 1e-20])
+def test_rows_of_equal_values(H, c):
+    # variance exactly 0: y is beta, and without eps the 0 * inf of the formula
+    x = torch.full((3, H), c, device="cuda")
+    f = torch.zeros_like(x)
+    g, b = torch.rand(H, device="cuda") + 0.5, torch.randn(H, device="cuda")
+    for kw in (dict(eps=1e-5), dict(eps=1e-12)):
+        _, y, st = mba.block_norm(f, x, pre="layer", pre_gamma=g, pre_beta=b, want_stats=True, **kw)
+        assert torch.equal(y, b.expand_as(y))
+        assert bool(((st[2] - c).abs() <= 2.0 ** -23 * abs(c)).all())
+    _, y, _ = mba.block_norm(f, x, pre="layer", pre_gamma=g, pre_beta=b, eps=0.0)
+    assert bool(torch.isnan(y).all())
+    # one value a single step off is a variance, where the square of a step is
+    # an fp32 value at all: (2^-23 * 1e-20)^2 is about 1e-54, below the least
+    # subnormal 1.4e-45, and the fp32 variance is then 0
+    if abs(c) < 1e-10:
+        return
+    x[1, H // 2] = torch.nextafter(x[1, 0], torch.tensor(float("inf"), device="cuda"))
+    _, y, _ = mba.block_norm(f, x, pre="layer", pre_gamma=torch.ones_like(g), eps=0.0)
+    assert bool(torch.isfinite(y[1]).all()) and bool(torch.isnan(y[0]).all())
+
+
+@pytest.mark.parametrize("post,pre", [("layer", None), (None, "layer")])
+def test_means_near_zero_keep_their_digits(post, pre):
+    # A mean that is small against the values.  Around the first estimate K of
+    # the mean, the roundings of d = v - K (u |d| / sqrt 3 each, independent)
+    # and of the sums of d (12 in a thread, 10 levels beyond, each of a partial
+    # sum of about sqrt(its length) spreads) give the mean of 768 values an rms
+    # error of about sqrt(1/3 + 22/3) u spread / sqrt(768) = 0.1 u spread, and
+    # the result's own rounding u |mean| / sqrt 3 with |mean| about 0.05; h adds
+    # u spread / sqrt(3 * 768).  Shifting by one value of the row instead costs
+    # roundings of that value's size, some u spread each.
+    f, x, p = make((200, 768), F16, post, pre, None, seed=77, loc=0.05)
+    _, _, st = mba.block_norm(f.cuda(), x.cuda(), post=post, pre=pre, eps=1e-12, want_stats=True, **cuda(p))
+    h, _, want, _, _ = forward(f, x, p, post, pre, 1.0, 1.0, 1e-12)
+    got, w, v = (st[0], want[0], f.double()) if post else (st[2], want[2], h)
+    rms = ((got.cpu().double() - w.reshape(-1)) ** 2).mean().sqrt()
+    assert float(rms) <= 2.0 ** -24 * float(v.std()) * 0.5
