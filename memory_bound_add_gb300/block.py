@@ -21,6 +21,7 @@ norms' gamma and beta are fp32 ``[H]``.  ``gate`` is one of
 from __future__ import annotations
 
 import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
@@ -88,24 +89,24 @@ def on_stream(device, stream, call):
         return call(stream.cuda_stream)
 
 
-def _tensor(t, name, dtype, shape, device):
-    """A contiguous CUDA tensor of this dtype and shape: its address."""
-    if (isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == device
-            and t.is_contiguous()):
+def _tensor(t, name, dtype, n, index):
+    """A contiguous CUDA tensor of this dtype, with n elements, on device
+    number `index`: its address (None for None, which the library refuses
+    where the tensor is required)."""
+    if t is None:
+        return None
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == n and t.get_device() == index \
+            and t.is_contiguous():
         return t.data_ptr()
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype != dtype:
         raise ValueError(f"{name} must be {dtype}, got {t.dtype}")
-    if t.shape != shape:
-        raise ValueError(f"{name} must have shape {tuple(shape)}, got {tuple(t.shape)}")
-    if t.device != device:
-        raise ValueError(f"{name} must be on {device}, got {t.device}")
+    if t.numel() != n:
+        raise ValueError(f"{name} has {t.numel()} elements, expected {n}")
+    if t.get_device() != index:
+        raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     raise ValueError(f"{name} must be contiguous")
-
-
-def _optional(t, name, dtype, shape, device):
-    return None if t is None else _tensor(t, name, dtype, shape, device)
 
 
 def _rows_tensor(t, name):
@@ -116,7 +117,7 @@ def _rows_tensor(t, name):
         raise ValueError(f"{name} must be a CUDA tensor")
     if t.dtype not in DTYPE_CODE:
         raise ValueError(f"unsupported dtype {t.dtype}")
-    if t.dim() < 1 or t.shape[-1] < 1:
+    if not t.dim() or t.shape[-1] < 1:
         raise ValueError(f"{name} must have a last dimension (the hidden one) of at least 1")
     H = t.shape[-1]
     return t.numel() // H, H
@@ -169,7 +170,7 @@ def _gate_args(gate, x):
     if not isinstance(gate, torch.Tensor):
         raise TypeError("gate must be a torch.Tensor")
     if gate.dim() == 1:
-        return _tensor(gate, "gate", torch.float32, x.shape[-1:], x.device), GATE_CHANNEL, 0, 0
+        return _tensor(gate, "gate", torch.float32, x.shape[-1], x.get_device()), GATE_CHANNEL, 0, 0
     if gate.dtype != x.dtype:
         raise ValueError(f"a gate with rows must be {x.dtype}, got {gate.dtype}")
     if gate.device != x.device:
@@ -190,19 +191,17 @@ _F32 = torch.float32
 
 def _forward(s, f, x, h, y, stats, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta,
              residual_scale, block_scale, eps):
-    dt, dev, shape = f.dtype, f.device, f.shape
-    vec, st = shape[-1:], (rows,)
+    dt, dev, n = f.dtype, f.get_device(), rows * H
     pm, pr, nm, nr = stats
     gp, gk, gs, rpg = _gate_args(gate, f)
     _check(lib().block_norm_fwd(
-        _tensor(f, "f", dt, shape, dev), _tensor(x, "x", dt, shape, dev), _norm_kind(post, "post"),
-        _optional(post_gamma, "post_gamma", _F32, vec, dev), _optional(post_beta, "post_beta", _F32, vec, dev),
+        _tensor(f, "f", dt, n, dev), _tensor(x, "x", dt, n, dev), _norm_kind(post, "post"),
+        _tensor(post_gamma, "post_gamma", _F32, H, dev), _tensor(post_beta, "post_beta", _F32, H, dev),
         gp, gk, gs, rpg, residual_scale, block_scale, _norm_kind(pre, "pre"),
-        _optional(pre_gamma, "pre_gamma", _F32, vec, dev), _optional(pre_beta, "pre_beta", _F32, vec, dev),
-        _tensor(h, "h", dt, shape, dev), _optional(y, "y", dt, shape, dev),
-        _optional(pm, "post_mean", _F32, st, dev), _optional(pr, "post_rstd", _F32, st, dev),
-        _optional(nm, "pre_mean", _F32, st, dev), _optional(nr, "pre_rstd", _F32, st, dev), rows, H, eps,
-        DTYPE_CODE[dt], s), "block_norm_fwd")
+        _tensor(pre_gamma, "pre_gamma", _F32, H, dev), _tensor(pre_beta, "pre_beta", _F32, H, dev),
+        _tensor(h, "h", dt, n, dev), _tensor(y, "y", dt, n, dev), _tensor(pm, "post_mean", _F32, rows, dev),
+        _tensor(pr, "post_rstd", _F32, rows, dev), _tensor(nm, "pre_mean", _F32, rows, dev),
+        _tensor(nr, "pre_rstd", _F32, rows, dev), rows, H, eps, DTYPE_CODE[dt], s), "block_norm_fwd")
 
 
 def block_norm_fwd(f, x, h, y=None, stats=None, *, post=None, post_gamma=None, post_beta=None,
@@ -262,6 +261,13 @@ def block_norm_bwd_workspace_size(rows: int, H: int, dtype: int, gate_kind: int 
     return n
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_size(rows, H, code, gate_kind, rows_per_gate, index):
+    """block_norm_bwd_workspace_size on device number `index`, which is
+    current: a number that these arguments alone decide."""
+    return block_norm_bwd_workspace_size(rows, H, code, gate_kind, rows_per_gate)
+
+
 def _given(dy, dh):
     """The gradient that is given, with its rows and H."""
     some, name = (dy, "dy") if dy is not None else (dh, "dh")
@@ -270,34 +276,33 @@ def _given(dy, dh):
 
 def _backward(s, some, rows, H, dy, dh, f, h, stats, df, dx, post, post_gamma, post_beta, gate, pre, pre_gamma,
               residual_scale, block_scale, dpost_gamma, dpost_beta, dgate, dpre_gamma, dpre_beta, workspace):
-    dt, dev, shape = some.dtype, some.device, some.shape
-    vec, st, code = shape[-1:], (rows,), DTYPE_CODE[dt]
+    dt, dev, n = some.dtype, some.get_device(), rows * H
+    code = DTYPE_CODE[dt]
     pm, pr, nm, nr = stats or _NO_STATS
     gp, gk, gs, rpg = _gate_args(gate, some)
     dgp = None
     if dgate is not None:
         if gate is None:
             raise ValueError("dgate without a gate")
-        dgp = _tensor(dgate, "dgate", _F32 if gk == GATE_CHANNEL else dt, gate.shape, dev)
+        dgp = _tensor(dgate, "dgate", _F32 if gk == GATE_CHANNEL else dt, gate.numel(), dev)
     if workspace is None:
-        size = block_norm_bwd_workspace_size(rows, H, code, gk, rpg or 1)
-        workspace = torch.empty(size, dtype=torch.uint8, device=dev)
-    elif not isinstance(workspace, torch.Tensor) or workspace.device != dev or not workspace.is_contiguous():
-        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+        size = _workspace_size(rows, H, code, gk, rpg or 1, dev)
+        workspace = torch.empty(size, dtype=torch.uint8, device=some.device)
+    elif not isinstance(workspace, torch.Tensor) or workspace.get_device() != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     else:
         size = workspace.numel() * workspace.element_size()
     _check(lib().block_norm_bwd(
-        _optional(dy, "dy", dt, shape, dev), _optional(dh, "dh", dt, shape, dev), _optional(f, "f", dt, shape, dev),
-        _optional(h, "h", dt, shape, dev), _norm_kind(post, "post"),
-        _optional(post_gamma, "post_gamma", _F32, vec, dev), _optional(post_beta, "post_beta", _F32, vec, dev),
-        _optional(pm, "post_mean", _F32, st, dev), _optional(pr, "post_rstd", _F32, st, dev), gp, gk, gs, rpg,
-        residual_scale, block_scale, _norm_kind(pre, "pre"), _optional(pre_gamma, "pre_gamma", _F32, vec, dev),
-        _optional(nm, "pre_mean", _F32, st, dev), _optional(nr, "pre_rstd", _F32, st, dev),
-        _tensor(df, "df", dt, shape, dev), _tensor(dx, "dx", dt, shape, dev),
-        _optional(dpost_gamma, "dpost_gamma", _F32, vec, dev), _optional(dpost_beta, "dpost_beta", _F32, vec, dev),
-        dgp, _optional(dpre_gamma, "dpre_gamma", _F32, vec, dev),
-        _optional(dpre_beta, "dpre_beta", _F32, vec, dev), rows, H, code, workspace.data_ptr(), size, s),
-        "block_norm_bwd")
+        _tensor(dy, "dy", dt, n, dev), _tensor(dh, "dh", dt, n, dev), _tensor(f, "f", dt, n, dev),
+        _tensor(h, "h", dt, n, dev), _norm_kind(post, "post"), _tensor(post_gamma, "post_gamma", _F32, H, dev),
+        _tensor(post_beta, "post_beta", _F32, H, dev), _tensor(pm, "post_mean", _F32, rows, dev),
+        _tensor(pr, "post_rstd", _F32, rows, dev), gp, gk, gs, rpg, residual_scale, block_scale,
+        _norm_kind(pre, "pre"), _tensor(pre_gamma, "pre_gamma", _F32, H, dev),
+        _tensor(nm, "pre_mean", _F32, rows, dev), _tensor(nr, "pre_rstd", _F32, rows, dev),
+        _tensor(df, "df", dt, n, dev), _tensor(dx, "dx", dt, n, dev),
+        _tensor(dpost_gamma, "dpost_gamma", _F32, H, dev), _tensor(dpost_beta, "dpost_beta", _F32, H, dev), dgp,
+        _tensor(dpre_gamma, "dpre_gamma", _F32, H, dev), _tensor(dpre_beta, "dpre_beta", _F32, H, dev), rows, H,
+        code, workspace.data_ptr(), size, s), "block_norm_bwd")
 
 
 def block_norm_bwd(dy, dh, f, h, stats, df, dx, *, post=None, post_gamma=None, post_beta=None,
