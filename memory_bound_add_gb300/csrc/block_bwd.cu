@@ -180,6 +180,20 @@ struct Sums {
   }
 };
 
+// Fetches a row of tensor I: the groups of the thread, the first at byte off.
+template <int I, int DT, int VE, int NV, int NT>
+__device__ __forceinline__ void fetch_row(Ring<DT, VE, NV, NT>& ring, const Cols<VE, NV>& cs, int slot,
+                                          const void* t, int64_t off, int site, int64_t extent) {
+  constexpr int kStepBytes = Cols<VE, NV>::kStep * Io<DT>::kBytes;
+  [[maybe_unused]] constexpr int GB = Grp<DT, VE>::kBytes;
+  const char* q = static_cast<const char*>(t) + off;
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    const bool in = ADDLN_IN(site, off + k * kStepBytes, cs.ok[k] ? GB : 0, extent);
+    ring.fetch(slot, I, k, q + k * kStepBytes, cs.ok[k] && in);
+  }
+}
+
 template <int DT, int VE, int NV, bool FULL, bool GR>
 constexpr int bwd_regs() {
   return 128;
@@ -225,9 +239,20 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
 
   const int n = static_cast<int>(r1 - r0);  // rows of the walker
   const int row_bytes = p.H * S;
+  // statistics of the next row, loaded a row ahead
+  float hm_n = 0.f, hr_n = 0.f, fm_n = 0.f, fr_n = 1.f;
+  auto stats = [&](int64_t r) {
+    if (r >= r1 || !ADDLN_IN(725, 4 * r, 4, 4 * p.rows)) return;
+    if (has_dy) hr_n = __ldg(p.pre_rstd + r);
+    if (post) fr_n = __ldg(p.post_rstd + r);
+    if constexpr (FULL) {
+      if (p.pre_mean) hm_n = __ldg(p.pre_mean + r);
+      if (p.post_mean) fm_n = __ldg(p.post_mean + r);
+    }
+  };
   // With gate rows: the byte offset of the gate row of the row to fetch next,
-  // and how many rows it still serves.
-  int gate_left = 0;
+  // how many rows it still serves, and the first of them in the range.
+  int gate_left = 0, gate_first = 0;
   int64_t gate_at = 0;
   auto clip = [](int64_t v) { return static_cast<int>(min(v, static_cast<int64_t>(0x7fffffff))); };
   auto gate_of = [&](int64_t r) {
@@ -239,27 +264,26 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
     gate_left = clip((g + 1) * p.rows_per_gate - r0);
     gate_at = (g * p.gate_stride + cs.c0) * S;
   }
-  // row number i of the range, whose group 0 of this thread is at byte `at`
-  auto fetch = [&](int slot, int i, int64_t at) {
+  // Row number i of the range, whose group 0 of this thread is at byte `at`,
+  // in two parts: dy and dh are read once, and their places are free again
+  // before those of h, f and the gate.
+  auto fetch_first = [&](int slot, int i, int64_t at) {
     if (i < n) {
-      auto one = [&](int i, const void* t, int64_t off, int site, int64_t ext) {
-        const char* q = static_cast<const char*>(t) + off;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-          const bool in = ADDLN_IN(site, off + k * kStepBytes, cs.ok[k] ? GB : 0, ext);
-          ring.fetch(slot, i, k, q + k * kStepBytes, cs.ok[k] && in);
-        }
-      };
-      if (has_dy) {
-        one(0, p.dy, at, 723, extent);
-        one(1, p.h, at, 724, extent);
-      }
-      if (has_dh) one(2, p.dh, at, 721, extent);
-      if (need_f) one(3, p.f, at, 722, extent);
+      if (has_dy) fetch_row<0>(ring, cs, slot, p.dy, at, 723, extent);
+      if (has_dh) fetch_row<2>(ring, cs, slot, p.dh, at, 721, extent);
+    }
+    ring.commit();
+  };
+  auto fetch_rest = [&](int slot, int i, int64_t at) {
+    if (i < n) {
+      if (has_dy) fetch_row<1>(ring, cs, slot, p.h, at, 724, extent);
+      if (need_f) fetch_row<3>(ring, cs, slot, p.f, at, 722, extent);
       if constexpr (GR) {
-        one(4, p.gate, gate_at, 731, b_gate_bytes(p, S));
+        // a gate row that the slot's last row had is there already
+        if (!R::kAsync || i - gate_first < slots) fetch_row<4>(ring, cs, slot, p.gate, gate_at, 731, b_gate_bytes(p, S));
         if (--gate_left == 0) {
           gate_left = clip(p.rows_per_gate);
+          if constexpr (R::kAsync) gate_first = i + 1;
           gate_at += p.gate_stride * S;
         }
       }
@@ -289,8 +313,13 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
     if (!has_dh) ring.clear(s, 2);
     if (!need_f) ring.clear(s, 3);
   }
-  if constexpr (R::kAsync)
-    for (int s = 0; s < slots; ++s) fetch(s, s, (r0 + s) * row_bytes + cs.c0 * S);
+  if constexpr (R::kAsync) {
+    for (int s = 0; s < slots; ++s) {
+      const int64_t at = (r0 + s) * row_bytes + cs.c0 * S;
+      fetch_first(s, s, at);
+      fetch_rest(s, s, at);
+    }
+  }
 
   // parameters, while the first rows arrive
 #pragma unroll
@@ -311,17 +340,6 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
     kept.put(1, k, w);
     if constexpr (FULL && GR) kept.put(2, k, b);
   }
-  // statistics of the next row, loaded a row ahead
-  float hm_n = 0.f, hr_n = 0.f, fm_n = 0.f, fr_n = 1.f;
-  auto stats = [&](int64_t r) {
-    if (r >= r1 || !ADDLN_IN(725, 4 * r, 4, 4 * p.rows)) return;
-    if (has_dy) hr_n = __ldg(p.pre_rstd + r);
-    if (post) fr_n = __ldg(p.post_rstd + r);
-    if constexpr (FULL) {
-      if (p.pre_mean) hm_n = __ldg(p.pre_mean + r);
-      if (p.post_mean) fm_n = __ldg(p.post_mean + r);
-    }
-  };
   stats(r0);
 
   // The gate's sums of single-element rows lie in shared memory (whose ring is
@@ -350,8 +368,12 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
   int slot = 0;
   int64_t off = r0 * row_bytes + cs.c0 * S;
   for (int it = 0; it < n; ++it, off += row_bytes) {
-    if constexpr (!R::kAsync) fetch(0, it, off);
-    if (slots == 1) ring.template wait<0>(); else ring.template wait<1>();
+    if constexpr (!R::kAsync) {
+      fetch_first(0, it, off);
+      fetch_rest(0, it, off);
+    }
+    // all but the next row's two parts
+    if (slots == 1) ring.template wait<0>(); else ring.template wait<2>();
     const float2 nhm = dup2(-hm_n), hr = dup2(hr_n), nfm = dup2(-fm_n), fr = dup2(fr_n);
     stats(r0 + it + 1);
     auto take = [&](int i, int k, float2 (&v)[N]) {
@@ -405,6 +427,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
         }
       }
     }
+    if constexpr (R::kAsync) fetch_first(slot, it + slots, off + slots * row_bytes);
     float m[K];
 #pragma unroll
     for (int i = 0; i < K; ++i) m[i] = q[i].x + q[i].y;
@@ -465,7 +488,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
         if (cs.ok[k + e] && ADDLN_IN(735, off + (k + e) * kStepBytes, GB, extent))
           store_group<DT, VE>(df + (k + e) * kStepBytes, o, e);
     }
-    if constexpr (R::kAsync) fetch(slot, it + slots, off + slots * row_bytes);  // the slot has been read
+    if constexpr (R::kAsync) fetch_rest(slot, it + slots, off + slots * row_bytes);
     slot = slot + 1 == slots ? 0 : slot + 1;
     if constexpr (GR) {
       if (--flush == 0 || it + 1 == n) {
