@@ -22,6 +22,7 @@ namespace blk {
 constexpr int kMaxThreads = 512;  // threads a CTA
 constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;    // the portable cluster size
+constexpr int kMaxSmem = 227 * 1024;  // dynamic shared memory of a CTA
 
 // VE elements of DT at p (element offset i), as 32-bit words or one 16-bit
 // value, and their fp32 values in slots [k VE, (k + 1) VE) of float2 v[NV VE / 2].
@@ -86,22 +87,25 @@ __device__ __forceinline__ void store_group(char* q, const float2 (&v)[P], int k
   }
 }
 
-// VE fp32 parameters at byte offset `off` into the slots of group k.
-template <int VE, int P>
-__device__ __forceinline__ void load_param(const float* p, uint32_t off, float2 (&v)[P], int k) {
+// VE fp32 parameters at byte offset `off`; `fill` where there are none.
+template <int VE>
+__device__ __forceinline__ void load_params(const float* p, uint32_t off, float fill, float (&v)[VE], int site,
+                                            int64_t extent) {
+#pragma unroll
+  for (int e = 0; e < VE; ++e) v[e] = fill;
+  if (p == nullptr || !ADDLN_IN(site, off, 4 * VE, extent)) return;
   const char* q = reinterpret_cast<const char*>(p) + off;
   if constexpr (VE >= 4) {
 #pragma unroll
     for (int h = 0; h < VE / 4; ++h) {
-      const float4 t = __ldg(reinterpret_cast<const float4*>(q) + h);
-      v[k * VE / 2 + 2 * h] = make_float2(t.x, t.y);
-      v[k * VE / 2 + 2 * h + 1] = make_float2(t.z, t.w);
+      const float4 u = __ldg(reinterpret_cast<const float4*>(q) + h);
+      v[4 * h] = u.x, v[4 * h + 1] = u.y, v[4 * h + 2] = u.z, v[4 * h + 3] = u.w;
     }
   } else if constexpr (VE == 2) {
-    v[k] = __ldg(reinterpret_cast<const float2*>(q));
+    const float2 u = __ldg(reinterpret_cast<const float2*>(q));
+    v[0] = u.x, v[1] = u.y;
   } else {
-    const float t = __ldg(reinterpret_cast<const float*>(q));
-    if (k & 1) v[k >> 1].y = t; else v[k >> 1].x = t;
+    v[0] = __ldg(reinterpret_cast<const float*>(q));
   }
 }
 
@@ -169,8 +173,8 @@ template <int DT, int VE, int NV, int NT>
 struct Ring {
   static constexpr int kBytes = Grp<DT, VE>::kBytes;
   static constexpr bool kAsync = kBytes >= 4;
-  static constexpr uint32_t kStep = 32 * kBytes;                               // between groups
-  static constexpr uint32_t kWarp = kAsync ? kMaxSlots * NT * NV * kStep : 0;  // bytes a warp needs
+  static constexpr uint32_t kStep = 32 * kBytes;                    // between groups
+  static constexpr uint32_t kSlot = kAsync ? NT * NV * kStep : 0;  // bytes of a warp's slot
   uint32_t base;  // this thread's first group of slot 0
   uint32_t held[kAsync ? 1 : NT][kAsync ? 1 : NV / 2];
 
@@ -235,27 +239,87 @@ struct Ring {
   }
 };
 
+// Parameters in shared memory, each thread's columns in places of its own (a
+// warp's in one piece [vector][group][part][lane]), so that a read costs half
+// of what a 16-byte load through L1 does.
+template <int VE, int NV>
+struct Kept {
+  static constexpr int kPart = VE >= 4 ? 16 : VE * 4;
+  static constexpr int Q = VE * 4 / kPart;
+  static constexpr uint32_t kStep = 32 * kPart;
+  template <int NP>
+  __device__ static constexpr uint32_t bytes() {
+    return NP * NV * Q * kStep;
+  }
+  uint32_t base;
+
+  __device__ __forceinline__ uint32_t at(int i, int k, int q) const {
+    return base + static_cast<uint32_t>((i * NV + k) * Q + q) * kStep;
+  }
+  __device__ __forceinline__ void put(int i, int k, const float (&v)[VE]) const {
+#pragma unroll
+    for (int q = 0; q < Q; ++q) {
+      if constexpr (VE >= 4)
+        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at(i, k, q)), "f"(v[4 * q]), "f"(v[4 * q + 1]),
+                     "f"(v[4 * q + 2]), "f"(v[4 * q + 3]) : "memory");
+      else if constexpr (VE == 2)
+        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at(i, k, q)), "f"(v[0]), "f"(v[1]) : "memory");
+      else
+        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at(i, k, q)), "f"(v[0]) : "memory");
+    }
+  }
+  // N groups from k0 on
+  template <int N>
+  __device__ __forceinline__ void get(int i, int k0, float2 (&v)[N * VE / 2]) const {
+#pragma unroll
+    for (int k = 0; k < N; ++k)
+#pragma unroll
+      for (int q = 0; q < Q; ++q) {
+        if constexpr (VE >= 4) {
+          const uint4 u = ld_shared_v4(at(i, k0 + k, q));
+          v[k * VE / 2 + 2 * q] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+          v[k * VE / 2 + 2 * q + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+        } else if constexpr (VE == 2) {
+          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v[k].x), "=f"(v[k].y) : "r"(at(i, k0 + k, q)));
+        } else {
+          float f;
+          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(at(i, k0 + k, q)));
+          if (k & 1) v[k >> 1].y = f; else v[k >> 1].x = f;
+        }
+      }
+  }
+};
+
 // --------------------------------------------------------- row reductions
 // Every warp publishes one float4; after exchange() every thread of the
-// walker may read all n of them, in the same order.  Two buffers in turn: a
+// walker may read all of them, in the same order.  Two buffers in turn: a
 // warp can write exchange i + 2's values only after the barrier of exchange
 // i + 1, which every warp passes only when it has read those of exchange i.
+// SIDES: a CTA may have walkers of several warps side by side, each with a
+// barrier of its own (a kernel that names barriers by number takes all 16 of
+// them, so that only four of its CTAs fit an SM).
+template <bool SIDES>
 struct Exchange {
-  float4 (*buf)[kMaxWarps * kMaxCluster];  // [2][...]
   const Walk& w;
-  int rank;  // this CTA's place among the walker's
+  int at;  // byte offset in shared memory of [2][warps], this walker's
   int par;
 
   __device__ __forceinline__ const float4* operator()(float4 v) {
-    float4* b = buf[par];
+    extern __shared__ __align__(128) unsigned char smem[];
+    float4* b = reinterpret_cast<float4*>(smem + at) + par * w.warps;
     par ^= 1;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int lane = threadIdx.x & 31, side = SIDES ? (threadIdx.x >> 5) / w.cta_warps : 0;
+    const int warp = (threadIdx.x >> 5) - side * w.cta_warps;
     if (w.C == 1) {
       if (lane == 0) b[warp] = v;
-      __syncthreads();
+      if constexpr (SIDES)
+        asm volatile("bar.sync %0, %1;" ::"r"(1 + side), "r"(w.cta_warps * 32) : "memory");
+      else
+        __syncthreads();
     } else {
       namespace cg = cooperative_groups;
       cg::cluster_group cl = cg::this_cluster();
+      const int rank = static_cast<int>(blockIdx.x % w.C);
       if (lane < w.C) cl.map_shared_rank(b, lane)[rank * w.cta_warps + warp] = v;
       cl.sync();
     }
@@ -263,9 +327,10 @@ struct Exchange {
   }
 };
 
-// Sums over the walker, the same bits in every thread: a warp butterfly, then
+// Sum over the walker, the same bits in every thread: a warp butterfly, then
 // the warps' sums in a fixed order.
-__device__ __forceinline__ float walker_sum(Exchange& ex, float v) {
+template <bool SIDES>
+__device__ __forceinline__ float walker_sum(Exchange<SIDES>& ex, float v) {
 #pragma unroll
   for (int off = 16; off > 0; off >>= 1) v += __shfl_xor_sync(0xffffffffu, v, off);
   if (ex.w.warps == 1) return v;
@@ -276,21 +341,6 @@ __device__ __forceinline__ float walker_sum(Exchange& ex, float v) {
   float t = 0.f;
   for (int i = (threadIdx.x & 31) & (width - 1); i < ex.w.warps; i += 32) t += b[i].x;
   for (int off = 1; off < width; off <<= 1) t += __shfl_xor_sync(0xffffffffu, t, off);
-  return t;
-}
-
-__device__ __forceinline__ float2 walker_sum2(Exchange& ex, float2 v) {
-#pragma unroll
-  for (int off = 16; off > 0; off >>= 1)
-    v = add2(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, off), __shfl_xor_sync(0xffffffffu, v.y, off)));
-  if (ex.w.warps == 1) return v;
-  const float4* b = ex(make_float4(v.x, v.y, 0.f, 0.f));
-  const int width = ex.w.width;
-  float2 t = dup2(0.f);
-  for (int i = (threadIdx.x & 31) & (width - 1); i < ex.w.warps; i += 32)
-    t = add2(t, *reinterpret_cast<const float2*>(b + i));
-  for (int off = 1; off < width; off <<= 1)
-    t = add2(t, make_float2(__shfl_xor_sync(0xffffffffu, t.x, off), __shfl_xor_sync(0xffffffffu, t.y, off)));
   return t;
 }
 
@@ -308,8 +358,8 @@ struct RowStat {
   float mean, m, M2;
 };
 
-template <int VE, int NV>
-__device__ __forceinline__ RowStat walker_stats(Exchange& ex, float2 (&v)[NV * VE / 2], const Cols<VE, NV>& cs) {
+template <int VE, int NV, bool SIDES>
+__device__ __forceinline__ RowStat walker_stats(Exchange<SIDES>& ex, float2 (&v)[NV * VE / 2], const Cols<VE, NV>& cs) {
   constexpr int P = NV * VE / 2;
   constexpr unsigned kAll = 0xffffffffu;
   float2 s[2] = {dup2(0.f), dup2(0.f)}, q[2] = {dup2(0.f), dup2(0.f)};

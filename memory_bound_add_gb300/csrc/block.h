@@ -39,7 +39,8 @@ struct BlockFwdArgs {
   int H;
   int post, pre, gate_kind;
   float a, s, eps, inv_h;
-  int slots;  // rows staged ahead, 1 or 2
+  int slots, ring_slots;  // rows staged ahead, 1 or 2; slots there are
+  int kept_at, sums_at;   // where parameters and row sums lie in shared memory
   Walk w;
 };
 

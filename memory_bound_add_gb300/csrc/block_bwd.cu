@@ -73,57 +73,6 @@ __device__ __forceinline__ void store_cols(float* t, const Cols<VE, NV>& cs, int
   }
 }
 
-// A thread's parameters in its own places of shared memory, a warp's in one
-// piece [vector][group][part][lane].  Vector 0: gamma of the pre norm; 1: the
-// factor c, or with gate rows s pg (c is then that times the gate); 2: s pb.
-template <int VE, int NV>
-struct Kept {
-  static constexpr int kPart = VE >= 4 ? 16 : VE * 4;
-  static constexpr int Q = VE * 4 / kPart;
-  static constexpr uint32_t kStep = 32 * kPart;
-  template <int NP>
-  __device__ static constexpr uint32_t bytes() {
-    return NP * NV * Q * kStep;
-  }
-  uint32_t base;
-
-  __device__ __forceinline__ uint32_t at(int i, int k, int q) const {
-    return base + static_cast<uint32_t>((i * NV + k) * Q + q) * kStep;
-  }
-  __device__ __forceinline__ void put(int i, int k, const float (&v)[VE]) const {
-#pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      if constexpr (VE >= 4)
-        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at(i, k, q)), "f"(v[4 * q]), "f"(v[4 * q + 1]),
-                     "f"(v[4 * q + 2]), "f"(v[4 * q + 3]) : "memory");
-      else if constexpr (VE == 2)
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at(i, k, q)), "f"(v[0]), "f"(v[1]) : "memory");
-      else
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at(i, k, q)), "f"(v[0]) : "memory");
-    }
-  }
-  // N groups from k0 on
-  template <int N>
-  __device__ __forceinline__ void get(int i, int k0, float2 (&v)[N * VE / 2]) const {
-#pragma unroll
-    for (int k = 0; k < N; ++k)
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        if constexpr (VE >= 4) {
-          const uint4 u = ld_shared_v4(at(i, k0 + k, q));
-          v[k * VE / 2 + 2 * q] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
-          v[k * VE / 2 + 2 * q + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
-        } else if constexpr (VE == 2) {
-          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v[k].x), "=f"(v[k].y) : "r"(at(i, k0 + k, q)));
-        } else {
-          float f;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(at(i, k0 + k, q)));
-          if (k & 1) v[k >> 1].y = f; else v[k >> 1].x = f;
-        }
-      }
-  }
-};
-
 // K sums (4 or 8) over the walker's threads, the same bits in every thread.
 // Within a warp each step halves the sums a lane carries: 6 (9) exchanges
 // instead of 5 K.
@@ -223,7 +172,9 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
   const int slots = R::kAsync ? p.slots : 1;
   R ring;
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  ring.base = smem_addr(smem) + warp * R::kWarp + lane * GB;
+  ring.base = smem_addr(smem) + warp * kMaxSlots * R::kSlot + lane * GB;
+  // vector 0: gamma of the pre norm; 1: the factor c, or with gate rows s pg
+  // (c is then that times the gate); 2: s pb
   Kept<VE, NV> kept;
   kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<NP>() + lane * Kept<VE, NV>::kPart;
   Sums<K> sums{reinterpret_cast<float*>(smem + p.sums_at) + side * 2 * p.w.warps * K, p.w, rank, 0, 1 + side};
@@ -324,16 +275,17 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
   // parameters, while the first rows arrive
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    float g[VE], w[VE], b[VE];
+    const int64_t ext = 4 * static_cast<int64_t>(p.H);
+    float g[VE], w[VE], b[VE], gt[VE];
+    load_params<VE>(has_dy ? p.pre_gamma : nullptr, cs.par[k], 0.f, g, 726, ext);
+    load_params<VE>(!GR && p.gate_kind == ADDLN_GATE_CHANNEL ? static_cast<const float*>(p.gate) : nullptr, cs.par[k], 1.f,
+                    gt, 728, ext);
+    load_params<VE>(p.post_gamma, cs.par[k], 1.f, w, 729, ext);
+    load_params<VE>(FULL && GR ? p.post_beta : nullptr, cs.par[k], 0.f, b, 730, ext);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
-      const uint32_t c = cs.par[k] / 4u + e;
-      const bool in = ADDLN_IN(726, 4 * c, 4, 4 * static_cast<int64_t>(p.H));
-      g[e] = has_dy && in ? __ldg(p.pre_gamma + c) : 0.f;
-      w[e] = p.s;
-      if (!GR && p.gate_kind == ADDLN_GATE_CHANNEL && in) w[e] *= __ldg(static_cast<const float*>(p.gate) + c);
-      if (post && in) w[e] *= __ldg(p.post_gamma + c);
-      b[e] = FULL && GR && p.post_beta && in ? p.s * __ldg(p.post_beta + c) : 0.f;
+      w[e] *= p.s * gt[e];
+      b[e] *= p.s;
       if (!cs.ok[k]) g[e] = w[e] = b[e] = 0.f;
     }
     kept.put(0, k, g);

@@ -25,12 +25,12 @@ __device__ __forceinline__ int64_t f_gate_bytes(const BlockFwdArgs& p, int S) {
 // 1 / sqrt(mean square + eps) (in M2's place) and the mean that precedes it,
 // of one row's slots; a layer norm leaves them shifted, an rms norm as they
 // were (mean 0).
-template <int VE, int NV, bool LN>
-__device__ __forceinline__ RowStat row_norm(Exchange& ex, float2 (&v)[NV * VE / 2], const Cols<VE, NV>& cs, bool layer,
+template <int VE, int NV, bool LN, bool SIDES>
+__device__ __forceinline__ RowStat row_norm(Exchange<SIDES>& ex, float2 (&v)[NV * VE / 2], const Cols<VE, NV>& cs, bool layer,
                                             float inv_h, float eps) {
   RowStat st{0.f, 0.f, 0.f};
   if (LN && layer) {
-    st = walker_stats<VE, NV>(ex, v, cs);
+    st = walker_stats(ex, v, cs);
   } else {
     // the slots of groups that do not exist hold zeros
     float2 q[2] = {dup2(0.f), dup2(0.f)};
@@ -45,59 +45,57 @@ __device__ __forceinline__ RowStat row_norm(Exchange& ex, float2 (&v)[NV * VE / 
 
 // The parameters as the row's arithmetic uses them: w = s gate gamma and
 // b = s gate beta of the post norm (gate: a per-channel one; without a post
-// norm w = s gate, b = 0), and gamma and beta of the pre norm.
+// norm w = s gate, b = 0), and gamma and beta of the pre norm.  Loading them
+// again for every row costs more of L1's bandwidth than the row itself: two
+// vectors (no layer norm, no bias) stay in registers, and four of at most
+// eight columns a thread; four of more lie in shared memory, one copy for all
+// rows that the CTA has side by side.
+__host__ __device__ constexpr bool in_registers(int columns, bool ln) { return !ln || columns <= 8; }
+
 template <int VE, int NV, bool LN>
 struct Params {
-  static constexpr int P = NV * VE / 2;
-  // they stay in registers where they are at most 64: loading them again for
-  // every row costs more of L1's bandwidth than the row itself
-  static constexpr bool kKept = NV * VE * (LN ? 4 : 2) <= (VE == 2 ? 32 : 64);
-  static constexpr int Q = kKept ? P : (VE >= 2 ? VE / 2 : 1);
-  float2 w[Q], b[LN ? Q : 1], g[Q], e[LN ? Q : 1];
+  static constexpr bool kRegs = in_registers(NV * VE, LN);
+  static constexpr int P = kRegs ? NV * VE / 2 : 1;
+  float2 r[LN ? 4 : 2][P];  // w, gamma, and with LN b, beta
+  Kept<VE, NV> kept;        // the same vectors
 
-  // slots of group k, at j of these arrays
-  __device__ __forceinline__ void load_post(const BlockFwdArgs& p, uint32_t off, int k) {
-    float2 gt[Q];
-    const bool channel = p.gate_kind == ADDLN_GATE_CHANNEL;
-    constexpr int n = VE >= 2 ? VE / 2 : 1;
-    const int j0 = VE >= 2 ? k * VE / 2 : k / 2;
-    if (channel) load_param<VE>(static_cast<const float*>(p.gate), off, gt, k);
-    if (p.post != ADDLN_NORM_NONE) load_param<VE>(p.post_gamma, off, w, k);
-    if (LN && p.post_beta) load_param<VE>(p.post_beta, off, b, k);
+  // vector i, group(s) k on
+  template <int KU, int N>
+  __device__ __forceinline__ void get(int i, int k, float2 (&v)[N]) const {
+    if constexpr (kRegs) {
 #pragma unroll
-    for (int i = 0; i < n; ++i) {
-      const int j = j0 + i;
-      if constexpr (VE >= 2) {
-        float2 f = dup2(p.s);
-        if (channel) f = mul2(f, gt[j]);
-        w[j] = p.post != ADDLN_NORM_NONE ? mul2(f, w[j]) : f;
-        if constexpr (LN) b[j] = p.post_beta ? mul2(f, b[j]) : dup2(0.f);
-      } else {
-        const float f = channel ? p.s * ((k & 1) ? gt[j].y : gt[j].x) : p.s;
-        float& u = (k & 1) ? w[j].y : w[j].x;
-        u = p.post != ADDLN_NORM_NONE ? f * u : f;
-        if constexpr (LN) {
-          float& c = (k & 1) ? b[j].y : b[j].x;
-          c = p.post_beta ? f * c : 0.f;
-        }
-      }
+      for (int j = 0; j < N; ++j) v[j] = r[i][k * VE / 2 + j];
+    } else {
+      kept.template get<KU>(i, k, v);
     }
   }
-  __device__ __forceinline__ void load_pre(const BlockFwdArgs& p, uint32_t off, int k) {
-    load_param<VE>(p.pre_gamma, off, g, k);
-    if constexpr (LN) {
-      constexpr int n = VE >= 2 ? VE / 2 : 1;
-      const int j0 = VE >= 2 ? k * VE / 2 : k / 2;
-      if (p.pre_beta) {
-        load_param<VE>(p.pre_beta, off, e, k);
-      } else {
+
+  // group k, from the call's arguments
+  __device__ __forceinline__ void load(const BlockFwdArgs& p, uint32_t off, int k) {
+    const int64_t extent = 4 * static_cast<int64_t>(p.H);
+    float v[4][VE], gt[VE];
+    load_params<VE>(p.gate_kind == ADDLN_GATE_CHANNEL ? static_cast<const float*>(p.gate) : nullptr, off, 1.f, gt, 702,
+                    extent);
+    load_params<VE>(p.post_gamma, off, 1.f, v[0], 704, extent);
+    load_params<VE>(p.pre_gamma, off, 0.f, v[1], 711, extent);
+    load_params<VE>(LN ? p.post_beta : nullptr, off, 0.f, v[2], 708, extent);
+    load_params<VE>(LN ? p.pre_beta : nullptr, off, 0.f, v[3], 712, extent);
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-          if constexpr (VE >= 2)
-            e[j0 + i] = dup2(0.f);
-          else
-            (k & 1 ? e[j0].y : e[j0].x) = 0.f;
+    for (int e = 0; e < VE; ++e) {
+      const float f = p.s * gt[e];
+      v[0][e] *= f;
+      v[2][e] *= f;
+    }
+#pragma unroll
+    for (int i = 0; i < (LN ? 4 : 2); ++i) {
+      if constexpr (kRegs) {
+#pragma unroll
+        for (int e = 0; e < VE; ++e) {
+          const int s = k * VE + e;
+          ((s & 1) ? r[i][s >> 1].y : r[i][s >> 1].x) = v[i][e];
         }
+      } else {
+        kept.put(i, k, v[i]);
       }
     }
   }
@@ -128,20 +126,19 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, VE, NV,
   constexpr int GB = Grp<DT, VE>::kBytes;
   constexpr int NT = GR ? 3 : 2;
   constexpr int kStepBytes = Cols<VE, NV>::kStep * S;
-  __shared__ float4 parts[2][kMaxWarps * kMaxCluster];
   extern __shared__ __align__(128) unsigned char smem[];
-  const bool row_warp = p.w.rows_per_cta > 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int lane = threadIdx.x & 31;
+  const int side = (threadIdx.x >> 5) / p.w.cta_warps, warp = (threadIdx.x >> 5) - side * p.w.cta_warps;
   const int rank = p.w.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.w.C);
   const int64_t stride = static_cast<int64_t>(gridDim.x / p.w.C) * p.w.rows_per_cta;
-  int64_t row = static_cast<int64_t>(blockIdx.x / p.w.C) * p.w.rows_per_cta + (row_warp ? warp : 0);
+  int64_t row = static_cast<int64_t>(blockIdx.x / p.w.C) * p.w.rows_per_cta + side;
   const int col0 = rank * p.w.slice;
-  Exchange ex{parts, p.w, rank, 0};
-  const bool leader = rank == 0 && lane == 0 && (row_warp || warp == 0);
+  Exchange<!in_registers(NV * VE, LN)> ex{p.w, p.sums_at + side * 2 * p.w.warps * 16, 0};
+  const bool leader = rank == 0 && lane == 0 && warp == 0;
   Ring<DT, VE, NV, NT> ring;
-  ring.base = smem_addr(smem) + warp * Ring<DT, VE, NV, NT>::kWarp + lane * GB;
+  ring.base = smem_addr(smem) + (threadIdx.x >> 5) * p.ring_slots * Ring<DT, VE, NV, NT>::kSlot + lane * GB;
   Cols<VE, NV> cs;
-  cs.init(row_warp ? 0 : warp, col0, min(p.w.slice, p.H - col0));
+  cs.init(warp, col0, min(p.w.slice, p.H - col0));
   // byte offset of this thread's group 0 in a row
   auto offset = [&](int64_t r) { return (r * p.H + cs.c0) * S; };
 
@@ -186,15 +183,14 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, VE, NV,
   pdl_wait();
   for (int s = 0; s < slots; ++s) fetch(s, row + s * stride);
   Params<VE, NV, LN> par;
-  constexpr bool kKept = Params<VE, NV, LN>::kKept;
-  if constexpr (kKept) {
+  constexpr bool kRegs = Params<VE, NV, LN>::kRegs;
+  if constexpr (!kRegs)
+    par.kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<4>() + lane * Kept<VE, NV>::kPart;
+  if (kRegs || side == 0) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k)
-      if (ADDLN_IN(702, cs.par[k], 4 * VE, 4 * static_cast<int64_t>(p.H))) {
-        par.load_post(p, cs.par[k], k);
-        if (p.pre != ADDLN_NORM_NONE) par.load_pre(p, cs.par[k], k);
-      }
+    for (int k = 0; k < NV; ++k) par.load(p, cs.par[k], k);
   }
+  if constexpr (!kRegs) __syncthreads();
 
   for (int slot = 0; row < p.rows; row += stride, slot = slot + 1 == slots ? 0 : slot + 1) {
     if (slots == 1) ring.template wait<0>(); else ring.template wait<1>();
@@ -234,12 +230,14 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, VE, NV,
           ring.template take<KU>(slot, 2, k, rg);
           to_slots<DT, VE, KU>(rg, gt);
         }
-        if constexpr (!kKept)
-          if (ADDLN_IN(711, cs.par[k], 4 * VE, 4 * static_cast<int64_t>(p.H))) par.load_post(p, cs.par[k], 0);
+        float2 w[n], b[n];
+        par.template get<KU>(0, k, w);
+        if constexpr (LN) par.template get<KU>(2, k, b);
 #pragma unroll
         for (int i = 0; i < n; ++i) {
-          const int j = (VE >= 2 ? k * VE / 2 : k / 2) + i, q = kKept ? j : i;
-          v[j] = affine(v[j], par.w[q], LN ? par.b[LN ? q : 0] : dup2(0.f), GR ? gt[i] : dup2(1.f), x[i]);
+          const int j = (VE >= 2 ? k * VE / 2 : k / 2) + i;
+          if constexpr (!LN) b[i] = dup2(0.f);
+          v[j] = affine(v[j], w[i], b[i], GR ? gt[i] : dup2(1.f), x[i]);
         }
       }
     }
@@ -261,23 +259,24 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, VE, NV,
     }
     char* y = static_cast<char*>(p.y) + off;
     const float2 negm = dup2(-st.m), r2 = dup2(st.M2);
+    constexpr int KU = VE >= 2 ? 1 : 2, n = VE >= 2 ? VE / 2 : 1;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if (!kKept && ADDLN_IN(708, cs.par[k], 4 * VE, 4 * static_cast<int64_t>(p.H))) par.load_pre(p, cs.par[k], 0);
-      constexpr int n = VE >= 2 ? VE / 2 : 1;
-      const int j0 = VE >= 2 ? k * VE / 2 : k / 2;
-      if (VE >= 2 || (k & 1) == 0) {
+    for (int k = 0; k < NV; k += KU) {
+      float2 g[n], e[n];
+      par.template get<KU>(1, k, g);
+      if constexpr (LN) par.template get<KU>(3, k, e);
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-          const int j = j0 + i, q = kKept ? j : i;
-          if constexpr (LN)
-            v[j] = fma2(mul2(add2(v[j], negm), r2), par.g[q], par.e[LN ? q : 0]);
-          else
-            v[j] = mul2(mul2(v[j], r2), par.g[q]);
-        }
+      for (int i = 0; i < n; ++i) {
+        const int j = (VE >= 2 ? k * VE / 2 : k / 2) + i;
+        if constexpr (LN)
+          v[j] = fma2(mul2(add2(v[j], negm), r2), g[i], e[i]);
+        else
+          v[j] = mul2(mul2(v[j], r2), g[i]);
       }
-      if (cs.ok[k] && ADDLN_IN(709, off + k * kStepBytes, GB, f_rows_bytes(p, S)))
-        store_group<DT, VE>(y + k * kStepBytes, v, k);
+#pragma unroll
+      for (int q = k; q < k + KU; ++q)
+        if (cs.ok[q] && ADDLN_IN(709, off + q * kStepBytes, GB, f_rows_bytes(p, S)))
+          store_group<DT, VE>(y + q * kStepBytes, v, q);
     }
   }
   // a CTA's shared memory has to outlive its peers' writes into it
@@ -307,37 +306,54 @@ std::unordered_map<Key, int, KeyHash> g_occ;
 struct Choice {
   void (*k)(BlockFwdArgs) = nullptr;
   Shape sh{};
-  int smem = 0;
+  int smem = 0, kept_at = 0, sums_at = 0, ring_slots = 0;
 };
 
-// Rows of `groups` groups of VE columns, NV groups a thread: a warp for a row
-// where 32 threads hold it, four rows to a CTA; else a CTA of up to
-// kMaxThreads; else a cluster.
+// Threads a CTA may give a row: half of them where parameters lie in shared
+// memory, so that those of a CTA's columns leave room for the ring.
+inline int most_threads(int columns, bool ln) { return in_registers(columns, ln) ? kMaxThreads : kMaxThreads / 2; }
+
+// NV groups of VE columns a thread.  With the parameters in registers: a warp
+// for a row where 32 threads hold it, four rows to a CTA; else a CTA of up to
+// kMaxThreads; else a cluster.  With parameters in shared memory: rows of up
+// to 256 threads side by side in a CTA of up to 512, as many as leave the
+// ring two slots, or one; wider rows in clusters.
 template <int DT, int VE, int NV>
 Choice make(const BlockFwdArgs& p, bool ln) {
   Choice c;
   const bool gr = p.gate_kind == ADDLN_GATE_ROWS;
-  c.k = gr ? &k_block_fwd<DT, VE, NV, false, true> : &k_block_fwd<DT, VE, NV, false, false>;
-  if constexpr (VE < 4 || NV < 4)  // layer norms keep more a column: fewer columns a thread
-    if (ln) c.k = gr ? &k_block_fwd<DT, VE, NV, true, true> : &k_block_fwd<DT, VE, NV, true, false>;
-  const int groups = p.H / VE;
-  c.sh.C = (groups + NV * kMaxThreads - 1) / (NV * kMaxThreads);
+  c.k = gr ? (ln ? &k_block_fwd<DT, VE, NV, true, true> : &k_block_fwd<DT, VE, NV, false, true>)
+           : (ln ? &k_block_fwd<DT, VE, NV, true, false> : &k_block_fwd<DT, VE, NV, false, false>);
+  const int groups = p.H / VE, most = most_threads(NV * VE, ln);
+  c.sh.C = (groups + NV * most - 1) / (NV * most);
   c.sh.slice = c.sh.C == 1 ? p.H : ((p.H + c.sh.C - 1) / c.sh.C + 15) / 16 * 16;
   const int threads = ((c.sh.slice / VE + NV - 1) / NV + 31) / 32 * 32;
-  c.sh.rows = threads == 32 ? 4 : 1;
+  const bool shared = !in_registers(NV * VE, ln);
+  c.sh.rows = c.sh.C > 1 ? 1 : shared ? kMaxThreads / threads : threads == 32 ? 4 : 1;
+  constexpr int GB = Grp<DT, VE>::kBytes;
+  const int slot = GB >= 4 ? (gr ? 3 : 2) * NV * threads * GB : 0;  // a row's
+  const int kept = shared ? 4 * NV * VE * 4 * threads : 0;
+  const int sums = 2 * (threads / 32) * c.sh.C * 16;                // a row's
+  auto bytes = [&] { return c.sh.rows * (c.ring_slots * slot + sums) + kept; };
+  c.ring_slots = kMaxSlots;
+  while (bytes() > kMaxSmem && c.ring_slots > 1) --c.ring_slots;
+  while (bytes() > kMaxSmem && c.sh.rows > 1) --c.sh.rows;
   c.sh.threads = threads * c.sh.rows;
-  const int nt = p.gate_kind == ADDLN_GATE_ROWS ? 3 : 2;
-  if (Grp<DT, VE>::kBytes >= 4) c.smem = kMaxSlots * nt * NV * c.sh.threads * Grp<DT, VE>::kBytes;
+  c.kept_at = c.sh.rows * c.ring_slots * slot;
+  c.sums_at = c.kept_at + kept;
+  c.smem = bytes();
   return c;
 }
 
-// Groups a thread: the number (of 1 to 4 16-byte groups) that leaves the
-// fewest of a row's threads' slots empty, the larger one where equal.
-inline int groups_a_thread(int groups, int most) {
-  int best = 1, waste = 1 << 30;
-  for (int nv = 1; nv <= most; ++nv) {
-    const int t = ((groups + nv - 1) / nv + 31) / 32 * 32;
-    if (t * nv - groups <= waste) waste = t * nv - groups, best = nv;
+// Groups a thread, of 1 to 4 16-byte groups: the number that needs the fewest
+// CTAs for a row, then that leaves the fewest of a row's threads' slots
+// empty, the larger one where equal.
+inline int groups_a_thread(int groups, int vec, bool ln) {
+  int best = 1, ctas = 1 << 30, waste = 1 << 30;
+  for (int nv = 1; nv <= 4; ++nv) {
+    const int most = nv * most_threads(nv * vec, ln), c = (groups + most - 1) / most;
+    const int t = ((groups + nv - 1) / nv + 31) / 32 * 32, w = t * nv - groups;
+    if (c < ctas || (c == ctas && w <= waste)) best = nv, ctas = c, waste = w;
   }
   return best;
 }
@@ -346,9 +362,7 @@ template <int DT>
 Choice choose(const BlockFwdArgs& p, int access, bool ln) {
   constexpr int VEC = Io<DT>::kVec;
   if (access == 16) {
-    // beyond a warp's reach, no more than keeps the parameters in registers
-    const int groups = p.H / VEC, most = !ln ? 4 : DT != kF32 && groups > 96 ? 2 : 3;
-    switch (groups_a_thread(groups, most)) {
+    switch (groups_a_thread(p.H / VEC, VEC, ln)) {
       case 1: return make<DT, VEC, 1>(p, ln);
       case 2: return make<DT, VEC, 2>(p, ln);
       case 3: return make<DT, VEC, 3>(p, ln);
@@ -430,12 +444,15 @@ int launch_block_fwd(int dtype, int access, bool layer_or_bias, const BlockFwdAr
   *name = access == 16 ? "block_fwd_v16" : access == 4 ? "block_fwd_v4" : "block_fwd_v2";
   BlockFwdArgs p = args;
   p.w = walk_of(ch.sh);
+  p.kept_at = ch.kept_at;
+  p.sums_at = ch.sums_at;
+  p.ring_slots = ch.ring_slots;
   const int fit = resident_units(reinterpret_cast<const void*>(ch.k), ch.sh, ch.smem, c.dev);
   if (fit < 0) return fit;
   // Rows staged ahead: two, or one where every walker has more than eight
   // rows (us a pass with one / two: 2048x4096 fp16, 3 or 4 rows a walker,
   // 14.8 / 13.5; 32768x8192 bf16, 108 rows, 331 / 348).
-  p.slots = p.rows > 8 * static_cast<int64_t>(fit) * ch.sh.rows ? 1 : 2;
+  p.slots = p.rows > 8 * static_cast<int64_t>(fit) * ch.sh.rows ? 1 : ch.ring_slots;
   const int64_t need = (p.rows + ch.sh.rows - 1) / ch.sh.rows;
   const cudaError_t e = launch_units(ch.k, need < fit ? need : fit, ch.sh, ch.smem, c, p);
   if (e != cudaSuccess) {
