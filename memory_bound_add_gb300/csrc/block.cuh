@@ -4,10 +4,16 @@
 //
 // Layout.  One walker handles one row at a time: a warp, a CTA, or for the
 // longest rows a cluster of C CTAs that each own a slice of the columns.  A
-// warp owns 32 NV groups of VE neighbouring columns, of which lane l has
-// groups l, l + 32, ...: the addresses of a thread's groups are constants
-// apart.  VE follows the alignment that all buffers of a call share: 16-byte
-// accesses, or 4-byte, or single elements.
+// warp owns 32 NV groups of VE neighbouring columns (16 bytes of the I/O
+// type), of which lane l has groups l, l + 32, ...: the addresses of a
+// thread's groups are constants apart.
+//
+// Rows that do not begin on 16-byte borders (SH: odd widths, offsets into a
+// buffer) move in 16-byte granules all the same: a lane copies the granule
+// that its group begins in, takes its group out of that and its neighbour's,
+// and writes the granule that holds its group's begin together with the end
+// of its neighbour's, which it gets by shuffle.  Accesses of single elements
+// (2 bytes each) took three to four times as long.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -20,98 +26,29 @@ namespace addln {
 namespace blk {
 
 constexpr int kMaxThreads = 512;  // threads a CTA
-constexpr int kMaxWarps = kMaxThreads / 32;
 constexpr int kMaxCluster = 8;    // the portable cluster size
 constexpr int kMaxSmem = 227 * 1024;  // dynamic shared memory of a CTA
 
-// VE elements of DT at p (element offset i), as 32-bit words or one 16-bit
-// value, and their fp32 values in slots [k VE, (k + 1) VE) of float2 v[NV VE / 2].
-template <int DT, int VE>
-struct Grp {
-  using IO = Io<DT>;
-  static constexpr int S = IO::kBytes;
-  static constexpr int kBytes = VE * S;
-  static constexpr int W = kBytes >= 4 ? kBytes / 4 : 1;  // words held
-  uint32_t w[W];
-
-  __device__ __forceinline__ void zero() {
-#pragma unroll
-    for (int j = 0; j < W; ++j) w[j] = 0u;
-  }
-  __device__ __forceinline__ void load(const char* q) {
-    if constexpr (kBytes == 16) {
-      const uint4 u = ld_stream_v4(q);
-      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
-    } else if constexpr (kBytes == 4) {
-      w[0] = __ldg(reinterpret_cast<const uint32_t*>(q));
-    } else {
-      w[0] = __ldg(reinterpret_cast<const unsigned short*>(q));
-    }
-  }
-  // value of element e of the group
-  __device__ __forceinline__ float get(int e) const {
-    if constexpr (DT == kF32) return __uint_as_float(w[e]);
-    const unsigned short b = static_cast<unsigned short>((e & 1) ? w[e >> 1] >> 16 : w[e >> 1] & 0xffffu);
-    if constexpr (DT == kF16) return __half2float(__ushort_as_half(b));
-    return __bfloat162float(__ushort_as_bfloat16(b));
-  }
-};
-
-template <int DT, int VE, int NV>
-__device__ __forceinline__ void to_slots(const Grp<DT, VE> (&g)[NV], float2 (&v)[NV * VE / 2]) {
-  if constexpr (VE >= 2) {
-#pragma unroll
-    for (int k = 0; k < NV; ++k)
-#pragma unroll
-      for (int q = 0; q < VE / 2; ++q) {
-        if constexpr (DT == kF32)
-          v[k * VE / 2 + q] = make_float2(__uint_as_float(g[k].w[2 * q]), __uint_as_float(g[k].w[2 * q + 1]));
-        else
-          v[k * VE / 2 + q] = Io<DT>::w2f(g[k].w[q]);
-      }
-  } else {
-#pragma unroll
-    for (int q = 0; q < NV / 2; ++q) v[q] = make_float2(g[2 * q].get(0), g[2 * q + 1].get(0));
-  }
-}
-
-// Stores group k of the slots, rounded to DT, at q.
-template <int DT, int VE, int P>
-__device__ __forceinline__ void store_group(char* q, const float2 (&v)[P], int k) {
-  if constexpr (VE * Io<DT>::kBytes == 16) {
-    st_stream_v4(q, Io<DT>::from_pairs(&v[k * VE / 2]));
-  } else if constexpr (VE == 2) {  // 16-bit pair
-    *reinterpret_cast<uint32_t*>(q) = Io<DT>::f2w(v[k].x, v[k].y);
-  } else {
-    Io<DT>::store1(q, 0, (k & 1) ? v[k >> 1].y : v[k >> 1].x);
-  }
-}
-
-// VE fp32 parameters at byte offset `off`; `fill` where there are none.
-template <int VE>
-__device__ __forceinline__ void load_params(const float* p, uint32_t off, float fill, float (&v)[VE], int site,
-                                            int64_t extent) {
+// VE fp32 parameters from column c on, of H; `fill` for a missing vector and
+// past the end.  SH: any address, and the end may lie within the group.
+template <int VE, bool SH>
+__device__ __forceinline__ void load_params(const float* p, int c, int H, float fill, float (&v)[VE], int site) {
 #pragma unroll
   for (int e = 0; e < VE; ++e) v[e] = fill;
-  if (p == nullptr || !ADDLN_IN(site, off, 4 * VE, extent)) return;
-  const char* q = reinterpret_cast<const char*>(p) + off;
-  if constexpr (VE >= 4) {
+  if (p == nullptr) return;
+  p += c;
+  if constexpr (SH) {
+#pragma unroll
+    for (int e = 0; e < VE; ++e)
+      if (c + e < H && ADDLN_IN(site, 4 * (c + e), 4, 4 * static_cast<int64_t>(H))) v[e] = __ldg(p + e);
+  } else {
+    if (c >= H || !ADDLN_IN(site, 4 * c, 4 * VE, 4 * static_cast<int64_t>(H))) return;
 #pragma unroll
     for (int h = 0; h < VE / 4; ++h) {
-      const float4 u = __ldg(reinterpret_cast<const float4*>(q) + h);
+      const float4 u = ld_param_f4(p + 4 * h);
       v[4 * h] = u.x, v[4 * h + 1] = u.y, v[4 * h + 2] = u.z, v[4 * h + 3] = u.w;
     }
-  } else if constexpr (VE == 2) {
-    const float2 u = __ldg(reinterpret_cast<const float2*>(q));
-    v[0] = u.x, v[1] = u.y;
-  } else {
-    v[0] = __ldg(reinterpret_cast<const float*>(q));
   }
-}
-
-template <int P>
-__device__ __forceinline__ float get_slot(const float2 (&v)[P], int e) {
-  return (e & 1) ? v[e >> 1].y : v[e >> 1].x;
 }
 
 // Asks L2 for the 128-byte line at p (a hint).
@@ -120,122 +57,220 @@ __device__ __forceinline__ void prefetch_line(const void* p) {
 }
 
 // A thread's groups of a row.  A group past the end of the slice does not
-// exist: it is fetched as zeros and never stored, and reads the parameters of
-// the slice's last group.
+// exist: it is fetched as zeros and never stored, and its parameters are
+// zeros.  With SH the slice's last group may hold fewer than VE columns.
 template <int VE, int NV>
 struct Cols {
   static constexpr int kStep = 32 * VE;  // columns between a thread's groups
+  static constexpr int P = NV * VE / 2;
   int c0;           // first column of group 0
-  bool ok[NV];
-  bool all;         // every group of the warp exists
+  int left;         // columns of the slice from c0 on (may be 0 or less)
+  bool all;         // every group of the warp is whole
   float n, inv_n;   // columns of the warp, 1 / n (0 for none)
-  uint32_t par[NV]; // byte offset of each group in an fp32 vector of H columns
 
   __device__ __forceinline__ void init(int warp, int col0, int cols) {
     const int at0 = warp * NV * kStep + (threadIdx.x & 31) * VE;
     c0 = col0 + at0;
+    left = cols - at0;
     const int own = min(max(cols - warp * NV * kStep, 0), NV * kStep);
     n = static_cast<float>(own);
     inv_n = own ? __frcp_rn(n) : 0.f;
-    bool full = true;
-#pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      const int at = at0 + k * kStep;
-      ok[k] = at < cols;
-      full = full && ok[k];
-      par[k] = 4u * static_cast<uint32_t>(col0 + (ok[k] ? at : cols - VE));
-    }
-    all = __all_sync(0xffffffffu, full);
+    all = own == NV * kStep;
   }
   __device__ __forceinline__ int col(int k) const { return c0 + k * kStep; }
-  // zeros in the slots of groups that do not exist
-  __device__ __forceinline__ void clear(float2 (&v)[NV * VE / 2]) const {
+  __device__ __forceinline__ bool ok(int k) const { return left > k * kStep; }
+  // columns of group k that exist
+  __device__ __forceinline__ int valid(int k) const { return min(max(left - k * kStep, 0), VE); }
+  // zeros in the slots of columns that do not exist
+  __device__ __forceinline__ void clear(float2 (&v)[P]) const {
     if (all) return;
 #pragma unroll
     for (int e = 0; e < NV * VE; ++e) {
       float& u = (e & 1) ? v[e >> 1].y : v[e >> 1].x;
-      u = ok[e / VE] ? u : 0.f;
+      u = left > (e / VE) * kStep + e % VE ? u : 0.f;
+    }
+  }
+};
+
+// ------------------------------------------------------- shifted granules
+// Bytes [sh, sh + 16) of the 32 bytes lo, hi; sh < 16, a multiple of 2.
+__device__ __forceinline__ uint4 window(const uint4& lo, const uint4& hi, int sh) {
+  uint32_t w[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+  if (sh & 8) {
+#pragma unroll
+    for (int i = 0; i < 6; ++i) w[i] = w[i + 2];
+  }
+  if (sh & 4) {
+#pragma unroll
+    for (int i = 0; i < 5; ++i) w[i] = w[i + 1];
+  }
+  const int bits = (sh & 3) * 8;
+  return make_uint4(__funnelshift_r(w[0], w[1], bits), __funnelshift_r(w[1], w[2], bits),
+                    __funnelshift_r(w[2], w[3], bits), __funnelshift_r(w[3], w[4], bits));
+}
+
+__device__ __forceinline__ int low4(const void* p, int64_t off) {
+  return (static_cast<int>(reinterpret_cast<uintptr_t>(p)) + static_cast<int>(off)) & 15;
+}
+
+// Element e (a constant) of a group, as it is stored.
+template <int S>
+__device__ __forceinline__ void store_element(char* p, const uint4& v, int e) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+  if constexpr (S == 4)
+    *reinterpret_cast<uint32_t*>(p) = w[e];
+  else
+    *reinterpret_cast<unsigned short*>(p) = static_cast<unsigned short>((e & 1) ? w[e >> 1] >> 16 : w[e >> 1]);
+}
+
+// Writes a row's groups in the order of k, 0 to NV - 1, to `base + off` of a
+// tensor of `extent` bytes.
+template <int DT, int NV, bool SH>
+struct Writer {
+  static constexpr int S = Io<DT>::kBytes, VE = Io<DT>::kVec;
+  uint4 prev;  // the last group, of lane 31
+
+  __device__ __forceinline__ void put(const Cols<VE, NV>& cs, void* base, int64_t off, int k, const uint4& v, int site,
+                                      int64_t extent) {
+    off += k * (cs.kStep * S);
+    char* p = static_cast<char*>(base) + off;
+    if constexpr (!SH) {
+      if (cs.ok(k) && ADDLN_IN(site, off, 16, extent)) st_stream_v4(p, v);
+      return;
+    } else {
+      constexpr unsigned kAll = 0xffffffffu;
+      const int lane = threadIdx.x & 31;
+      const int s = low4(p, 0);  // bytes past the border, the same for the warp
+      uint4 w = v;
+      int lo = 0, hi = cs.valid(k);  // elements of the granule to write
+      if (s != 0) {
+        uint4 n;
+        const uint4 send = lane == 31 && k > 0 ? prev : v;
+        n.x = __shfl_sync(kAll, send.x, (lane + 31) & 31);
+        n.y = __shfl_sync(kAll, send.y, (lane + 31) & 31);
+        n.z = __shfl_sync(kAll, send.z, (lane + 31) & 31);
+        n.w = __shfl_sync(kAll, send.w, (lane + 31) & 31);
+        prev = v;
+        w = window(n, v, 16 - s);
+        const int own = s / S;  // the first of this lane's elements in it
+        // the neighbour's group is there from the warp's second on
+        const bool has = k > 0 || lane > 0;
+        const int before = min(max(cs.left - (k * cs.kStep - VE), 0), VE) - (VE - own);
+        lo = has ? 0 : own;
+        hi = hi > 0 ? own + min(hi, VE - own) : has ? max(before, 0) : 0;
+        p -= s;
+        off -= s;
+      }
+      if (lo == 0 && hi == VE) {
+        if (ADDLN_IN(site, off, 16, extent)) st_stream_v4(p, w);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (e >= lo && e < hi && ADDLN_IN(site, off + e * S, S, extent)) store_element<S>(p + e * S, w, e);
+      }
+      // nobody follows the warp's last group: its own end
+      if (s != 0 && k == NV - 1 && lane == 31) {
+        const int own = s / S;
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (e >= VE - own && e < cs.valid(k) && ADDLN_IN(site, off + s + e * S, S, extent))
+            store_element<S>(p + s + e * S, v, e);
+      }
     }
   }
 };
 
 // --------------------------------------------------------------- staging
-// A thread's groups of the rows ahead, in a ring of slots of its own in
-// shared memory: it copies them itself (cp.async, 16 or 4 bytes at a time,
-// zeros for a group that does not exist) and alone reads them, so no barrier
-// is needed, and no register holds them.  A warp's ring is one piece,
-// [slot][tensor][group][lane], so that all its addresses are constants apart.
-// Two-byte groups cannot be copied that way; they wait in registers, two in
-// each (one slot).
+// A warp's groups of the rows ahead, in a ring of slots of its own in shared
+// memory, copied by cp.async, 16 bytes a lane (zeros for what does not
+// exist).  Without SH a lane alone reads what it has copied, so no barrier is
+// needed; with SH a group may reach into the next lane's granule, and the
+// warp meets before it reads and before it copies anew.  A warp's ring is one
+// piece, [slot][tensor][group][lane], with SH one granule more a tensor.
 constexpr int kMaxSlots = 2;
 
-template <int DT, int VE, int NV, int NT>
+template <int DT, int NV, int NT, bool SH>
 struct Ring {
-  static constexpr int kBytes = Grp<DT, VE>::kBytes;
-  static constexpr bool kAsync = kBytes >= 4;
-  static constexpr uint32_t kStep = 32 * kBytes;                    // between groups
-  static constexpr uint32_t kSlot = kAsync ? NT * NV * kStep : 0;  // bytes of a warp's slot
-  uint32_t base;  // this thread's first group of slot 0
-  uint32_t held[kAsync ? 1 : NT][kAsync ? 1 : NV / 2];
+  static constexpr int S = Io<DT>::kBytes, VE = Io<DT>::kVec;
+  static constexpr uint32_t kTensor = (NV * 32 + (SH ? 1 : 0)) * 16;
+  static constexpr uint32_t kSlot = NT * kTensor;  // bytes of a warp's slot
+  uint32_t base;  // this thread's granule of group 0 of slot 0
 
   __device__ __forceinline__ uint32_t at(int slot, int i, int k) const {
-    return base + static_cast<uint32_t>(slot) * (NT * NV * kStep) + static_cast<uint32_t>(i * NV + k) * kStep;
+    return base + static_cast<uint32_t>(slot) * kSlot + static_cast<uint32_t>(i) * kTensor + static_cast<uint32_t>(k) * 512u;
   }
-  // group k of tensor i from src, if it exists
-  __device__ __forceinline__ void fetch(int slot, int i, int k, const char* src, bool ok) {
-    if constexpr (kAsync) {
-      const uint32_t dst = at(slot, i, k);
-      const int n = ok ? kBytes : 0;
-      if constexpr (kBytes == 16)
-        asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
-      else
-        asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  // n of the 16 bytes at src, zeros for the rest
+  __device__ __forceinline__ static void copy(uint32_t dst, const char* src, int n) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(n) : "memory");
+  }
+  // A row of tensor I: group 0 of this thread at byte off of t.
+  template <int I>
+  __device__ __forceinline__ void fetch(const Cols<VE, NV>& cs, int slot, const void* t, int64_t off, int site,
+                                        int64_t extent) {
+    const char* p = static_cast<const char*>(t) + off;
+    if constexpr (!SH) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const bool in = cs.ok(k) && ADDLN_IN(site, off + k * (cs.kStep * S), 16, extent);
+        copy(at(slot, I, k), p + k * (cs.kStep * S), in ? 16 : 0);
+      }
     } else {
-      Grp<DT, VE> g;
-      g.zero();
-      if (ok) g.load(src);
-      held[i][k >> 1] = (k & 1) ? __byte_perm(held[i][k >> 1], g.w[0], 0x5410) : g.w[0];
-    }
-  }
-  // zeros for tensor i
-  __device__ __forceinline__ void clear(int slot, int i) {
+      const int s = low4(p, 0);
+      // bytes of the row's slice from this granule on; what lies past them is
+      // not read.  A granule that begins before the row has the bytes before
+      // it read along, which are the tensor's (the row before), but for the
+      // tensor's own first granule.
+      const int bytes = cs.left * S + s;
+      p -= s;
+      off -= s;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if constexpr (kAsync) {
-        const uint32_t dst = at(slot, i, k);
+      for (int k = 0; k <= NV; ++k) {
+        if (k == NV && (threadIdx.x & 31) != 0) continue;  // the granule after the last lane's
+        const int n = min(max(bytes - k * (cs.kStep * S), 0), 16);
+        const int64_t o = off + k * (cs.kStep * S);
+        if (k == 0 && o < 0) {
 #pragma unroll
-        for (int b = 0; b < kBytes; b += 4)
-          asm volatile("st.shared.u32 [%0], %1;" ::"r"(dst + b), "r"(0) : "memory");
-      } else {
-        held[i][k >> 1] = 0u;
+          for (int b = 0; b < 16; b += S)
+            if (b >= s && b < n && ADDLN_IN(site, o + b, S, extent)) {
+              if constexpr (S == 4)
+                asm volatile("st.shared.u32 [%0], %1;" ::"r"(at(slot, I, 0) + b),
+                             "r"(__ldg(reinterpret_cast<const uint32_t*>(p + b))) : "memory");
+              else
+                asm volatile("st.shared.u16 [%0], %1;" ::"r"(at(slot, I, 0) + b),
+                             "h"(__ldg(reinterpret_cast<const unsigned short*>(p + b))) : "memory");
+            }
+        } else {
+          copy(at(slot, I, k), p + k * (cs.kStep * S), n > 0 && ADDLN_IN(site, o, n, extent) ? n : 0);
+        }
       }
     }
   }
-  __device__ __forceinline__ void commit() {
-    if constexpr (kAsync) asm volatile("cp.async.commit_group;" ::: "memory");
+  // zeros for tensor I
+  template <int I>
+  __device__ __forceinline__ void clear(int slot) {
+#pragma unroll
+    for (int k = 0; k <= (SH ? NV : NV - 1); ++k) {
+      if (k == NV && (threadIdx.x & 31) != 0) continue;
+      asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at(slot, I, k)), "r"(0) : "memory");
+    }
   }
+  __device__ __forceinline__ static void commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
   // all but the AHEAD groups of copies committed last have arrived
   template <int AHEAD>
-  __device__ __forceinline__ void wait() {
-    if constexpr (kAsync) asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
+  __device__ __forceinline__ static void wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(AHEAD) : "memory");
   }
-  // groups k0 .. k0 + N - 1 of tensor i
-  template <int N>
-  __device__ __forceinline__ void take(int slot, int i, int k0, Grp<DT, VE> (&g)[N]) const {
-#pragma unroll
-    for (int k = 0; k < N; ++k) {
-      if constexpr (kAsync) {
-        const uint32_t src = at(slot, i, k0 + k);
-        if constexpr (kBytes == 16) {
-          const uint4 u = ld_shared_v4(src);
-          g[k].w[0] = u.x, g[k].w[1] = u.y, g[k].w[2] = u.z, g[k].w[3] = u.w;
-        } else {
-          asm volatile("ld.shared.u32 %0, [%1];" : "=r"(g[k].w[0]) : "r"(src));
-        }
-      } else {
-        g[k].w[0] = ((k0 + k) & 1) ? held[i][(k0 + k) >> 1] >> 16 : held[i][(k0 + k) >> 1] & 0xffffu;
-      }
-    }
+  // before the first read of a slot, and before it is copied into again
+  __device__ __forceinline__ static void meet() {
+    if constexpr (SH) __syncwarp();
+  }
+  // Group k of tensor i, whose row lies s bytes past the borders.
+  __device__ __forceinline__ uint4 take(int slot, int i, int k, int s) const {
+    const uint32_t a = at(slot, i, k);
+    const uint4 v = ld_shared_v4(a);
+    if constexpr (!SH) return v;
+    if (s == 0) return v;
+    return window(v, ld_shared_v4(a + 16), s);
   }
 };
 
@@ -244,11 +279,10 @@ struct Ring {
 // of what a 16-byte load through L1 does.
 template <int VE, int NV>
 struct Kept {
-  static constexpr int kPart = VE >= 4 ? 16 : VE * 4;
-  static constexpr int Q = VE * 4 / kPart;
-  static constexpr uint32_t kStep = 32 * kPart;
+  static constexpr int Q = VE / 4;  // 16-byte parts of a group
+  static constexpr uint32_t kStep = 32 * 16;
   template <int NP>
-  __device__ static constexpr uint32_t bytes() {
+  __host__ __device__ static constexpr uint32_t bytes() {
     return NP * NV * Q * kStep;
   }
   uint32_t base;
@@ -258,35 +292,17 @@ struct Kept {
   }
   __device__ __forceinline__ void put(int i, int k, const float (&v)[VE]) const {
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-      if constexpr (VE >= 4)
-        asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at(i, k, q)), "f"(v[4 * q]), "f"(v[4 * q + 1]),
-                     "f"(v[4 * q + 2]), "f"(v[4 * q + 3]) : "memory");
-      else if constexpr (VE == 2)
-        asm volatile("st.shared.v2.f32 [%0], {%1, %2};" ::"r"(at(i, k, q)), "f"(v[0]), "f"(v[1]) : "memory");
-      else
-        asm volatile("st.shared.f32 [%0], %1;" ::"r"(at(i, k, q)), "f"(v[0]) : "memory");
-    }
+    for (int q = 0; q < Q; ++q)
+      asm volatile("st.shared.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(at(i, k, q)), "f"(v[4 * q]), "f"(v[4 * q + 1]),
+                   "f"(v[4 * q + 2]), "f"(v[4 * q + 3]) : "memory");
   }
-  // N groups from k0 on
-  template <int N>
-  __device__ __forceinline__ void get(int i, int k0, float2 (&v)[N * VE / 2]) const {
+  __device__ __forceinline__ void get(int i, int k, float2 (&v)[VE / 2]) const {
 #pragma unroll
-    for (int k = 0; k < N; ++k)
-#pragma unroll
-      for (int q = 0; q < Q; ++q) {
-        if constexpr (VE >= 4) {
-          const uint4 u = ld_shared_v4(at(i, k0 + k, q));
-          v[k * VE / 2 + 2 * q] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
-          v[k * VE / 2 + 2 * q + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
-        } else if constexpr (VE == 2) {
-          asm volatile("ld.shared.v2.f32 {%0, %1}, [%2];" : "=f"(v[k].x), "=f"(v[k].y) : "r"(at(i, k0 + k, q)));
-        } else {
-          float f;
-          asm volatile("ld.shared.f32 %0, [%1];" : "=f"(f) : "r"(at(i, k0 + k, q)));
-          if (k & 1) v[k >> 1].y = f; else v[k >> 1].x = f;
-        }
-      }
+    for (int q = 0; q < Q; ++q) {
+      const uint4 u = ld_shared_v4(at(i, k, q));
+      v[2 * q] = make_float2(__uint_as_float(u.x), __uint_as_float(u.y));
+      v[2 * q + 1] = make_float2(__uint_as_float(u.z), __uint_as_float(u.w));
+    }
   }
 };
 

@@ -76,18 +76,17 @@ struct BlockBwdArgs {
   int post, pre, gate_kind;
   float a, s, inv_h;
   int kept_at, sums_at;  // where parameters and row sums lie in shared memory
-  int slots;
   Walk w;
 };
 
-// access: elements a thread moves at once, in bytes of the widest access all
-// of the call's buffers allow (16, 4 or the element).
-int launch_block_fwd(int dtype, int access, bool layer_or_bias, const BlockFwdArgs& p, const LaunchCtx& c,
+// aligned: every row of every tensor in the I/O dtype begins on a 16-byte
+// border and ends on one.
+int launch_block_fwd(int dtype, bool aligned, bool layer_or_bias, const BlockFwdArgs& p, const LaunchCtx& c,
                      const char** name);
 // Bytes of workspace of a backward call, or a negative code.
-int64_t block_bwd_workspace_bytes(int dtype, int access, bool full, int64_t rows, int H, int gate_kind,
+int64_t block_bwd_workspace_bytes(int dtype, bool aligned, bool full, int64_t rows, int H, int gate_kind,
                                   int64_t rows_per_gate, const DeviceInfo& dev);
-int launch_block_bwd(int dtype, int access, bool full, BlockBwdArgs p, void* ws, int64_t ws_bytes,
+int launch_block_bwd(int dtype, bool aligned, bool full, BlockBwdArgs p, void* ws, int64_t ws_bytes,
                      const LaunchCtx& c, const char** name);
 
 int read_bounds_block_fwd(unsigned long long* word);

@@ -1,5 +1,5 @@
 // C-ABI entry points declared in include/addln_block.h: the argument checks
-// (all before the first CUDA call) and the choice of access width.
+// (all before the first CUDA call), and whether rows lie on 16-byte borders.
 #include <math.h>
 
 #include <cuda_runtime.h>
@@ -40,17 +40,15 @@ int64_t gate_bytes(int gate_kind, int64_t gate_rows, int64_t gate_stride, int64_
   return 0;
 }
 
-// The widest access, in bytes, that rows of H elements at these addresses
-// allow (data: the tensors in the I/O dtype, ored; params: the fp32 vectors,
-// ored; stride: a gate's row stride): 16, 4 (16-bit types) or one element;
-// 0 if some address is not a multiple of its element.
-int access_of(uintptr_t data, uintptr_t params, int64_t H, int64_t stride, int es) {
-  if ((data & (es - 1)) || (params & 3)) return 0;
-  const uintptr_t rows = data | static_cast<uintptr_t>(H * es) | static_cast<uintptr_t>(stride * es);
-  if (!(rows & 15) && !(params & 15)) return 16;
-  if (es == 2 && !(rows & 3) && !(params & 7)) return 4;
-  return es;
+// Whether rows of H elements at these addresses (the tensors in the I/O
+// dtype, and the fp32 vectors, each ored; stride: a gate's row stride) begin
+// and end on 16-byte borders.
+bool rows_aligned(uintptr_t data, uintptr_t params, int64_t H, int64_t stride, int es) {
+  return ((data | params | static_cast<uintptr_t>(H * es) | static_cast<uintptr_t>(stride * es)) & 15) == 0;
 }
+
+// Whether some address is not a multiple of its element.
+bool misplaced(uintptr_t data, uintptr_t params, int es) { return (data & (es - 1)) || (params & 3); }
 
 }  // namespace
 
@@ -85,9 +83,9 @@ int block_norm_fwd(const void* f, const void* x, int post, const float* post_gam
   const uintptr_t data = bits(f) | bits(x) | bits(h) | bits(y) | (gr ? bits(gate) : 0);
   const uintptr_t params = bits(post_gamma) | bits(post_beta) | bits(pre_gamma) | bits(pre_beta) |
                            (gate_kind == ADDLN_GATE_CHANNEL ? bits(gate) : 0);
-  const int access = access_of(data, params, H, gr ? gate_stride : 0, es);
-  if (access == 0 || ((bits(post_mean) | bits(post_rstd) | bits(pre_mean) | bits(pre_rstd)) & 3))
+  if (misplaced(data, params | bits(post_mean) | bits(post_rstd) | bits(pre_mean) | bits(pre_rstd), es))
     return ADDLN_ERR_ALIGN;
+  const bool aligned = rows_aligned(data, params, H, gr ? gate_stride : 0, es);
 
   const int64_t tb = rows * H * es;
   const Range outs[6] = {range_of(h, tb), range_of(y, tb), range_of(post_mean, rows * 4),
@@ -111,7 +109,7 @@ int block_norm_fwd(const void* f, const void* x, int post, const float* post_gam
                         static_cast<float>(1.0 / static_cast<double>(H))};
   const bool layer_or_bias = post == ADDLN_NORM_LAYER || pre == ADDLN_NORM_LAYER || post_beta || pre_beta;
   const char* name = "none";
-  return addln::launch_block_fwd(dtype, access, layer_or_bias, p, c, &name);
+  return addln::launch_block_fwd(dtype, aligned, layer_or_bias, p, c, &name);
 } catch (...) {
   return ADDLN_ERR_HOST_MEMORY;
 }
@@ -126,17 +124,15 @@ int64_t block_norm_bwd_workspace_size(int64_t rows, int64_t H, int dtype, int ga
   LaunchCtx c;
   rc = addln::launch_context(nullptr, &c);
   if (rc != ADDLN_OK) return rc;
-  // the most over the access widths and kernels that the call may turn out to take
+  // the most over the kernels that the call may turn out to take
   int64_t most = 0;
-  const int widths[3] = {16, 4, elem_bytes(dtype)};
-  for (int w : widths) {
-    if (H * elem_bytes(dtype) % w != 0) continue;
-    for (int full = 0; full < 2; ++full) {
-      const int64_t n = addln::block_bwd_workspace_bytes(dtype, w, full != 0, rows, static_cast<int>(H), gate_kind,
-                                                         rows_per_gate, c.dev);
-      if (n < 0) return n;
-      if (n > most) most = n;
-    }
+  for (int kind = 0; kind < 4; ++kind) {
+    const bool aligned = kind & 1, full = kind & 2;
+    if (aligned && H * elem_bytes(dtype) % 16 != 0) continue;
+    const int64_t n = addln::block_bwd_workspace_bytes(dtype, aligned, full, rows, static_cast<int>(H), gate_kind,
+                                                       rows_per_gate, c.dev);
+    if (n < 0) return n;
+    if (n > most) most = n;
   }
   return most;
 } catch (...) {
@@ -188,9 +184,9 @@ int block_norm_bwd(const void* dy, const void* dh, const void* f, const void* h,
                          (gr ? bits(gate) | bits(dgate) : 0);
   const uintptr_t params = bits(post_gamma) | bits(post_beta) | bits(pre_gamma) |
                            (gate_kind == ADDLN_GATE_CHANNEL ? bits(gate) : 0);
-  const int access = access_of(data, params, H, gr ? gate_stride : 0, es);
-  if (access == 0 || ((bits(post_mean) | bits(post_rstd) | bits(pre_mean) | bits(pre_rstd)) & 3))
+  if (misplaced(data, params | bits(post_mean) | bits(post_rstd) | bits(pre_mean) | bits(pre_rstd), es))
     return ADDLN_ERR_ALIGN;
+  const bool aligned = rows_aligned(data, params, H, gr ? gate_stride : 0, es);
 
   const int64_t tb = rows * H * es;
   const bool scratch = outs32 != 0 || (gr && dgate && rows_per_gate > 1);
@@ -220,7 +216,7 @@ int block_norm_bwd(const void* dy, const void* dh, const void* f, const void* h,
                         static_cast<float>(1.0 / static_cast<double>(H))};
   const bool full = post == ADDLN_NORM_LAYER || pre == ADDLN_NORM_LAYER || post_beta || dpost_beta || dpre_beta;
   const char* name = "none";
-  return addln::launch_block_bwd(dtype, access, full, p, workspace, workspace_bytes, c, &name);
+  return addln::launch_block_bwd(dtype, aligned, full, p, workspace, workspace_bytes, c, &name);
 } catch (...) {
   return ADDLN_ERR_HOST_MEMORY;
 }

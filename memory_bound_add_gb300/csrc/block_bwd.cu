@@ -51,26 +51,19 @@ __device__ __forceinline__ int64_t b_gate_bytes(const BlockBwdArgs& p, int S) {
 // dbeta and sum(s D) or dpb.
 __host__ __device__ constexpr int sums_of(bool full) { return full ? 4 : 2; }
 
-// Stores slots as fp32 columns of an [Hp] vector.
+// Stores slots as fp32 columns of an [Hp] vector (16-byte aligned).
 template <int VE, int NV>
 __device__ __forceinline__ void store_cols(float* t, const Cols<VE, NV>& cs, int site, int Hp,
                                            const float2 (&v)[NV * VE / 2]) {
 #pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    if (!cs.ok[k] || !ADDLN_IN(site, 4 * cs.col(k), 4 * VE, 4 * static_cast<int64_t>(Hp))) continue;
-    float* q = t + cs.col(k);
-    if constexpr (VE >= 4) {
+  for (int k = 0; k < NV; ++k)
 #pragma unroll
-      for (int i = 0; i < VE / 4; ++i)
-        reinterpret_cast<float4*>(q)[i] =
-            make_float4(v[k * VE / 2 + 2 * i].x, v[k * VE / 2 + 2 * i].y, v[k * VE / 2 + 2 * i + 1].x,
-                        v[k * VE / 2 + 2 * i + 1].y);
-    } else if constexpr (VE == 2) {
-      *reinterpret_cast<float2*>(q) = v[k];
-    } else {
-      *q = get_slot(v, k);
+    for (int i = 0; i < VE / 4; ++i) {
+      // Hp is a multiple of 4: four columns of which one exists fit
+      if (cs.valid(k) <= 4 * i || !ADDLN_IN(site, 4 * (cs.col(k) + 4 * i), 16, 4 * static_cast<int64_t>(Hp))) continue;
+      const float2 a = v[k * VE / 2 + 2 * i], b = v[k * VE / 2 + 2 * i + 1];
+      *reinterpret_cast<float4*>(t + cs.col(k) + 4 * i) = make_float4(a.x, a.y, b.x, b.y);
     }
-  }
 }
 
 // K sums (4 or 8) over the walker's threads, the same bits in every thread.
@@ -129,39 +122,23 @@ struct Sums {
   }
 };
 
-// Fetches a row of tensor I: the groups of the thread, the first at byte off.
-template <int I, int DT, int VE, int NV, int NT>
-__device__ __forceinline__ void fetch_row(Ring<DT, VE, NV, NT>& ring, const Cols<VE, NV>& cs, int slot,
-                                          const void* t, int64_t off, int site, int64_t extent) {
-  constexpr int kStepBytes = Cols<VE, NV>::kStep * Io<DT>::kBytes;
-  [[maybe_unused]] constexpr int GB = Grp<DT, VE>::kBytes;
-  const char* q = static_cast<const char*>(t) + off;
-#pragma unroll
-  for (int k = 0; k < NV; ++k) {
-    const bool in = ADDLN_IN(site, off + k * kStepBytes, cs.ok[k] ? GB : 0, extent);
-    ring.fetch(slot, I, k, q + k * kStepBytes, cs.ok[k] && in);
-  }
-}
-
-template <int DT, int VE, int NV, bool FULL, bool GR>
+template <int DT, int NV, bool FULL, bool GR, bool SH>
 constexpr int bwd_regs() {
   return 128;
 }
 
-// FULL: some norm is a layer norm or has a bias.  GR: a gate with rows.
-template <int DT, int VE, int NV, bool FULL, bool GR>
-__global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV, FULL, GR>()))
+// FULL: some norm is a layer norm or has a bias.  GR: a gate with rows.  SH:
+// some rows do not begin on 16-byte borders.
+template <int DT, int NV, bool FULL, bool GR, bool SH>
+__global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, NV, FULL, GR, SH>()))
     k_block_bwd(const __grid_constant__ BlockBwdArgs p) {
-  constexpr int S = Io<DT>::kBytes;
-  constexpr int GB = Grp<DT, VE>::kBytes;
+  using IO = Io<DT>;
+  constexpr int S = IO::kBytes, VE = IO::kVec, N = VE / 2;
   constexpr int A = sums_of(FULL), K = FULL ? 8 : 4;
-  constexpr int NT = GR ? 5 : 4;
-  constexpr int P = NV * VE / 2;
+  constexpr int NT = GR ? 5 : 4, NP = FULL && GR ? 3 : 2;
+  constexpr int P = NV * N;
   constexpr int kStepBytes = Cols<VE, NV>::kStep * S;
-  // groups that share slots in pairs (single elements) go two at a time
-  constexpr int KU = VE >= 2 ? 1 : 2, N = VE >= 2 ? VE / 2 : 1;
-  constexpr int NP = FULL && GR ? 3 : 2;
-  using R = Ring<DT, VE, NV, NT>;
+  using R = Ring<DT, NV, NT, SH>;
   extern __shared__ __align__(128) unsigned char smem[];
   const int T = p.w.cta_warps * 32;
   const int side = p.w.rows_per_cta > 1 ? threadIdx.x / T : 0, tid = threadIdx.x - side * T;
@@ -169,14 +146,14 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
   const int64_t cta = blockIdx.x / p.w.C;
   const int64_t walker = cta * p.w.rows_per_cta + side;
   const int col0 = rank * p.w.slice;
-  const int slots = R::kAsync ? p.slots : 1;
+  constexpr int slots = kMaxSlots;
   R ring;
   const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  ring.base = smem_addr(smem) + warp * kMaxSlots * R::kSlot + lane * GB;
+  ring.base = smem_addr(smem) + warp * kMaxSlots * R::kSlot + lane * 16;
   // vector 0: gamma of the pre norm; 1: the factor c, or with gate rows s pg
   // (c is then that times the gate); 2: s pb
   Kept<VE, NV> kept;
-  kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<NP>() + lane * Kept<VE, NV>::kPart;
+  kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<NP>() + lane * 16;
   Sums<K> sums{reinterpret_cast<float*>(smem + p.sums_at) + side * 2 * p.w.warps * K, p.w, rank, 0, 1 + side};
   Cols<VE, NV> cs;
   cs.init(tid >> 5, col0, min(p.w.slice, p.H - col0));
@@ -220,21 +197,21 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
   // before those of h, f and the gate.
   auto fetch_first = [&](int slot, int i, int64_t at) {
     if (i < n) {
-      if (has_dy) fetch_row<0>(ring, cs, slot, p.dy, at, 723, extent);
-      if (has_dh) fetch_row<2>(ring, cs, slot, p.dh, at, 721, extent);
+      if (has_dy) ring.template fetch<0>(cs, slot, p.dy, at, 723, extent);
+      if (has_dh) ring.template fetch<2>(cs, slot, p.dh, at, 721, extent);
     }
     ring.commit();
   };
   auto fetch_rest = [&](int slot, int i, int64_t at) {
     if (i < n) {
-      if (has_dy) fetch_row<1>(ring, cs, slot, p.h, at, 724, extent);
-      if (need_f) fetch_row<3>(ring, cs, slot, p.f, at, 722, extent);
+      if (has_dy) ring.template fetch<1>(cs, slot, p.h, at, 724, extent);
+      if (need_f) ring.template fetch<3>(cs, slot, p.f, at, 722, extent);
       if constexpr (GR) {
         // a gate row that the slot's last row had is there already
-        if (!R::kAsync || i - gate_first < slots) fetch_row<4>(ring, cs, slot, p.gate, gate_at, 731, b_gate_bytes(p, S));
+        if (i - gate_first < slots) ring.template fetch<4>(cs, slot, p.gate, gate_at, 731, b_gate_bytes(p, S));
         if (--gate_left == 0) {
           gate_left = clip(p.rows_per_gate);
-          if constexpr (R::kAsync) gate_first = i + 1;
+          gate_first = i + 1;
           gate_at += p.gate_stride * S;
         }
       }
@@ -244,7 +221,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
   // While the previous kernel of the stream may still be finishing, ask L2
   // for the walker's first rows (hints alone, as in the forward).
   if (r0 < r1 && r1 - r0 <= 8) {
-    const int ln = tid & 31, chunk0 = cs.c0 * S - ln * GB;
+    const int ln = tid & 31, chunk0 = cs.c0 * S - ln * 16;
     const int bytes = min(NV * kStepBytes, (col0 + min(p.w.slice, p.H - col0)) * S - chunk0);
     for (int s = 0; s < slots && r0 + s < r1; ++s) {
       const int64_t at = (r0 + s) * p.H * S + chunk0 + ln * 128;
@@ -260,33 +237,31 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
   // arithmetic then needs no branches (u, hhat and dh are zeros, and rstd is
   // 0 or, for fhat, 1).
   for (int s = 0; s < slots; ++s) {
-    if (!has_dy) ring.clear(s, 0), ring.clear(s, 1);
-    if (!has_dh) ring.clear(s, 2);
-    if (!need_f) ring.clear(s, 3);
+    if (!has_dy) ring.template clear<0>(s), ring.template clear<1>(s);
+    if (!has_dh) ring.template clear<2>(s);
+    if (!need_f) ring.template clear<3>(s);
   }
-  if constexpr (R::kAsync) {
-    for (int s = 0; s < slots; ++s) {
-      const int64_t at = (r0 + s) * row_bytes + cs.c0 * S;
-      fetch_first(s, s, at);
-      fetch_rest(s, s, at);
-    }
+  for (int s = 0; s < slots; ++s) {
+    const int64_t at = (r0 + s) * row_bytes + cs.c0 * S;
+    fetch_first(s, s, at);
+    fetch_rest(s, s, at);
   }
 
   // parameters, while the first rows arrive
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
-    const int64_t ext = 4 * static_cast<int64_t>(p.H);
+    const int c = cs.col(k);
     float g[VE], w[VE], b[VE], gt[VE];
-    load_params<VE>(has_dy ? p.pre_gamma : nullptr, cs.par[k], 0.f, g, 726, ext);
-    load_params<VE>(!GR && p.gate_kind == ADDLN_GATE_CHANNEL ? static_cast<const float*>(p.gate) : nullptr, cs.par[k], 1.f,
-                    gt, 728, ext);
-    load_params<VE>(p.post_gamma, cs.par[k], 1.f, w, 729, ext);
-    load_params<VE>(FULL && GR ? p.post_beta : nullptr, cs.par[k], 0.f, b, 730, ext);
+    load_params<VE, SH>(has_dy ? p.pre_gamma : nullptr, c, p.H, 0.f, g, 726);
+    load_params<VE, SH>(!GR && p.gate_kind == ADDLN_GATE_CHANNEL ? static_cast<const float*>(p.gate) : nullptr, c, p.H, 1.f, gt,
+                    728);
+    load_params<VE, SH>(p.post_gamma, c, p.H, 1.f, w, 729);
+    load_params<VE, SH>(FULL && GR ? p.post_beta : nullptr, c, p.H, 0.f, b, 730);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
       w[e] *= p.s * gt[e];
       b[e] *= p.s;
-      if (!cs.ok[k]) g[e] = w[e] = b[e] = 0.f;
+      if (cs.valid(k) <= e) g[e] = w[e] = b[e] = 0.f;
     }
     kept.put(0, k, g);
     kept.put(1, k, w);
@@ -294,24 +269,12 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
   }
   stats(r0);
 
-  // The gate's sums of single-element rows lie in shared memory (whose ring is
-  // not used): beside the waiting elements they would spill.
-  constexpr bool kSdOut = GR && FULL && !R::kAsync;
-  float* sd_at = reinterpret_cast<float*>(smem) + threadIdx.x;
-  auto get_sd = [&](int j) {
-    return make_float2(sd_at[2 * j * blockDim.x], sd_at[(2 * j + 1) * blockDim.x]);
-  };
-  auto put_sd = [&](int j, float2 v) {
-    sd_at[2 * j * blockDim.x] = v.x;
-    sd_at[(2 * j + 1) * blockDim.x] = v.y;
-  };
-  float2 sg[P], s1[P], sb[FULL ? P : 1], s0[FULL ? P : 1], sd[GR && !kSdOut ? P : 1];
+  float2 sg[P], s1[P], sb[FULL ? P : 1], s0[FULL ? P : 1], sd[GR ? P : 1];
 #pragma unroll
   for (int j = 0; j < P; ++j) {
     sg[j] = s1[j] = dup2(0.f);
     if constexpr (FULL) sb[j] = s0[j] = dup2(0.f);
-    if constexpr (kSdOut) put_sd(j, dup2(0.f));
-    else if constexpr (GR) sd[j] = dup2(0.f);
+    if constexpr (GR) sd[j] = dup2(0.f);
   }
   // rows left of the current gate row
   int flush = 0;
@@ -320,23 +283,24 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
   int slot = 0;
   int64_t off = r0 * row_bytes + cs.c0 * S;
   for (int it = 0; it < n; ++it, off += row_bytes) {
-    if constexpr (!R::kAsync) {
-      fetch_first(0, it, off);
-      fetch_rest(0, it, off);
-    }
-    // all but the next row's two parts
-    if (slots == 1) ring.template wait<0>(); else ring.template wait<2>();
+    ring.template wait<2>();  // all but the next row's two parts
+    ring.meet();
     const float2 nhm = dup2(-hm_n), hr = dup2(hr_n), nfm = dup2(-fm_n), fr = dup2(fr_n);
     stats(r0 + it + 1);
-    auto take = [&](int i, int k, float2 (&v)[N]) {
-      Grp<DT, VE> r[KU];
-      ring.template take<KU>(slot, i, k, r);
-      to_slots<DT, VE, KU>(r, v);
-    };
+    // how far the row lies past 16-byte borders, tensor by tensor; zeros that
+    // stand for a missing tensor need no shift
+    int sh[NT];
+#pragma unroll
+    for (int i = 0; i < NT; ++i) sh[i] = 0;
+    if constexpr (SH) {
+      sh[0] = low4(p.dy, off), sh[1] = low4(p.h, off), sh[2] = low4(p.dh, off), sh[3] = low4(p.f, off);
+      if constexpr (GR) sh[4] = low4(p.gate, (gate_of(r0 + it) * p.gate_stride + cs.c0) * S);
+    }
+    auto take = [&](int i, int k, float2 (&v)[N]) { IO::to_pairs(ring.take(slot, i, k, sh[i]), v); };
     auto hat = [&](int i, int k, float2 negm, float2 r, float2 (&v)[N]) {
       take(i, k, v);
 #pragma unroll
-      for (int i = 0; i < N; ++i) v[i] = mul2(FULL ? add2(v[i], negm) : v[i], r);
+      for (int j = 0; j < N; ++j) v[j] = mul2(FULL ? add2(v[j], negm) : v[j], r);
     };
 
     float2 t[P];
@@ -344,15 +308,15 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
 #pragma unroll
     for (int i = 0; i < K; ++i) q[i] = dup2(0.f);
 #pragma unroll
-    for (int k = 0; k < NV; k += KU) {
+    for (int k = 0; k < NV; ++k) {
       float2 hh[N], fh[N], c[N], dy[N], d[N], u[N];
-      const int j0 = VE >= 2 ? k * VE / 2 : k / 2;
+      const int j0 = k * N;
       hat(1, k, nhm, hr, hh);
       hat(3, k, nfm, fr, fh);
       take(0, k, dy);
       take(2, k, d);
-      kept.template get<KU>(0, k, u);
-      kept.template get<KU>(1, k, c);
+      kept.get(0, k, u);
+      kept.get(1, k, c);
       if constexpr (GR) {
         float2 gt[N];
         take(4, k, gt);
@@ -379,7 +343,8 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
         }
       }
     }
-    if constexpr (R::kAsync) fetch_first(slot, it + slots, off + slots * row_bytes);
+    ring.meet();
+    fetch_first(slot, it + slots, off + slots * row_bytes);
     float m[K];
 #pragma unroll
     for (int i = 0; i < K; ++i) m[i] = q[i].x + q[i].y;
@@ -394,35 +359,30 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
     }
     v2 *= p.inv_h;
     const float2 na2 = dup2(-a2), na1 = dup2(-a1), nv2 = dup2(-v2), nv1 = dup2(-v1), pa = dup2(p.a);
-    char* dx = static_cast<char*>(p.dx) + off;
-    char* df = static_cast<char*>(p.df) + off;
+    Writer<DT, NV, SH> dx, df;
 #pragma unroll
-    for (int k = 0; k < NV; k += KU) {
+    for (int k = 0; k < NV; ++k) {
       float2 hh[N], fh[N], c[N], o[N];
-      const int j0 = VE >= 2 ? k * VE / 2 : k / 2;
+      const int j0 = k * N;
       hat(1, k, nhm, hr, hh);
       hat(3, k, nfm, fr, fh);
-      kept.template get<KU>(1, k, c);
+      kept.get(1, k, c);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
         t[j0 + i] = fma2(na2, hh[i], FULL ? add2(t[j0 + i], na1) : t[j0 + i]);
         o[i] = mul2(pa, t[j0 + i]);
       }
-#pragma unroll
-      for (int e = 0; e < KU; ++e)
-        if (cs.ok[k + e] && ADDLN_IN(727, off + (k + e) * kStepBytes, GB, extent))
-          store_group<DT, VE>(dx + (k + e) * kStepBytes, o, e);
+      dx.put(cs, p.dx, off, k, IO::from_pairs(o), 727, extent);
       if constexpr (GR) {
         // the gate's own gradient D (fhat w + b), and D times the gate
         float2 b[N], gt[N];
-        if constexpr (FULL) kept.template get<KU>(2, k, b);
+        if constexpr (FULL) kept.get(2, k, b);
         take(4, k, gt);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
           const float2 D = t[j0 + i];
           const float2 nn = FULL ? fma2(fh[i], c[i], b[i]) : mul2(fh[i], c[i]);
-          if constexpr (kSdOut) put_sd(j0 + i, fma2(D, nn, get_sd(j0 + i)));
-          else sd[j0 + i] = fma2(D, nn, sd[j0 + i]);
+          sd[j0 + i] = fma2(D, nn, sd[j0 + i]);
           t[j0 + i] = mul2(D, gt[i]);
         }
       }
@@ -435,40 +395,29 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, VE, NV,
       if (post)
 #pragma unroll
         for (int i = 0; i < N; ++i) o[i] = mul2(fr, fma2(fh[i], nv2, FULL ? add2(o[i], nv1) : o[i]));
-#pragma unroll
-      for (int e = 0; e < KU; ++e)
-        if (cs.ok[k + e] && ADDLN_IN(735, off + (k + e) * kStepBytes, GB, extent))
-          store_group<DT, VE>(df + (k + e) * kStepBytes, o, e);
+      df.put(cs, p.df, off, k, IO::from_pairs(o), 735, extent);
     }
-    if constexpr (R::kAsync) fetch_rest(slot, it + slots, off + slots * row_bytes);
+    ring.meet();
+    fetch_rest(slot, it + slots, off + slots * row_bytes);
     slot = slot + 1 == slots ? 0 : slot + 1;
     if constexpr (GR) {
       if (--flush == 0 || it + 1 == n) {
         const int64_t row = r0 + it, g = gate_of(row), begin = g * p.rows_per_gate;
         const bool whole = begin >= r0 && row + 1 == min(p.rows, begin + p.rows_per_gate);
-        float2 sv[P];
-#pragma unroll
-        for (int j = 0; j < P; ++j) {
-          if constexpr (kSdOut) {
-            sv[j] = get_sd(j);
-            put_sd(j, dup2(0.f));
-          } else {
-            sv[j] = sd[j];
-            sd[j] = dup2(0.f);
-          }
-        }
         if (whole) {
-          const int64_t gb = (g * p.H + cs.c0) * S;
-          char* out = static_cast<char*>(p.dgate) + gb;
+          if (p.dgate != nullptr) {
+            Writer<DT, NV, SH> out;
 #pragma unroll
-          for (int k = 0; k < NV; ++k)
-            if (p.dgate != nullptr && cs.ok[k] &&
-                ADDLN_IN(732, gb + k * kStepBytes, GB, p.gate_rows * static_cast<int64_t>(p.H) * S))
-              store_group<DT, VE>(out + k * kStepBytes, sv, k);
+            for (int k = 0; k < NV; ++k)
+              out.put(cs, p.dgate, (g * p.H + cs.c0) * S, k, IO::from_pairs(sd + k * N), 732,
+                      p.gate_rows * static_cast<int64_t>(p.H) * S);
+          }
         } else if (p.seg != nullptr) {
           // the range's first gate row, or its last
-          store_cols<VE, NV>(p.seg + (2 * walker + (begin <= r0 ? 0 : 1)) * p.Hp, cs, 733, p.Hp, sv);
+          store_cols<VE, NV>(p.seg + (2 * walker + (begin <= r0 ? 0 : 1)) * p.Hp, cs, 733, p.Hp, sd);
         }
+#pragma unroll
+        for (int j = 0; j < P; ++j) sd[j] = dup2(0.f);
         flush = clip(p.rows_per_gate);
       }
     }
@@ -680,56 +629,61 @@ struct Choice {
   int smem = 0, kept_at = 0, sums_at = 0;
 };
 
-// NV groups of VE columns a thread; a CTA of kSideThreads threads for as many
-// rows side by side as fit it, else one CTA of up to kMaxThreads for a row,
-// else a cluster.  Shared memory: two slots of the ring (at least what the
-// walkers need to join their sums), the parameters, the row sums.
+// NV groups of VE columns a thread; a CTA of up to kSideThreads threads for as
+// many rows side by side as fit it, else one CTA of up to kMaxThreads for a
+// row, else a cluster.  Shared memory: the ring (at least what the walkers
+// need to join their sums), the parameters, the row sums.
 constexpr int kSideThreads = 512;
 
-template <int DT, int VE, int NV, bool GR>
+template <int DT, int NV, bool GR, bool SH>
 Choice make(int H, bool full) {
+  constexpr int VE = Io<DT>::kVec;
   Choice c;
-  c.k = &k_block_bwd<DT, VE, NV, false, GR>;
-  if constexpr (NV * VE <= 8)
-    if (full) c.k = &k_block_bwd<DT, VE, NV, true, GR>;
-  const int groups = H / VE;
+  c.k = &k_block_bwd<DT, NV, false, GR, SH>;
+  if constexpr (NV * VE <= 8) {
+    if (full) c.k = &k_block_bwd<DT, NV, true, GR, SH>;
+  }
+  const int groups = (H + VE - 1) / VE;
   c.sh.C = (groups + NV * kMaxThreads - 1) / (NV * kMaxThreads);
   c.sh.slice = c.sh.C == 1 ? H : ((H + c.sh.C - 1) / c.sh.C + 15) / 16 * 16;
-  const int threads = ((c.sh.slice / VE + NV - 1) / NV + 31) / 32 * 32;
+  const int threads = ((c.sh.slice + VE - 1) / VE + 32 * NV - 1) / (32 * NV) * 32;
   c.sh.rows = c.sh.C > 1 || threads > kSideThreads / 2 ? 1 : kSideThreads / threads;
   c.sh.threads = threads * c.sh.rows;
-  const int nt = GR ? 5 : 4, np = full && GR ? 3 : 2, gb = Grp<DT, VE>::kBytes;
-  int ring = gb >= 4 ? kMaxSlots * nt * NV * c.sh.threads * gb : 0;
+  const int warps = c.sh.threads / 32;
+  int ring = warps * kMaxSlots * static_cast<int>(Ring<DT, NV, GR ? 5 : 4, SH>::kSlot);
   int half = 0;  // walkers that give their sums to another at once
   for (int top = 1; top < c.sh.rows; top *= 2) half = top;
   const int join = half * sums_of(full) * NV * VE * threads * 4;
   if (ring < join) ring = join;
-  const int sd = GR && gb < 4 ? NV * VE * 4 * c.sh.threads : 0;
-  if (ring < sd) ring = sd;
   c.kept_at = ring;
-  c.sums_at = c.kept_at + np * NV * VE * 4 * c.sh.threads;
+  c.sums_at = c.kept_at + warps * static_cast<int>(full && GR ? Kept<VE, NV>::template bytes<3>()
+                                                               : Kept<VE, NV>::template bytes<2>());
   c.smem = c.sums_at + c.sh.rows * 2 * (threads / 32) * c.sh.C * (full ? 8 : 4) * 4;
   return c;
 }
 
-template <int DT, bool GR>
-Choice choose(int H, int access, bool full) {
+template <int DT, bool GR, bool SH>
+Choice choose(int H, bool full) {
   constexpr int VEC = Io<DT>::kVec;
-  if constexpr (DT != kF32) {
-    // 16 columns a thread where the sums are two or three for a column, else 8
-    if (access == 16 && !full && H > 32 * VEC) return make<DT, VEC, 2, GR>(H, full);
-    if (access == 16) return make<DT, VEC, 1, GR>(H, full);
-    if (access == 4) return make<DT, 2, 4, GR>(H, full);
-    return make<DT, 1, 8, GR>(H, full);
-  } else {
-    return access == 16 ? make<DT, VEC, 2, GR>(H, full) : make<DT, 1, 8, GR>(H, full);
+  // 16 columns a thread where the sums are two or three for a column and the
+  // row is longer than a warp's 8, else 8
+  if constexpr (DT != kF32 && !SH) {
+    if (!full && H > 32 * VEC) return make<DT, 2, GR, SH>(H, full);
   }
+  // (4 of shifted fp32: 8 spill)
+  return make<DT, SH ? 1 : 8 / VEC, GR, SH>(H, full);
 }
 
-Choice choose(int dtype, int H, int access, bool full, bool gr) {
-  if (dtype == kF32) return gr ? choose<kF32, true>(H, access, full) : choose<kF32, false>(H, access, full);
-  if (dtype == kF16) return gr ? choose<kF16, true>(H, access, full) : choose<kF16, false>(H, access, full);
-  return gr ? choose<kBF16, true>(H, access, full) : choose<kBF16, false>(H, access, full);
+template <int DT>
+Choice choose(int H, bool aligned, bool full, bool gr) {
+  if (aligned) return gr ? choose<DT, true, false>(H, full) : choose<DT, false, false>(H, full);
+  return gr ? choose<DT, true, true>(H, full) : choose<DT, false, true>(H, full);
+}
+
+Choice choose(int dtype, int H, bool aligned, bool full, bool gr) {
+  return dtype == kF32   ? choose<kF32>(H, aligned, full, gr)
+         : dtype == kF16 ? choose<kF16>(H, aligned, full, gr)
+                         : choose<kBF16>(H, aligned, full, gr);
 }
 
 // Units (CTAs or clusters) of a launch: those that fit the device at once, no
@@ -762,22 +716,22 @@ BwdKernel pick_sums(bool full, int quads) {
 }  // namespace
 }  // namespace blk
 
-int64_t block_bwd_workspace_bytes(int dtype, int access, bool full, int64_t rows, int H, int gate_kind,
+int64_t block_bwd_workspace_bytes(int dtype, bool aligned, bool full, int64_t rows, int H, int gate_kind,
                                   int64_t rows_per_gate, const DeviceInfo& dev) {
   using namespace blk;
   const bool gr = gate_kind == ADDLN_GATE_ROWS;
-  const Choice ch = choose(dtype, H, access, full, gr);
+  const Choice ch = choose(dtype, H, aligned, full, gr);
   const int64_t units = units_of(ch, rows, dev);
   if (units < 0) return units;
   const int64_t Hp = (H + 3) / 4 * 4;
   return part_bytes(units, full, Hp) + seg_bytes(units * ch.sh.rows, gr, rows_per_gate, Hp);
 }
 
-int launch_block_bwd(int dtype, int access, bool full, BlockBwdArgs p, void* ws, int64_t ws_bytes,
+int launch_block_bwd(int dtype, bool aligned, bool full, BlockBwdArgs p, void* ws, int64_t ws_bytes,
                      const LaunchCtx& c, const char** name) {
   using namespace blk;
   const bool gr = p.gate_kind == ADDLN_GATE_ROWS;
-  const Choice ch = choose(dtype, p.H, access, full, gr);
+  const Choice ch = choose(dtype, p.H, aligned, full, gr);
   p.w = walk_of(ch.sh);
   p.parts = units_of(ch, p.rows, c.dev);
   if (p.parts < 0) return static_cast<int>(p.parts);
@@ -785,7 +739,6 @@ int launch_block_bwd(int dtype, int access, bool full, BlockBwdArgs p, void* ws,
   if (p.walkers > p.rows) p.walkers = p.rows;
   p.kept_at = ch.kept_at;
   p.sums_at = ch.sums_at;
-  p.slots = 2;
   p.Hp = (p.H + 3) / 4 * 4;
   const bool cols = p.dpre_gamma || p.dpre_beta || p.dpost_gamma || p.dpost_beta ||
                     (p.dgate && p.gate_kind == ADDLN_GATE_CHANNEL);
@@ -799,7 +752,7 @@ int launch_block_bwd(int dtype, int access, bool full, BlockBwdArgs p, void* ws,
     if (cols) p.part = static_cast<float*>(ws);
     if (seg) p.seg = reinterpret_cast<float*>(static_cast<char*>(ws) + pb);
   }
-  *name = access == 16 ? "block_bwd_v16" : access == 4 ? "block_bwd_v4" : "block_bwd_v2";
+  *name = aligned ? "block_bwd" : "block_bwd_shifted";
   cudaError_t e = launch_units(ch.k, p.parts, ch.sh, ch.smem, c, p);
   if (e == cudaSuccess && (cols || seg)) {
     const int quads = sums_quads(p.parts, full);

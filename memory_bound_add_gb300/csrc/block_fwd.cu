@@ -48,38 +48,35 @@ __device__ __forceinline__ RowStat row_norm(Exchange<SIDES>& ex, float2 (&v)[NV 
 // norm w = s gate, b = 0), and gamma and beta of the pre norm.  Loading them
 // again for every row costs more of L1's bandwidth than the row itself: two
 // vectors (no layer norm, no bias) stay in registers, and four of at most
-// eight columns a thread; four of more lie in shared memory, one copy for all
-// rows that the CTA has side by side.
-__host__ __device__ constexpr bool in_registers(int columns, bool ln) { return !ln || columns <= 8; }
+// eight columns a thread; four of more, and two of more of shifted rows, lie
+// in shared memory, one copy for all rows that the CTA has side by side.
+__host__ __device__ constexpr bool in_registers(int columns, bool ln, bool sh) { return columns <= 8 || !(ln || sh); }
 
-template <int VE, int NV, bool LN>
+template <int VE, int NV, bool LN, bool SH>
 struct Params {
-  static constexpr bool kRegs = in_registers(NV * VE, LN);
+  static constexpr bool kRegs = in_registers(NV * VE, LN, SH);
   static constexpr int P = kRegs ? NV * VE / 2 : 1;
   float2 r[LN ? 4 : 2][P];  // w, gamma, and with LN b, beta
   Kept<VE, NV> kept;        // the same vectors
 
-  // vector i, group(s) k on
-  template <int KU, int N>
-  __device__ __forceinline__ void get(int i, int k, float2 (&v)[N]) const {
+  // vector i of group k
+  __device__ __forceinline__ void get(int i, int k, float2 (&v)[VE / 2]) const {
     if constexpr (kRegs) {
 #pragma unroll
-      for (int j = 0; j < N; ++j) v[j] = r[i][k * VE / 2 + j];
+      for (int j = 0; j < VE / 2; ++j) v[j] = r[i][k * VE / 2 + j];
     } else {
-      kept.template get<KU>(i, k, v);
+      kept.get(i, k, v);
     }
   }
 
-  // group k, from the call's arguments
-  __device__ __forceinline__ void load(const BlockFwdArgs& p, uint32_t off, int k) {
-    const int64_t extent = 4 * static_cast<int64_t>(p.H);
+  // group k, at column c, from the call's arguments
+  __device__ __forceinline__ void load(const BlockFwdArgs& p, int c, int k) {
     float v[4][VE], gt[VE];
-    load_params<VE>(p.gate_kind == ADDLN_GATE_CHANNEL ? static_cast<const float*>(p.gate) : nullptr, off, 1.f, gt, 702,
-                    extent);
-    load_params<VE>(p.post_gamma, off, 1.f, v[0], 704, extent);
-    load_params<VE>(p.pre_gamma, off, 0.f, v[1], 711, extent);
-    load_params<VE>(LN ? p.post_beta : nullptr, off, 0.f, v[2], 708, extent);
-    load_params<VE>(LN ? p.pre_beta : nullptr, off, 0.f, v[3], 712, extent);
+    load_params<VE, SH>(p.gate_kind == ADDLN_GATE_CHANNEL ? static_cast<const float*>(p.gate) : nullptr, c, p.H, 1.f, gt, 702);
+    load_params<VE, SH>(p.post_gamma, c, p.H, 1.f, v[0], 704);
+    load_params<VE, SH>(p.pre_gamma, c, p.H, 0.f, v[1], 711);
+    load_params<VE, SH>(LN ? p.post_beta : nullptr, c, p.H, 0.f, v[2], 708);
+    load_params<VE, SH>(LN ? p.pre_beta : nullptr, c, p.H, 0.f, v[3], 712);
 #pragma unroll
     for (int e = 0; e < VE; ++e) {
       const float f = p.s * gt[e];
@@ -90,10 +87,7 @@ struct Params {
     for (int i = 0; i < (LN ? 4 : 2); ++i) {
       if constexpr (kRegs) {
 #pragma unroll
-        for (int e = 0; e < VE; ++e) {
-          const int s = k * VE + e;
-          ((s & 1) ? r[i][s >> 1].y : r[i][s >> 1].x) = v[i][e];
-        }
+        for (int e = 0; e < VE / 2; ++e) r[i][k * VE / 2 + e] = make_float2(v[i][2 * e], v[i][2 * e + 1]);
       } else {
         kept.put(i, k, v[i]);
       }
@@ -105,7 +99,7 @@ struct Params {
 // Caps of 96, 80 and 64 (5, 6 and 8 CTAs) spill or reload and measured slower:
 // 2048x4096 fp16 rms/rms 13.3 us a pass at 128, 20.0 at 80, 22.7 at 64;
 // 32768x8192 bf16 335, 471, 575.
-template <int DT, int VE, int NV, bool LN, bool GR>
+template <int DT, int NV, bool LN, bool GR, bool SH>
 constexpr int fwd_regs() {
   return 128;
 }
@@ -116,52 +110,42 @@ __device__ __forceinline__ int64_t gate_row_of(int64_t row, int64_t rpg, bool sm
 }
 
 // LN: some norm of the call is a layer norm, or has a bias.  GR: a gate with
-// rows.
-template <int DT, int VE, int NV, bool LN, bool GR>
-__global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, VE, NV, LN, GR>()))
+// rows.  SH: some rows do not begin on 16-byte borders.
+template <int DT, int NV, bool LN, bool GR, bool SH>
+__global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, NV, LN, GR, SH>()))
     k_block_fwd(const __grid_constant__ BlockFwdArgs p) {
-  constexpr int S = Io<DT>::kBytes;
-  constexpr int P = NV * VE / 2;
-  const int slots = Ring<DT, VE, NV, 2>::kAsync ? p.slots : 1;
-  constexpr int GB = Grp<DT, VE>::kBytes;
+  using IO = Io<DT>;
+  constexpr int S = IO::kBytes, VE = IO::kVec, Q = VE / 2;
+  constexpr int P = NV * Q;
   constexpr int NT = GR ? 3 : 2;
   constexpr int kStepBytes = Cols<VE, NV>::kStep * S;
+  using R = Ring<DT, NV, NT, SH>;
   extern __shared__ __align__(128) unsigned char smem[];
+  const int slots = p.slots;
   const int lane = threadIdx.x & 31;
   const int side = (threadIdx.x >> 5) / p.w.cta_warps, warp = (threadIdx.x >> 5) - side * p.w.cta_warps;
   const int rank = p.w.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.w.C);
   const int64_t stride = static_cast<int64_t>(gridDim.x / p.w.C) * p.w.rows_per_cta;
   int64_t row = static_cast<int64_t>(blockIdx.x / p.w.C) * p.w.rows_per_cta + side;
   const int col0 = rank * p.w.slice;
-  Exchange<!in_registers(NV * VE, LN)> ex{p.w, p.sums_at + side * 2 * p.w.warps * 16, 0};
+  Exchange<!in_registers(NV * VE, LN, SH)> ex{p.w, p.sums_at + side * 2 * p.w.warps * 16, 0};
   const bool leader = rank == 0 && lane == 0 && warp == 0;
-  Ring<DT, VE, NV, NT> ring;
-  ring.base = smem_addr(smem) + (threadIdx.x >> 5) * p.ring_slots * Ring<DT, VE, NV, NT>::kSlot + lane * GB;
+  R ring;
+  ring.base = smem_addr(smem) + (threadIdx.x >> 5) * p.ring_slots * R::kSlot + lane * 16;
   Cols<VE, NV> cs;
   cs.init(warp, col0, min(p.w.slice, p.H - col0));
-  // byte offset of this thread's group 0 in a row
+  // byte offset of this thread's group 0 in a row, and in its gate row
   auto offset = [&](int64_t r) { return (r * p.H + cs.c0) * S; };
+  auto gate_offset = [&](int64_t r) {
+    return (gate_row_of(r, p.rows_per_gate, p.rows <= 0x7fffffff) * p.gate_stride + cs.c0) * S;
+  };
 
   auto fetch = [&](int slot, int64_t r) {
     if (r < p.rows) {
       const int64_t at = offset(r);
-      const char* f = static_cast<const char*>(p.f) + at;
-      const char* x = static_cast<const char*>(p.x) + at;
-#pragma unroll
-      for (int k = 0; k < NV; ++k) {
-        const bool in = ADDLN_IN(701, at + k * kStepBytes, cs.ok[k] ? GB : 0, f_rows_bytes(p, S));
-        ring.fetch(slot, 0, k, f + k * kStepBytes, cs.ok[k] && in);
-        ring.fetch(slot, 1, k, x + k * kStepBytes, cs.ok[k] && in);
-      }
-      if constexpr (GR) {
-        const int64_t ga = (gate_row_of(r, p.rows_per_gate, p.rows <= 0x7fffffff) * p.gate_stride + cs.c0) * S;
-        const char* g = static_cast<const char*>(p.gate) + ga;
-#pragma unroll
-        for (int k = 0; k < NV; ++k) {
-          const bool in = ADDLN_IN(705, ga + k * kStepBytes, cs.ok[k] ? GB : 0, f_gate_bytes(p, S));
-          ring.fetch(slot, 2, k, g + k * kStepBytes, cs.ok[k] && in);
-        }
-      }
+      ring.template fetch<0>(cs, slot, p.f, at, 701, f_rows_bytes(p, S));
+      ring.template fetch<1>(cs, slot, p.x, at, 701, f_rows_bytes(p, S));
+      if constexpr (GR) ring.template fetch<2>(cs, slot, p.gate, gate_offset(r), 705, f_gate_bytes(p, S));
     }
     ring.commit();
   };
@@ -169,7 +153,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, VE, NV,
   // for the first rows (a hint: nothing is read before the wait below, and
   // every SM's writes land in L2), where a walker has few of them.
   if (p.rows <= 8 * stride) {
-    const int chunk0 = cs.c0 * S - lane * GB;  // the warp's chunk of a row
+    const int chunk0 = cs.c0 * S - lane * 16;  // the warp's chunk of a row
     const int bytes = min(NV * kStepBytes, (col0 + min(p.w.slice, p.H - col0)) * S - chunk0);
     for (int s = 0; s < slots; ++s) {
       const int64_t at = (row + s * stride) * p.H * S + chunk0 + lane * 128;
@@ -182,23 +166,26 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, VE, NV,
   pdl_trigger();
   pdl_wait();
   for (int s = 0; s < slots; ++s) fetch(s, row + s * stride);
-  Params<VE, NV, LN> par;
-  constexpr bool kRegs = Params<VE, NV, LN>::kRegs;
+  Params<VE, NV, LN, SH> par;
+  constexpr bool kRegs = Params<VE, NV, LN, SH>::kRegs;
   if constexpr (!kRegs)
-    par.kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<4>() + lane * Kept<VE, NV>::kPart;
+    par.kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<LN ? 4 : 2>() + lane * 16;
   if (kRegs || side == 0) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) par.load(p, cs.par[k], k);
+    for (int k = 0; k < NV; ++k) par.load(p, cs.col(k), k);
   }
   if constexpr (!kRegs) __syncthreads();
 
   for (int slot = 0; row < p.rows; row += stride, slot = slot + 1 == slots ? 0 : slot + 1) {
     if (slots == 1) ring.template wait<0>(); else ring.template wait<1>();
+    ring.meet();
+    const int64_t off = offset(row);
     float2 v[P];
     {
-      Grp<DT, VE> r[NV];
-      ring.template take<NV>(slot, 0, 0, r);
-      to_slots<DT, VE, NV>(r, v);
+      const int s = SH ? low4(p.f, off) : 0;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) IO::to_pairs(ring.take(slot, 0, k, s), v + k * Q);
+      if constexpr (SH) cs.clear(v);
     }
     RowStat st{0.f, 0.f, 1.f};
     if (p.post != ADDLN_NORM_NONE) {
@@ -211,6 +198,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, VE, NV,
     // v = ((v - m) rstd) w + b, times the row's gate, plus a x
     {
       const float2 negm = dup2(-st.m), r2 = dup2(st.M2), a2 = dup2(p.a);
+      const int sx = SH ? low4(p.x, off) : 0, sg = SH && GR ? low4(p.gate, gate_offset(row)) : 0;
       auto affine = [&](float2 u, float2 w, float2 b, float2 gt, float2 x) {
         if constexpr (LN) u = add2(u, negm);
         u = mul2(u, r2);
@@ -218,38 +206,27 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, VE, NV,
         if constexpr (GR) return fma2(LN ? fma2(u, w, b) : mul2(u, w), gt, ax);
         return fma2(u, w, LN ? add2(b, ax) : ax);
       };
-      // groups that share slots in pairs (single elements) go two at a time
-      constexpr int KU = VE >= 2 ? 1 : 2, n = VE >= 2 ? VE / 2 : 1;
 #pragma unroll
-      for (int k = 0; k < NV; k += KU) {
-        Grp<DT, VE> rg[KU], rx[KU];
-        float2 gt[n], x[n];
-        ring.template take<KU>(slot, 1, k, rx);
-        to_slots<DT, VE, KU>(rx, x);
-        if constexpr (GR) {
-          ring.template take<KU>(slot, 2, k, rg);
-          to_slots<DT, VE, KU>(rg, gt);
-        }
-        float2 w[n], b[n];
-        par.template get<KU>(0, k, w);
-        if constexpr (LN) par.template get<KU>(2, k, b);
+      for (int k = 0; k < NV; ++k) {
+        float2 gt[Q], x[Q], w[Q], b[Q];
+        IO::to_pairs(ring.take(slot, 1, k, sx), x);
+        if constexpr (GR) IO::to_pairs(ring.take(slot, 2, k, sg), gt);
+        par.get(0, k, w);
+        if constexpr (LN) par.get(2, k, b);
 #pragma unroll
-        for (int i = 0; i < n; ++i) {
-          const int j = (VE >= 2 ? k * VE / 2 : k / 2) + i;
+        for (int i = 0; i < Q; ++i) {
           if constexpr (!LN) b[i] = dup2(0.f);
-          v[j] = affine(v[j], w[i], b[i], GR ? gt[i] : dup2(1.f), x[i]);
+          v[k * Q + i] = affine(v[k * Q + i], w[i], b[i], GR ? gt[i] : dup2(1.f), x[i]);
         }
       }
     }
     cs.clear(v);
+    ring.meet();
     fetch(slot, row + slots * stride);  // the slot has been read
-    const int64_t off = offset(row);
     {
-      char* h = static_cast<char*>(p.h) + off;
+      Writer<DT, NV, SH> out;
 #pragma unroll
-      for (int k = 0; k < NV; ++k)
-        if (cs.ok[k] && ADDLN_IN(706, off + k * kStepBytes, GB, f_rows_bytes(p, S)))
-          store_group<DT, VE>(h + k * kStepBytes, v, k);
+      for (int k = 0; k < NV; ++k) out.put(cs, p.h, off, k, IO::from_pairs(v + k * Q), 706, f_rows_bytes(p, S));
     }
     if (p.pre == ADDLN_NORM_NONE) continue;
     st = row_norm<VE, NV, LN>(ex, v, cs, p.pre == ADDLN_NORM_LAYER, p.inv_h, p.eps);
@@ -257,26 +234,22 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, VE, NV,
       if (p.pre_rstd) p.pre_rstd[row] = st.M2;
       if (LN && p.pre_mean) p.pre_mean[row] = st.mean;
     }
-    char* y = static_cast<char*>(p.y) + off;
     const float2 negm = dup2(-st.m), r2 = dup2(st.M2);
-    constexpr int KU = VE >= 2 ? 1 : 2, n = VE >= 2 ? VE / 2 : 1;
+    Writer<DT, NV, SH> out;
 #pragma unroll
-    for (int k = 0; k < NV; k += KU) {
-      float2 g[n], e[n];
-      par.template get<KU>(1, k, g);
-      if constexpr (LN) par.template get<KU>(3, k, e);
+    for (int k = 0; k < NV; ++k) {
+      float2 g[Q], e[Q];
+      par.get(1, k, g);
+      if constexpr (LN) par.get(3, k, e);
 #pragma unroll
-      for (int i = 0; i < n; ++i) {
-        const int j = (VE >= 2 ? k * VE / 2 : k / 2) + i;
+      for (int i = 0; i < Q; ++i) {
+        const int j = k * Q + i;
         if constexpr (LN)
           v[j] = fma2(mul2(add2(v[j], negm), r2), g[i], e[i]);
         else
           v[j] = mul2(mul2(v[j], r2), g[i]);
       }
-#pragma unroll
-      for (int q = k; q < k + KU; ++q)
-        if (cs.ok[q] && ADDLN_IN(709, off + q * kStepBytes, GB, f_rows_bytes(p, S)))
-          store_group<DT, VE>(y + q * kStepBytes, v, q);
+      out.put(cs, p.y, off, k, IO::from_pairs(v + k * Q), 709, f_rows_bytes(p, S));
     }
   }
   // a CTA's shared memory has to outlive its peers' writes into it
@@ -311,29 +284,29 @@ struct Choice {
 
 // Threads a CTA may give a row: half of them where parameters lie in shared
 // memory, so that those of a CTA's columns leave room for the ring.
-inline int most_threads(int columns, bool ln) { return in_registers(columns, ln) ? kMaxThreads : kMaxThreads / 2; }
+inline int most_threads(int columns, bool ln, bool sh) { return in_registers(columns, ln, sh) ? kMaxThreads : kMaxThreads / 2; }
 
 // NV groups of VE columns a thread.  With the parameters in registers: a warp
 // for a row where 32 threads hold it, four rows to a CTA; else a CTA of up to
 // kMaxThreads; else a cluster.  With parameters in shared memory: rows of up
 // to 256 threads side by side in a CTA of up to 512, as many as leave the
 // ring two slots, or one; wider rows in clusters.
-template <int DT, int VE, int NV>
+template <int DT, int NV, bool SH>
 Choice make(const BlockFwdArgs& p, bool ln) {
+  constexpr int VE = Io<DT>::kVec;
   Choice c;
   const bool gr = p.gate_kind == ADDLN_GATE_ROWS;
-  c.k = gr ? (ln ? &k_block_fwd<DT, VE, NV, true, true> : &k_block_fwd<DT, VE, NV, false, true>)
-           : (ln ? &k_block_fwd<DT, VE, NV, true, false> : &k_block_fwd<DT, VE, NV, false, false>);
-  const int groups = p.H / VE, most = most_threads(NV * VE, ln);
+  c.k = gr ? (ln ? &k_block_fwd<DT, NV, true, true, SH> : &k_block_fwd<DT, NV, false, true, SH>)
+           : (ln ? &k_block_fwd<DT, NV, true, false, SH> : &k_block_fwd<DT, NV, false, false, SH>);
+  const int groups = (p.H + VE - 1) / VE, most = most_threads(NV * VE, ln, SH);
   c.sh.C = (groups + NV * most - 1) / (NV * most);
   c.sh.slice = c.sh.C == 1 ? p.H : ((p.H + c.sh.C - 1) / c.sh.C + 15) / 16 * 16;
-  const int threads = ((c.sh.slice / VE + NV - 1) / NV + 31) / 32 * 32;
-  const bool shared = !in_registers(NV * VE, ln);
+  const int threads = ((c.sh.slice + VE - 1) / VE + 32 * NV - 1) / (32 * NV) * 32;
+  const bool shared = !in_registers(NV * VE, ln, SH);
   c.sh.rows = c.sh.C > 1 ? 1 : shared ? kMaxThreads / threads : threads == 32 ? 4 : 1;
-  constexpr int GB = Grp<DT, VE>::kBytes;
-  const int slot = GB >= 4 ? (gr ? 3 : 2) * NV * threads * GB : 0;  // a row's
-  const int kept = shared ? 4 * NV * VE * 4 * threads : 0;
-  const int sums = 2 * (threads / 32) * c.sh.C * 16;                // a row's
+  const int slot = threads / 32 * static_cast<int>(gr ? Ring<DT, NV, 3, SH>::kSlot : Ring<DT, NV, 2, SH>::kSlot);
+  const int kept = shared ? threads / 32 * static_cast<int>(ln ? Kept<VE, NV>::template bytes<4>() : Kept<VE, NV>::template bytes<2>()) : 0;
+  const int sums = 2 * (threads / 32) * c.sh.C * 16;
   auto bytes = [&] { return c.sh.rows * (c.ring_slots * slot + sums) + kept; };
   c.ring_slots = kMaxSlots;
   while (bytes() > kMaxSmem && c.ring_slots > 1) --c.ring_slots;
@@ -345,33 +318,37 @@ Choice make(const BlockFwdArgs& p, bool ln) {
   return c;
 }
 
-// Groups a thread, of 1 to 4 16-byte groups: the number that needs the fewest
+// Groups a thread, of 1 to 4: the number that needs the fewest
 // CTAs for a row, then that leaves the fewest of a row's threads' slots
 // empty, the larger one where equal.
-inline int groups_a_thread(int groups, int vec, bool ln) {
+inline int groups_a_thread(int groups, int vec, bool ln, bool sh) {
   int best = 1, ctas = 1 << 30, waste = 1 << 30;
   for (int nv = 1; nv <= 4; ++nv) {
-    const int most = nv * most_threads(nv * vec, ln), c = (groups + most - 1) / most;
-    const int t = ((groups + nv - 1) / nv + 31) / 32 * 32, w = t * nv - groups;
+    const int most = nv * most_threads(nv * vec, ln, sh), c = (groups + most - 1) / most;
+    const int t = (groups + 32 * nv - 1) / (32 * nv) * 32, w = t * nv - groups;
     if (c < ctas || (c == ctas && w <= waste)) best = nv, ctas = c, waste = w;
   }
   return best;
 }
 
 template <int DT>
-Choice choose(const BlockFwdArgs& p, int access, bool ln) {
+Choice choose(const BlockFwdArgs& p, bool aligned, bool ln) {
   constexpr int VEC = Io<DT>::kVec;
-  if (access == 16) {
-    switch (groups_a_thread(p.H / VEC, VEC, ln)) {
-      case 1: return make<DT, VEC, 1>(p, ln);
-      case 2: return make<DT, VEC, 2>(p, ln);
-      case 3: return make<DT, VEC, 3>(p, ln);
-      default: return make<DT, VEC, 4>(p, ln);
+  const int nv = groups_a_thread((p.H + VEC - 1) / VEC, VEC, ln, !aligned);
+  if (!aligned) {
+    switch (nv) {
+      case 1: return make<DT, 1, true>(p, ln);
+      case 2: return make<DT, 2, true>(p, ln);
+      case 3: return make<DT, 3, true>(p, ln);
+      default: return make<DT, 4, true>(p, ln);
     }
   }
-  if constexpr (DT != kF32)
-    if (access == 4) return p.H <= 256 ? make<DT, 2, 4>(p, ln) : make<DT, 2, 8>(p, ln);
-  return p.H <= 128 ? make<DT, 1, 4>(p, ln) : make<DT, 1, 8>(p, ln);
+  switch (nv) {
+    case 1: return make<DT, 1, false>(p, ln);
+    case 2: return make<DT, 2, false>(p, ln);
+    case 3: return make<DT, 3, false>(p, ln);
+    default: return make<DT, 4, false>(p, ln);
+  }
 }
 
 }  // namespace
@@ -435,13 +412,13 @@ Walk walk_of(const Shape& sh) {
 
 }  // namespace blk
 
-int launch_block_fwd(int dtype, int access, bool layer_or_bias, const BlockFwdArgs& args,
+int launch_block_fwd(int dtype, bool aligned, bool layer_or_bias, const BlockFwdArgs& args,
                      const LaunchCtx& c, const char** name) {
   using namespace blk;
-  const Choice ch = dtype == kF32 ? choose<kF32>(args, access, layer_or_bias)
-                    : dtype == kF16 ? choose<kF16>(args, access, layer_or_bias)
-                                    : choose<kBF16>(args, access, layer_or_bias);
-  *name = access == 16 ? "block_fwd_v16" : access == 4 ? "block_fwd_v4" : "block_fwd_v2";
+  const Choice ch = dtype == kF32 ? choose<kF32>(args, aligned, layer_or_bias)
+                    : dtype == kF16 ? choose<kF16>(args, aligned, layer_or_bias)
+                                    : choose<kBF16>(args, aligned, layer_or_bias);
+  *name = aligned ? "block_fwd" : "block_fwd_shifted";
   BlockFwdArgs p = args;
   p.w = walk_of(ch.sh);
   p.kept_at = ch.kept_at;
