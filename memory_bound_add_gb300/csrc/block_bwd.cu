@@ -122,15 +122,22 @@ struct Sums {
   }
 };
 
+// Threads a CTA, and the registers each may have.  Shifted rows without layer
+// norms and gate rows fit 96: 640 threads, so that a row of 5000 columns takes
+// one CTA instead of a cluster of two.
+__host__ __device__ constexpr bool bwd_lean(bool full, bool gr, bool sh) { return sh && !full && !gr; }
+__host__ __device__ constexpr int bwd_threads(bool full, bool gr, bool sh) {
+  return bwd_lean(full, gr, sh) ? 640 : kMaxThreads;
+}
 template <int DT, int NV, bool FULL, bool GR, bool SH>
 constexpr int bwd_regs() {
-  return 128;
+  return bwd_lean(FULL, GR, SH) ? 96 : 128;
 }
 
 // FULL: some norm is a layer norm or has a bias.  GR: a gate with rows.  SH:
 // some rows do not begin on 16-byte borders.
 template <int DT, int NV, bool FULL, bool GR, bool SH>
-__global__ void __launch_bounds__(kMaxThreads) __maxnreg__((bwd_regs<DT, NV, FULL, GR, SH>()))
+__global__ void __launch_bounds__(bwd_threads(FULL, GR, SH)) __maxnreg__((bwd_regs<DT, NV, FULL, GR, SH>()))
     k_block_bwd(const __grid_constant__ BlockBwdArgs p) {
   using IO = Io<DT>;
   constexpr int S = IO::kBytes, VE = IO::kVec, N = VE / 2;
@@ -635,16 +642,13 @@ struct Choice {
 // need to join their sums), the parameters, the row sums.
 constexpr int kSideThreads = 512;
 
-template <int DT, int NV, bool GR, bool SH>
-Choice make(int H, bool full) {
-  constexpr int VE = Io<DT>::kVec;
+template <int DT, int NV, bool FULL, bool GR, bool SH>
+Choice make(int H) {
+  constexpr int VE = Io<DT>::kVec, kMost = bwd_threads(FULL, GR, SH);
   Choice c;
-  c.k = &k_block_bwd<DT, NV, false, GR, SH>;
-  if constexpr (NV * VE <= 8) {
-    if (full) c.k = &k_block_bwd<DT, NV, true, GR, SH>;
-  }
+  c.k = &k_block_bwd<DT, NV, FULL, GR, SH>;
   const int groups = (H + VE - 1) / VE;
-  c.sh.C = (groups + NV * kMaxThreads - 1) / (NV * kMaxThreads);
+  c.sh.C = (groups + NV * kMost - 1) / (NV * kMost);
   c.sh.slice = c.sh.C == 1 ? H : ((H + c.sh.C - 1) / c.sh.C + 15) / 16 * 16;
   const int threads = ((c.sh.slice + VE - 1) / VE + 32 * NV - 1) / (32 * NV) * 32;
   c.sh.rows = c.sh.C > 1 || threads > kSideThreads / 2 ? 1 : kSideThreads / threads;
@@ -653,37 +657,40 @@ Choice make(int H, bool full) {
   int ring = warps * kMaxSlots * static_cast<int>(Ring<DT, NV, GR ? 5 : 4, SH>::kSlot);
   int half = 0;  // walkers that give their sums to another at once
   for (int top = 1; top < c.sh.rows; top *= 2) half = top;
-  const int join = half * sums_of(full) * NV * VE * threads * 4;
+  const int join = half * sums_of(FULL) * NV * VE * threads * 4;
   if (ring < join) ring = join;
   c.kept_at = ring;
-  c.sums_at = c.kept_at + warps * static_cast<int>(full && GR ? Kept<VE, NV>::template bytes<3>()
-                                                               : Kept<VE, NV>::template bytes<2>());
-  c.smem = c.sums_at + c.sh.rows * 2 * (threads / 32) * c.sh.C * (full ? 8 : 4) * 4;
+  c.sums_at = c.kept_at + warps * static_cast<int>(Kept<VE, NV>::template bytes<FULL && GR ? 3 : 2>());
+  c.smem = c.sums_at + c.sh.rows * 2 * (threads / 32) * c.sh.C * (FULL ? 8 : 4) * 4;
   return c;
 }
 
-template <int DT, bool GR, bool SH>
-Choice choose(int H, bool full) {
+// 16 columns of a 16-bit type a thread where the sums are two or three for a
+// column, rows are not shifted and longer than a warp's 8 a thread; else 8
+// (4 of fp32 where 8 spill).
+template <int DT, bool FULL, bool GR, bool SH>
+Choice choose(int H) {
   constexpr int VEC = Io<DT>::kVec;
-  // 16 columns a thread where the sums are two or three for a column and the
-  // row is longer than a warp's 8, else 8
-  if constexpr (DT != kF32 && !SH) {
-    if (!full && H > 32 * VEC) return make<DT, 2, GR, SH>(H, full);
+  if constexpr (DT == kF32) {
+    return make<DT, SH && FULL && GR ? 1 : 2, FULL, GR, SH>(H);
+  } else {
+    if constexpr (!SH && !FULL) {
+      if (H > 32 * VEC) return make<DT, 2, FULL, GR, SH>(H);
+    }
+    return make<DT, 1, FULL, GR, SH>(H);
   }
-  // (4 of shifted fp32: 8 spill)
-  return make<DT, SH ? 1 : 8 / VEC, GR, SH>(H, full);
 }
 
-template <int DT>
-Choice choose(int H, bool aligned, bool full, bool gr) {
-  if (aligned) return gr ? choose<DT, true, false>(H, full) : choose<DT, false, false>(H, full);
-  return gr ? choose<DT, true, true>(H, full) : choose<DT, false, true>(H, full);
+template <int DT, bool FULL>
+Choice choose(int H, bool aligned, bool gr) {
+  if (aligned) return gr ? choose<DT, FULL, true, false>(H) : choose<DT, FULL, false, false>(H);
+  return gr ? choose<DT, FULL, true, true>(H) : choose<DT, FULL, false, true>(H);
 }
 
 Choice choose(int dtype, int H, bool aligned, bool full, bool gr) {
-  return dtype == kF32   ? choose<kF32>(H, aligned, full, gr)
-         : dtype == kF16 ? choose<kF16>(H, aligned, full, gr)
-                         : choose<kBF16>(H, aligned, full, gr);
+  if (dtype == kF32) return full ? choose<kF32, true>(H, aligned, gr) : choose<kF32, false>(H, aligned, gr);
+  if (dtype == kF16) return full ? choose<kF16, true>(H, aligned, gr) : choose<kF16, false>(H, aligned, gr);
+  return full ? choose<kBF16, true>(H, aligned, gr) : choose<kBF16, false>(H, aligned, gr);
 }
 
 // Units (CTAs or clusters) of a launch: those that fit the device at once, no
