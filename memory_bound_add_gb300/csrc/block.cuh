@@ -13,7 +13,8 @@
 // that its group begins in, takes its group out of that and its neighbour's,
 // and writes the granule that holds its group's begin together with the end
 // of its neighbour's, which it gets by shuffle.  Accesses of single elements
-// (2 bytes each) took three to four times as long.
+// (2 bytes each) took twice as long: 8192x5001 bf16 rms/rms forward 204 us,
+// with granules 99; backward 404 and 177.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -234,10 +235,10 @@ struct Ring {
             if (b >= s && b < n && ADDLN_IN(site, o + b, S, extent)) {
               if constexpr (S == 4)
                 asm volatile("st.shared.u32 [%0], %1;" ::"r"(at(slot, I, 0) + b),
-                             "r"(__ldg(reinterpret_cast<const uint32_t*>(p + b))) : "memory");
+                             "r"(__ldcg(reinterpret_cast<const uint32_t*>(p + b))) : "memory");
               else
                 asm volatile("st.shared.u16 [%0], %1;" ::"r"(at(slot, I, 0) + b),
-                             "h"(__ldg(reinterpret_cast<const unsigned short*>(p + b))) : "memory");
+                             "h"(__ldcg(reinterpret_cast<const unsigned short*>(p + b))) : "memory");
             }
         } else {
           copy(at(slot, I, k), p + k * (cs.kStep * S), n > 0 && ADDLN_IN(site, o, n, extent) ? n : 0);

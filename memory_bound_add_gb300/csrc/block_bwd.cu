@@ -294,8 +294,8 @@ __global__ void __launch_bounds__(bwd_threads(FULL, GR, SH)) __maxnreg__((bwd_re
     ring.meet();
     const float2 nhm = dup2(-hm_n), hr = dup2(hr_n), nfm = dup2(-fm_n), fr = dup2(fr_n);
     stats(r0 + it + 1);
-    // how far the row lies past 16-byte borders, tensor by tensor; zeros that
-    // stand for a missing tensor need no shift
+    // how far the row lies past 16-byte borders, tensor by tensor (of no
+    // account for the zeros of a missing one)
     int sh[NT];
 #pragma unroll
     for (int i = 0; i < NT; ++i) sh[i] = 0;

@@ -120,6 +120,7 @@ struct Piece {
   uint32_t e;      // the one element, or 0
 };
 
+// Loads past L1: in place, this kernel writes what it reads.
 template <int S>
 __device__ __forceinline__ void load_share(const Entry& e, Piece& p) {
   const Share<S> s(e, p.chunk);
@@ -129,15 +130,15 @@ __device__ __forceinline__ void load_share(const Entry& e, Piece& p) {
     const int r = (threadIdx.x + j * kThreads) * s.VEC;
     p.v[j] = make_uint4(0, 0, 0, 0);
     if (s.whole(r) && ADDLN_IN(801, (s.begin + r) * S, 16, e.n * S))
-      p.v[j] = __ldg(reinterpret_cast<const uint4*>(g + r * S));
+      p.v[j] = __ldcg(reinterpret_cast<const uint4*>(g + r * S));
   }
   p.e = 0;
   const int r = s.one();
   if (r >= 0 && ADDLN_IN(802, (s.begin + r) * S, S, e.n * S)) {
     if constexpr (S == 4)
-      p.e = __ldg(reinterpret_cast<const uint32_t*>(g) + r);
+      p.e = __ldcg(reinterpret_cast<const uint32_t*>(g) + r);
     else
-      p.e = __ldg(reinterpret_cast<const unsigned short*>(g) + r);
+      p.e = __ldcg(reinterpret_cast<const unsigned short*>(g) + r);
   }
 }
 

@@ -1,9 +1,11 @@
 """Global gradient norm and clipping against 64 bits.
 
-With u = 2^-24: a thread sums at most 64 squares in fp32 over four
-accumulators (16 roundings, 2 more to join them, one of the square each: 19 u
-relative, all terms being positive), fp64 does the rest; the root halves it
-and the last rounding adds 1 u: below 12 u.  The factor adds the roundings of
+With u = 2^-24: a thread sums at most 33 squares in fp32 over four
+accumulators (9 roundings, 2 more to join them, one of the square each: 12 u
+relative, all terms being positive); the shares are added as hi + lo, whose
+roundings are of order u^2 each, and rounded to fp32 once (1 u).  The root
+halves that, and its own rounding and scale's product add 2 u: below 12 u.  The
+factor adds the roundings of
 norm + 1e-6, the quotient and scale's product (3 u), out one more beside its
 own rounding: below 17 u."""
 from __future__ import annotations
