@@ -285,6 +285,8 @@ def _backward(s, some, rows, H, dy, dh, f, h, stats, df, dx, post, post_gamma, p
         if gate is None:
             raise ValueError("dgate without a gate")
         dgp = _tensor(dgate, "dgate", _F32 if gk == GATE_CHANNEL else dt, gate.numel(), dev)
+    if rows == 0 and gk == GATE_ROWS and dgp is not None:
+        dgate.zero_()  # gate rows of empty sequences, which the library does not know of
     if workspace is None:
         size = _workspace_size(rows, H, code, gk, rpg or 1, dev)
         workspace = torch.empty(size, dtype=torch.uint8, device=some.device)
@@ -348,6 +350,8 @@ class BlockNormFunction(torch.autograd.Function):
     @staticmethod
     def forward(ctx, f, x, post_gamma, post_beta, gate, pre_gamma, pre_beta, post, pre, residual_scale,
                 block_scale, eps):
+        if f.shape != x.shape:
+            raise ValueError(f"f of shape {tuple(f.shape)} beside x of {tuple(x.shape)}")
         f, x = f.contiguous(), x.contiguous()
         cont = lambda t: None if t is None else t.contiguous()  # noqa: E731
         post_gamma, post_beta, pre_gamma, pre_beta = map(cont, (post_gamma, post_beta, pre_gamma, pre_beta))

@@ -171,6 +171,107 @@ def test_addresses_off_the_vector_width(dtype, H):
                       torch.finfo(dtype).eps * ref[1].cpu().double().abs(), which)
 
 
+def at_offset(t, k):
+    """t's values k elements into a buffer of its own whose other elements
+    are 7, and that buffer."""
+    buf = torch.full((t.numel() + 32,), 7.0, dtype=t.dtype, device="cuda")
+    v = buf[k:k + t.numel()].view(t.shape)
+    v.copy_(t)
+    return v, buf
+
+
+def untouched(buf, k, n):
+    return bool((buf[:k] == 7).all()) and bool((buf[k + n:] == 7).all())
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("H,post,pre", [(520, "rms", "rms"), (520, "layer", "layer"), (4099, "rms", "rms"),
+                                        (1003, "layer", "rms")])
+def test_each_buffer_off_the_borders(dtype, H, post, pre):
+    # one buffer in turn (and all of them, each by its own distance) off the
+    # 16-byte borders: values as ever, nothing written beside the outputs
+    rows = 7
+    f, x, p = make((rows, H), dtype, post, pre, (rows, H), beta=post == "layer", seed=H)
+    wh, wy, wst, eh, ey = forward(f, x, p, post, pre, 0.9, 0.5, 1e-5)
+    h0 = wh.to(dtype)
+    st = tuple(None if t is None else t.reshape(-1).float().cuda() for t in wst)
+    g = torch.Generator().manual_seed(3)
+    dy, dh = torch.randn(rows, H, generator=g).to(dtype), torch.randn(rows, H, generator=g).to(dtype)
+    want, err = backward(dy, dh, f, h0, [None if t is None else t.cpu() for t in st], p, post, pre, 0.9, 0.5)
+    names = ["f", "x", "h", "y", "dy", "dh", "df", "dx", "gate", "dgate", "post_gamma", "pre_gamma"]
+    for which in names + ["all"]:
+        bufs = {}
+
+        def place(name, t):
+            k = 1 + names.index(name) if which == "all" else int(which == name)
+            v, buf = at_offset(t, k)
+            bufs[name] = (buf, k, t.numel())
+            return v
+
+        q = {k: place(k, v) if k in names else v.cuda() for k, v in p.items()}
+        fc, xc = place("f", f), place("x", x)
+        h, y = place("h", torch.zeros_like(f)), place("y", torch.zeros_like(f))
+        mba.block_norm_fwd(fc, xc, h, y, post=post, pre=pre, residual_scale=0.9, block_scale=0.5, **q)
+        torch.cuda.synchronize()
+        assert_within(h, wh, eh, which + " h")
+        assert_within(y, wy, ey, which + " y")
+        assert all(untouched(*bufs[k]) for k in ("h", "y")), which
+        h.copy_(h0)
+        got = {k: place(k, torch.zeros_like(f)) for k in ("df", "dx", "dgate")}
+        q.pop("pre_beta", None)
+        mba.block_norm_bwd(place("dy", dy), place("dh", dh), fc, h, st, got["df"], got["dx"], post=post, pre=pre,
+                           residual_scale=0.9, block_scale=0.5, dgate=got["dgate"], **q)
+        torch.cuda.synchronize()
+        for k, v in got.items():
+            assert_within(v, want[k].reshape(v.shape), err[k].reshape(v.shape), f"{which} {k}")
+            assert untouched(*bufs[k]), f"{which}: beside {k}"
+
+
+@pytest.mark.parametrize("dtype", [F32, BF16], ids=["fp32", "bf16"])
+@pytest.mark.parametrize("B,S,H,parts", [(3, 50, 333, 3), (40, 7, 1002, 2), (2, 300, 4099, 2), (5, 1, 71, 6)])
+def test_gate_rows_that_lie_off_the_borders(dtype, B, S, H, parts):
+    # the parts of a projection of an odd width, each row shifted by its own
+    # distance
+    f, x, p = make((B, S, H), dtype, "rms", "layer", None, seed=H)
+    wide = torch.randn(B, parts * H, generator=torch.Generator().manual_seed(2)).to(dtype)
+    dy = torch.randn(B, S, H, generator=torch.Generator().manual_seed(3)).to(dtype)
+    dev = wide.cuda()
+    for part in (0, parts - 1):
+        q = dict(p, gate=wide.chunk(parts, -1)[part].unsqueeze(1))
+        dq = dict(cuda(p), gate=dev.chunk(parts, -1)[part].unsqueeze(1))
+        wh, wy, wst, eh, ey = forward(f, x, q, "rms", "layer", 1.0, 1.0, 1e-5)
+        h, y, _ = mba.block_norm(f.cuda(), x.cuda(), post="rms", pre="layer", **dq)
+        assert_within(h, wh, eh, "h")
+        assert_within(y, wy, ey, "y")
+        hs, sts = wh.to(dtype), [None if t is None else t.reshape(-1).float() for t in wst]
+        want, err = backward(dy, None, f, hs, sts, q, "rms", "layer", 1.0, 1.0)
+        got = mba.block_norm_backward(dy.cuda(), None, f.cuda(), hs.cuda(),
+                                      tuple(None if t is None else t.cuda() for t in sts), post="rms", pre="layer", **dq)
+        for k in ("df", "dx", "dgate", "dpost_gamma", "dpre_gamma"):
+            v = getattr(got, k)
+            assert_within(v, want[k].reshape(v.shape), err[k].reshape(v.shape), k)
+
+
+def test_in_place_off_the_borders():
+    # rows that share 16-byte granules with their neighbours', written over
+    for H, dtype in ((1001, BF16), (37, F16), (4101, F32), (16389, BF16)):
+        f, x, p = make((300 if H < 2000 else 9, H), dtype, "rms", "rms", "channel", seed=H)
+        q = cuda(p)
+        h, y, st = mba.block_norm(f.cuda(), x.cuda(), post="rms", pre="rms", want_stats=True, **q)
+        (f1, b1), (x1, b2) = at_offset(f, 3), at_offset(x, 5)
+        mba.block_norm_fwd(f1, x1, x1, f1, post="rms", pre="rms", **q)
+        torch.cuda.synchronize()
+        assert torch.equal(x1, h) and torch.equal(f1, y)
+        assert untouched(b1, 3, f.numel()) and untouched(b2, 5, f.numel())
+        dy = torch.randn_like(h)
+        want = mba.block_norm_backward(dy, h, f.cuda(), h, st, post="rms", pre="rms", **q)
+        (d1, b1), (h1, b2) = at_offset(dy, 1), at_offset(h, 2)
+        mba.block_norm_bwd(d1, h.clone(), f.cuda(), h1, st, d1, h1, post="rms", pre="rms", **q)
+        torch.cuda.synchronize()
+        assert torch.equal(d1, want.df) and torch.equal(h1, want.dx)
+        assert untouched(b1, 1, f.numel()) and untouched(b2, 2, f.numel())
+
+
 def test_gate_with_a_stride():
     # one part of a wider projection, as a modulation layer gives it
     B, S, H = 3, 50, 256
@@ -269,6 +370,23 @@ def test_no_rows():
         assert t.shape == (64,) and not t.any()
 
 
+def test_gate_rows_of_empty_sequences():
+    # four sequences of no rows: their gate rows served nothing
+    p = cuda(make((1, 64), F16, "rms", "rms", seed=0)[2])
+    f, gate = torch.empty(4, 0, 64, dtype=F16, device="cuda"), torch.ones(4, 1, 64, dtype=F16, device="cuda")
+    h, y, st = mba.block_norm(f, f, post="rms", pre="rms", gate=gate, want_stats=True, **p)
+    assert h.shape == f.shape and st[1].shape == (0,)
+    dgate = torch.full_like(gate, 5.0)
+    mba.block_norm_bwd(f, f, f, f, st, torch.empty_like(f), torch.empty_like(f), post="rms", pre="rms", gate=gate,
+                       dgate=dgate, **p)
+    torch.cuda.synchronize()
+    assert not dgate.any()
+    g = gate.requires_grad_(True)
+    h, y = mba.block_norm_train(f.requires_grad_(True), f.detach(), post="rms", pre="rms", gate=g, **p)
+    (h.sum() + y.sum()).backward()
+    assert g.grad.shape == gate.shape and not g.grad.any()
+
+
 def test_same_bits_again_and_on_another_stream():
     f, x, p = make((3, 400, 520), F16, "layer", "rms", (3, 1, 520), beta=True, seed=11)
     q = cuda(p)
@@ -331,6 +449,39 @@ def test_captured_and_replayed():
         torch.cuda.synchronize()
         assert torch.equal(h, h2) and torch.equal(y, y2)
         assert all(u is None or torch.equal(u, v) for u, v in zip(gr, gr2))
+
+
+def test_captured_training_step():
+    # forward and backward through autograd in one graph, on leaves without an
+    # eager graph of their own
+    f, x, p = make((64, 1000), F16, "layer", "rms", "channel", beta=True, seed=15)
+    fc, xc = f.cuda().requires_grad_(True), x.cuda().requires_grad_(True)
+    q = {k: v.cuda().requires_grad_(True) for k, v in p.items()}
+    leaves_ = [fc, xc, *q.values()]
+
+    def step():
+        h, y = mba.block_norm_train(fc, xc, post="layer", pre="rms", **q)
+        return torch.autograd.grad((h.float() * 0.5 + y.float() ** 2).sum(), leaves_)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        for _ in range(2):
+            step()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        got = step()
+    for k in range(2):
+        with torch.no_grad():
+            fc.copy_(torch.randn_like(fc))
+        g.replay()
+        torch.cuda.synchronize()
+        mine = [t.clone() for t in got]
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(mine, want))
 
 
 def test_two_graphs_with_one_workspace():
@@ -540,6 +691,8 @@ def test_refusals_of_the_wrapper():
         mba.block_norm_backward(y[:, :32].contiguous(), None, fc, h, st, **kw)
     with pytest.raises(TypeError):
         mba.block_norm_backward(None, None, fc, h, st, **kw)
+    with pytest.raises(ValueError):  # as many elements, but another shape
+        mba.block_norm_train(fc, xc.view(8, 32), **kw)
 
 
 @pytest.mark.parametrize("H", [64, 1000, 1001, 4096, 8200])
