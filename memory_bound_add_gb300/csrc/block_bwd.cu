@@ -122,22 +122,26 @@ struct Sums {
   }
 };
 
-// Threads a CTA, and the registers each may have.  Shifted rows without layer
-// norms and gate rows fit 96: 640 threads, so that a row of 5000 columns takes
-// one CTA instead of a cluster of two.
-__host__ __device__ constexpr bool bwd_lean(bool full, bool gr, bool sh) { return sh && !full && !gr; }
-__host__ __device__ constexpr int bwd_threads(bool full, bool gr, bool sh) {
-  return bwd_lean(full, gr, sh) ? 640 : kMaxThreads;
+// Threads a CTA, and the registers each may have.  Without gate rows, shifted
+// rows of rms norms and 16-bit rows of layer norms that are not shifted fit
+// 96: 640 threads, so that a row of 5120 columns takes one CTA instead of a
+// cluster of two (us, cluster / CTA: 8192x5001 bf16 rms 296 / 177, 8192x5120
+// bf16 layer 214 / 116; rows of up to 4096 columns 97 / 96).  The others spill.
+__host__ __device__ constexpr bool bwd_lean(int dt, bool full, bool gr, bool sh) {
+  return !gr && (sh ? !full : full && dt != kF32);
+}
+__host__ __device__ constexpr int bwd_threads(int dt, bool full, bool gr, bool sh) {
+  return bwd_lean(dt, full, gr, sh) ? 640 : kMaxThreads;
 }
 template <int DT, int NV, bool FULL, bool GR, bool SH>
 constexpr int bwd_regs() {
-  return bwd_lean(FULL, GR, SH) ? 96 : 128;
+  return bwd_lean(DT, FULL, GR, SH) ? 96 : 128;
 }
 
 // FULL: some norm is a layer norm or has a bias.  GR: a gate with rows.  SH:
 // some rows do not begin on 16-byte borders.
 template <int DT, int NV, bool FULL, bool GR, bool SH>
-__global__ void __launch_bounds__(bwd_threads(FULL, GR, SH)) __maxnreg__((bwd_regs<DT, NV, FULL, GR, SH>()))
+__global__ void __launch_bounds__(bwd_threads(DT, FULL, GR, SH)) __maxnreg__((bwd_regs<DT, NV, FULL, GR, SH>()))
     k_block_bwd(const __grid_constant__ BlockBwdArgs p) {
   using IO = Io<DT>;
   constexpr int S = IO::kBytes, VE = IO::kVec, N = VE / 2;
@@ -637,14 +641,16 @@ struct Choice {
 };
 
 // NV groups of VE columns a thread; a CTA of up to kSideThreads threads for as
-// many rows side by side as fit it, else one CTA of up to kMaxThreads for a
-// row, else a cluster.  Shared memory: the ring (at least what the walkers
-// need to join their sums), the parameters, the row sums.
+// many rows side by side as fit it, else one CTA for a row, else a cluster of
+// as few CTAs as hold it: its barrier costs more than several clusters to an
+// SM give back (8192x6144 bf16 layer, clusters of 2 / 4 / 8: 230, 265, 400 us;
+// 8192x5120 fp32 rms 168, 268, 421).  Shared memory: the ring (at least what
+// the walkers need to join their sums), the parameters, the row sums.
 constexpr int kSideThreads = 512;
 
 template <int DT, int NV, bool FULL, bool GR, bool SH>
 Choice make(int H) {
-  constexpr int VE = Io<DT>::kVec, kMost = bwd_threads(FULL, GR, SH);
+  constexpr int VE = Io<DT>::kVec, kMost = bwd_threads(DT, FULL, GR, SH);
   Choice c;
   c.k = &k_block_bwd<DT, NV, FULL, GR, SH>;
   const int groups = (H + VE - 1) / VE;
