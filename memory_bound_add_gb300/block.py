@@ -124,9 +124,10 @@ def _rows_tensor(t, name):
 
 
 def _norm_kind(kind, name):
-    if kind not in _NORMS:
+    code = _NORMS.get(kind)
+    if code is None:
         raise ValueError(f'{name} must be None, "rms" or "layer", got {kind!r}')
-    return _NORMS[kind]
+    return code
 
 
 def gate_layout(gate, shape):
@@ -189,19 +190,26 @@ _NO_STATS = (None, None, None, None)
 _F32 = torch.float32
 
 
-def _forward(s, f, x, h, y, stats, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta,
-             residual_scale, block_scale, eps):
+def _addresses(ts):
+    """Addresses of tensors that were allocated here (None for None)."""
+    return [None if t is None else t.data_ptr() for t in ts]
+
+
+def _forward(s, f, x, outs, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta, residual_scale,
+             block_scale, eps):
+    """outs: the addresses of h, y and the statistics, checked."""
     dt, dev, n = f.dtype, f.get_device(), rows * H
-    pm, pr, nm, nr = stats
-    gp, gk, gs, rpg = _gate_args(gate, f)
-    _check(lib().block_norm_fwd(
+    gp, gk, gs, rpg = (None, GATE_NONE, 0, 0) if gate is None else _gate_args(gate, f)
+    rc = (_lib or lib()).block_norm_fwd(
         _tensor(f, "f", dt, n, dev), _tensor(x, "x", dt, n, dev), _norm_kind(post, "post"),
-        _tensor(post_gamma, "post_gamma", _F32, H, dev), _tensor(post_beta, "post_beta", _F32, H, dev),
+        None if post_gamma is None else _tensor(post_gamma, "post_gamma", _F32, H, dev),
+        None if post_beta is None else _tensor(post_beta, "post_beta", _F32, H, dev),
         gp, gk, gs, rpg, residual_scale, block_scale, _norm_kind(pre, "pre"),
-        _tensor(pre_gamma, "pre_gamma", _F32, H, dev), _tensor(pre_beta, "pre_beta", _F32, H, dev),
-        _tensor(h, "h", dt, n, dev), _tensor(y, "y", dt, n, dev), _tensor(pm, "post_mean", _F32, rows, dev),
-        _tensor(pr, "post_rstd", _F32, rows, dev), _tensor(nm, "pre_mean", _F32, rows, dev),
-        _tensor(nr, "pre_rstd", _F32, rows, dev), rows, H, eps, DTYPE_CODE[dt], s), "block_norm_fwd")
+        None if pre_gamma is None else _tensor(pre_gamma, "pre_gamma", _F32, H, dev),
+        None if pre_beta is None else _tensor(pre_beta, "pre_beta", _F32, H, dev),
+        *outs, rows, H, eps, DTYPE_CODE[dt], s)
+    if rc:
+        raise AddLNError(rc, "block_norm_fwd")
 
 
 def block_norm_fwd(f, x, h, y=None, stats=None, *, post=None, post_gamma=None, post_beta=None,
@@ -211,9 +219,14 @@ def block_norm_fwd(f, x, h, y=None, stats=None, *, post=None, post_gamma=None, p
     may be f or x itself) and, with stats = (post_mean, post_rstd, pre_mean,
     pre_rstd), into [rows] fp32 tensors (None: not written)."""
     rows, H = _rows_tensor(f, "f")
+    dt, dev, n = f.dtype, f.get_device(), rows * H
+    pm, pr, nm, nr = stats or _NO_STATS
+    outs = (_tensor(h, "h", dt, n, dev), _tensor(y, "y", dt, n, dev), _tensor(pm, "post_mean", _F32, rows, dev),
+            _tensor(pr, "post_rstd", _F32, rows, dev), _tensor(nm, "pre_mean", _F32, rows, dev),
+            _tensor(nr, "pre_rstd", _F32, rows, dev))
     on_stream(f.device, stream, lambda s: _forward(
-        s, f, x, h, y, stats or _NO_STATS, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta,
-        residual_scale, block_scale, eps))
+        s, f, x, outs, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta, residual_scale,
+        block_scale, eps))
 
 
 def block_norm(f, x, *, post=None, post_gamma=None, post_beta=None, gate=None, pre="rms",
@@ -230,11 +243,13 @@ def block_norm(f, x, *, post=None, post_gamma=None, post_beta=None, gate=None, p
         h = torch.empty_like(f)
         y = torch.empty_like(f) if pre is not None else None
         stats = None
+        outs = [h.data_ptr(), None if y is None else y.data_ptr()]
         if want_stats:
             new = lambda w: torch.empty(rows, dtype=_F32, device=f.device) if w else None  # noqa: E731
             stats = (new(post == "layer"), new(post is not None), new(pre == "layer"), new(pre is not None))
-        _forward(s, f, x, h, y, stats or _NO_STATS, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma,
-                 pre_beta, residual_scale, block_scale, eps)
+        outs.extend(_addresses(stats or _NO_STATS))
+        _forward(s, f, x, outs, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta,
+                 residual_scale, block_scale, eps)
         return h, y, stats
 
     return on_stream(f.device, stream, call)
@@ -274,19 +289,13 @@ def _given(dy, dh):
     return (some, *_rows_tensor(some, name))
 
 
-def _backward(s, some, rows, H, dy, dh, f, h, stats, df, dx, post, post_gamma, post_beta, gate, pre, pre_gamma,
-              residual_scale, block_scale, dpost_gamma, dpost_beta, dgate, dpre_gamma, dpre_beta, workspace):
+def _backward(s, some, rows, H, dy, dh, f, h, stats, outs, post, post_gamma, post_beta, gate_args, pre, pre_gamma,
+              residual_scale, block_scale, workspace):
+    """outs: the addresses of df, dx and the parameters' gradients, checked."""
     dt, dev, n = some.dtype, some.get_device(), rows * H
     code = DTYPE_CODE[dt]
     pm, pr, nm, nr = stats or _NO_STATS
-    gp, gk, gs, rpg = _gate_args(gate, some)
-    dgp = None
-    if dgate is not None:
-        if gate is None:
-            raise ValueError("dgate without a gate")
-        dgp = _tensor(dgate, "dgate", _F32 if gk == GATE_CHANNEL else dt, gate.numel(), dev)
-    if rows == 0 and gk == GATE_ROWS and dgp is not None:
-        dgate.zero_()  # gate rows of empty sequences, which the library does not know of
+    gp, gk, gs, rpg = gate_args
     if workspace is None:
         size = _workspace_size(rows, H, code, gk, rpg or 1, dev)
         workspace = torch.empty(size, dtype=torch.uint8, device=some.device)
@@ -294,17 +303,20 @@ def _backward(s, some, rows, H, dy, dh, f, h, stats, df, dx, post, post_gamma, p
         raise ValueError(f"workspace must be a contiguous tensor on cuda:{dev}")
     else:
         size = workspace.numel() * workspace.element_size()
-    _check(lib().block_norm_bwd(
-        _tensor(dy, "dy", dt, n, dev), _tensor(dh, "dh", dt, n, dev), _tensor(f, "f", dt, n, dev),
-        _tensor(h, "h", dt, n, dev), _norm_kind(post, "post"), _tensor(post_gamma, "post_gamma", _F32, H, dev),
-        _tensor(post_beta, "post_beta", _F32, H, dev), _tensor(pm, "post_mean", _F32, rows, dev),
-        _tensor(pr, "post_rstd", _F32, rows, dev), gp, gk, gs, rpg, residual_scale, block_scale,
-        _norm_kind(pre, "pre"), _tensor(pre_gamma, "pre_gamma", _F32, H, dev),
-        _tensor(nm, "pre_mean", _F32, rows, dev), _tensor(nr, "pre_rstd", _F32, rows, dev),
-        _tensor(df, "df", dt, n, dev), _tensor(dx, "dx", dt, n, dev),
-        _tensor(dpost_gamma, "dpost_gamma", _F32, H, dev), _tensor(dpost_beta, "dpost_beta", _F32, H, dev), dgp,
-        _tensor(dpre_gamma, "dpre_gamma", _F32, H, dev), _tensor(dpre_beta, "dpre_beta", _F32, H, dev), rows, H,
-        code, workspace.data_ptr(), size, s), "block_norm_bwd")
+    rc = (_lib or lib()).block_norm_bwd(
+        None if dy is None else _tensor(dy, "dy", dt, n, dev), None if dh is None else _tensor(dh, "dh", dt, n, dev),
+        None if f is None else _tensor(f, "f", dt, n, dev), None if h is None else _tensor(h, "h", dt, n, dev),
+        _norm_kind(post, "post"), None if post_gamma is None else _tensor(post_gamma, "post_gamma", _F32, H, dev),
+        None if post_beta is None else _tensor(post_beta, "post_beta", _F32, H, dev),
+        None if pm is None else _tensor(pm, "post_mean", _F32, rows, dev),
+        None if pr is None else _tensor(pr, "post_rstd", _F32, rows, dev), gp, gk, gs, rpg, residual_scale,
+        block_scale, _norm_kind(pre, "pre"),
+        None if pre_gamma is None else _tensor(pre_gamma, "pre_gamma", _F32, H, dev),
+        None if nm is None else _tensor(nm, "pre_mean", _F32, rows, dev),
+        None if nr is None else _tensor(nr, "pre_rstd", _F32, rows, dev), *outs, rows, H, code,
+        workspace.data_ptr(), size, s)
+    if rc:
+        raise AddLNError(rc, "block_norm_bwd")
 
 
 def block_norm_bwd(dy, dh, f, h, stats, df, dx, *, post=None, post_gamma=None, post_beta=None,
@@ -317,9 +329,23 @@ def block_norm_bwd(dy, dh, f, h, stats, df, dx, *, post=None, post_gamma=None, p
     block_norm_bwd_workspace_size(...) bytes, reusable call after call
     (allocated here when None)."""
     some, rows, H = _given(dy, dh)
-    on_stream(some.device, stream, lambda s: _backward(
-        s, some, rows, H, dy, dh, f, h, stats, df, dx, post, post_gamma, post_beta, gate, pre, pre_gamma,
-        residual_scale, block_scale, dpost_gamma, dpost_beta, dgate, dpre_gamma, dpre_beta, workspace))
+    dt, dev, n = some.dtype, some.get_device(), rows * H
+    gate_args = _gate_args(gate, some)
+    if dgate is not None and gate is None:
+        raise ValueError("dgate without a gate")
+    outs = (_tensor(df, "df", dt, n, dev), _tensor(dx, "dx", dt, n, dev),
+            _tensor(dpost_gamma, "dpost_gamma", _F32, H, dev), _tensor(dpost_beta, "dpost_beta", _F32, H, dev),
+            None if dgate is None else _tensor(dgate, "dgate", _F32 if gate_args[1] == GATE_CHANNEL else dt,
+                                               gate.numel(), dev),
+            _tensor(dpre_gamma, "dpre_gamma", _F32, H, dev), _tensor(dpre_beta, "dpre_beta", _F32, H, dev))
+
+    def call(s):
+        if rows == 0 and dgate is not None:
+            dgate.zero_()  # gate rows of empty sequences, which the library does not know of
+        _backward(s, some, rows, H, dy, dh, f, h, stats, outs, post, post_gamma, post_beta, gate_args, pre, pre_gamma,
+                  residual_scale, block_scale, workspace)
+
+    on_stream(some.device, stream, call)
 
 
 def block_norm_backward(dy, dh, f, h, stats, *, post=None, post_gamma=None, post_beta=None, gate=None,
@@ -328,16 +354,19 @@ def block_norm_backward(dy, dh, f, h, stats, *, post=None, post_gamma=None, post
     """Allocate the gradients with PyTorch and run block_norm_bwd: the
     gradient of every input that is given (beta's gradients where a beta is)."""
     some, rows, H = _given(dy, dh)
-
-    def like(t):
-        return None if t is None else torch.empty(t.shape, dtype=t.dtype, device=t.device)
+    gate_args = _gate_args(gate, some)
+    if pre_beta is not None:
+        _tensor(pre_beta, "pre_beta", _F32, H, some.get_device())
 
     def call(s):
-        df, dx = torch.empty_like(some), torch.empty_like(some)
-        dpg, dpb, dg, dng, dnb = like(post_gamma), like(post_beta), like(gate), like(pre_gamma), like(pre_beta)
-        _backward(s, some, rows, H, dy, dh, f, h, stats, df, dx, post, post_gamma, post_beta, gate, pre, pre_gamma,
-                  residual_scale, block_scale, dpg, dpb, dg, dng, dnb, None)
-        return BlockNormGrads(df, dx, dpg, dpb, dg, dng, dnb)
+        new = torch.empty_like if rows else torch.zeros_like
+        g = [torch.empty_like(some), torch.empty_like(some), None if post_gamma is None else new(post_gamma),
+             None if post_beta is None else new(post_beta), None if gate is None else
+             new(gate) if gate.is_contiguous() else new(gate, memory_format=torch.contiguous_format),
+             None if pre_gamma is None else new(pre_gamma), None if pre_beta is None else new(pre_beta)]
+        _backward(s, some, rows, H, dy, dh, f, h, stats, _addresses(g), post, post_gamma, post_beta, gate_args, pre,
+                  pre_gamma, residual_scale, block_scale, None)
+        return BlockNormGrads(*g)
 
     return on_stream(some.device, stream, call)
 
