@@ -114,8 +114,9 @@ int block_norm_bwd(const void *dy, const void *dh, const void *f, const void *h,
                    float *dpre_gamma, float *dpre_beta, int64_t rows, int64_t H, int dtype,
                    void *workspace, int64_t workspace_bytes, void *stream);
 
-/* Bytes of workspace block_norm_bwd needs on the current device, whatever
- * the buffers' alignment (0 when rows == 0), or a negative code. */
+/* Bytes of workspace block_norm_bwd needs on the current device for this many
+ * rows or fewer, whatever the buffers' alignment (0 when rows == 0), or a
+ * negative code. */
 int64_t block_norm_bwd_workspace_size(int64_t rows, int64_t H, int dtype, int gate_kind,
                                       int64_t rows_per_gate);
 

@@ -649,7 +649,7 @@ struct Choice {
 constexpr int kSideThreads = 512;
 
 template <int DT, int NV, bool FULL, bool GR, bool SH>
-Choice make(int H) {
+Choice make(int H, int64_t rows, int sms) {
   constexpr int VE = Io<DT>::kVec, kMost = bwd_threads(DT, FULL, GR, SH);
   Choice c;
   c.k = &k_block_bwd<DT, NV, FULL, GR, SH>;
@@ -658,6 +658,7 @@ Choice make(int H) {
   c.sh.slice = c.sh.C == 1 ? H : ((H + c.sh.C - 1) / c.sh.C + 15) / 16 * 16;
   const int threads = ((c.sh.slice + VE - 1) / VE + 32 * NV - 1) / (32 * NV) * 32;
   c.sh.rows = c.sh.C > 1 || threads > kSideThreads / 2 ? 1 : kSideThreads / threads;
+  c.sh.rows = rows_side_by_side(c.sh.rows, rows, sms);
   c.sh.threads = threads * c.sh.rows;
   const int warps = c.sh.threads / 32;
   int ring = warps * kMaxSlots * static_cast<int>(Ring<DT, NV, GR ? 5 : 4, SH>::kSlot);
@@ -671,32 +672,40 @@ Choice make(int H) {
   return c;
 }
 
+// The rows that walkers of VE columns a thread have eight each of.
+inline int64_t few_rows(int H, int VE, int sms) {
+  return 8 * static_cast<int64_t>(sms) * (kSideThreads / ((H + 32 * VE - 1) / (32 * VE) * 32));
+}
+
 // 16 columns of a 16-bit type a thread where the sums are two or three for a
-// column, rows are not shifted and longer than a warp's 8 a thread; else 8
-// (4 of fp32 where 8 spill).
+// column, rows are not shifted and, with 8 a thread, longer than a warp's and
+// more than eight to a walker; else 8 (4 of fp32 where 8 spill).  us with 8 /
+// 16: 300x768 bf16 rms 5.2 / 7.0, 8192x512 (7 rows to a walker) 14.2 / 14.9,
+// 8192x1024 (13 rows) 23.8 / 21.5, 2048x4096 fp16 (13 rows) 32.7 / 28.4,
+// 32768x256 (a warp's) 21.9 / 28.1.
 template <int DT, bool FULL, bool GR, bool SH>
-Choice choose(int H) {
+Choice choose(int H, int64_t rows, int sms) {
   constexpr int VEC = Io<DT>::kVec;
   if constexpr (DT == kF32) {
-    return make<DT, SH && FULL && GR ? 1 : 2, FULL, GR, SH>(H);
+    return make<DT, SH && FULL && GR ? 1 : 2, FULL, GR, SH>(H, rows, sms);
   } else {
     if constexpr (!SH && !FULL) {
-      if (H > 32 * VEC) return make<DT, 2, FULL, GR, SH>(H);
+      if (H > 32 * VEC && rows > few_rows(H, VEC, sms)) return make<DT, 2, FULL, GR, SH>(H, rows, sms);
     }
-    return make<DT, 1, FULL, GR, SH>(H);
+    return make<DT, 1, FULL, GR, SH>(H, rows, sms);
   }
 }
 
 template <int DT, bool FULL>
-Choice choose(int H, bool aligned, bool gr) {
-  if (aligned) return gr ? choose<DT, FULL, true, false>(H) : choose<DT, FULL, false, false>(H);
-  return gr ? choose<DT, FULL, true, true>(H) : choose<DT, FULL, false, true>(H);
+Choice choose(int H, bool aligned, bool gr, int64_t rows, int sms) {
+  if (aligned) return gr ? choose<DT, FULL, true, false>(H, rows, sms) : choose<DT, FULL, false, false>(H, rows, sms);
+  return gr ? choose<DT, FULL, true, true>(H, rows, sms) : choose<DT, FULL, false, true>(H, rows, sms);
 }
 
-Choice choose(int dtype, int H, bool aligned, bool full, bool gr) {
-  if (dtype == kF32) return full ? choose<kF32, true>(H, aligned, gr) : choose<kF32, false>(H, aligned, gr);
-  if (dtype == kF16) return full ? choose<kF16, true>(H, aligned, gr) : choose<kF16, false>(H, aligned, gr);
-  return full ? choose<kBF16, true>(H, aligned, gr) : choose<kBF16, false>(H, aligned, gr);
+Choice choose(int dtype, int H, bool aligned, bool full, bool gr, int64_t rows, int sms) {
+  if (dtype == kF32) return full ? choose<kF32, true>(H, aligned, gr, rows, sms) : choose<kF32, false>(H, aligned, gr, rows, sms);
+  if (dtype == kF16) return full ? choose<kF16, true>(H, aligned, gr, rows, sms) : choose<kF16, false>(H, aligned, gr, rows, sms);
+  return full ? choose<kBF16, true>(H, aligned, gr, rows, sms) : choose<kBF16, false>(H, aligned, gr, rows, sms);
 }
 
 // Units (CTAs or clusters) of a launch: those that fit the device at once, no
@@ -714,7 +723,8 @@ int64_t seg_bytes(int64_t walkers, bool gr, int64_t rpg, int64_t Hp) {
 }
 
 // Quads a block: the most (of 2, 4, 8) whose partials a thread still loads in
-// one round.
+// one round (us of the backward with 2 / 8 throughout: 64x768 fp32 5.3 / 5.0,
+// 4096x768 fp16 16.5 / 17.7, 32768x256 bf16 21.7 / 23.3).
 inline int sums_quads(int64_t parts, bool full) {
   const int64_t one_round = kSumThreads * (8 / sums_of(full));
   return 8 * parts <= one_round ? 8 : 4 * parts <= one_round ? 4 : 2;
@@ -729,22 +739,32 @@ BwdKernel pick_sums(bool full, int quads) {
 }  // namespace
 }  // namespace blk
 
+// What any number of rows up to this one needs, so that a workspace serves
+// shorter calls too: their CTAs are no more than SMs, or than those of either
+// kernel, with as many rows side by side as there is room for, that fit.
 int64_t block_bwd_workspace_bytes(int dtype, bool aligned, bool full, int64_t rows, int H, int gate_kind,
                                   int64_t rows_per_gate, const DeviceInfo& dev) {
   using namespace blk;
   const bool gr = gate_kind == ADDLN_GATE_ROWS;
-  const Choice ch = choose(dtype, H, aligned, full, gr);
-  const int64_t units = units_of(ch, rows, dev);
-  if (units < 0) return units;
+  int64_t units = dev.sms, side = 1;
+  for (const int64_t r : {few_rows(H, dtype == kF32 ? 4 : 8, dev.sms), INT64_MAX / 2}) {
+    if (r == 0) continue;  // wider than one CTA
+    const Choice ch = choose(dtype, H, aligned, full, gr, r, dev.sms);
+    const int64_t fit = units_of(ch, INT64_MAX / 2, dev);
+    if (fit < 0) return fit;
+    units = units > fit ? units : fit;
+    side = side > ch.sh.rows ? side : ch.sh.rows;
+  }
+  if (units > rows) units = rows;
   const int64_t Hp = (H + 3) / 4 * 4;
-  return part_bytes(units, full, Hp) + seg_bytes(units * ch.sh.rows, gr, rows_per_gate, Hp);
+  return part_bytes(units, full, Hp) + seg_bytes(units * side, gr, rows_per_gate, Hp);
 }
 
 int launch_block_bwd(int dtype, bool aligned, bool full, BlockBwdArgs p, void* ws, int64_t ws_bytes,
                      const LaunchCtx& c, const char** name) {
   using namespace blk;
   const bool gr = p.gate_kind == ADDLN_GATE_ROWS;
-  const Choice ch = choose(dtype, p.H, aligned, full, gr);
+  const Choice ch = choose(dtype, p.H, aligned, full, gr, p.rows, c.dev.sms);
   p.w = walk_of(ch.sh);
   p.parts = units_of(ch, p.rows, c.dev);
   if (p.parts < 0) return static_cast<int>(p.parts);

@@ -49,7 +49,10 @@ __device__ __forceinline__ RowStat row_norm(Exchange<SIDES>& ex, float2 (&v)[NV 
 // again for every row costs more of L1's bandwidth than the row itself: two
 // vectors (no layer norm, no bias) stay in registers, and four of at most
 // eight columns a thread; four of more, and two of more of shifted rows, lie
-// in shared memory, one copy for all rows that the CTA has side by side.
+// in shared memory, one copy for all rows that the CTA has side by side.  us,
+// all in registers / as here / all in shared memory: 2048x4096 fp16 rms 12.1,
+// 12.0, 15.1; one row of 4096 2.8, 2.8, 3.2; 65536x768 bf16 layer 80.8, 68.8,
+// 68.9; 8192x5001 bf16 rms 121, 100, 100.
 __host__ __device__ constexpr bool in_registers(int columns, bool ln, bool sh) { return columns <= 8 || !(ln || sh); }
 
 template <int VE, int NV, bool LN, bool SH>
@@ -282,32 +285,34 @@ struct Choice {
   int smem = 0, kept_at = 0, sums_at = 0, ring_slots = 0;
 };
 
-// Threads a CTA may give a row: half of them where parameters lie in shared
-// memory, so that those of a CTA's columns leave room for the ring.
-inline int most_threads(int columns, bool ln, bool sh) { return in_registers(columns, ln, sh) ? kMaxThreads : kMaxThreads / 2; }
-
 // NV groups of VE columns a thread.  With the parameters in registers: a warp
-// for a row where 32 threads hold it, four rows to a CTA; else a CTA of up to
-// kMaxThreads; else a cluster.  With parameters in shared memory: rows of up
-// to 256 threads side by side in a CTA of up to 512, as many as leave the
-// ring two slots, or one; wider rows in clusters.
+// for a row where 32 threads hold it, four rows to a CTA (one: 32768x256 bf16
+// 12.4 us instead of 11.4); else a CTA of up to kMaxThreads; else a cluster.
+// With parameters in shared memory: rows side by side in a CTA of up to
+// kMaxThreads, as many as leave the ring two slots, or one; a cluster where one
+// row's parameters and ring do not fit (us of a cluster of two / of one CTA:
+// 4096x10240 bf16 layer 202 / 99).
 template <int DT, int NV, bool SH>
-Choice make(const BlockFwdArgs& p, bool ln) {
+Choice make(const BlockFwdArgs& p, bool ln, int sms) {
   constexpr int VE = Io<DT>::kVec;
   Choice c;
   const bool gr = p.gate_kind == ADDLN_GATE_ROWS;
   c.k = gr ? (ln ? &k_block_fwd<DT, NV, true, true, SH> : &k_block_fwd<DT, NV, false, true, SH>)
            : (ln ? &k_block_fwd<DT, NV, true, false, SH> : &k_block_fwd<DT, NV, false, false, SH>);
-  const int groups = (p.H + VE - 1) / VE, most = most_threads(NV * VE, ln, SH);
-  c.sh.C = (groups + NV * most - 1) / (NV * most);
-  c.sh.slice = c.sh.C == 1 ? p.H : ((p.H + c.sh.C - 1) / c.sh.C + 15) / 16 * 16;
-  const int threads = ((c.sh.slice + VE - 1) / VE + 32 * NV - 1) / (32 * NV) * 32;
+  const int groups = (p.H + VE - 1) / VE;
   const bool shared = !in_registers(NV * VE, ln, SH);
-  c.sh.rows = c.sh.C > 1 ? 1 : shared ? kMaxThreads / threads : threads == 32 ? 4 : 1;
-  const int slot = threads / 32 * static_cast<int>(gr ? Ring<DT, NV, 3, SH>::kSlot : Ring<DT, NV, 2, SH>::kSlot);
-  const int kept = shared ? threads / 32 * static_cast<int>(ln ? Kept<VE, NV>::template bytes<4>() : Kept<VE, NV>::template bytes<2>()) : 0;
-  const int sums = 2 * (threads / 32) * c.sh.C * 16;
+  int threads, slot, kept, sums;
   auto bytes = [&] { return c.sh.rows * (c.ring_slots * slot + sums) + kept; };
+  for (c.sh.C = (groups + NV * kMaxThreads - 1) / (NV * kMaxThreads);; ++c.sh.C) {
+    c.sh.slice = c.sh.C == 1 ? p.H : ((p.H + c.sh.C - 1) / c.sh.C + 15) / 16 * 16;
+    threads = ((c.sh.slice + VE - 1) / VE + 32 * NV - 1) / (32 * NV) * 32;
+    slot = threads / 32 * static_cast<int>(gr ? Ring<DT, NV, 3, SH>::kSlot : Ring<DT, NV, 2, SH>::kSlot);
+    kept = shared ? threads / 32 * static_cast<int>(ln ? Kept<VE, NV>::template bytes<4>() : Kept<VE, NV>::template bytes<2>()) : 0;
+    sums = 2 * (threads / 32) * c.sh.C * 16;
+    c.sh.rows = c.ring_slots = 1;
+    if (bytes() <= kMaxSmem || c.sh.C == kMaxCluster) break;
+  }
+  c.sh.rows = c.sh.C > 1 ? 1 : rows_side_by_side(shared ? kMaxThreads / threads : threads == 32 ? 4 : 1, p.rows, sms);
   c.ring_slots = kMaxSlots;
   while (bytes() > kMaxSmem && c.ring_slots > 1) --c.ring_slots;
   while (bytes() > kMaxSmem && c.sh.rows > 1) --c.sh.rows;
@@ -318,13 +323,15 @@ Choice make(const BlockFwdArgs& p, bool ln) {
   return c;
 }
 
-// Groups a thread, of 1 to 4: the number that needs the fewest
-// CTAs for a row, then that leaves the fewest of a row's threads' slots
-// empty, the larger one where equal.
-inline int groups_a_thread(int groups, int vec, bool ln, bool sh) {
+// Groups a thread, of 1 to 4: the number that needs the fewest CTAs for a row,
+// then that leaves the fewest of a row's threads' slots empty, the larger one
+// where equal (us with at most one / two / four: 4096x768 fp16 layer 13.5,
+// 13.4, 8.4; 2048x4096 fp16 rms 25.7, 13.1, 12.0; 32768x8192 bf16 rms 790, 437,
+// 332).
+inline int groups_a_thread(int groups) {
   int best = 1, ctas = 1 << 30, waste = 1 << 30;
   for (int nv = 1; nv <= 4; ++nv) {
-    const int most = nv * most_threads(nv * vec, ln, sh), c = (groups + most - 1) / most;
+    const int most = nv * kMaxThreads, c = (groups + most - 1) / most;
     const int t = (groups + 32 * nv - 1) / (32 * nv) * 32, w = t * nv - groups;
     if (c < ctas || (c == ctas && w <= waste)) best = nv, ctas = c, waste = w;
   }
@@ -332,22 +339,22 @@ inline int groups_a_thread(int groups, int vec, bool ln, bool sh) {
 }
 
 template <int DT>
-Choice choose(const BlockFwdArgs& p, bool aligned, bool ln) {
+Choice choose(const BlockFwdArgs& p, bool aligned, bool ln, int sms) {
   constexpr int VEC = Io<DT>::kVec;
-  const int nv = groups_a_thread((p.H + VEC - 1) / VEC, VEC, ln, !aligned);
+  const int nv = groups_a_thread((p.H + VEC - 1) / VEC);
   if (!aligned) {
     switch (nv) {
-      case 1: return make<DT, 1, true>(p, ln);
-      case 2: return make<DT, 2, true>(p, ln);
-      case 3: return make<DT, 3, true>(p, ln);
-      default: return make<DT, 4, true>(p, ln);
+      case 1: return make<DT, 1, true>(p, ln, sms);
+      case 2: return make<DT, 2, true>(p, ln, sms);
+      case 3: return make<DT, 3, true>(p, ln, sms);
+      default: return make<DT, 4, true>(p, ln, sms);
     }
   }
   switch (nv) {
-    case 1: return make<DT, 1, false>(p, ln);
-    case 2: return make<DT, 2, false>(p, ln);
-    case 3: return make<DT, 3, false>(p, ln);
-    default: return make<DT, 4, false>(p, ln);
+    case 1: return make<DT, 1, false>(p, ln, sms);
+    case 2: return make<DT, 2, false>(p, ln, sms);
+    case 3: return make<DT, 3, false>(p, ln, sms);
+    default: return make<DT, 4, false>(p, ln, sms);
   }
 }
 
@@ -415,9 +422,9 @@ Walk walk_of(const Shape& sh) {
 int launch_block_fwd(int dtype, bool aligned, bool layer_or_bias, const BlockFwdArgs& args,
                      const LaunchCtx& c, const char** name) {
   using namespace blk;
-  const Choice ch = dtype == kF32 ? choose<kF32>(args, aligned, layer_or_bias)
-                    : dtype == kF16 ? choose<kF16>(args, aligned, layer_or_bias)
-                                    : choose<kBF16>(args, aligned, layer_or_bias);
+  const Choice ch = dtype == kF32 ? choose<kF32>(args, aligned, layer_or_bias, c.dev.sms)
+                    : dtype == kF16 ? choose<kF16>(args, aligned, layer_or_bias, c.dev.sms)
+                                    : choose<kBF16>(args, aligned, layer_or_bias, c.dev.sms);
   *name = aligned ? "block_fwd" : "block_fwd_shifted";
   BlockFwdArgs p = args;
   p.w = walk_of(ch.sh);

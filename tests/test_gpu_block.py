@@ -513,6 +513,34 @@ def test_two_graphs_with_one_workspace():
         assert all(torch.equal(u, v) for u, v in zip(t, want))
 
 
+@pytest.mark.parametrize("dtype,H", [(F32, 768), (F16, 264), (BF16, 1024), (BF16, 4096), (F16, 5001), (BF16, 32768)])
+def test_a_workspace_serves_shorter_calls(dtype, H):
+    code = block.DTYPE_CODE[dtype]
+    for kind, rpg in ((block.GATE_NONE, 1), (block.GATE_ROWS, 1), (block.GATE_ROWS, 7)):
+        sizes = [mba.block_norm_bwd_workspace_size(r, H, code, kind, rpg)
+                 for r in (1, 2, 100, 151, 152, 153, 200, 304, 305, 700, 1216, 1217, 5000, 9729, 40000, 1 << 20)]
+        assert sizes == sorted(sizes) and sizes[0] > 0
+    most = 700 if H < 30000 else 40
+    f, x, p = make((most, H), dtype, "rms", "rms", None, seed=H)
+    q = dict(cuda(p), gate=torch.randn(most // 7 + 1, H, device="cuda").to(dtype))
+    ws = torch.empty(mba.block_norm_bwd_workspace_size(most, H, code, block.GATE_ROWS, 7), dtype=torch.uint8,
+                     device="cuda")
+    for r in (most, most // 2, 153, 152, 35, 1):
+        r = max(1, min(r, most) // 7 * 7)
+        if r < 7:
+            continue
+        fc, xc = f[:r].cuda().view(-1, 7, H), x[:r].cuda().view(-1, 7, H)
+        gate = q["gate"][:r // 7].unsqueeze(1)
+        kw = dict(post="rms", pre="rms", **dict(q, gate=gate))
+        h, _, st = mba.block_norm(fc, xc, want_stats=True, **kw)
+        want = mba.block_norm_backward(h, None, fc, h, st, **kw)
+        got = {k: torch.empty_like(getattr(want, k)) for k in ("df", "dx", "dgate", "dpost_gamma", "dpre_gamma")}
+        mba.block_norm_bwd(h, None, fc, h, st, got["df"], got["dx"], workspace=ws, dgate=got["dgate"],
+                           dpost_gamma=got["dpost_gamma"], dpre_gamma=got["dpre_gamma"], **kw)
+        torch.cuda.synchronize()
+        assert all(torch.equal(v, getattr(want, k)) for k, v in got.items())
+
+
 def test_rows_behind_the_last_are_left():
     f, x, p = make((5, 1001), BF16, "rms", "rms", "channel", seed=8)
     big = [torch.full((8, 1001), 3.0, dtype=BF16, device="cuda") for _ in range(2)]
