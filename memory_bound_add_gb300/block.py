@@ -110,7 +110,7 @@ def _tensor(t, name, dtype, n, index):
 
 
 def _rows_tensor(t, name):
-    """rows and H of a [..., H] activation."""
+    """rows and H of a contiguous [..., H] activation."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not t.is_cuda:
@@ -119,6 +119,8 @@ def _rows_tensor(t, name):
         raise ValueError(f"unsupported dtype {t.dtype}")
     if not t.dim() or t.shape[-1] < 1:
         raise ValueError(f"{name} must have a last dimension (the hidden one) of at least 1")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
     H = t.shape[-1]
     return t.numel() // H, H
 
@@ -197,11 +199,11 @@ def _addresses(ts):
 
 def _forward(s, f, x, outs, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta, residual_scale,
              block_scale, eps):
-    """outs: the addresses of h, y and the statistics, checked."""
+    """f, and outs, the addresses of h, y and the statistics, are checked."""
     dt, dev, n = f.dtype, f.get_device(), rows * H
     gp, gk, gs, rpg = (None, GATE_NONE, 0, 0) if gate is None else _gate_args(gate, f)
     rc = (_lib or lib()).block_norm_fwd(
-        _tensor(f, "f", dt, n, dev), _tensor(x, "x", dt, n, dev), _norm_kind(post, "post"),
+        f.data_ptr(), _tensor(x, "x", dt, n, dev), _norm_kind(post, "post"),
         None if post_gamma is None else _tensor(post_gamma, "post_gamma", _F32, H, dev),
         None if post_beta is None else _tensor(post_beta, "post_beta", _F32, H, dev),
         gp, gk, gs, rpg, residual_scale, block_scale, _norm_kind(pre, "pre"),

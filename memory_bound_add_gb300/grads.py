@@ -14,6 +14,7 @@ fill their memory without gaps or repeats, in any order of dimensions.
 from __future__ import annotations
 
 import ctypes
+import functools
 
 import torch
 
@@ -56,6 +57,10 @@ def grad_norm_workspace_size(count: int) -> int:
     return n
 
 
+# a number that the count alone decides
+_workspace_size = functools.lru_cache(maxsize=256)(grad_norm_workspace_size)
+
+
 def _dense(t) -> bool:
     """Whether t's elements fill their memory without gaps or repeats."""
     want = 1
@@ -68,10 +73,10 @@ def _dense(t) -> bool:
 
 def _lists(ts, name):
     """(pointers, sizes, dtypes) as ctypes arrays, and the device's index."""
-    for t in ts:
-        if not isinstance(t, _Tensor):
-            raise TypeError(f"{name} must hold torch.Tensors, got {type(t).__name__}")
-    devices = set(map(_Tensor.get_device, ts))
+    try:
+        devices = set(map(_Tensor.get_device, ts))
+    except TypeError:
+        raise TypeError(f"{name} must hold torch.Tensors alone") from None
     if len(devices) != 1 or -1 in devices:
         raise ValueError(f"{name} must be CUDA tensors of one device")
     if not all(map(_Tensor.is_contiguous, ts)):
@@ -105,7 +110,7 @@ def grad_norm(grads, scale: float = 1.0, stream=None):
 
     def call(s):
         norm = torch.empty((), dtype=torch.float32, device=device)
-        size = grad_norm_workspace_size(count)
+        size = _workspace_size(count)
         ws = torch.empty(size, dtype=torch.uint8, device=device)
         out.append(norm)
         return lib().grad_norm(p, n, d, count, scale, norm.data_ptr(), ws.data_ptr(), size, s)
@@ -150,14 +155,17 @@ def clip_grads(grads, max_norm: float, out=None, scale: float = 1.0, norm=None, 
             ret.append(norm)
             return lib().grad_clip(p, op, n, d, od, count, scale, max_norm, _norm_tensor(norm, device), s)
         ret.append(torch.empty((), dtype=torch.float32, device=device))
-        size = grad_norm_workspace_size(count)
+        size = _workspace_size(count)
         ws = torch.empty(size, dtype=torch.uint8, device=device)
         return lib().grad_norm_clip(p, op, n, d, od, count, scale, max_norm, ret[0].data_ptr(), ws.data_ptr(), size,
                                     s)
 
     _check(on_stream(device, stream, call), "clip_grads")
-    # autograd has to see that these tensors changed
-    torch.autograd.graph.increment_version([t for t in written if not t.is_inference()])
+    # autograd has to see that these tensors changed; inference tensors have
+    # no versions
+    if any(map(_Tensor.is_inference, written)):
+        written = [t for t in written if not t.is_inference()]
+    torch.autograd.graph.increment_version(written)
     return ret[0]
 
 
