@@ -230,6 +230,8 @@ struct Ring {
         const int n = min(max(bytes - k * (cs.kStep * S), 0), 16);
         const int64_t o = off + k * (cs.kStep * S);
         if (k == 0 && o < 0) {
+          // zeros first: the row may end within this granule
+          asm volatile("st.shared.v4.u32 [%0], {%1, %1, %1, %1};" ::"r"(at(slot, I, 0)), "r"(0) : "memory");
 #pragma unroll
           for (int b = 0; b < 16; b += S)
             if (b >= s && b < n && ADDLN_IN(site, o + b, S, extent)) {

@@ -762,3 +762,42 @@ def test_means_near_zero_keep_their_digits(post, pre):
     got, w, v = (st[0], want[0], f.double()) if post else (st[2], want[2], h)
     rms = ((got.cpu().double() - w.reshape(-1)) ** 2).mean().sqrt()
     assert float(rms) <= 2.0 ** -24 * float(v.std()) * 0.5
+
+
+def fill_shared_memory_with_nan():
+    """A backward over rows of NaN, whose staged rows stay behind in the
+    shared memory of every SM."""
+    bad = torch.full((2048, 4096), float("nan"), dtype=BF16, device="cuda")
+    one, r = torch.ones(4096, device="cuda"), torch.ones(2048, device="cuda")
+    mba.block_norm_backward(bad, bad, bad, bad, (None, r, None, r), post="rms", post_gamma=one, pre="rms",
+                            pre_gamma=one)
+
+
+@pytest.mark.parametrize("dtype,H", [(F32, 1), (F32, 2), (F32, 3)] + [(t, h) for t in (F16, BF16) for h in range(1, 8)])
+@pytest.mark.parametrize("post,pre", [("rms", "rms"), ("layer", "layer"), (None, "rms")])
+def test_shortest_rows_off_the_borders(dtype, H, post, pre):
+    # the first row of a buffer ends within its first 16 bytes: what the rest of
+    # them held in shared memory before must not matter
+    rows = 3
+    for k in range(1, 16 // torch.empty((), dtype=dtype).element_size()):
+        for gate in (None, "channel", (rows, H), (1, H)):
+            f, x, p = make((rows, H), dtype, post, pre, gate, beta=True, seed=100 * H + k)
+            wh, wy, wst, eh, ey = forward(f, x, p, post, pre, 1.0, 1.0, 1e-5)
+            q = {n: at_offset(v, k)[0] if n == "gate" and v.dim() > 1 else v.cuda() for n, v in p.items()}
+            fc, xc = at_offset(f, k)[0], at_offset(x, k)[0]
+            what = f"offset {k} gate {gate}"
+            fill_shared_memory_with_nan()
+            h, y, _ = mba.block_norm(fc, xc, post=post, pre=pre, **q)
+            assert_within(h, wh, eh, what + " h")
+            assert_within(y, wy, ey, what + " y")
+            g = torch.Generator().manual_seed(k)
+            dy, dh = torch.randn(rows, H, generator=g).to(dtype), torch.randn(rows, H, generator=g).to(dtype)
+            h0, st = wh.to(dtype), [None if t is None else t.reshape(-1).float() for t in wst]
+            want, err = backward(dy, dh, f, h0, st, p, post, pre, 1.0, 1.0)
+            args = [at_offset(t, k)[0] for t in (dy, dh)] + [fc, at_offset(h0, k)[0]]
+            fill_shared_memory_with_nan()
+            got = mba.block_norm_backward(*args, tuple(None if t is None else t.cuda() for t in st), post=post,
+                                          pre=pre, **q)
+            for n, v in got._asdict().items():
+                if v is not None:
+                    assert_within(v, want[n].reshape(v.shape), err[n].reshape(v.shape), f"{what} {n}")
