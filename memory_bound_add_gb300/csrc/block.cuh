@@ -309,6 +309,16 @@ struct Kept {
   }
 };
 
+// A CTA of a cluster may write into a peer's shared memory only once the peer
+// has started: every thread arrives when it begins, and waits before its first
+// exchange, behind the row's copies and the parameters, which take longer.
+__device__ __forceinline__ void cluster_started() {
+  asm volatile("barrier.cluster.arrive.relaxed;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait_started() {
+  asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
 // --------------------------------------------------------- row reductions
 // Every warp publishes one float4; after exchange() every thread of the
 // walker may read all of them, in the same order.  Two buffers in turn: a

@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(bwd_threads(DT, FULL, GR, SH)) __maxnreg__((bw
   constexpr int kStepBytes = Cols<VE, NV>::kStep * S;
   using R = Ring<DT, NV, NT, SH>;
   extern __shared__ __align__(128) unsigned char smem[];
+  if (p.w.C > 1) cluster_started();
   const int T = p.w.cta_warps * 32;
   const int side = p.w.rows_per_cta > 1 ? threadIdx.x / T : 0, tid = threadIdx.x - side * T;
   const int rank = p.w.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.w.C);
@@ -290,6 +291,7 @@ __global__ void __launch_bounds__(bwd_threads(DT, FULL, GR, SH)) __maxnreg__((bw
     if constexpr (FULL && GR) kept.put(2, k, b);
   }
   stats(r0);
+  if (p.w.C > 1) cluster_wait_started();
 
   float2 sg[P], s1[P], sb[FULL ? P : 1], s0[FULL ? P : 1], sd[GR ? P : 1];
 #pragma unroll

@@ -134,6 +134,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, NV, LN,
   constexpr int kStepBytes = Cols<VE, NV>::kStep * S;
   using R = Ring<DT, NV, NT, SH>;
   extern __shared__ __align__(128) unsigned char smem[];
+  if (p.w.C > 1) cluster_started();
   const int slots = p.slots;
   const int lane = threadIdx.x & 31;
   const int side = (threadIdx.x >> 5) / p.w.cta_warps, warp = (threadIdx.x >> 5) - side * p.w.cta_warps;
@@ -188,6 +189,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, NV, LN,
     for (int k = 0; k < NV; ++k) par.load(p, cs.col(k), k);
   }
   if constexpr (!kRegs) __syncthreads();
+  if (p.w.C > 1) cluster_wait_started();
 
   for (int slot = 0; row < p.rows; row += stride, slot = slot + 1 == slots ? 0 : slot + 1) {
     if (slots == 1) ring.template wait<0>(); else ring.template wait<1>();

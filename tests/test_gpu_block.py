@@ -801,3 +801,27 @@ def test_shortest_rows_off_the_borders(dtype, H, post, pre):
             for n, v in got._asdict().items():
                 if v is not None:
                     assert_within(v, want[n].reshape(v.shape), err[n].reshape(v.shape), f"{what} {n}")
+
+
+@pytest.mark.parametrize("dtype,H", [(F32, 16384), (F16, 32760), (BF16, 32768), (BF16, 20001)])
+def test_rows_of_a_cluster_call_after_call(dtype, H):
+    # rows that several CTAs share, in short calls one close upon another and on
+    # two streams at once: the CTAs of a cluster write into each other's shared
+    # memory from the first row on
+    f, x, p = make((3, H), dtype, "layer", "layer", "channel", beta=True, seed=H)
+    q, fc, xc = cuda(p), f.cuda(), x.cuda()
+    kw = dict(post="layer", pre="layer", **q)
+    h, y, st = check_fwd(f, x, p, "layer", "layer", what=f"{H}")
+    check_bwd(f, x, p, "layer", "layer", what=f"{H}")
+    want = mba.block_norm_backward(y, h, fc, h, st, **kw)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = []
+    for i in range(20):
+        s = streams[i % 2]
+        got.append((mba.block_norm(fc, xc, want_stats=True, stream=s, **kw)[:2],
+                    mba.block_norm_backward(y, h, fc, h, st, stream=s, **kw)))
+    torch.cuda.synchronize()
+    for (h2, y2), g in got:
+        assert torch.equal(h, h2) and torch.equal(y, y2)
+        assert all(u is None or torch.equal(u, v) for u, v in zip(want, g))
