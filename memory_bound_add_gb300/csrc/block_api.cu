@@ -18,7 +18,9 @@ bool valid_norm(int k) { return k >= ADDLN_NORM_NONE && k <= ADDLN_NORM_LAYER; }
 uintptr_t bits(const void* p) { return reinterpret_cast<uintptr_t>(p); }
 
 // Dtype, shape, kinds and scales; *gate_rows: rows of a per-row gate.
-int check_spec(int post, int pre, int gate_kind, int64_t gate_stride, int64_t rows_per_gate, float a,
+// *rows_per_gate is cut to the rows there are, which changes no row's gate row:
+// the kernels' 32-bit arithmetic of gate rows holds wherever rows fits 32 bits.
+int check_spec(int post, int pre, int gate_kind, int64_t gate_stride, int64_t* rows_per_gate, float a,
                float s, int64_t rows, int64_t H, int dtype, int64_t* gate_rows) {
   if (!valid_dtype(dtype)) return ADDLN_ERR_DTYPE;
   if (rows < 0 || H <= 0 || H > max_hidden(dtype) || rows > INT64_MAX / (H * 4)) return ADDLN_ERR_SHAPE;
@@ -27,8 +29,9 @@ int check_spec(int post, int pre, int gate_kind, int64_t gate_stride, int64_t ro
   if (!isfinite(a) || !isfinite(s)) return ADDLN_ERR_SCALE;
   *gate_rows = 0;
   if (gate_kind == ADDLN_GATE_ROWS) {
-    if (rows_per_gate < 1 || gate_stride < H) return ADDLN_ERR_SHAPE;
-    *gate_rows = rows / rows_per_gate + (rows % rows_per_gate != 0);
+    if (*rows_per_gate < 1 || gate_stride < H) return ADDLN_ERR_SHAPE;
+    if (rows > 0 && *rows_per_gate > rows) *rows_per_gate = rows;
+    *gate_rows = rows / *rows_per_gate + (rows % *rows_per_gate != 0);
     if (*gate_rows > 0 && gate_stride > INT64_MAX / 8 / *gate_rows) return ADDLN_ERR_SHAPE;
   }
   return ADDLN_OK;
@@ -61,7 +64,7 @@ int block_norm_fwd(const void* f, const void* x, int post, const float* post_gam
                    float* pre_mean, float* pre_rstd, int64_t rows, int64_t H, float eps, int dtype,
                    void* stream) try {
   int64_t gate_rows;
-  int rc = check_spec(post, pre, gate_kind, gate_stride, rows_per_gate, residual_scale, block_scale, rows, H,
+  int rc = check_spec(post, pre, gate_kind, gate_stride, &rows_per_gate, residual_scale, block_scale, rows, H,
                       dtype, &gate_rows);
   if (rc != ADDLN_OK) return rc;
   if (!(eps >= 0.0f) || isinf(eps)) return ADDLN_ERR_EPS;
@@ -117,7 +120,7 @@ int block_norm_fwd(const void* f, const void* x, int post, const float* post_gam
 int64_t block_norm_bwd_workspace_size(int64_t rows, int64_t H, int dtype, int gate_kind,
                                       int64_t rows_per_gate) try {
   int64_t gate_rows;
-  int rc = check_spec(ADDLN_NORM_NONE, ADDLN_NORM_NONE, gate_kind, H, rows_per_gate, 1.f, 1.f, rows, H, dtype,
+  int rc = check_spec(ADDLN_NORM_NONE, ADDLN_NORM_NONE, gate_kind, H, &rows_per_gate, 1.f, 1.f, rows, H, dtype,
                       &gate_rows);
   if (rc != ADDLN_OK) return rc;
   if (rows == 0) return 0;
@@ -148,7 +151,7 @@ int block_norm_bwd(const void* dy, const void* dh, const void* f, const void* h,
                    int64_t rows, int64_t H, int dtype, void* workspace, int64_t workspace_bytes,
                    void* stream) try {
   int64_t gate_rows;
-  int rc = check_spec(post, pre, gate_kind, gate_stride, rows_per_gate, residual_scale, block_scale, rows, H,
+  int rc = check_spec(post, pre, gate_kind, gate_stride, &rows_per_gate, residual_scale, block_scale, rows, H,
                       dtype, &gate_rows);
   if (rc != ADDLN_OK) return rc;
   const bool has_post = post != ADDLN_NORM_NONE, has_pre = pre != ADDLN_NORM_NONE;

@@ -825,3 +825,35 @@ def test_rows_of_a_cluster_call_after_call(dtype, H):
     for (h2, y2), g in got:
         assert torch.equal(h, h2) and torch.equal(y, y2)
         assert all(u is None or torch.equal(u, v) for u, v in zip(want, g))
+
+
+@pytest.mark.parametrize("rpg", [9, 1 << 31, (1 << 32) - 1, 1 << 32, (1 << 32) + 1, 1 << 40, (1 << 63) - 1])
+@pytest.mark.parametrize("rows,H,dtype", [(8, 64, F32), (8, 1001, BF16), (1, 96, F16)])
+def test_a_gate_row_for_more_rows_than_there_are(rpg, rows, H, dtype):
+    # the library's own entry points: one gate row for all rows, whatever the
+    # number of rows that it could serve
+    lib, code = block.lib(), block.DTYPE_CODE[dtype]
+    f, x, p = make((rows, H), dtype, "rms", "rms", (1, H), seed=H)
+    q, fc, xc = cuda(p), f.cuda(), x.cuda()
+    kw = dict(post="rms", pre="rms", **q)
+    h, y, st = mba.block_norm(fc, xc, want_stats=True, **kw)
+    want = mba.block_norm_backward(y, h, fc, h, st, **kw)
+    h2, y2 = torch.empty_like(h), torch.empty_like(y)
+    stream = torch.cuda.current_stream().cuda_stream
+    pg, ng, gate = (q[k].data_ptr() for k in ("post_gamma", "pre_gamma", "gate"))
+    assert lib.block_norm_fwd(fc.data_ptr(), xc.data_ptr(), block.NORM_RMS, pg, None, gate, block.GATE_ROWS, H, rpg, 1.0,
+                              1.0, block.NORM_RMS, ng, None, h2.data_ptr(), y2.data_ptr(), None, None, None, None, rows,
+                              H, 1e-5, code, stream) == 0
+    assert torch.equal(h, h2) and torch.equal(y, y2)
+    size = mba.block_norm_bwd_workspace_size(rows, H, code, block.GATE_ROWS, rpg)
+    assert size == mba.block_norm_bwd_workspace_size(rows, H, code, block.GATE_ROWS, rows)
+    ws = torch.empty(size, dtype=torch.uint8, device="cuda")
+    got = {k: torch.empty_like(getattr(want, k)) for k in ("df", "dx", "dgate", "dpost_gamma", "dpre_gamma")}
+    at = {k: v.data_ptr() for k, v in got.items()}
+    assert lib.block_norm_bwd(y.data_ptr(), h.data_ptr(), fc.data_ptr(), h.data_ptr(), block.NORM_RMS, pg, None, None,
+                              st[1].data_ptr(), gate, block.GATE_ROWS, H, rpg, 1.0, 1.0, block.NORM_RMS, ng, None,
+                              st[3].data_ptr(), at["df"], at["dx"], at["dpost_gamma"], None, at["dgate"],
+                              at["dpre_gamma"], None, rows, H, code, ws.data_ptr(), size, stream) == 0
+    torch.cuda.synchronize()
+    for k, v in got.items():
+        assert torch.equal(v, getattr(want, k)), k
