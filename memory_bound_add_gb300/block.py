@@ -7,8 +7,10 @@ the residual stream x,
     n = post(f);  h = residual_scale * x + block_scale * gate * n;  y = pre(h)
 
 ``post`` and ``pre`` are ``None``, ``"rms"`` or ``"layer"``.  f and x are
-contiguous ``[..., H]`` CUDA tensors of one dtype (fp32, fp16 or bf16); the
-norms' gamma and beta are fp32 ``[H]``.  ``gate`` is one of
+contiguous ``[..., H]`` CUDA tensors of one dtype (fp32, fp16 or bf16); what
+stands beside f row for row (x, h, y and the gradients) has f's shape, but that
+leading sizes may be joined (``[B * S, H]`` beside ``[B, S, H]``).  The norms'
+gamma and beta are fp32 ``[H]``.  ``gate`` is one of
 
     None                 no gate
     fp32 ``[H]``         one value a column (a learnt layer scale)
@@ -22,6 +24,8 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import itertools
+import operator
 from typing import NamedTuple, Optional
 
 import torch
@@ -107,6 +111,24 @@ def _tensor(t, name, dtype, n, index):
     if t.get_device() != index:
         raise ValueError(f"{name} must be on cuda:{index}, got {t.device}")
     raise ValueError(f"{name} must be contiguous")
+
+
+def _same_rows(a, b) -> bool:
+    """Whether these [..., H] shapes are the same rows in the same order: equal
+    but for leading sizes that one of them has joined."""
+    cuts = lambda s: set(itertools.accumulate(s[:-1], operator.mul)) - {1}  # noqa: E731
+    return len(a) > 0 and len(b) > 0 and a[-1] == b[-1] and (cuts(a) <= cuts(b) or cuts(b) <= cuts(a))
+
+
+def _beside(t, name, like, index):
+    """_tensor for what stands row for row beside the activation `like`."""
+    if isinstance(t, torch.Tensor) and t.shape == like.shape and t.dtype is like.dtype and t.get_device() == index \
+            and t.is_contiguous():
+        return t.data_ptr()
+    at = _tensor(t, name, like.dtype, like.numel(), index)
+    if t is not None and not _same_rows(t.shape, like.shape):
+        raise ValueError(f"{name} of shape {tuple(t.shape)} beside {tuple(like.shape)}")
+    return at
 
 
 def _rows_tensor(t, name):
@@ -200,10 +222,10 @@ def _addresses(ts):
 def _forward(s, f, x, outs, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta, residual_scale,
              block_scale, eps):
     """f, and outs, the addresses of h, y and the statistics, are checked."""
-    dt, dev, n = f.dtype, f.get_device(), rows * H
+    dt, dev = f.dtype, f.get_device()
     gp, gk, gs, rpg = (None, GATE_NONE, 0, 0) if gate is None else _gate_args(gate, f)
     rc = (_lib or lib()).block_norm_fwd(
-        f.data_ptr(), _tensor(x, "x", dt, n, dev), _norm_kind(post, "post"),
+        f.data_ptr(), _beside(x, "x", f, dev), _norm_kind(post, "post"),
         None if post_gamma is None else _tensor(post_gamma, "post_gamma", _F32, H, dev),
         None if post_beta is None else _tensor(post_beta, "post_beta", _F32, H, dev),
         gp, gk, gs, rpg, residual_scale, block_scale, _norm_kind(pre, "pre"),
@@ -221,9 +243,9 @@ def block_norm_fwd(f, x, h, y=None, stats=None, *, post=None, post_gamma=None, p
     may be f or x itself) and, with stats = (post_mean, post_rstd, pre_mean,
     pre_rstd), into [rows] fp32 tensors (None: not written)."""
     rows, H = _rows_tensor(f, "f")
-    dt, dev, n = f.dtype, f.get_device(), rows * H
+    dev = f.get_device()
     pm, pr, nm, nr = stats or _NO_STATS
-    outs = (_tensor(h, "h", dt, n, dev), _tensor(y, "y", dt, n, dev), _tensor(pm, "post_mean", _F32, rows, dev),
+    outs = (_beside(h, "h", f, dev), _beside(y, "y", f, dev), _tensor(pm, "post_mean", _F32, rows, dev),
             _tensor(pr, "post_rstd", _F32, rows, dev), _tensor(nm, "pre_mean", _F32, rows, dev),
             _tensor(nr, "pre_rstd", _F32, rows, dev))
     on_stream(f.device, stream, lambda s: _forward(
@@ -294,8 +316,8 @@ def _given(dy, dh):
 def _backward(s, some, rows, H, dy, dh, f, h, stats, outs, post, post_gamma, post_beta, gate_args, pre, pre_gamma,
               residual_scale, block_scale, workspace):
     """outs: the addresses of df, dx and the parameters' gradients, checked."""
-    dt, dev, n = some.dtype, some.get_device(), rows * H
-    code = DTYPE_CODE[dt]
+    dev = some.get_device()
+    code = DTYPE_CODE[some.dtype]
     pm, pr, nm, nr = stats or _NO_STATS
     gp, gk, gs, rpg = gate_args
     if workspace is None:
@@ -306,8 +328,8 @@ def _backward(s, some, rows, H, dy, dh, f, h, stats, outs, post, post_gamma, pos
     else:
         size = workspace.numel() * workspace.element_size()
     rc = (_lib or lib()).block_norm_bwd(
-        None if dy is None else _tensor(dy, "dy", dt, n, dev), None if dh is None else _tensor(dh, "dh", dt, n, dev),
-        None if f is None else _tensor(f, "f", dt, n, dev), None if h is None else _tensor(h, "h", dt, n, dev),
+        None if dy is None else _beside(dy, "dy", some, dev), None if dh is None else _beside(dh, "dh", some, dev),
+        None if f is None else _beside(f, "f", some, dev), None if h is None else _beside(h, "h", some, dev),
         _norm_kind(post, "post"), None if post_gamma is None else _tensor(post_gamma, "post_gamma", _F32, H, dev),
         None if post_beta is None else _tensor(post_beta, "post_beta", _F32, H, dev),
         None if pm is None else _tensor(pm, "post_mean", _F32, rows, dev),
@@ -331,15 +353,17 @@ def block_norm_bwd(dy, dh, f, h, stats, df, dx, *, post=None, post_gamma=None, p
     block_norm_bwd_workspace_size(...) bytes, reusable call after call
     (allocated here when None)."""
     some, rows, H = _given(dy, dh)
-    dt, dev, n = some.dtype, some.get_device(), rows * H
+    dt, dev = some.dtype, some.get_device()
     gate_args = _gate_args(gate, some)
     if dgate is not None and gate is None:
         raise ValueError("dgate without a gate")
-    outs = (_tensor(df, "df", dt, n, dev), _tensor(dx, "dx", dt, n, dev),
+    outs = (_beside(df, "df", some, dev), _beside(dx, "dx", some, dev),
             _tensor(dpost_gamma, "dpost_gamma", _F32, H, dev), _tensor(dpost_beta, "dpost_beta", _F32, H, dev),
             None if dgate is None else _tensor(dgate, "dgate", _F32 if gate_args[1] == GATE_CHANNEL else dt,
                                                gate.numel(), dev),
             _tensor(dpre_gamma, "dpre_gamma", _F32, H, dev), _tensor(dpre_beta, "dpre_beta", _F32, H, dev))
+    if dgate is not None and dgate.shape != gate.shape and not _same_rows(dgate.shape, gate.shape):
+        raise ValueError(f"dgate of shape {tuple(dgate.shape)} beside a gate of {tuple(gate.shape)}")
 
     def call(s):
         if rows == 0 and dgate is not None:

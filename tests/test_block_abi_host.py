@@ -129,3 +129,13 @@ def test_gate_layouts():
                        (e(4, 3, 32).transpose(0, 1), (3, 4, 32))]:
         with pytest.raises(ValueError):
             gate_layout(bad, shape)
+
+
+def test_the_same_rows():
+    from memory_bound_add_gb300.block import _same_rows
+    for a, b in [((4, 6, 32), (24, 32)), ((4, 6, 32), (24, 1, 32)), ((1, 4, 6, 32), (4, 2, 3, 32)), ((32,), (1, 32)),
+                 ((5, 1, 32), (5, 32)), ((2, 3, 4, 8), (6, 4, 8)), ((7, 32), (7, 32)), ((0, 32), (0, 32))]:
+        assert _same_rows(a, b) and _same_rows(b, a)
+    for a, b in [((4, 6, 32), (6, 4, 32)), ((4, 6, 32), (2, 12, 32)), ((4, 64), (8, 32)), ((2, 3, 4, 8), (3, 2, 4, 8)),
+                 ((), (1, 1)), ((2, 16), (32,))]:
+        assert not _same_rows(a, b) and not _same_rows(b, a)

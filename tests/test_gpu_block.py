@@ -857,3 +857,39 @@ def test_a_gate_row_for_more_rows_than_there_are(rpg, rows, H, dtype):
     torch.cuda.synchronize()
     for k, v in got.items():
         assert torch.equal(v, getattr(want, k)), k
+
+
+def test_refusals_of_other_shapes():
+    # as many elements, but rows that are not each other's
+    kw = dict(post="rms", pre="rms", post_gamma=torch.ones(32, device="cuda"), pre_gamma=torch.ones(32, device="cuda"))
+    f = torch.randn(4, 6, 32, device="cuda")
+    other = [f.transpose(0, 1).contiguous(), f.view(2, 12, 32), f.view(3, 8, 32), f.view(12, 64), f.view(4, 3, 64)]
+    h, y, st = mba.block_norm(f, f, want_stats=True, **kw)
+    new = lambda: torch.empty_like(f)  # noqa: E731
+    for t in other:
+        for call in (lambda: mba.block_norm(f, t, **kw), lambda: mba.block_norm_fwd(f, t, new(), new(), **kw),
+                     lambda: mba.block_norm_fwd(f, f, torch.empty_like(t), new(), **kw),
+                     lambda: mba.block_norm_fwd(f, f, new(), torch.empty_like(t), **kw),
+                     lambda: mba.block_norm_backward(y, t, f, h, st, **kw),
+                     lambda: mba.block_norm_backward(y, None, t, h, st, **kw),
+                     lambda: mba.block_norm_backward(y, None, f, t, st, **kw),
+                     lambda: mba.block_norm_bwd(y, h, f, h, st, torch.empty_like(t), new(), **kw),
+                     lambda: mba.block_norm_bwd(y, h, f, h, st, new(), torch.empty_like(t), **kw)):
+            with pytest.raises(ValueError):
+                call()
+    gate = torch.randn(4, 1, 32, device="cuda")
+    for bad in (torch.empty(8, 16, device="cuda"), torch.empty(2, 64, device="cuda"), torch.empty(128, device="cuda")):
+        with pytest.raises(ValueError):
+            mba.block_norm_bwd(y, h, f, h, st, new(), new(), gate=gate, dgate=bad, **kw)
+    # the same rows with leading sizes joined or split are no other rows
+    for shape in ((24, 1, 32), (4, 2, 3, 32), (1, 4, 6, 32)):
+        h2, y2, _ = mba.block_norm(f, f.view(shape), **kw)
+        assert torch.equal(h2, h) and torch.equal(y2, y)
+    flat = lambda t: t.view(24, 32)  # noqa: E731
+    h2, y2, _ = mba.block_norm(f, flat(f), **kw)
+    h3, y3, _ = mba.block_norm(flat(f), f, **kw)
+    assert torch.equal(h2, h) and torch.equal(h3, flat(h)) and torch.equal(y2, y) and torch.equal(y3, flat(y))
+    want = mba.block_norm_backward(y, h, f, h, st, gate=gate, **kw)
+    df, dx, dg = torch.empty(24, 32, device="cuda"), new(), torch.empty(4, 32, device="cuda")
+    mba.block_norm_bwd(y, flat(h), flat(f), h, st, df, dx, gate=gate, dgate=dg, **kw)
+    assert torch.equal(df, flat(want.df)) and torch.equal(dx, want.dx) and torch.equal(dg, want.dgate.view(4, 32))
