@@ -10,7 +10,8 @@
  *     out    = g factor                         rounded once to out's dtype
  * scale is 1 / loss scale (1: none).  A NaN among the gradients makes norm
  * and every out NaN, an infinite norm a factor of 0 (and NaN where g is
- * infinite), as the formulas say.
+ * infinite), as the formulas say.  An infinite max_norm is no limit: the
+ * factor is scale whatever the norm, unless that is NaN.
  *
  * Arrays of pointers, sizes and dtypes are HOST arrays of count entries; they
  * are read before the call returns (a captured call keeps their values).

@@ -376,7 +376,8 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) k_grad_clip(const __grid
   } else {
     norm = __ldcg(a.norm);
   }
-  const float coef = a.max_norm / (norm + 1e-6f);
+  // without a limit nothing is scaled down, an infinite norm no more than another
+  const float coef = isinf(a.max_norm) && !isnan(norm) ? 1.f : a.max_norm / (norm + 1e-6f);
   const float factor = a.scale * (coef > 1.f ? 1.f : coef);  // a NaN stays
   // from the last chunk to the first; in place with factor 1 there is
   // nothing to write

@@ -126,7 +126,8 @@ def clip_grads(grads, max_norm: float, out=None, scale: float = 1.0, norm=None, 
     out: one tensor for each gradient, of its shape and strides, fp32 or the
     gradient's dtype (None: in place).  scale: 1 / loss scale.  norm: the norm
     where it is on the device already (one fp32 element, e.g. joined over
-    several GPUs); otherwise it is computed here.  max_norm may be infinite.
+    several GPUs); otherwise it is computed here.  max_norm may be infinite:
+    no limit, the factor is `scale` even where the norm is infinite too.
     """
     grads = list(grads)
     if not grads:

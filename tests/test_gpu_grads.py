@@ -329,3 +329,25 @@ def test_training_step(post, pre):
     assert abs(float(norm) - total) <= 3 * 3 * 128 * U * total
     check(before, [p.grad for p in params], norm, 0.05)
     assert float(norm) > 0.05
+
+
+def test_an_infinite_norm_without_a_limit():
+    # max_norm infinite: no limit, so what is finite is unscaled and infinities stay
+    gs = draw([1000, 70], F32, seed=11)
+    gs[0][3], gs[0][5] = math.inf, -math.inf
+    for scale in (1.0, 0.25):
+        want = [g * scale for g in gs]
+        mine = [g.clone() for g in gs]
+        norm = mba.clip_grads(mine, math.inf, scale=scale)
+        assert float(norm) == math.inf and all(torch.equal(a, b) for a, b in zip(mine, want))
+        outs = [torch.empty_like(g) for g in gs]
+        mba.clip_grads(gs, math.inf, out=outs, scale=scale, norm=norm)
+        assert all(torch.equal(a, b) for a, b in zip(outs, want))
+    # a norm that leaves fp32 without an infinity among the gradients
+    big = [torch.full((5000,), 2.0 ** 127, dtype=BF16, device="cuda")]
+    mine = [big[0].clone()]
+    assert float(mba.clip_grads(mine, math.inf)) == math.inf and torch.equal(mine[0], big[0])
+    # a NaN stays one
+    gs[1][0] = math.nan
+    mba.clip_grads(gs, math.inf)
+    assert all(bool(torch.isnan(g).all()) for g in gs)
