@@ -164,9 +164,11 @@ __device__ __forceinline__ float value_of(uint32_t raw) {
 }
 
 // Sum of squares of a thread's share.  At most 33 elements, so fp32 keeps it
-// to a few roundings.  Where the sum leaves [1e-30, 1e30], squares may have
-// been lost to fp32's range: 0 is returned and *lost set, unless all elements
-// are zeros.
+// to a few roundings.  Where the sum is below 1e-30, squares may have been lost
+// to fp32's range, and 2^43 elements (the most a call takes) in shares of up to
+// 1e25 each stay below 1e38, within it: beyond either end 0 is returned and
+// *lost set, unless all elements are zeros.  (Sums of fp16 squares are below
+// 2e11; only a NaN or an infinity leaves the range.)
 template <int DT>
 __device__ __forceinline__ float squares(const Piece& p, bool* lost) {
   using IO = Io<DT>;
@@ -183,7 +185,7 @@ __device__ __forceinline__ float squares(const Piece& p, bool* lost) {
     any |= p.v[j].x | p.v[j].y | p.v[j].z | p.v[j].w;
   }
   const float s = (acc[0].x + acc[1].x) + (acc[0].y + acc[1].y);
-  if (DT == kF16 ? s <= 1e30f : s >= 1e-30f && s <= 1e30f) return s;
+  if (DT == kF16 ? s <= 1e25f : s >= 1e-30f && s <= 1e25f) return s;
   *lost = (any & (DT == kF32 ? 0x7fffffffu : 0x7fff7fffu)) != 0;
   return 0.f;
 }

@@ -351,3 +351,15 @@ def test_an_infinite_norm_without_a_limit():
     gs[1][0] = math.nan
     mba.clip_grads(gs, math.inf)
     assert all(bool(torch.isnan(g).all()) for g in gs)
+
+
+def test_many_large_squares():
+    # the squares' sum leaves fp32 although no thread's share of them does: 32
+    # squares of 1.7e14 are 9e29, and 1.25e10 of them 3.6e38
+    n = 12_500_000_000
+    if torch.cuda.mem_get_info()[0] < 2 * n + (4 << 30):
+        pytest.skip("needs 30 GB of device memory")
+    g = torch.full((n,), 1.7e14, dtype=BF16, device="cuda")
+    want = float(g[0]) * math.sqrt(n)
+    assert 32 * float(g[0]) ** 2 < 1e30 and want ** 2 > torch.finfo(F32).max
+    assert abs(float(mba.grad_norm([g])) - want) <= 12 * U * want
