@@ -204,6 +204,15 @@ def _gate_args(gate, x):
     return gate.data_ptr(), GATE_ROWS, stride, rpg
 
 
+def changed(ts):
+    """Autograd has to see that the tensors of this list were written, so that a
+    graph that saved one of them refuses to use it.  Inference tensors have no
+    versions."""
+    if any(map(torch.Tensor.is_inference, ts)):
+        ts = [t for t in ts if not t.is_inference()]
+    torch.autograd.graph.increment_version(ts)
+
+
 def _check(rc, where):
     if rc != binding.OK:
         raise AddLNError(rc, where)
@@ -251,6 +260,7 @@ def block_norm_fwd(f, x, h, y=None, stats=None, *, post=None, post_gamma=None, p
     on_stream(f.device, stream, lambda s: _forward(
         s, f, x, outs, rows, H, post, post_gamma, post_beta, gate, pre, pre_gamma, pre_beta, residual_scale,
         block_scale, eps))
+    changed([t for t in (h, y, pm, pr, nm, nr) if t is not None])
 
 
 def block_norm(f, x, *, post=None, post_gamma=None, post_beta=None, gate=None, pre="rms",
@@ -372,6 +382,7 @@ def block_norm_bwd(dy, dh, f, h, stats, df, dx, *, post=None, post_gamma=None, p
                   residual_scale, block_scale, workspace)
 
     on_stream(some.device, stream, call)
+    changed([t for t in (df, dx, dpost_gamma, dpost_beta, dgate, dpre_gamma, dpre_beta) if t is not None])
 
 
 def block_norm_backward(dy, dh, f, h, stats, *, post=None, post_gamma=None, post_beta=None, gate=None,

@@ -20,7 +20,7 @@ import torch
 
 from . import binding
 from .binding import DTYPE_CODE
-from .block import _check, on_stream
+from .block import _check, changed, on_stream
 
 # Every symbol include/addln_grad.h declares, with its ctypes signature.
 _P, _I64, _F, _I = ctypes.c_void_p, ctypes.c_int64, ctypes.c_float, ctypes.c_int
@@ -162,11 +162,7 @@ def clip_grads(grads, max_norm: float, out=None, scale: float = 1.0, norm=None, 
                                     s)
 
     _check(on_stream(device, stream, call), "clip_grads")
-    # autograd has to see that these tensors changed; inference tensors have
-    # no versions
-    if any(map(_Tensor.is_inference, written)):
-        written = [t for t in written if not t.is_inference()]
-    torch.autograd.graph.increment_version(written)
+    changed(written)
     return ret[0]
 
 

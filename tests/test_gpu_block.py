@@ -893,3 +893,37 @@ def test_refusals_of_other_shapes():
     df, dx, dg = torch.empty(24, 32, device="cuda"), new(), torch.empty(4, 32, device="cuda")
     mba.block_norm_bwd(y, flat(h), flat(f), h, st, df, dx, gate=gate, dgate=dg, **kw)
     assert torch.equal(df, flat(want.df)) and torch.equal(dx, want.dx) and torch.equal(dg, want.dgate.view(4, 32))
+
+
+def test_autograd_sees_what_is_written():
+    # every tensor that a call is given to write into has changed for autograd,
+    # so that a graph that saved it refuses to go on
+    f, x, p = make((4, 64), F32, "rms", "rms", "channel", seed=21)
+    q = cuda(p)
+    kw = dict(post="rms", pre="rms", **q)
+    new = lambda *s: torch.zeros(*(s or (4, 64)), device="cuda")  # noqa: E731
+    fc, xc = f.cuda(), x.cuda()
+    h, y, st = new(), new(), (None, new(4), None, new(4))
+    outs = [h, y, st[1], st[3]]
+    before = [t._version for t in outs]
+    mba.block_norm_fwd(fc, xc, h, y, st, **kw)
+    assert all(t._version > v for t, v in zip(outs, before))
+    g = dict(dpost_gamma=new(64), dgate=new(64), dpre_gamma=new(64))
+    outs = [new(), new(), *g.values()]
+    before = [t._version for t in outs]
+    mba.block_norm_bwd(y, h, fc, h, st, outs[0], outs[1], **g, **kw)
+    assert all(t._version > v for t, v in zip(outs, before))
+    # in place over a tensor that a graph has saved
+    a = x.cuda().requires_grad_(True)
+    b = a * 1.0
+    loss = (b * b).sum()
+    with torch.no_grad():
+        mba.block_norm_fwd(fc, b.detach(), b.detach(), y, **kw)
+    with pytest.raises(RuntimeError, match="modified by an inplace operation"):
+        loss.backward()
+    # tensors without versions are written all the same
+    with torch.inference_mode():
+        h2, y2 = new(), new()
+    mba.block_norm_fwd(fc, xc, h2, y2, **kw)
+    want = mba.block_norm(fc, xc, **kw)
+    assert torch.equal(h2, want[0]) and torch.equal(y2, want[1])
