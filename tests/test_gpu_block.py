@@ -927,3 +927,45 @@ def test_autograd_sees_what_is_written():
     mba.block_norm_fwd(fc, xc, h2, y2, **kw)
     want = mba.block_norm(fc, xc, **kw)
     assert torch.equal(h2, want[0]) and torch.equal(y2, want[1])
+
+
+def test_two_graphs_with_one_workspace_write_their_outputs():
+    # each replay by itself fills outputs that were NaN before
+    f, x, p = make((300, 768), F16, "rms", "rms", "channel", seed=6)
+    q, fc = cuda(p), f.cuda()
+    h, _, st = mba.block_norm(fc, x.cuda(), post="rms", pre="rms", want_stats=True, **q)
+    ws = torch.empty(mba.block_norm_bwd_workspace_size(300, 768, mba.FP16, 1), dtype=torch.uint8, device="cuda")
+    outs, graphs = [], []
+    for i in range(2):
+        dy = torch.randn_like(h)
+        t = [torch.empty_like(h), torch.empty_like(h)] + [torch.empty(768, device="cuda") for _ in range(3)]
+
+        def call(dy=dy, t=t):
+            mba.block_norm_bwd(dy, None, fc, h, st, t[0], t[1], post="rms", pre="rms", dpost_gamma=t[2], dgate=t[3],
+                               dpre_gamma=t[4], workspace=ws, **q)
+        call()
+        torch.cuda.synchronize()
+        want = [v.clone() for v in t]
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            call()
+        outs.append((t, want, dy))  # a graph does not keep its inputs alive
+        graphs.append(g)
+
+    def clear():
+        for t, _, _ in outs:
+            for v in t:
+                v.fill_(float("nan"))
+        ws.fill_(255)  # NaN patterns
+
+    for g, (t, want, _) in list(zip(graphs, outs)) * 2:
+        clear()
+        g.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(u, v) for u, v in zip(t, want))
+    clear()
+    for g in graphs + graphs[::-1]:
+        g.replay()
+    torch.cuda.synchronize()
+    for t, want, _ in outs:
+        assert all(torch.equal(u, v) for u, v in zip(t, want))
