@@ -51,6 +51,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_F32 = torch.float32
 
 
 def bind(handle):
@@ -194,7 +195,7 @@ def _gate_args(gate, x):
         return None, GATE_NONE, 0, 0
     if not isinstance(gate, torch.Tensor):
         raise TypeError("gate must be a torch.Tensor")
-    if gate.dim() == 1:
+    if gate.dim() == 1 and (x.dim() > 1 or gate.dtype is _F32):
         return _tensor(gate, "gate", torch.float32, x.shape[-1], x.get_device()), GATE_CHANNEL, 0, 0
     if gate.dtype != x.dtype:
         raise ValueError(f"a gate with rows must be {x.dtype}, got {gate.dtype}")
@@ -220,7 +221,6 @@ def _check(rc, where):
 
 # ------------------------------------------------------------------ forward
 _NO_STATS = (None, None, None, None)
-_F32 = torch.float32
 
 
 def _addresses(ts):

@@ -969,3 +969,27 @@ def test_two_graphs_with_one_workspace_write_their_outputs():
     torch.cuda.synchronize()
     for t, want, _ in outs:
         assert all(torch.equal(u, v) for u, v in zip(t, want))
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=["fp32", "fp16", "bf16"])
+def test_a_single_row_of_one_dimension(dtype):
+    # f, x and a gate of f's dtype, all [H]
+    f, x, p = make((200,), dtype, "rms", "layer", None, seed=3)
+    p["gate"] = torch.randn(200, generator=torch.Generator().manual_seed(4)).to(dtype)
+    wh, wy, wst, eh, ey = forward(f, x, p, "rms", "layer", 1.0, 1.0, 1e-5)
+    h, y, st = mba.block_norm(f.cuda(), x.cuda(), post="rms", pre="layer", want_stats=True, **cuda(p))
+    assert_within(h, wh, eh, "h")
+    assert_within(y, wy, ey, "y")
+    row = lambda t: t.cuda().view(1, 200)  # noqa: E731
+    q = dict(cuda(p), gate=row(p["gate"]))
+    dy = torch.randn(200, generator=torch.Generator().manual_seed(5)).to(dtype)
+    got = mba.block_norm_backward(dy.cuda(), None, f.cuda(), h, st, post="rms", pre="layer", **cuda(p))
+    want = mba.block_norm_backward(row(dy), None, row(f), h.view(1, 200), st, post="rms", pre="layer", **q)
+    assert got.dgate.dtype == dtype and got.dgate.shape == (200,)
+    for u, v in zip(got, want):
+        # the same sums of one row: a channel gate's go through fp32 columns
+        assert u is None or u.dtype is F32 and dtype is F32 or torch.equal(u.reshape(-1), v.reshape(-1))
+    leaf = p["gate"].cuda().requires_grad_(True)
+    _, y2 = mba.block_norm_train(f.cuda(), x.cuda(), post="rms", pre="layer", **dict(cuda(p), gate=leaf))
+    (y2.float() * dy.cuda().float()).sum().backward()
+    assert torch.equal(leaf.grad, got.dgate)
