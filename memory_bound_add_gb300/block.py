@@ -171,6 +171,8 @@ def gate_layout(gate, shape):
     rpg = 1
     for n in want[k:]:
         rpg *= n
+    if gate.numel() == 0:
+        return 0, H, max(rpg, 1)
     stride, rows = None, 1
     for n, st in zip(reversed(lead), reversed(gate.stride()[:-1])):
         if n == 1:

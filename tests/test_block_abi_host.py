@@ -139,3 +139,13 @@ def test_the_same_rows():
     for a, b in [((4, 6, 32), (6, 4, 32)), ((4, 6, 32), (2, 12, 32)), ((4, 64), (8, 32)), ((2, 3, 4, 8), (3, 2, 4, 8)),
                  ((), (1, 1)), ((2, 16), (32,))]:
         assert not _same_rows(a, b) and not _same_rows(b, a)
+
+
+def test_gate_layouts_of_no_rows():
+    # a gate of its own for every row, where there are none
+    from memory_bound_add_gb300.block import gate_layout
+    for shape in ((5, 0, 32), (0, 5, 32), (2, 0, 3, 32), (0, 32)):
+        assert gate_layout(torch.empty(shape), shape) == (0, 32, 1)
+    assert gate_layout(torch.empty(5, 0, 1, 32), (5, 0, 4, 32)) == (0, 32, 4)
+    with pytest.raises(ValueError):
+        gate_layout(torch.empty(5, 0, 31), (5, 0, 32))

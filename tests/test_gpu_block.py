@@ -993,3 +993,17 @@ def test_a_single_row_of_one_dimension(dtype):
     _, y2 = mba.block_norm_train(f.cuda(), x.cuda(), post="rms", pre="layer", **dict(cuda(p), gate=leaf))
     (y2.float() * dy.cuda().float()).sum().backward()
     assert torch.equal(leaf.grad, got.dgate)
+
+
+@pytest.mark.parametrize("shape", [(5, 0, 64), (0, 5, 64), (2, 0, 3, 64)])
+def test_gates_of_no_rows(shape):
+    # a gate of its own for every row, where there are none
+    p = cuda(make((1, 64), F16, "rms", "rms", seed=0)[2])
+    f = torch.empty(shape, dtype=F16, device="cuda", requires_grad=True)
+    gate = torch.empty(shape, dtype=F16, device="cuda", requires_grad=True)
+    q = {k: v.requires_grad_(True) for k, v in p.items()}
+    h, y = mba.block_norm_train(f, f.detach(), post="rms", pre="rms", gate=gate, **q)
+    (h.sum() + y.sum()).backward()
+    torch.cuda.synchronize()
+    assert h.shape == y.shape == f.grad.shape == gate.grad.shape == shape
+    assert all(not v.grad.any() for v in q.values())
