@@ -549,7 +549,7 @@ int run(const Lists& l, bool want_norm, bool scaled, float scale, float max_norm
 }
 
 int64_t workspace_size(int64_t count) {
-  if (count < 0 || count > INT64_MAX / 64) return ADDLN_ERR_SHAPE;
+  if (count < 0 || count > INT64_MAX / 1024) return ADDLN_ERR_SHAPE;
   // every launch but the last takes at least kFewTensors tensors
   return (count / kFewTensors + 1) * kMaxCtas * static_cast<int64_t>(sizeof(Partial));
 }

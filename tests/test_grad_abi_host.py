@@ -100,3 +100,13 @@ def test_dense():
         assert _dense(t)
     for t in (e(3, 4)[:, :2], e(4, 1).expand(4, 3), e(6)[::2], e(3, 8)[:, ::2]):
         assert not _dense(t)
+
+
+def test_workspace_size_of_absurd_counts(lib):
+    # 32 KB for each 120 tensors or part of them, or refused: never a size that
+    # does not fit 64 bits
+    from memory_bound_add_gb300 import binding as b
+    for e in range(10, 63):
+        for n in ((1 << e) - 1, 1 << e, 3 << (e - 1)):
+            size = lib.grad_norm_workspace_size(n)
+            assert size == (n // 120 + 1) * (1 << 15) or size == b.ERR_SHAPE and n >= 1 << 48, n
