@@ -81,13 +81,12 @@ struct BlockBwdArgs {
 
 // aligned: every row of every tensor in the I/O dtype begins on a 16-byte
 // border and ends on one.
-int launch_block_fwd(int dtype, bool aligned, bool layer_or_bias, const BlockFwdArgs& p, const LaunchCtx& c,
-                     const char** name);
+int launch_block_fwd(int dtype, bool aligned, bool layer_or_bias, const BlockFwdArgs& p, const LaunchCtx& c);
 // Bytes of workspace of a backward call, or a negative code.
 int64_t block_bwd_workspace_bytes(int dtype, bool aligned, bool full, int64_t rows, int H, int gate_kind,
                                   int64_t rows_per_gate, const DeviceInfo& dev);
 int launch_block_bwd(int dtype, bool aligned, bool full, BlockBwdArgs p, void* ws, int64_t ws_bytes,
-                     const LaunchCtx& c, const char** name);
+                     const LaunchCtx& c);
 
 int read_bounds_block_fwd(unsigned long long* word);
 int read_bounds_block_bwd(unsigned long long* word);

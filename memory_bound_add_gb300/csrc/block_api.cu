@@ -111,8 +111,7 @@ int block_norm_fwd(const void* f, const void* x, int post, const float* post_gam
                         post, pre, gate_kind, residual_scale, block_scale, eps,
                         static_cast<float>(1.0 / static_cast<double>(H))};
   const bool layer_or_bias = post == ADDLN_NORM_LAYER || pre == ADDLN_NORM_LAYER || post_beta || pre_beta;
-  const char* name = "none";
-  return addln::launch_block_fwd(dtype, aligned, layer_or_bias, p, c, &name);
+  return addln::launch_block_fwd(dtype, aligned, layer_or_bias, p, c);
 } catch (...) {
   return ADDLN_ERR_HOST_MEMORY;
 }
@@ -218,8 +217,7 @@ int block_norm_bwd(const void* dy, const void* dh, const void* f, const void* h,
                         pre, gate_kind, residual_scale, block_scale,
                         static_cast<float>(1.0 / static_cast<double>(H))};
   const bool full = post == ADDLN_NORM_LAYER || pre == ADDLN_NORM_LAYER || post_beta || dpost_beta || dpre_beta;
-  const char* name = "none";
-  return addln::launch_block_bwd(dtype, aligned, full, p, workspace, workspace_bytes, c, &name);
+  return addln::launch_block_bwd(dtype, aligned, full, p, workspace, workspace_bytes, c);
 } catch (...) {
   return ADDLN_ERR_HOST_MEMORY;
 }

@@ -133,7 +133,7 @@ __host__ __device__ constexpr bool bwd_lean(int dt, bool full, bool gr, bool sh)
 __host__ __device__ constexpr int bwd_threads(int dt, bool full, bool gr, bool sh) {
   return bwd_lean(dt, full, gr, sh) ? 640 : kMaxThreads;
 }
-template <int DT, int NV, bool FULL, bool GR, bool SH>
+template <int DT, bool FULL, bool GR, bool SH>
 constexpr int bwd_regs() {
   return bwd_lean(DT, FULL, GR, SH) ? 96 : 128;
 }
@@ -152,7 +152,7 @@ constexpr int bwd_regs() {
 // takes a contiguous range of rows, not a stride: a gate row then meets few
 // walkers.
 template <int DT, int NV, bool FULL, bool GR, bool SH>
-__global__ void __launch_bounds__(bwd_threads(DT, FULL, GR, SH)) __maxnreg__((bwd_regs<DT, NV, FULL, GR, SH>()))
+__global__ void __launch_bounds__(bwd_threads(DT, FULL, GR, SH)) __maxnreg__((bwd_regs<DT, FULL, GR, SH>()))
     k_block_bwd(const __grid_constant__ BlockBwdArgs p) {
   using IO = Io<DT>;
   constexpr int S = IO::kBytes, VE = IO::kVec, N = VE / 2;
@@ -775,7 +775,7 @@ int64_t block_bwd_workspace_bytes(int dtype, bool aligned, bool full, int64_t ro
 }
 
 int launch_block_bwd(int dtype, bool aligned, bool full, BlockBwdArgs p, void* ws, int64_t ws_bytes,
-                     const LaunchCtx& c, const char** name) {
+                     const LaunchCtx& c) {
   using namespace blk;
   const bool gr = p.gate_kind == ADDLN_GATE_ROWS;
   const Choice ch = choose(dtype, p.H, aligned, full, gr, p.rows, c.dev.sms);
@@ -799,7 +799,6 @@ int launch_block_bwd(int dtype, bool aligned, bool full, BlockBwdArgs p, void* w
     if (cols) p.part = static_cast<float*>(ws);
     if (seg) p.seg = reinterpret_cast<float*>(static_cast<char*>(ws) + pb);
   }
-  *name = aligned ? "block_bwd" : "block_bwd_shifted";
   cudaError_t e = launch_units(ch.k, p.parts, ch.sh, ch.smem, c, p);
   if (e == cudaSuccess && (cols || seg)) {
     const int quads = sums_quads(p.parts, full);

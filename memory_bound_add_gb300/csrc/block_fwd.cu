@@ -101,11 +101,11 @@ struct Params {
 // Registers a thread: with the parameters kept, 128-thread CTAs four to an SM.
 // Caps of 96, 80 and 64 (5, 6 and 8 CTAs) spill or reload and measured slower:
 // 2048x4096 fp16 rms/rms 13.3 us a pass at 128, 20.0 at 80, 22.7 at 64;
-// 32768x8192 bf16 335, 471, 575.
-template <int DT, int NV, bool LN, bool GR, bool SH>
-constexpr int fwd_regs() {
-  return 128;
-}
+// 32768x8192 bf16 335, 471, 575.  Left to the thread count alone (which allows
+// as many), the compiler goes for 64 where it can, and spills.  A template, since
+// nvcc takes this beside a thread count only where it depends on one.
+template <int DT>
+constexpr int kFwdRegs = 128;
 
 // The gate row of a row.
 __device__ __forceinline__ int64_t gate_row_of(int64_t row, int64_t rpg, bool small) {
@@ -125,7 +125,7 @@ __device__ __forceinline__ int64_t gate_row_of(int64_t row, int64_t rpg, bool sm
 // (0.44); shifted rows add shuffles and halved stores: 8192x5001 bf16 100 us
 // (0.48).  One row of 4096 takes 2.8 us, a launch.
 template <int DT, int NV, bool LN, bool GR, bool SH>
-__global__ void __launch_bounds__(kMaxThreads) __maxnreg__((fwd_regs<DT, NV, LN, GR, SH>()))
+__global__ void __launch_bounds__(kMaxThreads) __maxnreg__((kFwdRegs<DT>))
     k_block_fwd(const __grid_constant__ BlockFwdArgs p) {
   using IO = Io<DT>;
   constexpr int S = IO::kBytes, VE = IO::kVec, Q = VE / 2;
@@ -432,12 +432,11 @@ Walk walk_of(const Shape& sh) {
 }  // namespace blk
 
 int launch_block_fwd(int dtype, bool aligned, bool layer_or_bias, const BlockFwdArgs& args,
-                     const LaunchCtx& c, const char** name) {
+                     const LaunchCtx& c) {
   using namespace blk;
   const Choice ch = dtype == kF32 ? choose<kF32>(args, aligned, layer_or_bias, c.dev.sms)
                     : dtype == kF16 ? choose<kF16>(args, aligned, layer_or_bias, c.dev.sms)
                                     : choose<kBF16>(args, aligned, layer_or_bias, c.dev.sms);
-  *name = aligned ? "block_fwd" : "block_fwd_shifted";
   BlockFwdArgs p = args;
   p.w = walk_of(ch.sh);
   p.kept_at = ch.kept_at;
