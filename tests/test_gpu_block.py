@@ -1007,3 +1007,26 @@ def test_gates_of_no_rows(shape):
     torch.cuda.synchronize()
     assert h.shape == y.shape == f.grad.shape == gate.grad.shape == shape
     assert all(not v.grad.any() for v in q.values())
+
+
+@pytest.mark.parametrize("dtype", [F32, F16, BF16], ids=["fp32", "fp16", "bf16"])
+@pytest.mark.parametrize("post,pre", [("layer", "layer"), ("rms", "layer"), ("layer", "rms"), ("rms", "rms")])
+@pytest.mark.parametrize("offset", [10.0, 100.0])
+def test_gradients_with_an_offset(dtype, post, pre, offset):
+    # a dy, and a dh, whose mean is large against its spread: the bounds go by
+    # the magnitudes, which the offset raises
+    rows, H = 6, 4096
+    f, x, p = make((rows, H), dtype, post, pre, "channel", beta=True, seed=31)
+    wh, _, wst, _, _ = forward(f, x, p, post, pre, 1.0, 1.0, 1e-5)
+    h, st = wh.to(dtype), [None if t is None else t.reshape(-1).float() for t in wst]
+    g = torch.Generator().manual_seed(32)
+    dy, dh = ((torch.randn(rows, H, generator=g) + offset).to(dtype) for _ in range(2))
+    c = lambda t: None if t is None else t.cuda()  # noqa: E731
+    for one, other in ((dy, None), (None, dh), (dy, dh)):
+        want, err = backward(one, other, f, h, st, p, post, pre, 1.0, 1.0)
+        got = mba.block_norm_backward(c(one), c(other), f.cuda(), h.cuda(), tuple(map(c, st)), post=post, pre=pre,
+                                      **cuda(p))
+        torch.cuda.synchronize()
+        for k, v in got._asdict().items():
+            if v is not None:
+                assert_within(v, want[k].reshape(v.shape), err[k].reshape(v.shape), k)
