@@ -12,8 +12,12 @@
 //   sum v      = sum c t      - r_h mean(u) sum c      - r_h mean(u hhat) sum c hhat
 //   sum v fhat = sum c fhat t - r_h mean(u) sum c fhat - r_h mean(u hhat) sum c fhat hhat
 // so all the sums a row needs (8, without layer norms 3) are taken together.
-// The absolute error of such a difference is that of summing D itself, whose
-// elements are the same differences.
+// Where dy's mean is large against its spread, D's elements carry a common error
+// (of a mean(u) of that size), which a mean(v) of D itself would take out again and
+// the written-out sum does not.  Error of df relative to 64 bits, so / by two
+// exchanges, 64x4096 fp32 layer/layer, dy of spread 1 and mean 0, 10, 100:
+// 7.1e-8 / 7.1e-8, 4.6e-7 / 2.8e-7, 5.0e-7 / 3.3e-7; dx, which has the common error
+// either way, 5.1e-8, 4.4e-7, 5.1e-7.
 //
 // Column sums.  A walker takes a contiguous range of rows and a thread
 // always the same columns, so its sums stay in registers.  Where one gate
@@ -146,7 +150,8 @@ constexpr int bwd_regs() {
 // copy), 8192x4096 bf16 68 us (0.87).  The column sums take the registers for
 // more rows at once: an SM has one CTA of 512 threads, whose warps meet once a
 // row.  Short calls pay for that row's latency (about 2 us a row of a walker)
-// and for the second kernel: 2048x4096 fp16 28.3 us (0.70).  Layer norms need 8
+// and for the second kernel: 2048x4096 fp16 28.3 us (0.70).  Gate rows that serve
+// a sequence each cost that kernel more than this one where they are many: below.  Layer norms need 8
 // sums a row and twice the column sums, and are bound by instructions and that
 // latency: 8192x4096 bf16 96 us (0.62), 4096x768 fp16 16.5 us (0.34).  A walker
 // takes a contiguous range of rows, not a stride: a gate row then meets few
@@ -504,9 +509,17 @@ __global__ void __launch_bounds__(bwd_threads(DT, FULL, GR, SH)) __maxnreg__((bw
 // quad and the warps in order), and from them the gradients of both norms
 // and of a per-channel gate.  blockIdx.y > 0: the gate rows that several
 // walkers share, the walkers in order.  The partials sit in L2 (2 to 10 MB) and
-// the kernel's time is its latency (64x768 fp32 2.6 us behind the rows' kernel,
-// 4096x768 fp16 3.8, 2048x4096 fp16 5.0), so a thread's loads of all A sums are
-// in flight together.
+// without shared gate rows the kernel's time is its latency (64x768 fp32 2.6 us
+// behind the rows' kernel, 4096x768 fp16 3.8, 2048x4096 fp16 5.0), so a thread's
+// loads of all A sums are in flight together.
+//
+// Shared gate rows are another matter: each that may be shared has Hp / 4 / QUADS
+// CTAs, which add a few partials or none, and their number is what the kernel then
+// takes (us of the rows' kernel / the column sums / the gate rows' CTAs, and
+// how many of these; bf16 but for the last): 32768x8192 rms, 4096 rows a gate row,
+// 494 / 7 / 15, 4096; 65536x1152, 256 rows, rms 172 / 6 / 58, 18432, layer 233 / 5 /
+// 135, 36864; 8192x4096, 64 rows, rms 65 / 6 / 102, 32768, layer 100 / 6 / 241, 65536;
+// 2048x4096 fp16 rms, 2 rows, 21 / 6 / 147, 77568.
 constexpr int kSumThreads = 256;
 
 __device__ __forceinline__ float4 add4(float4 a, float4 b) {
