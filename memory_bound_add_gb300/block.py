@@ -474,7 +474,8 @@ class FusedBlockNorm(torch.nn.Module):
     """The block boundary as a module: learnable fp32 parameters of size
     `hidden` (norms: gamma ones, and beta zeros with bias; layer_scale: a
     per-channel gate that starts at this value).  A gate with rows is passed
-    to forward instead.  Returns (h, y)."""
+    to forward instead.  Returns (h, y).  The parameters are fp32 whatever the
+    activations (moved to a 16-bit type, they are refused)."""
 
     def __init__(self, hidden: int, post: Optional[str] = "rms", pre: Optional[str] = "rms",
                  bias: bool = False, layer_scale: Optional[float] = None, residual_scale: float = 1.0,
