@@ -51,4 +51,19 @@ from .block import (  # noqa: F401
     block_norm_fwd,
     block_norm_train,
 )
+from .drop import (  # noqa: F401
+    DropoutAddNormFunction,
+    DropoutAddNormGrads,
+    DropoutFunction,
+    FusedDropoutAddNorm,
+    dropout,
+    dropout_add_norm,
+    dropout_add_norm_backward,
+    dropout_add_norm_bwd,
+    dropout_add_norm_bwd_workspace_size,
+    dropout_add_norm_fwd,
+    dropout_add_norm_train,
+    dropout_fwd,
+    dropout_train,
+)
 from .grads import clip_grad_norm_, clip_grads, grad_norm, grad_norm_workspace_size  # noqa: F401

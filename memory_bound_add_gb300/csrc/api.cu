@@ -19,6 +19,7 @@
 #include "../../include/addln_grad.h"
 #include "abi.h"
 #include "block.h"
+#include "drop.h"
 #include "launch.h"
 
 using addln::DeviceInfo;
@@ -419,7 +420,8 @@ int addln_get_device_error(void* stream) {
       addln::read_bounds_rows_warp, addln::read_bounds_rows_cta, addln::read_bounds_softmax,
       addln::read_bounds_bgr,       addln::read_bounds_add,      addln::read_bounds_bwd,
       addln::read_bounds_host,      addln::read_bounds_block_fwd, addln::read_bounds_block_bwd,
-      addln::read_bounds_grad};
+      addln::read_bounds_grad,      addln::read_bounds_drop,      addln::read_bounds_drop_fwd,
+      addln::read_bounds_drop_bwd};
   unsigned long long word = 0;
   for (auto f : readers) {
     unsigned long long w = 0;

@@ -442,6 +442,98 @@ __device__ __forceinline__ RowStat walker_stats(Exchange<SIDES>& ex, float2 (&v)
   return st;
 }
 
+// 1 / sqrt(mean square + eps) (in M2's place) and the mean that precedes it,
+// of one row's slots; a layer norm leaves them shifted, an rms norm as they
+// were (mean 0).
+template <int VE, int NV, bool LN, bool SIDES>
+__device__ __forceinline__ RowStat row_norm(Exchange<SIDES>& ex, float2 (&v)[NV * VE / 2], const Cols<VE, NV>& cs, bool layer,
+                                            float inv_h, float eps) {
+  RowStat st{0.f, 0.f, 0.f};
+  if (LN && layer) {
+    st = walker_stats(ex, v, cs);
+  } else {
+    // the slots of groups that do not exist hold zeros
+    float2 q[2] = {dup2(0.f), dup2(0.f)};
+#pragma unroll
+    for (int j = 0; j < NV * VE / 2; ++j) q[j & 1] = fma2(v[j], v[j], q[j & 1]);
+    q[0] = add2(q[0], q[1]);
+    st.M2 = walker_sum(ex, q[0].x + q[0].y);
+  }
+  st.M2 = row_rstd(st.M2, inv_h, eps);
+  return st;
+}
+
+// ------------------------------------------------------------ column sums
+// Stores slots as fp32 columns of an [Hp] vector (16-byte aligned).
+template <int VE, int NV>
+__device__ __forceinline__ void store_cols(float* t, const Cols<VE, NV>& cs, int site, int Hp,
+                                           const float2 (&v)[NV * VE / 2]) {
+#pragma unroll
+  for (int k = 0; k < NV; ++k)
+#pragma unroll
+    for (int i = 0; i < VE / 4; ++i) {
+      // Hp is a multiple of 4: four columns of which one exists fit
+      if (cs.valid(k) <= 4 * i || !ADDLN_IN(site, 4 * (cs.col(k) + 4 * i), 16, 4 * static_cast<int64_t>(Hp))) continue;
+      const float2 a = v[k * VE / 2 + 2 * i], b = v[k * VE / 2 + 2 * i + 1];
+      *reinterpret_cast<float4*>(t + cs.col(k) + 4 * i) = make_float4(a.x, a.y, b.x, b.y);
+    }
+}
+
+constexpr int kSumThreads = 256;
+
+__device__ __forceinline__ float4 add4(float4 a, float4 b) {
+  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
+}
+
+// r[a] = sum over i < n of the quad at src + i * ld + a * la (in floats);
+// every thread of the block takes part, the result is in the threads below
+// QUADS.
+template <int A, int QUADS>
+__device__ __forceinline__ void block_quad_sums(const float* src, int64_t n, int64_t ld, int64_t la, bool in,
+                                                int64_t extent, float4 (*wsum)[A][QUADS], float4 (&r)[A]) {
+  constexpr int kU = 8 / A;  // partials a thread has in flight
+  constexpr int kStep = kSumThreads / QUADS;
+  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+#pragma unroll
+  for (int a = 0; a < A; ++a) r[a] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (in)
+    for (int64_t i0 = t / QUADS; i0 < n; i0 += kStep * kU) {
+      float4 v[kU][A];
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int a = 0; a < A; ++a) {
+          const int64_t i = i0 + u * kStep;
+          v[u][a] = make_float4(0.f, 0.f, 0.f, 0.f);
+          if (i < n && ADDLN_IN(741, (i * ld + a * la) * 4, 16, extent))
+            v[u][a] = __ldcg(reinterpret_cast<const float4*>(src + i * ld + a * la));
+        }
+#pragma unroll
+      for (int u = 0; u < kU; ++u)
+#pragma unroll
+        for (int a = 0; a < A; ++a) r[a] = add4(r[a], v[u][a]);
+    }
+#pragma unroll
+  for (int a = 0; a < A; ++a) {
+#pragma unroll
+    for (int off = QUADS; off < 32; off <<= 1) {
+      r[a].x += __shfl_xor_sync(0xffffffffu, r[a].x, off);
+      r[a].y += __shfl_xor_sync(0xffffffffu, r[a].y, off);
+      r[a].z += __shfl_xor_sync(0xffffffffu, r[a].z, off);
+      r[a].w += __shfl_xor_sync(0xffffffffu, r[a].w, off);
+    }
+    if (lane < QUADS) wsum[warp][a][lane] = r[a];
+  }
+  __syncthreads();
+  if (t < QUADS)
+#pragma unroll
+    for (int a = 0; a < A; ++a) {
+      r[a] = wsum[0][a][t];
+#pragma unroll
+      for (int w = 1; w < kSumThreads / 32; ++w) r[a] = add4(r[a], wsum[w][a][t]);
+    }
+}
+
 // ------------------------------------------------------------------ host
 // How a call's rows are spread over threads and CTAs.
 struct Shape {
@@ -466,6 +558,65 @@ inline int rows_side_by_side(int most, int64_t rows, int sms) {
   int n = 1;
   while (n < most && static_cast<int64_t>(n) * sms < rows) n *= 2;
   return n < most ? n : most;
+}
+
+// Groups a thread, of 1 to 4: the number that needs the fewest CTAs for a row,
+// then that leaves the fewest of a row's threads' slots empty, the larger one
+// where equal (us with at most one / two / four: 4096x768 fp16 layer 13.5,
+// 13.4, 8.4; 2048x4096 fp16 rms 25.7, 13.1, 12.0; 32768x8192 bf16 rms 790, 437,
+// 332).
+inline int groups_a_thread(int groups) {
+  int best = 1, ctas = 1 << 30, waste = 1 << 30;
+  for (int nv = 1; nv <= 4; ++nv) {
+    const int most = nv * kMaxThreads, c = (groups + most - 1) / most;
+    const int t = (groups + 32 * nv - 1) / (32 * nv) * 32, w = t * nv - groups;
+    if (c < ctas || (c == ctas && w <= waste)) best = nv, ctas = c, waste = w;
+  }
+  return best;
+}
+
+// How a forward's rows are spread: threads and CTAs, and its shared memory (a
+// ring of slots a warp, the parameters that are kept there, the rows' sums).
+struct Spread {
+  Shape sh{};
+  int smem = 0, kept_at = 0, sums_at = 0, ring_slots = 0;
+};
+
+// NV groups of VE columns a thread; slot_bytes and kept_bytes: of a warp's ring
+// slot and of its parameters (0: in registers); a CTA's slice of a row is a
+// multiple of `multiple` columns.  As in block_fwd.cu: with the parameters in
+// registers a warp for a row where 32 threads hold it, four rows to a CTA, else a
+// CTA, else a cluster; with parameters in shared memory rows side by side in a
+// CTA of up to kMaxThreads, as many as leave the ring two slots, or one.
+inline Spread spread(int H, int VE, int NV, int64_t rows, int sms, int slot_bytes, int kept_bytes, int multiple) {
+  Spread c;
+  const int groups = (H + VE - 1) / VE;
+  int threads, slot, kept, sums;
+  auto bytes = [&] { return c.sh.rows * (c.ring_slots * slot + sums) + kept; };
+  for (c.sh.C = (groups + NV * kMaxThreads - 1) / (NV * kMaxThreads);; ++c.sh.C) {
+    c.sh.slice = c.sh.C == 1 ? H : ((H + c.sh.C - 1) / c.sh.C + multiple - 1) / multiple * multiple;
+    threads = ((c.sh.slice + VE - 1) / VE + 32 * NV - 1) / (32 * NV) * 32;
+    slot = threads / 32 * slot_bytes;
+    kept = threads / 32 * kept_bytes;
+    sums = 2 * (threads / 32) * c.sh.C * 16;
+    c.sh.rows = c.ring_slots = 1;
+    if ((bytes() <= kMaxSmem && threads <= kMaxThreads) || c.sh.C == kMaxCluster) break;
+  }
+  c.sh.rows = c.sh.C > 1 ? 1 : rows_side_by_side(kept_bytes ? kMaxThreads / threads : threads == 32 ? 4 : 1, rows, sms);
+  c.ring_slots = kMaxSlots;
+  while (bytes() > kMaxSmem && c.ring_slots > 1) --c.ring_slots;
+  while (bytes() > kMaxSmem && c.sh.rows > 1) --c.sh.rows;
+  c.sh.threads = threads * c.sh.rows;
+  c.kept_at = c.sh.rows * c.ring_slots * slot;
+  c.sums_at = c.kept_at + kept;
+  c.smem = bytes();
+  return c;
+}
+
+// Rows staged ahead: two, or one where every walker has more than eight rows
+// (as in block_fwd.cu).
+inline int slots_ahead(int64_t rows, int fit, const Spread& s) {
+  return rows > 8 * static_cast<int64_t>(fit) * s.sh.rows ? 1 : s.ring_slots;
 }
 
 // Launches kernel(args...) as units * C CTAs.

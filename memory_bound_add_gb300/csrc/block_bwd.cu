@@ -55,21 +55,6 @@ __device__ __forceinline__ int64_t b_gate_bytes(const BlockBwdArgs& p, int S) {
 // dbeta and sum(s D) or dpb.
 __host__ __device__ constexpr int sums_of(bool full) { return full ? 4 : 2; }
 
-// Stores slots as fp32 columns of an [Hp] vector (16-byte aligned).
-template <int VE, int NV>
-__device__ __forceinline__ void store_cols(float* t, const Cols<VE, NV>& cs, int site, int Hp,
-                                           const float2 (&v)[NV * VE / 2]) {
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < VE / 4; ++i) {
-      // Hp is a multiple of 4: four columns of which one exists fit
-      if (cs.valid(k) <= 4 * i || !ADDLN_IN(site, 4 * (cs.col(k) + 4 * i), 16, 4 * static_cast<int64_t>(Hp))) continue;
-      const float2 a = v[k * VE / 2 + 2 * i], b = v[k * VE / 2 + 2 * i + 1];
-      *reinterpret_cast<float4*>(t + cs.col(k) + 4 * i) = make_float4(a.x, a.y, b.x, b.y);
-    }
-}
-
 // K sums (4 or 8) over the walker's threads, the same bits in every thread.
 // Within a warp each step halves the sums a lane carries: 6 (9) exchanges
 // instead of 5 K.
@@ -520,61 +505,6 @@ __global__ void __launch_bounds__(bwd_threads(DT, FULL, GR, SH)) __maxnreg__((bw
 // 494 / 7 / 15, 4096; 65536x1152, 256 rows, rms 172 / 6 / 58, 18432, layer 233 / 5 /
 // 135, 36864; 8192x4096, 64 rows, rms 65 / 6 / 102, 32768, layer 100 / 6 / 241, 65536;
 // 2048x4096 fp16 rms, 2 rows, 21 / 6 / 147, 77568.
-constexpr int kSumThreads = 256;
-
-__device__ __forceinline__ float4 add4(float4 a, float4 b) {
-  return make_float4(a.x + b.x, a.y + b.y, a.z + b.z, a.w + b.w);
-}
-
-// r[a] = sum over i < n of the quad at src + i * ld + a * la (in floats);
-// every thread of the block takes part, the result is in the threads below
-// QUADS.
-template <int A, int QUADS>
-__device__ __forceinline__ void block_quad_sums(const float* src, int64_t n, int64_t ld, int64_t la, bool in,
-                                                int64_t extent, float4 (*wsum)[A][QUADS], float4 (&r)[A]) {
-  constexpr int kU = 8 / A;  // partials a thread has in flight
-  constexpr int kStep = kSumThreads / QUADS;
-  const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-#pragma unroll
-  for (int a = 0; a < A; ++a) r[a] = make_float4(0.f, 0.f, 0.f, 0.f);
-  if (in)
-    for (int64_t i0 = t / QUADS; i0 < n; i0 += kStep * kU) {
-      float4 v[kU][A];
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-#pragma unroll
-        for (int a = 0; a < A; ++a) {
-          const int64_t i = i0 + u * kStep;
-          v[u][a] = make_float4(0.f, 0.f, 0.f, 0.f);
-          if (i < n && ADDLN_IN(741, (i * ld + a * la) * 4, 16, extent))
-            v[u][a] = __ldcg(reinterpret_cast<const float4*>(src + i * ld + a * la));
-        }
-#pragma unroll
-      for (int u = 0; u < kU; ++u)
-#pragma unroll
-        for (int a = 0; a < A; ++a) r[a] = add4(r[a], v[u][a]);
-    }
-#pragma unroll
-  for (int a = 0; a < A; ++a) {
-#pragma unroll
-    for (int off = QUADS; off < 32; off <<= 1) {
-      r[a].x += __shfl_xor_sync(0xffffffffu, r[a].x, off);
-      r[a].y += __shfl_xor_sync(0xffffffffu, r[a].y, off);
-      r[a].z += __shfl_xor_sync(0xffffffffu, r[a].z, off);
-      r[a].w += __shfl_xor_sync(0xffffffffu, r[a].w, off);
-    }
-    if (lane < QUADS) wsum[warp][a][lane] = r[a];
-  }
-  __syncthreads();
-  if (t < QUADS)
-#pragma unroll
-    for (int a = 0; a < A; ++a) {
-      r[a] = wsum[0][a][t];
-#pragma unroll
-      for (int w = 1; w < kSumThreads / 32; ++w) r[a] = add4(r[a], wsum[w][a][t]);
-    }
-}
-
 // The gate rows that more than one walker shares.  Where walkers have at
 // least as many rows as a gate row, a gate row meets at most one border
 // between walkers, and border b (between walkers b - 1 and b) has one if it

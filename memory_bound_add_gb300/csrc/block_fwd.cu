@@ -22,27 +22,6 @@ __device__ __forceinline__ int64_t f_gate_bytes(const BlockFwdArgs& p, int S) {
   return ((p.gate_rows - 1) * p.gate_stride + p.H) * S;
 }
 
-// 1 / sqrt(mean square + eps) (in M2's place) and the mean that precedes it,
-// of one row's slots; a layer norm leaves them shifted, an rms norm as they
-// were (mean 0).
-template <int VE, int NV, bool LN, bool SIDES>
-__device__ __forceinline__ RowStat row_norm(Exchange<SIDES>& ex, float2 (&v)[NV * VE / 2], const Cols<VE, NV>& cs, bool layer,
-                                            float inv_h, float eps) {
-  RowStat st{0.f, 0.f, 0.f};
-  if (LN && layer) {
-    st = walker_stats(ex, v, cs);
-  } else {
-    // the slots of groups that do not exist hold zeros
-    float2 q[2] = {dup2(0.f), dup2(0.f)};
-#pragma unroll
-    for (int j = 0; j < NV * VE / 2; ++j) q[j & 1] = fma2(v[j], v[j], q[j & 1]);
-    q[0] = add2(q[0], q[1]);
-    st.M2 = walker_sum(ex, q[0].x + q[0].y);
-  }
-  st.M2 = row_rstd(st.M2, inv_h, eps);
-  return st;
-}
-
 // The parameters as the row's arithmetic uses them: w = s gate gamma and
 // b = s gate beta of the post norm (gate: a per-channel one; without a post
 // norm w = s gate, b = 0), and gamma and beta of the pre norm.  Loading them
@@ -333,21 +312,6 @@ Choice make(const BlockFwdArgs& p, bool ln, int sms) {
   c.sums_at = c.kept_at + kept;
   c.smem = bytes();
   return c;
-}
-
-// Groups a thread, of 1 to 4: the number that needs the fewest CTAs for a row,
-// then that leaves the fewest of a row's threads' slots empty, the larger one
-// where equal (us with at most one / two / four: 4096x768 fp16 layer 13.5,
-// 13.4, 8.4; 2048x4096 fp16 rms 25.7, 13.1, 12.0; 32768x8192 bf16 rms 790, 437,
-// 332).
-inline int groups_a_thread(int groups) {
-  int best = 1, ctas = 1 << 30, waste = 1 << 30;
-  for (int nv = 1; nv <= 4; ++nv) {
-    const int most = nv * kMaxThreads, c = (groups + most - 1) / most;
-    const int t = (groups + 32 * nv - 1) / (32 * nv) * 32, w = t * nv - groups;
-    if (c < ctas || (c == ctas && w <= waste)) best = nv, ctas = c, waste = w;
-  }
-  return best;
 }
 
 template <int DT>

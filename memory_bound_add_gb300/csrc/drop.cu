@@ -1,0 +1,105 @@
+// y = dropout(x), element by element.  Bound by memory: 2 S bytes an element.
+#include "philox.cuh"
+
+namespace addln {
+namespace blk {
+
+constexpr int kThreads = 256;
+constexpr int kBlocks = 4;  // blocks of 8 elements a thread, all in flight
+
+// VEC: x and y lie on 16-byte borders.  A thread has kBlocks blocks of 8
+// elements, a CTA's threads apart; the tensor's last block may be shorter.
+template <int DT, bool VEC>
+__global__ void __launch_bounds__(kThreads) k_dropout(const void* x, void* y, int64_t n, const DropSpec d) {
+  using IO = Io<DT>;
+  constexpr int S = IO::kBytes, U = S / 2;  // 16-byte vectors a block
+  pdl_trigger();
+  pdl_wait();
+  Philox rng;
+  rng.init(d);
+  const float2 scale = dup2(d.scale);
+  const int64_t b0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kBlocks) + threadIdx.x;
+  const int64_t whole = VEC ? n / 8 : 0, extent = n * S;
+  uint4 v[kBlocks][U];
+#pragma unroll
+  for (int j = 0; j < kBlocks; ++j) {
+    const int64_t b = b0 + j * kThreads;
+    if (b >= whole) continue;
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      v[j][u] = make_uint4(0, 0, 0, 0);
+      const int64_t at = b * 8 * S + 16 * u;
+      // not the read-only path: y may be x
+      if (ADDLN_IN(761, at, 16, extent)) v[j][u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(x) + at));
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < kBlocks; ++j) {
+    const int64_t b = b0 + j * kThreads;
+    if (b * 8 >= n) break;
+    uint4 w = make_uint4(0, 0, 0, 0);
+    uint32_t above = d.above;
+    if (d.on) w = rng(b);
+    const uint32_t t[4] = {w.x, w.y, w.z, w.w};
+    if (b < whole) {
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        uint4 o = v[j][u];
+        if (d.on) {
+          float2 f[IO::kVec / 2];
+          IO::to_pairs(o, f);
+#pragma unroll
+          for (int i = 0; i < IO::kVec / 2; ++i) {
+            const uint32_t ww = t[u * (IO::kVec / 2) + i];
+            const float2 s = mul2(f[i], scale);
+            f[i] = make_float2(keep_lo(ww, above) ? s.x : 0.f, keep_hi(ww, above) ? s.y : 0.f);
+          }
+          o = IO::from_pairs(f);
+        }
+        const int64_t at = b * 8 * S + 16 * u;
+        if (ADDLN_IN(762, at, 16, extent)) st_stream_v4(static_cast<char*>(y) + at, o);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int64_t i = b * 8 + e;
+        if (i >= n || !ADDLN_IN(763, i * S, S, extent)) continue;
+        const bool keep = (e & 1) ? keep_hi(t[e >> 1], above) : keep_lo(t[e >> 1], above);
+        if constexpr (DT == kF32) {
+          const float f = __ldcs(static_cast<const float*>(x) + i);
+          static_cast<float*>(y)[i] = !d.on ? f : keep ? f * d.scale : 0.f;
+        } else {
+          const unsigned short h = __ldcs(static_cast<const unsigned short*>(x) + i);
+          const float f = DT == kF16 ? __half2float(__ushort_as_half(h)) : __bfloat162float(__ushort_as_bfloat16(h));
+          if (d.on)
+            IO::store1(y, i, keep ? f * d.scale : 0.f);
+          else
+            static_cast<unsigned short*>(y)[i] = h;
+        }
+      }
+    }
+  }
+}
+
+}  // namespace blk
+
+int launch_dropout(int dtype, const void* x, void* y, int64_t n, const DropSpec& drop, const LaunchCtx& c) {
+  using namespace blk;
+  const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & 15) == 0;
+  void (*k)(const void*, void*, int64_t, const DropSpec) =
+      dtype == kF32 ? (vec ? &k_dropout<kF32, true> : &k_dropout<kF32, false>)
+      : dtype == kF16 ? (vec ? &k_dropout<kF16, true> : &k_dropout<kF16, false>)
+                      : (vec ? &k_dropout<kBF16, true> : &k_dropout<kBF16, false>);
+  const int64_t per = 8 * kThreads * kBlocks, ctas = (n + per - 1) / per;
+  if (ctas > 0x7fffffff) return ADDLN_ERR_SHAPE;
+  const cudaError_t e = launch_kernel(k, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, c.stream, c.pdl, x, y, n, drop);
+  if (e != cudaSuccess) {
+    note_cuda_error(static_cast<int>(e));
+    return ADDLN_ERR_LAUNCH;
+  }
+  return ADDLN_OK;
+}
+
+ADDLN_BOUNDS_READER(read_bounds_drop)
+
+}  // namespace addln

@@ -1,0 +1,388 @@
+// Backward of bias, dropout, residual sum and norm (drop_fwd.cu), in one pass
+// over the rows.  With hhat = (h - mean) rstd and u = dy gamma:
+//   D  = rstd (u - mean(u) - hhat mean(u hhat)) + dh    (rms: no mean(u))
+//   dx = D,  df = keep ? D scale : 0
+// and over the rows dgamma = sum dy hhat, dbeta = sum dy, dbias = sum df.
+//
+// Column sums.  A thread always has the same columns, so its sums stay in
+// registers; the walkers of a CTA join them at the end, each CTA leaves one
+// fp32 partial, and k_drop_sums adds the partials in a fixed order.
+#include "philox.cuh"
+
+namespace addln {
+namespace blk {
+
+// Sums of both parts of v over the walker's threads, the same bits in every
+// one: a warp butterfly, then the warps' sums in a fixed order.
+__device__ __forceinline__ float2 walker_sum2(Exchange<true>& ex, float2 v) {
+  constexpr unsigned kAll = 0xffffffffu;
+#pragma unroll
+  for (int off = 16; off > 0; off >>= 1)
+    v = add2(v, make_float2(__shfl_xor_sync(kAll, v.x, off), __shfl_xor_sync(kAll, v.y, off)));
+  if (ex.w.warps == 1) return v;
+  const float4* b = ex(make_float4(v.x, v.y, 0.f, 0.f));
+  const int width = ex.w.width;
+  float2 t = dup2(0.f);
+  for (int i = (threadIdx.x & 31) & (width - 1); i < ex.w.warps; i += 32) t = add2(t, make_float2(b[i].x, b[i].y));
+  for (int off = 1; off < width; off <<= 1)
+    t = add2(t, make_float2(__shfl_xor_sync(kAll, t.x, off), __shfl_xor_sync(kAll, t.y, off)));
+  return t;
+}
+
+// Column sums of a kernel: dgamma, with FULL dbeta, with BIAS dbias.
+__host__ __device__ constexpr int drop_sums(bool full, bool bias) { return 1 + full + bias; }
+
+// FULL: a layer norm, or dbeta is wanted.  BIAS: dbias is wanted.  SH: some
+// rows do not begin on 16-byte borders.
+template <int DT, int NV, bool FULL, bool BIAS, bool SH>
+__global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
+    k_drop_bwd(const __grid_constant__ DropBwdArgs p) {
+  using IO = Io<DT>;
+  constexpr int S = IO::kBytes, VE = IO::kVec, N = VE / 2;
+  constexpr int A = drop_sums(FULL, BIAS), NT = 3;
+  constexpr int P = NV * N;
+  using R = Ring<DT, NV, NT, SH>;
+  extern __shared__ __align__(128) unsigned char smem[];
+  if (p.w.C > 1) cluster_started();
+  const int T = p.w.cta_warps * 32;
+  const int side = p.w.rows_per_cta > 1 ? threadIdx.x / T : 0, tid = threadIdx.x - side * T;
+  const int rank = p.w.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.w.C);
+  const int64_t cta = blockIdx.x / p.w.C;
+  const int64_t stride = static_cast<int64_t>(gridDim.x / p.w.C) * p.w.rows_per_cta;
+  int64_t row = cta * p.w.rows_per_cta + side;
+  const int col0 = rank * p.w.slice;
+  constexpr int slots = kMaxSlots;
+  const int64_t extent = p.rows * static_cast<int64_t>(p.H) * S;
+  const uint32_t warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  R ring;
+  ring.base = smem_addr(smem) + warp * kMaxSlots * R::kSlot + lane * 16;
+  Kept<VE, NV> kept;  // gamma
+  kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<1>() + lane * 16;
+  Exchange<true> ex{p.w, p.sums_at + side * 2 * p.w.warps * 16, 0};
+  Cols<VE, NV> cs;
+  cs.init(tid >> 5, col0, min(p.w.slice, p.H - col0));
+  const bool has_dy = p.dy != nullptr, has_dh = p.dh != nullptr;
+
+  auto offset = [&](int64_t r) { return (r * p.H + cs.c0) * S; };
+  auto fetch = [&](int slot, int64_t r) {
+    if (r < p.rows) {
+      const int64_t at = offset(r);
+      if (has_dy) {
+        ring.template fetch<0>(cs, slot, p.dy, at, 780, extent);
+        ring.template fetch<1>(cs, slot, p.h, at, 781, extent);
+      }
+      if (has_dh) ring.template fetch<2>(cs, slot, p.dh, at, 782, extent);
+    }
+    ring.commit();
+  };
+  float mean_n = 0.f, rstd_n = 0.f;  // of the next row
+  auto stats = [&](int64_t r) {
+    if (r >= p.rows || !has_dy || !ADDLN_IN(783, 4 * r, 4, 4 * p.rows)) return;
+    rstd_n = __ldg(p.rstd + r);
+    if constexpr (FULL)
+      if (p.mean) mean_n = __ldg(p.mean + r);
+  };
+  pdl_trigger();
+  pdl_wait();
+  // a tensor that the call does not have is zeros, written once
+  for (int s = 0; s < slots; ++s) {
+    if (!has_dy) ring.template clear<0>(s), ring.template clear<1>(s);
+    if (!has_dh) ring.template clear<2>(s);
+  }
+  for (int s = 0; s < slots; ++s) fetch(s, row + s * stride);
+  Philox rng;
+  rng.init(p.drop);
+#pragma unroll
+  for (int k = 0; k < NV; ++k) {
+    float g[VE];
+    load_params<VE, SH>(has_dy ? p.gamma : nullptr, cs.col(k), p.H, 0.f, g, 784);
+    kept.put(0, k, g);
+  }
+  stats(row);
+  if (p.w.C > 1) cluster_wait_started();
+
+  float2 sg[P], sb[FULL ? P : 1], sf[BIAS ? P : 1];
+#pragma unroll
+  for (int j = 0; j < P; ++j) {
+    sg[j] = dup2(0.f);
+    if constexpr (FULL) sb[j] = dup2(0.f);
+    if constexpr (BIAS) sf[j] = dup2(0.f);
+  }
+  const float2 scale = dup2(p.drop.scale);
+  for (int slot = 0; row < p.rows; row += stride, slot = slot + 1 == slots ? 0 : slot + 1) {
+    const int64_t off = offset(row);
+    const uint64_t at = static_cast<uint64_t>(row) * static_cast<uint32_t>(p.H) + static_cast<uint32_t>(cs.c0);
+    Mask<VE, NV, SH> mask;
+    if (p.drop.on) mask.row(rng, at, p.drop.above);
+    ring.template wait<1>();
+    ring.meet();
+    const float2 nm = dup2(-mean_n), rs = dup2(rstd_n);
+    stats(row + stride);
+    int sh[NT] = {0, 0, 0};
+    if constexpr (SH) sh[0] = low4(p.dy, off), sh[1] = low4(p.h, off), sh[2] = low4(p.dh, off);
+    auto take = [&](int i, int k, float2 (&v)[N]) { IO::to_pairs(ring.take(slot, i, k, sh[i]), v); };
+    auto hat = [&](int k, float2 (&v)[N]) {
+      take(1, k, v);
+#pragma unroll
+      for (int j = 0; j < N; ++j) v[j] = mul2(FULL ? add2(v[j], nm) : v[j], rs);
+    };
+    float2 t[P];
+    float2 q0 = dup2(0.f), q1 = dup2(0.f);
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float2 hh[N], dy[N], d[N], u[N];
+      const int j0 = k * N;
+      hat(k, hh);
+      take(0, k, dy);
+      take(2, k, d);
+      kept.get(0, k, u);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        u[i] = mul2(u[i], dy[i]);
+        sg[j0 + i] = fma2(dy[i], hh[i], sg[j0 + i]);
+        q0 = fma2(u[i], hh[i], q0);
+        if constexpr (FULL) {
+          sb[j0 + i] = add2(sb[j0 + i], dy[i]);
+          q1 = add2(q1, u[i]);
+        }
+        t[j0 + i] = fma2(rs, u[i], d[i]);
+      }
+    }
+    float2 m = make_float2(q0.x + q0.y, q1.x + q1.y);
+    if (has_dy) m = walker_sum2(ex, m);
+    // rstd mean(u hhat), rstd mean(u)
+    const float2 na2 = dup2(-rs.x * (m.x * p.inv_h));
+    const float2 na1 = dup2(FULL && p.norm == ADDLN_NORM_LAYER ? -rs.x * (m.y * p.inv_h) : 0.f);
+    Writer<DT, NV, SH> dx, df;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      float2 hh[N], o[N];
+      hat(k, hh);
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        const float2 v = t[k * N + i];
+        o[i] = fma2(na2, hh[i], FULL ? add2(v, na1) : v);
+      }
+      if (p.dx != nullptr) dx.put(cs, p.dx, off, k, IO::from_pairs(o), 785, extent);
+      if (p.drop.on) mask.apply(rng, at, k, p.drop.above, scale, o);
+      if constexpr (BIAS) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) sf[k * N + i] = add2(sf[k * N + i], o[i]);
+      }
+      df.put(cs, p.df, off, k, IO::from_pairs(o), 786, extent);
+    }
+    ring.meet();
+    fetch(slot, row + slots * stride);
+  }
+  if (p.part != nullptr) {
+    // the CTA's walkers join their sums in shared memory, halving their number
+    // (the ring is free: what is in flight arrives first)
+    int top = 1;
+    while (top < p.w.rows_per_cta) top *= 2;
+    if (top > 1) {
+      ring.template wait<0>();
+      __syncthreads();
+    }
+    for (int half = top / 2; half > 0; half /= 2) {
+      const int to = side < half ? side : side - half;
+      float* at = reinterpret_cast<float*>(smem) + static_cast<int64_t>(to) * A * 2 * P * T + tid;
+      const bool gives = side >= half && side < 2 * half, gets = side < half && side + half < p.w.rows_per_cta;
+      auto give = [&](const float2 (&v)[P], int a) {
+#pragma unroll
+        for (int j = 0; j < P; ++j) {
+          at[(a * 2 * P + 2 * j) * T] = v[j].x;
+          at[(a * 2 * P + 2 * j + 1) * T] = v[j].y;
+        }
+      };
+      auto get = [&](float2 (&v)[P], int a) {
+#pragma unroll
+        for (int j = 0; j < P; ++j)
+          v[j] = add2(v[j], make_float2(at[(a * 2 * P + 2 * j) * T], at[(a * 2 * P + 2 * j + 1) * T]));
+      };
+      if (gives) {
+        give(sg, 0);
+        if constexpr (FULL) give(sb, 1);
+        if constexpr (BIAS) give(sf, A - 1);
+      }
+      __syncthreads();
+      if (gets) {
+        get(sg, 0);
+        if constexpr (FULL) get(sb, 1);
+        if constexpr (BIAS) get(sf, A - 1);
+      }
+      __syncthreads();
+    }
+    if (side == 0) {
+      float* out = p.part + cta * A * p.Hp;
+      store_cols<VE, NV>(out, cs, 787, p.Hp, sg);
+      if constexpr (FULL) store_cols<VE, NV>(out + p.Hp, cs, 788, p.Hp, sb);
+      if constexpr (BIAS) store_cols<VE, NV>(out + (A - 1) * p.Hp, cs, 789, p.Hp, sf);
+    }
+  }
+  if (p.w.C > 1) cooperative_groups::this_cluster().sync();
+}
+
+// The CTAs' column sums of QUADS column quads, added in a fixed order.
+template <bool FULL, bool BIAS, int QUADS>
+__global__ void __launch_bounds__(kSumThreads) k_drop_sums(const __grid_constant__ DropBwdArgs p) {
+  constexpr int A = drop_sums(FULL, BIAS);
+  __shared__ float4 wsum[kSumThreads / 32][A][QUADS];
+  pdl_trigger();
+  pdl_wait();
+  const int t = threadIdx.x;
+  const int j = (blockIdx.x * QUADS + t % QUADS) * 4;  // the thread's first column
+  float4 r[A];
+  block_quad_sums<A, QUADS>(p.part + j, p.parts, static_cast<int64_t>(A) * p.Hp, p.Hp, j < p.H,
+                            (p.parts * A * p.Hp - j) * 4, wsum, r);
+  if (t >= QUADS) return;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) {
+    const int c = j + q;
+    if (c >= p.H || !ADDLN_IN(790, 4 * c, 4, 4 * static_cast<int64_t>(p.H))) continue;
+    auto at = [&](int a) { return q == 0 ? r[a].x : q == 1 ? r[a].y : q == 2 ? r[a].z : r[a].w; };
+    if (p.dgamma) p.dgamma[c] = at(0);
+    if (FULL && p.dbeta) p.dbeta[c] = at(FULL ? 1 : 0);
+    if (BIAS && p.dbias) p.dbias[c] = at(A - 1);
+  }
+}
+
+// ------------------------------------------------------------------ host
+namespace {
+
+using BwdKernel = void (*)(DropBwdArgs);
+
+struct Choice {
+  BwdKernel k = nullptr;
+  Shape sh{};
+  int smem = 0, kept_at = 0, sums_at = 0;
+};
+
+// NV groups of VE columns a thread; a CTA of up to kMaxThreads threads for as
+// many rows side by side as fit it, else one CTA for a row, else a cluster of
+// as few CTAs as hold it.  Shared memory: the ring (at least what the walkers
+// need to join their sums), gamma, the row sums.
+template <int DT, int NV, bool FULL, bool BIAS, bool SH>
+Choice make(int H, int64_t rows, int sms) {
+  constexpr int VE = Io<DT>::kVec;
+  Choice c;
+  c.k = &k_drop_bwd<DT, NV, FULL, BIAS, SH>;
+  const int groups = (H + VE - 1) / VE;
+  c.sh.C = (groups + NV * kMaxThreads - 1) / (NV * kMaxThreads);
+  c.sh.slice = c.sh.C == 1 ? H : ((H + c.sh.C - 1) / c.sh.C + 15) / 16 * 16;
+  const int threads = ((c.sh.slice + VE - 1) / VE + 32 * NV - 1) / (32 * NV) * 32;
+  c.sh.rows = c.sh.C > 1 ? 1 : rows_side_by_side(kMaxThreads / threads, rows, sms);
+  c.sh.threads = threads * c.sh.rows;
+  const int warps = c.sh.threads / 32;
+  int ring = warps * kMaxSlots * static_cast<int>(Ring<DT, NV, 3, SH>::kSlot);
+  int half = 0;  // walkers that give their sums to another at once
+  for (int top = 1; top < c.sh.rows; top *= 2) half = top;
+  const int join = half * drop_sums(FULL, BIAS) * NV * VE * threads * 4;
+  if (ring < join) ring = join;
+  c.kept_at = ring;
+  c.sums_at = c.kept_at + warps * static_cast<int>(Kept<VE, NV>::template bytes<1>());
+  c.smem = c.sums_at + c.sh.rows * 2 * (threads / 32) * c.sh.C * 16;
+  return c;
+}
+
+// 16 columns of a 16-bit type a thread where a row is longer than a warp's 8;
+// else 8 (fp32: 8 and 4).  Three column sums of shifted rows spill with 16.
+template <int DT, bool FULL, bool BIAS, bool SH>
+Choice choose(int H, int64_t rows, int sms) {
+  if constexpr (!(FULL && BIAS && SH && DT != kF32)) {
+    if (H > 32 * Io<DT>::kVec) return make<DT, 2, FULL, BIAS, SH>(H, rows, sms);
+  }
+  return make<DT, 1, FULL, BIAS, SH>(H, rows, sms);
+}
+
+template <int DT, bool SH>
+Choice choose(int H, bool full, bool bias, int64_t rows, int sms) {
+  if (full) return bias ? choose<DT, true, true, SH>(H, rows, sms) : choose<DT, true, false, SH>(H, rows, sms);
+  return bias ? choose<DT, false, true, SH>(H, rows, sms) : choose<DT, false, false, SH>(H, rows, sms);
+}
+
+template <int DT>
+Choice choose(int H, bool aligned, bool full, bool bias, int64_t rows, int sms) {
+  return aligned ? choose<DT, false>(H, full, bias, rows, sms) : choose<DT, true>(H, full, bias, rows, sms);
+}
+
+Choice choose(int dtype, int H, bool aligned, bool full, bool bias, int64_t rows, int sms) {
+  return dtype == kF32   ? choose<kF32>(H, aligned, full, bias, rows, sms)
+         : dtype == kF16 ? choose<kF16>(H, aligned, full, bias, rows, sms)
+                         : choose<kBF16>(H, aligned, full, bias, rows, sms);
+}
+
+// Units (CTAs or clusters) of a launch: those that fit the device at once, no
+// more than the rows need.
+int64_t units_of(const Choice& c, int64_t rows, const DeviceInfo& dev) {
+  const int fit = resident_units(reinterpret_cast<const void*>(c.k), c.sh, c.smem, dev);
+  if (fit < 0) return fit;
+  const int64_t need = (rows + c.sh.rows - 1) / c.sh.rows;
+  return need < fit ? need : fit;
+}
+
+int64_t part_bytes(int64_t parts, int sums, int64_t Hp) { return parts * sums * Hp * 4; }
+
+// Quads a block: the most (of 2, 4, 8) whose partials a thread still loads in
+// one round.
+inline int sums_quads(int64_t parts, int sums) {
+  const int64_t one_round = kSumThreads * (8 / sums);
+  return 8 * parts <= one_round ? 8 : 4 * parts <= one_round ? 4 : 2;
+}
+
+template <bool FULL, bool BIAS>
+BwdKernel pick_sums(int quads) {
+  return quads == 8 ? &k_drop_sums<FULL, BIAS, 8> : quads == 4 ? &k_drop_sums<FULL, BIAS, 4> : &k_drop_sums<FULL, BIAS, 2>;
+}
+
+}  // namespace
+}  // namespace blk
+
+// What any number of rows up to this one needs: their CTAs are no more than
+// SMs, or than those that fit with as many rows side by side as there is room
+// for.
+int64_t drop_bwd_workspace_bytes(int dtype, bool aligned, bool full, bool bias, int64_t rows, int H,
+                                 const DeviceInfo& dev) {
+  using namespace blk;
+  const Choice ch = choose(dtype, H, aligned, full, bias, INT64_MAX / 2, dev.sms);
+  const int64_t fit = units_of(ch, INT64_MAX / 2, dev);
+  if (fit < 0) return fit;
+  int64_t units = fit > dev.sms ? fit : dev.sms;
+  if (units > rows) units = rows;
+  return part_bytes(units, drop_sums(full, bias), (H + 3) / 4 * 4);
+}
+
+int launch_drop_bwd(int dtype, bool aligned, const DropBwdArgs& args, void* ws, int64_t ws_bytes, const LaunchCtx& c) {
+  using namespace blk;
+  DropBwdArgs p = args;
+  const bool full = p.norm == ADDLN_NORM_LAYER || p.dbeta, bias = p.dbias != nullptr;
+  const Choice ch = choose(dtype, p.H, aligned, full, bias, p.rows, c.dev.sms);
+  p.w = walk_of(ch.sh);
+  p.parts = units_of(ch, p.rows, c.dev);
+  if (p.parts < 0) return static_cast<int>(p.parts);
+  p.kept_at = ch.kept_at;
+  p.sums_at = ch.sums_at;
+  p.Hp = (p.H + 3) / 4 * 4;
+  const bool cols = p.dgamma || p.dbeta || p.dbias;
+  p.part = nullptr;
+  if (cols) {
+    if (ws == nullptr || ws_bytes < part_bytes(p.parts, drop_sums(full, bias), p.Hp) || (reinterpret_cast<uintptr_t>(ws) & 15u))
+      return ADDLN_ERR_WORKSPACE;
+    p.part = static_cast<float*>(ws);
+  }
+  cudaError_t e = launch_units(ch.k, p.parts, ch.sh, ch.smem, c, p);
+  if (e == cudaSuccess && cols) {
+    const int quads = sums_quads(p.parts, drop_sums(full, bias));
+    const BwdKernel ks = full ? (bias ? pick_sums<true, true>(quads) : pick_sums<true, false>(quads))
+                              : (bias ? pick_sums<false, true>(quads) : pick_sums<false, false>(quads));
+    e = launch_kernel(ks, dim3(static_cast<unsigned>((p.Hp / 4 + quads - 1) / quads)), dim3(kSumThreads), 0, c.stream, c.pdl, p);
+  }
+  if (e != cudaSuccess) {
+    note_cuda_error(static_cast<int>(e));
+    return ADDLN_ERR_LAUNCH;
+  }
+  return ADDLN_OK;
+}
+
+ADDLN_BOUNDS_READER(read_bounds_drop_bwd)
+
+}  // namespace addln
