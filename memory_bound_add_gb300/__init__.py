@@ -67,3 +67,10 @@ from .drop import (  # noqa: F401
     dropout_train,
 )
 from .grads import clip_grad_norm_, clip_grads, grad_norm, grad_norm_workspace_size  # noqa: F401
+from .quant import (  # noqa: F401
+    NormQuant,
+    dequant_rows,
+    dequantise,
+    norm_quant,
+    norm_quant_fwd,
+)

@@ -21,6 +21,7 @@
 #include "block.h"
 #include "drop.h"
 #include "launch.h"
+#include "quant.h"
 
 using addln::DeviceInfo;
 using addln::LaunchCtx;
@@ -421,7 +422,7 @@ int addln_get_device_error(void* stream) {
       addln::read_bounds_bgr,       addln::read_bounds_add,      addln::read_bounds_bwd,
       addln::read_bounds_host,      addln::read_bounds_block_fwd, addln::read_bounds_block_bwd,
       addln::read_bounds_grad,      addln::read_bounds_drop,      addln::read_bounds_drop_fwd,
-      addln::read_bounds_drop_bwd};
+      addln::read_bounds_drop_bwd,  addln::read_bounds_quant,     addln::read_bounds_dequant};
   unsigned long long word = 0;
   for (auto f : readers) {
     unsigned long long w = 0;

@@ -1,0 +1,297 @@
+// Residual sum, norm and an output in 8 bits with its scales, in one pass:
+//   h = x + r,  y = norm(h),  q = round(y / scale)
+// x and r are read once, h, q and the scales written once; statistics and
+// largest values are of values in registers.
+#include "quant.cuh"
+
+namespace addln {
+namespace blk {
+
+// |v| of the largest, as bits: the order of non-negative floats is that of
+// their bits, with infinity and then NaN above all.
+template <int P>
+__device__ __forceinline__ uint32_t abs_max(const float2* v) {
+  uint32_t m = 0;
+#pragma unroll
+  for (int j = 0; j < P; ++j) m = max(m, max(__float_as_uint(v[j].x) & 0x7fffffffu, __float_as_uint(v[j].y) & 0x7fffffffu));
+  return m;
+}
+
+// Largest over the walker, in every thread.
+template <bool SIDES>
+__device__ __forceinline__ uint32_t walker_max(Exchange<SIDES>& ex, uint32_t m) {
+  m = __reduce_max_sync(0xffffffffu, m);
+  if (ex.w.warps == 1) return m;
+  const float4* b = ex(make_float4(__uint_as_float(m), 0.f, 0.f, 0.f));
+  m = 0;
+  for (int i = threadIdx.x & 31; i < ex.w.warps; i += 32) m = max(m, __float_as_uint(b[i].x));
+  return __reduce_max_sync(0xffffffffu, m);
+}
+
+// A scale and its reciprocal, of the largest |y|.
+struct Scale {
+  float s, inv;
+};
+
+__device__ __forceinline__ float reciprocal(float v) {
+  float r;
+  asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+  return r;
+}
+
+// amax: bits.  The quotient amax / top is taken as a product with 1 / top, and
+// y / scale later as one with the scale's reciprocal, which is good to a unit in
+// the last place: y's position between two values of 8 bits moves by some 2^-22
+// of itself.
+__device__ __forceinline__ Scale scale_of(uint32_t amax, float inv_top) {
+  const float nan = __uint_as_float(0x7fffffffu);
+  if (amax >= 0x7f800000u) return {nan, nan};
+  const float s = fmaxf(__uint_as_float(amax) * inv_top, 0x1p-126f);
+  return {s, reciprocal(s)};
+}
+
+// The least power of two 2^e with amax <= top 2^e: top = m 2^t, and amax's
+// exponent goes up by one where its mantissa is above m's.
+__device__ __forceinline__ Scale pow2_of(uint32_t amax, int format) {
+  const float nan = __uint_as_float(0x7fffffffu);
+  if (amax >= 0x7f800000u) return {nan, nan};
+  const uint32_t mantissa = format == ADDLN_Q_INT8 ? 0x7e0000u : 0x600000u;
+  const int t = format == ADDLN_Q_E4M3 ? 8 : format == ADDLN_Q_E5M2 ? 15 : 6;
+  const int e = max(static_cast<int>((amax + (0x7fffffu - mantissa)) >> 23) - t, 1);  // biased
+  return {__uint_as_float(static_cast<uint32_t>(e) << 23), __uint_as_float(static_cast<uint32_t>(254 - e) << 23)};
+}
+
+// gamma and, with FULL, beta: in registers or in shared memory, as in
+// block_fwd.cu.
+__host__ __device__ constexpr bool quant_in_registers(int columns, bool full, bool sh) { return columns <= 8 || !(full || sh); }
+
+template <int VE, int NV, bool FULL, bool SH>
+struct QuantParams {
+  static constexpr bool kRegs = quant_in_registers(NV * VE, FULL, SH);
+  static constexpr int P = kRegs ? NV * VE / 2 : 1, N = FULL ? 2 : 1;
+  float2 r[N][P];
+  Kept<VE, NV> kept;
+
+  __device__ __forceinline__ void get(int i, int k, float2 (&v)[VE / 2]) const {
+    if constexpr (kRegs) {
+#pragma unroll
+      for (int j = 0; j < VE / 2; ++j) v[j] = r[i][k * VE / 2 + j];
+    } else {
+      kept.get(i, k, v);
+    }
+  }
+  __device__ __forceinline__ void load(const QuantArgs& p, int c, int k) {
+    const float* from[2] = {p.gamma, p.beta};
+#pragma unroll
+    for (int i = 0; i < N; ++i) {
+      float v[VE];
+      load_params<VE, SH>(from[i], c, p.H, 0.f, v, 800 + i);
+      if constexpr (kRegs) {
+#pragma unroll
+        for (int e = 0; e < VE / 2; ++e) r[i][k * VE / 2 + e] = make_float2(v[2 * e], v[2 * e + 1]);
+      } else {
+        kept.put(i, k, v);
+      }
+    }
+  }
+};
+
+// FULL: a layer norm or a beta.  SH: some rows do not begin on borders.
+template <int DT, int NV, bool FULL, bool SH>
+__global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
+    k_norm_quant(const __grid_constant__ QuantArgs p) {
+  using IO = Io<DT>;
+  constexpr int S = IO::kBytes, VE = IO::kVec, Q = VE / 2;
+  constexpr int P = NV * Q;
+  using R = Ring<DT, NV, 2, SH>;
+  using W = typename Bytes<VE>::W;
+  extern __shared__ __align__(128) unsigned char smem[];
+  if (p.w.C > 1) cluster_started();
+  const int slots = p.slots;
+  const int lane = threadIdx.x & 31;
+  const int side = (threadIdx.x >> 5) / p.w.cta_warps, warp = (threadIdx.x >> 5) - side * p.w.cta_warps;
+  const int rank = p.w.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.w.C);
+  const int64_t stride = static_cast<int64_t>(gridDim.x / p.w.C) * p.w.rows_per_cta;
+  int64_t row = static_cast<int64_t>(blockIdx.x / p.w.C) * p.w.rows_per_cta + side;
+  const int col0 = rank * p.w.slice;
+  const int64_t elements = p.rows * static_cast<int64_t>(p.H), extent = elements * S;
+  Exchange<!quant_in_registers(NV * VE, FULL, SH)> ex{p.w, p.sums_at + side * 2 * p.w.warps * 16, 0};
+  const bool leader = rank == 0 && lane == 0 && warp == 0;
+  const bool has_r = p.r != nullptr, has_norm = p.norm != ADDLN_NORM_NONE;
+  R ring;
+  ring.base = smem_addr(smem) + (threadIdx.x >> 5) * p.ring_slots * R::kSlot + lane * 16;
+  Cols<VE, NV> cs;
+  cs.init(warp, col0, min(p.w.slice, p.H - col0));
+  auto fetch = [&](int slot, int64_t r) {
+    if (r < p.rows) {
+      const int64_t at = (r * p.H + cs.c0) * S;
+      ring.template fetch<0>(cs, slot, p.x, at, 802, extent);
+      if (has_r) ring.template fetch<1>(cs, slot, p.r, at, 803, extent);
+    }
+    ring.commit();
+  };
+  pdl_trigger();
+  pdl_wait();
+  for (int s = 0; s < slots; ++s) fetch(s, row + s * stride);
+  QuantParams<VE, NV, FULL, SH> par;
+  constexpr bool kRegs = QuantParams<VE, NV, FULL, SH>::kRegs;
+  if constexpr (!kRegs)
+    par.kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<FULL ? 2 : 1>() + lane * 16;
+  if (kRegs || side == 0) {
+#pragma unroll
+    for (int k = 0; k < NV; ++k) par.load(p, cs.col(k), k);
+  }
+  if constexpr (!kRegs) __syncthreads();
+  const int format = p.s.format, scaling = p.s.scaling;
+  const float inv_top = 1.f / static_cast<float>(q_top(format));
+  float given = 0.f;
+  if (scaling == ADDLN_SCALE_TENSOR && ADDLN_IN(804, 0, 4, 4)) given = reciprocal(__ldg(static_cast<const float*>(p.s.scale)));
+  if (p.w.C > 1) cluster_wait_started();
+
+  for (int slot = 0; row < p.rows; row += stride, slot = slot + 1 == slots ? 0 : slot + 1) {
+    if (slots == 1) ring.template wait<0>(); else ring.template wait<1>();
+    ring.meet();
+    const int64_t at = row * p.H + cs.c0, off = at * S;
+    const int sx = SH ? low4(p.x, off) : 0, sr = SH && has_r ? low4(p.r, off) : 0;
+    float2 v[P];
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      IO::to_pairs(ring.take(slot, 0, k, sx), v + k * Q);
+      if (has_r) {
+        float2 r[Q];
+        IO::to_pairs(ring.take(slot, 1, k, sr), r);
+#pragma unroll
+        for (int i = 0; i < Q; ++i) v[k * Q + i] = add2(v[k * Q + i], r[i]);
+      }
+    }
+    if constexpr (SH) cs.clear(v);
+    ring.meet();
+    fetch(slot, row + slots * stride);  // the slot has been read
+    if (p.h != nullptr) {
+      Writer<DT, NV, SH> out;
+#pragma unroll
+      for (int k = 0; k < NV; ++k) out.put(cs, p.h, off, k, IO::from_pairs(v + k * Q), 805, extent);
+    }
+    if (has_norm) {
+      const RowStat st = row_norm<VE, NV, FULL>(ex, v, cs, p.norm == ADDLN_NORM_LAYER, p.inv_h, p.eps);
+      if (leader && ADDLN_IN(806, 4 * row, 4, 4 * p.rows)) {
+        if (p.rstd) p.rstd[row] = st.M2;
+        if (FULL && p.mean) p.mean[row] = st.mean;
+      }
+      const float2 negm = dup2(-st.m), r2 = dup2(st.M2);
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        float2 g[Q], e[Q];
+        par.get(0, k, g);
+        if constexpr (FULL) par.get(1, k, e);
+#pragma unroll
+        for (int i = 0; i < Q; ++i) {
+          const int j = k * Q + i;
+          if constexpr (FULL)
+            v[j] = fma2(mul2(add2(v[j], negm), r2), g[i], e[i]);
+          else
+            v[j] = mul2(mul2(v[j], r2), g[i]);
+        }
+      }
+    }
+    Scale sc{0.f, given};
+    if (scaling == ADDLN_SCALE_ROW) {
+      sc = scale_of(walker_max(ex, abs_max<P>(v)), inv_top);
+      if (leader && ADDLN_IN(807, 4 * row, 4, 4 * p.rows)) static_cast<float*>(p.s.scale)[row] = sc.s;
+    }
+    ByteWriter<VE, NV, SH> out;
+#pragma unroll
+    for (int k = 0; k < NV; ++k) {
+      if (scaling == ADDLN_SCALE_GROUP || scaling == ADDLN_SCALE_POW2) {
+        const int lanes = (1 << p.s.lanes_shift) / VE;  // of a group
+        uint32_t m = abs_max<Q>(v + k * Q);
+        for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
+        const bool pow2 = scaling == ADDLN_SCALE_POW2;
+        sc = pow2 ? pow2_of(m, format) : scale_of(m, inv_top);
+        if ((lane & (lanes - 1)) == 0 && cs.ok(k)) {
+          const int g = cs.col(k) >> p.s.lanes_shift;
+          const int64_t i = p.s.group_major ? g * p.rows + row : row * p.s.groups + g;
+          if (ADDLN_IN(808, i, 1, p.rows * p.s.groups)) {
+            if (pow2)
+              static_cast<uint8_t*>(p.s.scale)[i] = static_cast<uint8_t>(min(__float_as_uint(sc.s) >> 23, 255u));
+            else
+              static_cast<float*>(p.s.scale)[i] = sc.s;
+          }
+        }
+      }
+      const float2 inv = dup2(sc.inv);
+      W w = to_q(format, mul2(v[k * Q], inv), mul2(v[k * Q + 1], inv));
+      if constexpr (VE == 8)
+        w |= static_cast<W>(to_q(format, mul2(v[k * Q + 2], inv), mul2(v[k * Q + 3], inv))) << 32;
+      out.put(cs, p.q, at, k, w, 809, elements);
+    }
+  }
+  // a CTA's shared memory has to outlive its peers' writes into it
+  if (p.w.C > 1) cooperative_groups::this_cluster().sync();
+}
+
+// ------------------------------------------------------------------ host
+namespace {
+
+struct Choice {
+  void (*k)(QuantArgs) = nullptr;
+  Spread s;
+};
+
+template <int DT, int NV, bool SH>
+Choice make(const QuantArgs& p, bool full, int sms) {
+  constexpr int VE = Io<DT>::kVec;
+  Choice c;
+  c.k = full ? &k_norm_quant<DT, NV, true, SH> : &k_norm_quant<DT, NV, false, SH>;
+  const bool shared = !quant_in_registers(NV * VE, full, SH);
+  // a CTA's slice of a row holds whole groups
+  c.s = spread(p.H, VE, NV, p.rows, sms, Ring<DT, NV, 2, SH>::kSlot,
+               !shared ? 0 : full ? Kept<VE, NV>::template bytes<2>() : Kept<VE, NV>::template bytes<1>(), 128);
+  return c;
+}
+
+template <int DT, bool SH>
+Choice choose(const QuantArgs& p, bool full, int sms) {
+  constexpr int VE = Io<DT>::kVec;
+  switch (groups_a_thread((p.H + VE - 1) / VE)) {
+    case 1: return make<DT, 1, SH>(p, full, sms);
+    case 2: return make<DT, 2, SH>(p, full, sms);
+    case 3: return make<DT, 3, SH>(p, full, sms);
+    default: return make<DT, 4, SH>(p, full, sms);
+  }
+}
+
+template <int DT>
+Choice choose(const QuantArgs& p, bool aligned, bool full, int sms) {
+  return aligned ? choose<DT, false>(p, full, sms) : choose<DT, true>(p, full, sms);
+}
+
+}  // namespace
+}  // namespace blk
+
+int launch_norm_quant(int dtype, bool aligned, const QuantArgs& args, const LaunchCtx& c) {
+  using namespace blk;
+  const bool full = args.norm == ADDLN_NORM_LAYER || args.beta;
+  const Choice ch = dtype == kF32 ? choose<kF32>(args, aligned, full, c.dev.sms)
+                    : dtype == kF16 ? choose<kF16>(args, aligned, full, c.dev.sms)
+                                    : choose<kBF16>(args, aligned, full, c.dev.sms);
+  QuantArgs p = args;
+  p.w = walk_of(ch.s.sh);
+  p.kept_at = ch.s.kept_at;
+  p.sums_at = ch.s.sums_at;
+  p.ring_slots = ch.s.ring_slots;
+  const int fit = resident_units(reinterpret_cast<const void*>(ch.k), ch.s.sh, ch.s.smem, c.dev);
+  if (fit < 0) return fit;
+  p.slots = slots_ahead(p.rows, fit, ch.s);
+  const int64_t need = (p.rows + ch.s.sh.rows - 1) / ch.s.sh.rows;
+  const cudaError_t e = launch_units(ch.k, need < fit ? need : fit, ch.s.sh, ch.s.smem, c, p);
+  if (e != cudaSuccess) {
+    note_cuda_error(static_cast<int>(e));
+    return ADDLN_ERR_LAUNCH;
+  }
+  return ADDLN_OK;
+}
+
+ADDLN_BOUNDS_READER(read_bounds_quant)
+
+}  // namespace addln

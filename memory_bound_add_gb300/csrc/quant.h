@@ -1,0 +1,57 @@
+// Internal interface between the 8-bit entry points (quant_api.cu) and their
+// kernels.
+#pragma once
+
+#include <stdint.h>
+
+#include "block.h"
+
+namespace addln {
+
+// Where the scales of a call are: as quant_api.cu's callers give them; group a
+// power of two (0: one for the row, or given), groups: of a row.
+struct ScaleSpec {
+  void* scale;
+  int format, scaling, group_major;
+  int lanes_shift;  // log2(group)
+  int groups;
+};
+
+// Arguments of one norm_quant_fwd launch; the meaning of each is the entry
+// point's.
+struct QuantArgs {
+  const void* x;
+  const void* r;
+  const float* gamma;
+  const float* beta;
+  void* q;
+  void* h;
+  float* mean;
+  float* rstd;
+  ScaleSpec s;
+  int64_t rows;
+  int H, norm;
+  float eps, inv_h;
+  int slots, ring_slots;
+  int kept_at, sums_at;
+  Walk w;
+};
+
+struct DequantArgs {
+  const void* q;
+  void* out;
+  ScaleSpec s;
+  int64_t rows;
+  int H;
+};
+
+// aligned: every row of every tensor in the I/O dtype, and every vector, begins
+// and ends on 16-byte borders, and every row of q on borders of 16 bytes over
+// the I/O type's size.
+int launch_norm_quant(int dtype, bool aligned, const QuantArgs& p, const LaunchCtx& c);
+int launch_dequant(int dtype, bool aligned, const DequantArgs& p, const LaunchCtx& c);
+
+int read_bounds_quant(unsigned long long* word);
+int read_bounds_dequant(unsigned long long* word);
+
+}  // namespace addln
