@@ -66,7 +66,7 @@ struct Cols {
   static constexpr int P = NV * VE / 2;
   int c0;           // first column of group 0
   int left;         // columns of the slice from c0 on (may be 0 or less)
-  bool all;         // every group of the warp is whole
+  int whole;        // groups k below this are whole in every lane of the warp
   float n, inv_n;   // columns of the warp, 1 / n (0 for none)
 
   __device__ __forceinline__ void init(int warp, int col0, int cols) {
@@ -76,7 +76,7 @@ struct Cols {
     const int own = min(max(cols - warp * NV * kStep, 0), NV * kStep);
     n = static_cast<float>(own);
     inv_n = own ? __frcp_rn(n) : 0.f;
-    all = own == NV * kStep;
+    whole = own / kStep;
   }
   __device__ __forceinline__ int col(int k) const { return c0 + k * kStep; }
   __device__ __forceinline__ bool ok(int k) const { return left > k * kStep; }
@@ -84,11 +84,15 @@ struct Cols {
   __device__ __forceinline__ int valid(int k) const { return min(max(left - k * kStep, 0), VE); }
   // zeros in the slots of columns that do not exist
   __device__ __forceinline__ void clear(float2 (&v)[P]) const {
-    if (all) return;
+    if (whole == NV) return;
 #pragma unroll
-    for (int e = 0; e < NV * VE; ++e) {
-      float& u = (e & 1) ? v[e >> 1].y : v[e >> 1].x;
-      u = left > (e / VE) * kStep + e % VE ? u : 0.f;
+    for (int k = 0; k < NV; ++k) {
+      if (k < whole) continue;  // the same for the warp
+#pragma unroll
+      for (int e = k * VE; e < (k + 1) * VE; ++e) {
+        float& u = (e & 1) ? v[e >> 1].y : v[e >> 1].x;
+        u = left > k * kStep + e % VE ? u : 0.f;
+      }
     }
   }
 };

@@ -6,98 +6,194 @@ namespace addln {
 namespace blk {
 
 constexpr int kDequantThreads = 256;
-constexpr int kPieces = 4;  // pieces of a row that a warp has in flight
 
-// VE bytes from offset `at` of q on, which may be any; what lies past `n` of
-// them is 0 and not read.
+// A warp's row of words from offset `at` of q on, this lane's first; n: bytes of
+// the row from there on.  Rows that begin off the words' borders (SH): each lane
+// reads the word that its bytes begin in and takes the rest from the next lane's;
+// words that reach over the tensor's own ends are put together from their bytes.
 template <int VE, bool SH>
-__device__ __forceinline__ typename Bytes<VE>::W load_bytes(const void* q, int64_t at, int n, int64_t extent) {
+__device__ __forceinline__ typename Bytes<VE>::W load_word(const void* q, int64_t at, int n, int64_t extent) {
   using W = typename Bytes<VE>::W;
   const char* p = static_cast<const char*>(q) + at;
   if constexpr (!SH) {
     return n > 0 && ADDLN_IN(820, at, VE, extent) ? __ldcs(reinterpret_cast<const W*>(p)) : 0;
   } else {
-    W w = 0;
+    const int s = static_cast<int>(reinterpret_cast<uintptr_t>(p) & (VE - 1));  // the same for the warp
+    auto word = [&](int64_t o) {
+      const char* a = static_cast<const char*>(q) + o;
+      if (o >= 0 && o + VE <= extent) return __ldg(reinterpret_cast<const W*>(a));
+      W w = 0;
 #pragma unroll
-    for (int e = 0; e < VE; ++e)
-      if (e < n && ADDLN_IN(821, at + e, 1, extent))
-        w |= static_cast<W>(__ldg(reinterpret_cast<const uint8_t*>(p) + e)) << (8 * e);
-    return w;
+      for (int e = 0; e < VE; ++e)
+        if (o + e >= 0 && o + e < extent) w |= static_cast<W>(__ldg(reinterpret_cast<const uint8_t*>(a) + e)) << (8 * e);
+      return w;
+    };
+    const W lo = n + s > 0 ? word(at - s) : 0;  // of a lane past the end: its neighbour's last bytes
+    if (s == 0) return lo;
+    W hi = __shfl_down_sync(0xffffffffu, lo, 1);
+    if ((threadIdx.x & 31) == 31) hi = n > VE - s ? word(at - s + VE) : 0;
+    return (lo >> (8 * s)) | (hi << (8 * (VE - s)));
   }
 }
 
-// A warp takes pieces of 32 VE columns of a row, kPieces at a time.
-template <int DT, bool SH>
-__global__ void __launch_bounds__(kDequantThreads) k_dequant(const __grid_constant__ DequantArgs p, int pieces) {
+// A scale from its bits.  2^(e - 127) as bits is e << 23, but for 2^-127 and NaN.
+__device__ __forceinline__ float scale_from(uint32_t e, bool pow2) {
+  return __uint_as_float(!pow2 ? e : e == 255 ? 0x7fffffffu : e == 0 ? 0x400000u : e << 23);
+}
+__device__ __forceinline__ uint32_t load_scale(const DequantArgs& p, int64_t i, bool pow2) {
+  if (!ADDLN_IN(822, i, 1, p.scales)) return 0;
+  return pow2 ? __ldg(static_cast<const uint8_t*>(p.s.scale) + i) : __ldg(static_cast<const uint32_t*>(p.s.scale) + i);
+}
+
+// Rows that are whole vectors of 32 bytes of out on such borders: the tensor is
+// one run of vectors, of which a CTA takes kRun a thread.  32-byte stores, and
+// 16 bytes of q a load (8 for fp32): 32768x8192 from e4m3 to bf16 110 us (7.3 TB/s)
+// where warps of rows, 8 bytes a load, take 183.
+constexpr int kRun = 4;
+
+template <int DT, int FMT>
+__global__ void __launch_bounds__(kDequantThreads) k_dequant_run(const __grid_constant__ DequantArgs p) {
+  using IO = Io<DT>;
+  constexpr int S = IO::kBytes, VW = 32 / S, N = VW / 4;  // columns and words of q a vector
+  pdl_trigger();
+  pdl_wait();
+  const uint32_t G = static_cast<uint32_t>(p.H / VW);  // vectors a row
+  const uint64_t v0 = static_cast<uint64_t>(blockIdx.x) * (kDequantThreads * kRun);
+  const uint64_t row0 = (v0 >> 32) ? v0 / G : static_cast<uint32_t>(v0) / G;
+  const uint32_t in_row = static_cast<uint32_t>(v0 - row0 * G);
+  const uint64_t vectors = static_cast<uint64_t>(p.rows) * G;
+  const bool pow2 = p.s.scaling == ADDLN_SCALE_POW2;
+  uint32_t w[kRun][N], s[kRun];
+#pragma unroll
+  for (int j = 0; j < kRun; ++j) {
+    const uint32_t t = j * kDequantThreads + threadIdx.x;
+    const uint64_t v = v0 + t;
+    s[j] = 0;
+#pragma unroll
+    for (int i = 0; i < N; ++i) w[j][i] = 0;
+    if (v >= vectors) continue;
+    // in_row + t is below G + 1024, far below 2^32 / G: the product's upper half
+    // with 2^32 / G rounded up is the exact quotient
+    const uint32_t r = __umulhi(in_row + t, p.reciprocal), c = in_row + t - r * G;
+    const int64_t at = static_cast<int64_t>(v) * VW;
+    if (ADDLN_IN(825, at, VW, p.rows * static_cast<int64_t>(p.H))) {
+      const char* q = static_cast<const char*>(p.q) + at;
+      if constexpr (N == 4) {
+        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(q));
+        w[j][0] = u.x, w[j][1] = u.y, w[j][2] = u.z, w[j][3] = u.w;
+      } else {
+        const uint2 u = __ldcs(reinterpret_cast<const uint2*>(q));
+        w[j][0] = u.x, w[j][1] = u.y;
+      }
+    }
+    s[j] = load_scale(p, static_cast<int64_t>(row0 + r) * p.scale_row + ((c * VW) >> p.s.lanes_shift) * p.scale_group, pow2);
+  }
+#pragma unroll
+  for (int j = 0; j < kRun; ++j) {
+    const uint64_t v = v0 + j * kDequantThreads + threadIdx.x;
+    if (v >= vectors) break;
+    const float2 sc = dup2(scale_from(s[j], pow2));
+    float2 f[VW / 2];
+#pragma unroll
+    for (int i = 0; i < N; ++i) from_q<FMT>(w[j][i], f[2 * i], f[2 * i + 1]);
+#pragma unroll
+    for (int i = 0; i < VW / 2; ++i) f[i] = mul2(f[i], sc);
+    const int64_t at = static_cast<int64_t>(v) * 32;
+    if (!ADDLN_IN(826, at, 32, p.rows * static_cast<int64_t>(p.H) * S)) continue;
+    const uint4 a = IO::from_pairs(f), b = IO::from_pairs(f + VW / 4);
+    asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(static_cast<char*>(p.out) + at),
+                 "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w), "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+                 : "memory");
+  }
+}
+
+// Other rows: a warp takes 32 VE columns of R rows, whose loads are all in flight.
+constexpr int R = 4;
+
+template <int DT, int FMT, bool SH>
+__global__ void __launch_bounds__(kDequantThreads) k_dequant(const __grid_constant__ DequantArgs p) {
   using IO = Io<DT>;
   constexpr int S = IO::kBytes, VE = IO::kVec, Q = VE / 2;
   using W = typename Bytes<VE>::W;
-  using C = Cols<VE, 1>;
   pdl_trigger();
   pdl_wait();
-  const int lane = threadIdx.x & 31;
-  const int64_t u0 = (static_cast<int64_t>(blockIdx.x) * (kDequantThreads / 32) + (threadIdx.x >> 5)) * kPieces;
+  const uint32_t warp = blockIdx.x * (kDequantThreads / 32) + (threadIdx.x >> 5);
+  const uint32_t block = warp / static_cast<uint32_t>(p.pieces);
+  const int piece = static_cast<int>(warp - block * static_cast<uint32_t>(p.pieces));
+  const int64_t row0 = static_cast<int64_t>(block) * R;
+  if (row0 >= p.rows) return;
+  const int n = static_cast<int>(min(static_cast<int64_t>(R), p.rows - row0));
   const int64_t elements = p.rows * static_cast<int64_t>(p.H);
-  int64_t row = u0 / pieces;
-  int piece = static_cast<int>(u0 - row * pieces);
-  const int format = p.s.format, scaling = p.s.scaling;
-  W w[kPieces];
-  float s[kPieces];
-  int64_t rows[kPieces];
-  int at[kPieces];
+  Cols<VE, 1> cs;
+  cs.c0 = piece * (32 * VE) + (threadIdx.x & 31) * VE;
+  cs.left = p.H - cs.c0;
+  const int64_t at0 = row0 * p.H + cs.c0;
+  const bool pow2 = p.s.scaling == ADDLN_SCALE_POW2;
+  const int64_t s0 = row0 * p.scale_row + (cs.c0 >> p.s.lanes_shift) * p.scale_group;
+  W w[R];
+  uint32_t s[R];
 #pragma unroll
-  for (int j = 0; j < kPieces; ++j) {
-    rows[j] = row, at[j] = piece * C::kStep;
-    const int c = at[j] + lane * VE;
-    w[j] = 0, s[j] = 0.f;
-    if (row < p.rows && c < p.H) {
-      w[j] = load_bytes<VE, SH>(p.q, row * p.H + c, p.H - c, elements);
-      if (scaling == ADDLN_SCALE_TENSOR || scaling == ADDLN_SCALE_ROW) {
-        const int64_t i = scaling == ADDLN_SCALE_ROW ? row : 0;
-        if (ADDLN_IN(822, 4 * i, 4, scaling == ADDLN_SCALE_ROW ? 4 * p.rows : 4)) s[j] = __ldg(static_cast<const float*>(p.s.scale) + i);
-      } else {
-        const int g = c >> p.s.lanes_shift;
-        const int64_t i = p.s.group_major ? g * p.rows + row : row * p.s.groups + g;
-        if (ADDLN_IN(823, i, 1, p.rows * p.s.groups)) {
-          if (scaling == ADDLN_SCALE_GROUP) {
-            s[j] = __ldg(static_cast<const float*>(p.s.scale) + i);
-          } else {
-            // 2^(e - 127): as bits e << 23, but for 2^-127 and NaN
-            const uint32_t e = __ldg(static_cast<const uint8_t*>(p.s.scale) + i);
-            s[j] = __uint_as_float(e == 255 ? 0x7fffffffu : e == 0 ? 0x400000u : e << 23);
-          }
-        }
-      }
+  for (int j = 0; j < R; ++j) {
+    w[j] = 0, s[j] = 0;
+    if (j < n) {
+      w[j] = load_word<VE, SH>(p.q, at0 + static_cast<int64_t>(j) * p.H, cs.left, elements);
+      if (cs.left > 0) s[j] = load_scale(p, s0 + j * p.scale_row, pow2);
     }
-    if (++piece == pieces) piece = 0, ++row;
   }
 #pragma unroll
-  for (int j = 0; j < kPieces; ++j) {
-    if (rows[j] >= p.rows) break;
-    C cs;
-    cs.c0 = at[j] + lane * VE;
-    cs.left = p.H - cs.c0;
+  for (int j = 0; j < R; ++j) {
+    if (j >= n) break;
+    const float2 sc = dup2(scale_from(s[j], pow2));
     float2 v[Q];
-    from_q(format, static_cast<uint32_t>(w[j]), v[0], v[1]);
-    if constexpr (VE == 8) from_q(format, static_cast<uint32_t>(w[j] >> 32), v[2], v[3]);
+    from_q<FMT>(static_cast<uint32_t>(w[j]), v[0], v[1]);
+    if constexpr (VE == 8) from_q<FMT>(static_cast<uint32_t>(w[j] >> 32), v[2], v[3]);
 #pragma unroll
-    for (int i = 0; i < Q; ++i) v[i] = mul2(v[i], dup2(s[j]));
+    for (int i = 0; i < Q; ++i) v[i] = mul2(v[i], sc);
     Writer<DT, 1, SH> out;
-    out.put(cs, p.out, (rows[j] * p.H + cs.c0) * S, 0, IO::from_pairs(v), 824, elements * S);
+    out.put(cs, p.out, (at0 + static_cast<int64_t>(j) * p.H) * S, 0, IO::from_pairs(v), 824, elements * S);
   }
 }
 
+namespace {
+using DequantKernel = void (*)(DequantArgs);
+template <int DT, int FMT>
+DequantKernel pick(bool run, bool aligned) {
+  return run ? &k_dequant_run<DT, FMT> : aligned ? &k_dequant<DT, FMT, false> : &k_dequant<DT, FMT, true>;
+}
+template <int DT>
+DequantKernel pick(int format, bool run, bool aligned) {
+  return format == ADDLN_Q_E4M3   ? pick<DT, ADDLN_Q_E4M3>(run, aligned)
+         : format == ADDLN_Q_E5M2 ? pick<DT, ADDLN_Q_E5M2>(run, aligned)
+                                  : pick<DT, ADDLN_Q_INT8>(run, aligned);
+}
+}  // namespace
 }  // namespace blk
 
-int launch_dequant(int dtype, bool aligned, const DequantArgs& p, const LaunchCtx& c) {
+int launch_dequant(int dtype, bool aligned, const DequantArgs& args, const LaunchCtx& c) {
   using namespace blk;
-  void (*k)(DequantArgs, int) = dtype == kF32   ? (aligned ? &k_dequant<kF32, false> : &k_dequant<kF32, true>)
-                                : dtype == kF16 ? (aligned ? &k_dequant<kF16, false> : &k_dequant<kF16, true>)
-                                                : (aligned ? &k_dequant<kBF16, false> : &k_dequant<kBF16, true>);
-  const int step = dtype == kF32 ? 128 : 256, pieces = (p.H + step - 1) / step;
-  const int64_t per = kDequantThreads / 32 * kPieces, ctas = (p.rows * pieces + per - 1) / per;
-  if (ctas > 0x7fffffff) return ADDLN_ERR_SHAPE;
-  const cudaError_t e = launch_kernel(k, dim3(static_cast<unsigned>(ctas)), dim3(kDequantThreads), 0, c.stream, c.pdl, p, pieces);
+  DequantArgs p = args;
+  const int step = dtype == kF32 ? 128 : 256;
+  p.pieces = (p.H + step - 1) / step;
+  const bool group = p.s.scaling == ADDLN_SCALE_GROUP || p.s.scaling == ADDLN_SCALE_POW2;
+  p.scale_row = p.s.scaling == ADDLN_SCALE_TENSOR ? 0 : p.s.group_major ? 1 : p.s.groups;
+  p.scale_group = !group ? 0 : p.s.group_major ? p.rows : 1;
+  p.scales = p.s.scaling == ADDLN_SCALE_TENSOR ? 1 : p.rows * p.s.groups;
+  const int VW = step / 16;
+  // (rows of one vector: 2^32 / G does not fit a word)
+  const bool run = aligned && p.H > VW && p.H % VW == 0 && (reinterpret_cast<uintptr_t>(p.out) & 31) == 0 &&
+                   (reinterpret_cast<uintptr_t>(p.q) & (VW - 1)) == 0;
+  const DequantKernel k = dtype == kF32   ? pick<kF32>(p.s.format, run, aligned)
+                          : dtype == kF16 ? pick<kF16>(p.s.format, run, aligned)
+                                          : pick<kBF16>(p.s.format, run, aligned);
+  int64_t units = (p.rows + R - 1) / R * p.pieces, per = kDequantThreads / 32;  // warps
+  if (run) {
+    const uint32_t G = static_cast<uint32_t>(p.H / VW);
+    p.reciprocal = static_cast<uint32_t>(((uint64_t{1} << 32) + G - 1) / G);
+    units = p.rows * G, per = kDequantThreads * kRun;
+  }
+  const int64_t ctas = (units + per - 1) / per;
+  if (ctas > (int64_t{1} << 28)) return ADDLN_ERR_SHAPE;  // a warp's number has 32 bits
+  const cudaError_t e = launch_kernel(k, dim3(static_cast<unsigned>(ctas)), dim3(kDequantThreads), 0, c.stream, c.pdl, p);
   if (e != cudaSuccess) {
     note_cuda_error(static_cast<int>(e));
     return ADDLN_ERR_LAUNCH;

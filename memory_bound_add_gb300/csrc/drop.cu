@@ -39,7 +39,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const void* x, void* y, in
     if (b * 8 >= n) break;
     uint4 w = make_uint4(0, 0, 0, 0);
     uint32_t above = d.above;
-    if (d.on) w = rng(b);
+    if (d.on) w = rng(b, d.wide);
     const uint32_t t[4] = {w.x, w.y, w.z, w.w};
     if (b < whole) {
 #pragma unroll

@@ -10,12 +10,13 @@ namespace addln {
 
 // A mask, as the kernels take it.  above: an element is kept where its 16
 // bits, in the upper half of a word, make that word larger (t 65536 - 1).
-// on: something is dropped (t > 0).  scale: of what is kept.
+// on: something is dropped (t > 0).  wide: the tensor has more than 2^32 blocks
+// of 8 elements.  scale: of what is kept.
 struct DropSpec {
   const int64_t* rng;  // seed and offset in device memory, or NULL
   uint64_t seed, offset;
   uint32_t above;
-  int on;
+  int on, wide;
   float scale;
 };
 

@@ -22,8 +22,8 @@ int check_shape(int64_t rows, int64_t H, int dtype) {
   return ADDLN_OK;
 }
 
-// The mask's numbers for p in [0, 1].
-int drop_spec(double p, const int64_t* rng, uint64_t seed, uint64_t offset, DropSpec* d) {
+// The mask's numbers for p in [0, 1] and n elements.
+int drop_spec(double p, const int64_t* rng, uint64_t seed, uint64_t offset, int64_t n, DropSpec* d) {
   if (!(p >= 0.0 && p <= 1.0)) return ADDLN_ERR_SCALE;
   const int64_t t = static_cast<int64_t>(nearbyint(p * 65536.0));
   d->rng = rng;
@@ -31,6 +31,7 @@ int drop_spec(double p, const int64_t* rng, uint64_t seed, uint64_t offset, Drop
   d->offset = offset;
   d->above = static_cast<uint32_t>(t * 65536 - 1);
   d->on = t > 0;
+  d->wide = n > (int64_t{1} << 35);
   d->scale = t < 65536 ? static_cast<float>(65536.0 / static_cast<double>(65536 - t)) : 0.f;
   return (bits(rng) & 7) ? ADDLN_ERR_ALIGN : ADDLN_OK;
 }
@@ -58,7 +59,7 @@ int dropout_fwd(const void* x, void* y, int64_t n, double p, const int64_t* rng,
   if (!valid_dtype(dtype)) return ADDLN_ERR_DTYPE;
   if (n < 0 || n > INT64_MAX / 4) return ADDLN_ERR_SHAPE;
   DropSpec d;
-  int rc = drop_spec(p, rng, seed, offset, &d);
+  int rc = drop_spec(p, rng, seed, offset, n, &d);
   if (rc != ADDLN_OK || n == 0) return rc;
   if (!x || !y) return ADDLN_ERR_NULL;
   const int es = elem_bytes(dtype);
@@ -81,7 +82,7 @@ int dropout_add_norm_fwd(const void* f, const void* x, const float* bias, double
   if (rc != ADDLN_OK) return rc;
   if (!valid_norm(norm)) return ADDLN_ERR_KIND;
   DropSpec d;
-  rc = drop_spec(p, rng, seed, offset, &d);
+  rc = drop_spec(p, rng, seed, offset, rows * H, &d);
   if (rc != ADDLN_OK) return rc;
   if (!(eps >= 0.0f) || isinf(eps)) return ADDLN_ERR_EPS;
   const bool has = norm != ADDLN_NORM_NONE;
@@ -138,7 +139,7 @@ int dropout_add_norm_bwd(const void* dy, const void* dh, const void* h, double p
   if (rc != ADDLN_OK) return rc;
   if (!valid_norm(norm)) return ADDLN_ERR_KIND;
   DropSpec d;
-  rc = drop_spec(p, rng, seed, offset, &d);
+  rc = drop_spec(p, rng, seed, offset, rows * H, &d);
   if (rc != ADDLN_OK) return rc;
   if (norm == ADDLN_NORM_NONE && (dy || gamma || mean || rstd || dgamma || dbeta)) return ADDLN_ERR_KIND;
   if (workspace_bytes < 0) return ADDLN_ERR_WORKSPACE;

@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     const int64_t off = offset(row);
     const uint64_t at = static_cast<uint64_t>(row) * static_cast<uint32_t>(p.H) + static_cast<uint32_t>(cs.c0);
     Mask<VE, NV, SH> mask;
-    if (p.drop.on) mask.row(rng, at, p.drop.above);
+    if (p.drop.on) mask.row(rng, at, p.drop.above, p.drop.wide);
     ring.template wait<1>();
     ring.meet();
     const float2 nm = dup2(-mean_n), rs = dup2(rstd_n);
@@ -164,7 +164,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
         o[i] = fma2(na2, hh[i], FULL ? add2(v, na1) : v);
       }
       if (p.dx != nullptr) dx.put(cs, p.dx, off, k, IO::from_pairs(o), 785, extent);
-      if (p.drop.on) mask.apply(rng, at, k, p.drop.above, scale, o);
+      if (p.drop.on) mask.apply(rng, at, k, p.drop.above, p.drop.wide, scale, o);
       if constexpr (BIAS) {
 #pragma unroll
         for (int i = 0; i < N; ++i) sf[k * N + i] = add2(sf[k * N + i], o[i]);

@@ -99,7 +99,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     const int64_t off = offset(row);
     const uint64_t at = static_cast<uint64_t>(row) * static_cast<uint32_t>(p.H) + static_cast<uint32_t>(cs.c0);
     Mask<VE, NV, SH> mask;
-    if (p.drop.on) mask.row(rng, at, p.drop.above);
+    if (p.drop.on) mask.row(rng, at, p.drop.above, p.drop.wide);
     if (slots == 1) ring.template wait<0>(); else ring.template wait<1>();
     ring.meet();
     const int sf = SH ? low4(p.f, off) : 0, sx = SH && has_x ? low4(p.x, off) : 0;
@@ -113,7 +113,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
 #pragma unroll
         for (int i = 0; i < Q; ++i) z[i] = add2(z[i], b[i]);
       }
-      if (p.drop.on) mask.apply(rng, at, k, p.drop.above, scale, z);
+      if (p.drop.on) mask.apply(rng, at, k, p.drop.above, p.drop.wide, scale, z);
       if (has_x) {
         IO::to_pairs(ring.take(slot, 1, k, sx), x);
 #pragma unroll

@@ -17,32 +17,64 @@
 namespace addln {
 namespace blk {
 
+// What the first two rounds make of the offset, of the counter's second word
+// (the upper half of the block's number) and of the key is the same for all
+// blocks that share that word: two of the 20 products, and the xors beside them,
+// are made once, which leaves 18 products a block.  The keys are the same for the
+// whole grid: a warp reduction says so to the compiler, which then keeps the ten
+// rounds' keys in uniform registers instead of adding them up for every block.
+// Both together: 32768x8192 bf16 dropout 187 us to 159, the boundary forward 347 to
+// 320.
 struct Philox {
-  uint32_t k0, k1, o0, o1;  // key, upper half of the counter
+  uint32_t k0, k1, o0, o1;      // key, upper half of the counter
+  uint32_t hi, a0, a2, b0, b3;  // second word, and what it gives
 
+  __device__ __forceinline__ static void mul(uint32_t a, uint32_t m, uint32_t& h, uint32_t& l) {
+    const uint64_t p = static_cast<uint64_t>(a) * m;
+    h = static_cast<uint32_t>(p >> 32), l = static_cast<uint32_t>(p);
+  }
+  __device__ __forceinline__ void head(uint32_t second) {
+    uint32_t h, l, c0;
+    hi = second;
+    mul(o0, kM1, h, l);
+    c0 = h ^ hi ^ k0;         // round 0: words 0 and 1 are c0 and l
+    a2 = o1 ^ k1;             // word 2: the product's upper half ^ a2
+    a0 = l ^ (k0 + kW0);      // round 1: word 0
+    mul(c0, kM0, h, b3);      // word 3
+    b0 = h ^ (k1 + kW1);      // word 2: round 0's word 3 ^ b0
+  }
+  // every thread of the warp takes part
   __device__ __forceinline__ void init(const DropSpec& d) {
     uint64_t seed = d.seed, offset = d.offset;
     if (d.rng != nullptr && ADDLN_IN(760, 0, 16, 16)) {
       seed = __ldcg(reinterpret_cast<const unsigned long long*>(d.rng));
       offset = __ldcg(reinterpret_cast<const unsigned long long*>(d.rng) + 1);
     }
-    k0 = static_cast<uint32_t>(seed), k1 = static_cast<uint32_t>(seed >> 32);
-    o0 = static_cast<uint32_t>(offset), o1 = static_cast<uint32_t>(offset >> 32);
+    auto same = [](uint64_t v) { return __reduce_or_sync(0xffffffffu, static_cast<uint32_t>(v)); };
+    k0 = same(seed), k1 = same(seed >> 32);
+    o0 = same(offset), o1 = same(offset >> 32);
+    head(0);
   }
-  // the four words of block `at`
-  __device__ __forceinline__ uint4 operator()(uint64_t at) const {
-    uint32_t c0 = static_cast<uint32_t>(at), c1 = static_cast<uint32_t>(at >> 32), c2 = o0, c3 = o1;
-    uint32_t a = k0, b = k1;
+  // the four words of block `at`; wide: its number may have an upper half
+  __device__ __forceinline__ uint4 operator()(uint64_t at, bool wide) {
+    if (wide && static_cast<uint32_t>(at >> 32) != hi) head(static_cast<uint32_t>(at >> 32));
+    uint32_t h, l, c0, c1, c2, c3;
+    mul(static_cast<uint32_t>(at), kM0, h, l);
+    c2 = h ^ a2;
+    mul(c2, kM1, h, c1);
+    c0 = h ^ a0, c2 = l ^ b0, c3 = b3;
 #pragma unroll
-    for (int r = 0; r < 10; ++r) {
-      const uint64_t p0 = static_cast<uint64_t>(c0) * 0xD2511F53u, p1 = static_cast<uint64_t>(c2) * 0xCD9E8D57u;
-      c0 = static_cast<uint32_t>(p1 >> 32) ^ c1 ^ a;
-      c2 = static_cast<uint32_t>(p0 >> 32) ^ c3 ^ b;
-      c1 = static_cast<uint32_t>(p1), c3 = static_cast<uint32_t>(p0);
-      a += 0x9E3779B9u, b += 0xBB67AE85u;
+    for (uint32_t r = 2; r < 10; ++r) {
+      uint32_t h0, l0, h1, l1;
+      mul(c0, kM0, h0, l0);
+      mul(c2, kM1, h1, l1);
+      c0 = h1 ^ c1 ^ (k0 + r * kW0);
+      c2 = h0 ^ c3 ^ (k1 + r * kW1);
+      c1 = l1, c3 = l0;
     }
     return make_uint4(c0, c1, c2, c3);
   }
+  static constexpr uint32_t kM0 = 0xD2511F53u, kM1 = 0xCD9E8D57u, kW0 = 0x9E3779B9u, kW1 = 0xBB67AE85u;
 };
 
 // Whether the elements of the low and the high half of a word are kept.
@@ -71,14 +103,14 @@ struct Mask {
   uint32_t bits;  // SH: of group k from bit 8 k on
 
   // at: index in the tensor of this thread's first column of group 0
-  __device__ __forceinline__ void row(const Philox& rng, uint64_t at, uint32_t above) {
+  __device__ __forceinline__ void row(Philox& rng, uint64_t at, uint32_t above, bool wide) {
     if constexpr (SH) {
       constexpr unsigned kAll = 0xffffffffu;
       const int lane = threadIdx.x & 31;
       uint32_t own = 0;
 #pragma unroll
-      for (int k = 0; k < NV; ++k) own |= keep_bits(rng((at + k * 32 * VE) >> 3), above) << (8 * k);
-      const uint32_t end = keep_bits(rng((at + ((NV - 1) * 32 + 1) * VE) >> 3), above);
+      for (int k = 0; k < NV; ++k) own |= keep_bits(rng((at + k * 32 * VE) >> 3, wide), above) << (8 * k);
+      const uint32_t end = keep_bits(rng((at + ((NV - 1) * 32 + 1) * VE) >> 3, wide), above);
       uint32_t next = __shfl_sync(kAll, own, (lane + 1) & 31);
       if (lane == 31) next = (NV > 1 ? next >> 8 : 0u) | end << (8 * (NV - 1));
       const int s = static_cast<int>(at & 7);
@@ -91,7 +123,7 @@ struct Mask {
     }
   }
   // v[i] of group k: kept ones times `scale`, dropped ones 0
-  __device__ __forceinline__ void apply(const Philox& rng, uint64_t at, int k, uint32_t above, float2 scale,
+  __device__ __forceinline__ void apply(Philox& rng, uint64_t at, int k, uint32_t above, bool wide, float2 scale,
                                         float2 (&v)[VE / 2]) const {
     if constexpr (SH) {
 #pragma unroll
@@ -101,7 +133,7 @@ struct Mask {
         v[i].y = (bits >> (8 * k + 2 * i)) & 2u ? u.y : 0.f;
       }
     } else {
-      const uint4 w = rng((at + k * 32 * VE) >> 3);
+      const uint4 w = rng((at + k * 32 * VE) >> 3, wide);
       uint32_t t[4] = {w.x, w.y, w.z, w.w};
       if constexpr (VE == 4) {
         const bool up = ((at >> 2) & 1) != 0;

@@ -2,30 +2,45 @@
 //   h = x + r,  y = norm(h),  q = round(y / scale)
 // x and r are read once, h, q and the scales written once; statistics and
 // largest values are of values in registers.
+#include <type_traits>
+
 #include "quant.cuh"
 
 namespace addln {
 namespace blk {
 
-// |v| of the largest, as bits: the order of non-negative floats is that of
-// their bits, with infinity and then NaN above all.
-template <int P>
-__device__ __forceinline__ uint32_t abs_max(const float2* v) {
-  uint32_t m = 0;
-#pragma unroll
-  for (int j = 0; j < P; ++j) m = max(m, max(__float_as_uint(v[j].x) & 0x7fffffffu, __float_as_uint(v[j].y) & 0x7fffffffu));
+// Largest |v|; a NaN stays one.
+__device__ __forceinline__ float abs_max(float m, float2 v) {
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(v.x), "f"(v.y));
   return m;
 }
+__device__ __forceinline__ float max_nan(float a, float b) {
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(b));
+  return a;
+}
+// Over a warp's lanes, of numbers that are not negative: their bits have the same
+// order, with infinity and then NaN above all.
+__device__ __forceinline__ float warp_max(float m) {
+  return __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+}
 
-// Largest over the walker, in every thread.
-template <bool SIDES>
-__device__ __forceinline__ uint32_t walker_max(Exchange<SIDES>& ex, uint32_t m) {
-  m = __reduce_max_sync(0xffffffffu, m);
-  if (ex.w.warps == 1) return m;
-  const float4* b = ex(make_float4(__uint_as_float(m), 0.f, 0.f, 0.f));
-  m = 0;
-  for (int i = threadIdx.x & 31; i < ex.w.warps; i += 32) m = max(m, __float_as_uint(b[i].x));
-  return __reduce_max_sync(0xffffffffu, m);
+// Largest over the walker, and with SUM the sum of q, in every thread, in one
+// exchange.
+template <bool SUM, bool SIDES>
+__device__ __forceinline__ void walker_max(Exchange<SIDES>& ex, float& m, float& q) {
+  m = warp_max(m);
+  if constexpr (SUM) {
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
+  }
+  if (ex.w.warps == 1) return;
+  const float4* b = ex(make_float4(m, q, 0.f, 0.f));
+  const int width = ex.w.width;
+  m = 0.f, q = 0.f;
+  for (int i = (threadIdx.x & 31) & (width - 1); i < ex.w.warps; i += 32) m = max_nan(m, b[i].x), q += b[i].y;
+  m = warp_max(m);
+  if constexpr (SUM)
+    for (int off = 1; off < width; off <<= 1) q += __shfl_xor_sync(0xffffffffu, q, off);
 }
 
 // A scale and its reciprocal, of the largest |y|.
@@ -39,21 +54,21 @@ __device__ __forceinline__ float reciprocal(float v) {
   return r;
 }
 
-// amax: bits.  The quotient amax / top is taken as a product with 1 / top, and
+// The quotient amax / top is taken as a product with 1 / top, and
 // y / scale later as one with the scale's reciprocal, which is good to a unit in
 // the last place: y's position between two values of 8 bits moves by some 2^-22
 // of itself.
-__device__ __forceinline__ Scale scale_of(uint32_t amax, float inv_top) {
-  const float nan = __uint_as_float(0x7fffffffu);
-  if (amax >= 0x7f800000u) return {nan, nan};
-  const float s = fmaxf(__uint_as_float(amax) * inv_top, 0x1p-126f);
+__device__ __forceinline__ Scale scale_of(float amax, float inv_top) {
+  // NaN for NaN and infinities
+  const float s = max_nan(amax * inv_top, 0x1p-126f) + (amax - amax);
   return {s, reciprocal(s)};
 }
 
 // The least power of two 2^e with amax <= top 2^e: top = m 2^t, and amax's
 // exponent goes up by one where its mantissa is above m's.
-__device__ __forceinline__ Scale pow2_of(uint32_t amax, int format) {
+__device__ __forceinline__ Scale pow2_of(float largest, int format) {
   const float nan = __uint_as_float(0x7fffffffu);
+  const uint32_t amax = __float_as_uint(largest);
   if (amax >= 0x7f800000u) return {nan, nan};
   const uint32_t mantissa = format == ADDLN_Q_INT8 ? 0x7e0000u : 0x600000u;
   const int t = format == ADDLN_Q_E4M3 ? 8 : format == ADDLN_Q_E5M2 ? 15 : 6;
@@ -172,59 +187,150 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
 #pragma unroll
       for (int k = 0; k < NV; ++k) out.put(cs, p.h, off, k, IO::from_pairs(v + k * Q), 805, extent);
     }
+    // y = v f from here on: an rms norm's 1 / rms is left out of v, and goes
+    // into the scale
+    float f = 1.f, m = 0.f;
     if (has_norm) {
-      const RowStat st = row_norm<VE, NV, FULL>(ex, v, cs, p.norm == ADDLN_NORM_LAYER, p.inv_h, p.eps);
+      RowStat st{0.f, 0.f, 0.f};
+      if constexpr (FULL) {
+        st = row_norm<VE, NV, FULL>(ex, v, cs, p.norm == ADDLN_NORM_LAYER, p.inv_h, p.eps);
+        const float2 negm = dup2(-st.m), r2 = dup2(st.M2);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          float2 g[Q], e[Q];
+          par.get(0, k, g);
+          par.get(1, k, e);
+#pragma unroll
+          for (int i = 0; i < Q; ++i) v[k * Q + i] = fma2(mul2(add2(v[k * Q + i], negm), r2), g[i], e[i]);
+        }
+      } else {
+        float2 q[2] = {dup2(0.f), dup2(0.f)};
+#pragma unroll
+        for (int j = 0; j < P; ++j) q[j & 1] = fma2(v[j], v[j], q[j & 1]);
+        q[0] = add2(q[0], q[1]);
+#pragma unroll
+        for (int k = 0; k < NV; ++k) {
+          float2 g[Q];
+          par.get(0, k, g);
+#pragma unroll
+          for (int i = 0; i < Q; ++i) v[k * Q + i] = mul2(v[k * Q + i], g[i]);
+        }
+        float sum = q[0].x + q[0].y;
+        if (scaling == ADDLN_SCALE_ROW) {
+#pragma unroll
+          for (int j = 0; j < P; ++j) m = abs_max(m, v[j]);
+          walker_max<true>(ex, m, sum);
+        } else {
+          sum = walker_sum(ex, sum);
+        }
+        st.M2 = f = row_rstd(sum, p.inv_h, p.eps);
+      }
       if (leader && ADDLN_IN(806, 4 * row, 4, 4 * p.rows)) {
         if (p.rstd) p.rstd[row] = st.M2;
         if (FULL && p.mean) p.mean[row] = st.mean;
       }
-      const float2 negm = dup2(-st.m), r2 = dup2(st.M2);
+    }
+    float inv[NV];  // 1 / scale of group k
+    if (scaling == ADDLN_SCALE_ROW || scaling == ADDLN_SCALE_TENSOR) {
+      float one = given;
+      if (scaling == ADDLN_SCALE_ROW) {
+        if (FULL || !has_norm) {
+#pragma unroll
+          for (int j = 0; j < P; ++j) m = abs_max(m, v[j]);
+          float unused = 0.f;
+          walker_max<false>(ex, m, unused);
+        }
+        const Scale sc = scale_of(m * f, inv_top);
+        if (leader && ADDLN_IN(807, 4 * row, 4, 4 * p.rows)) static_cast<float*>(p.s.scale)[row] = sc.s;
+        one = sc.inv;
+      }
+#pragma unroll
+      for (int k = 0; k < NV; ++k) inv[k] = one;
+    } else {
+      // A lane's NV largest values, over the 4 to 32 lanes of a group.  The first
+      // two steps halve the values that a lane carries, so that lane l of four ends
+      // with value k = 2 (l & 1) + (l >> 1 & 1) and makes its scale alone, and the
+      // scales' reciprocals go back.
+      constexpr int N = NV == 3 ? 4 : NV;
+      const int lanes = (1 << p.s.lanes_shift) / VE;
+      float x[N];
+#pragma unroll
+      for (int k = 0; k < N; ++k) {
+        x[k] = 0.f;
+        if (k < NV)
+#pragma unroll
+          for (int i = 0; i < Q; ++i) x[k] = abs_max(x[k], v[k * Q + i]);
+      }
+      int o = 1;
+      if constexpr (N >= 2) {
+        const bool up = lane & 1;
+#pragma unroll
+        for (int i = 0; i < N / 2; ++i) {
+          const float keep = up ? x[i + N / 2] : x[i], give = up ? x[i] : x[i + N / 2];
+          x[i] = max_nan(keep, __shfl_xor_sync(0xffffffffu, give, 1));
+        }
+        o = 2;
+      }
+      if constexpr (N == 4) {
+        const bool up = lane & 2;
+        const float keep = up ? x[1] : x[0], give = up ? x[0] : x[1];
+        x[0] = max_nan(keep, __shfl_xor_sync(0xffffffffu, give, 2));
+        o = 4;
+      }
+      for (; o < lanes; o <<= 1) x[0] = max_nan(x[0], __shfl_xor_sync(0xffffffffu, x[0], o));
+      const bool pow2 = scaling == ADDLN_SCALE_POW2;
+      const Scale sc = pow2 ? pow2_of(x[0] * f, format) : scale_of(x[0] * f, inv_top);
+      const int l = lane & (lanes - 1);  // of the group
+      const int k = N == 1 ? 0 : N == 2 ? l & 1 : (l & 1) * 2 + (l >> 1 & 1);
+      if (l < N && k < NV && cs.left + l * VE > k * cs.kStep) {
+        const int g = (cs.c0 - l * VE + k * cs.kStep) >> p.s.lanes_shift;
+        const int64_t i = p.s.group_major ? g * p.rows + row : row * p.s.groups + g;
+        if (ADDLN_IN(808, i, 1, p.rows * p.s.groups)) {
+          if (pow2)
+            static_cast<uint8_t*>(p.s.scale)[i] = static_cast<uint8_t>(min(__float_as_uint(sc.s) >> 23, 255u));
+          else
+            static_cast<float*>(p.s.scale)[i] = sc.s;
+        }
+      }
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
-        float2 g[Q], e[Q];
-        par.get(0, k, g);
-        if constexpr (FULL) par.get(1, k, e);
+        const int from = N == 1 ? 0 : N == 2 ? k : (k >> 1) + (k & 1) * 2;
+        inv[k] = __shfl_sync(0xffffffffu, sc.inv, (lane & -N) + from);
+      }
+    }
+    if constexpr (!FULL) {
 #pragma unroll
-        for (int i = 0; i < Q; ++i) {
-          const int j = k * Q + i;
-          if constexpr (FULL)
-            v[j] = fma2(mul2(add2(v[j], negm), r2), g[i], e[i]);
-          else
-            v[j] = mul2(mul2(v[j], r2), g[i]);
+      for (int k = 0; k < NV; ++k) {
+        const float both = inv[k] * f;
+        // beyond fp32's range (values near 0, such as a group of zeros in a row
+        // that has others): one after the other
+        if (isinf(both)) {
+#pragma unroll
+          for (int i = 0; i < Q; ++i) v[k * Q + i] = mul2(v[k * Q + i], dup2(f));
+        } else {
+          inv[k] = both;
         }
       }
     }
-    Scale sc{0.f, given};
-    if (scaling == ADDLN_SCALE_ROW) {
-      sc = scale_of(walker_max(ex, abs_max<P>(v)), inv_top);
-      if (leader && ADDLN_IN(807, 4 * row, 4, 4 * p.rows)) static_cast<float*>(p.s.scale)[row] = sc.s;
-    }
+    W w[NV];
+    auto round = [&](auto fmt) {
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const float2 i2 = dup2(inv[k]);
+        w[k] = to_q<decltype(fmt)::value>(mul2(v[k * Q], i2), mul2(v[k * Q + 1], i2));
+        if constexpr (VE == 8)
+          w[k] |= static_cast<W>(to_q<decltype(fmt)::value>(mul2(v[k * Q + 2], i2), mul2(v[k * Q + 3], i2))) << 32;
+      }
+    };
+    if (format == ADDLN_Q_E4M3)
+      round(std::integral_constant<int, ADDLN_Q_E4M3>());
+    else if (format == ADDLN_Q_E5M2)
+      round(std::integral_constant<int, ADDLN_Q_E5M2>());
+    else
+      round(std::integral_constant<int, ADDLN_Q_INT8>());
     ByteWriter<VE, NV, SH> out;
 #pragma unroll
-    for (int k = 0; k < NV; ++k) {
-      if (scaling == ADDLN_SCALE_GROUP || scaling == ADDLN_SCALE_POW2) {
-        const int lanes = (1 << p.s.lanes_shift) / VE;  // of a group
-        uint32_t m = abs_max<Q>(v + k * Q);
-        for (int o = 1; o < lanes; o <<= 1) m = max(m, __shfl_xor_sync(0xffffffffu, m, o));
-        const bool pow2 = scaling == ADDLN_SCALE_POW2;
-        sc = pow2 ? pow2_of(m, format) : scale_of(m, inv_top);
-        if ((lane & (lanes - 1)) == 0 && cs.ok(k)) {
-          const int g = cs.col(k) >> p.s.lanes_shift;
-          const int64_t i = p.s.group_major ? g * p.rows + row : row * p.s.groups + g;
-          if (ADDLN_IN(808, i, 1, p.rows * p.s.groups)) {
-            if (pow2)
-              static_cast<uint8_t*>(p.s.scale)[i] = static_cast<uint8_t>(min(__float_as_uint(sc.s) >> 23, 255u));
-            else
-              static_cast<float*>(p.s.scale)[i] = sc.s;
-          }
-        }
-      }
-      const float2 inv = dup2(sc.inv);
-      W w = to_q(format, mul2(v[k * Q], inv), mul2(v[k * Q + 1], inv));
-      if constexpr (VE == 8)
-        w |= static_cast<W>(to_q(format, mul2(v[k * Q + 2], inv), mul2(v[k * Q + 3], inv))) << 32;
-      out.put(cs, p.q, at, k, w, 809, elements);
-    }
+    for (int k = 0; k < NV; ++k) out.put(cs, p.q, at, k, w[k], 809, elements);
   }
   // a CTA's shared memory has to outlive its peers' writes into it
   if (p.w.C > 1) cooperative_groups::this_cluster().sync();

@@ -28,38 +28,45 @@ __device__ __forceinline__ int q_top(int format) {
 // Four values to the four bytes of a word.  The fp8 conversions and the integer
 // one round to nearest, ties to even, and cut; a NaN becomes the format's NaN,
 // as an integer 0.
-__device__ __forceinline__ uint32_t to_q(int format, float2 a, float2 b) {
+template <int FMT>
+__device__ __forceinline__ uint32_t to_q(float2 a, float2 b) {
   uint16_t lo, hi;
-  if (format == ADDLN_Q_E4M3) {
+  if constexpr (FMT == ADDLN_Q_E4M3) {
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
     asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
-  } else if (format == ADDLN_Q_E5M2) {
+  } else if constexpr (FMT == ADDLN_Q_E5M2) {
     asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
     asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
   } else {
-    auto whole = [](float v) { return static_cast<uint32_t>(min(max(__float2int_rn(v), -127), 127)) & 0xffu; };
-    return whole(a.x) | whole(a.y) << 8 | whole(b.x) << 16 | whole(b.y) << 24;
+    auto whole = [](float v) { return static_cast<uint32_t>(min(max(__float2int_rn(v), -127), 127)); };
+    // the low bytes of four words
+    return __byte_perm(__byte_perm(whole(a.x), whole(a.y), 0x0040), __byte_perm(whole(b.x), whole(b.y), 0x0040), 0x5410);
   }
   return lo | static_cast<uint32_t>(hi) << 16;
 }
 
-// Four bytes of a word to what they are without their scale.
-__device__ __forceinline__ void from_q(int format, uint32_t w, float2& a, float2& b) {
-  if (format == ADDLN_Q_INT8) {
-    a = make_float2(static_cast<float>(static_cast<int8_t>(w)), static_cast<float>(static_cast<int8_t>(w >> 8)));
-    b = make_float2(static_cast<float>(static_cast<int8_t>(w >> 16)), static_cast<float>(static_cast<int8_t>(w >> 24)));
-    return;
-  }
-  uint32_t u, v;
-  const uint16_t lo = static_cast<uint16_t>(w), hi = static_cast<uint16_t>(w >> 16);
-  if (format == ADDLN_Q_E4M3) {
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(u) : "h"(lo));
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v) : "h"(hi));
+// Four bytes of a word to what they are without their scale.  Integers: a byte
+// with its sign turned becomes the low mantissa byte of 2^23, which is then taken
+// off again (a conversion has a quarter of the rate).
+template <int FMT>
+__device__ __forceinline__ void from_q(uint32_t w, float2& a, float2& b) {
+  if constexpr (FMT == ADDLN_Q_INT8) {
+    w ^= 0x80808080u;
+    auto at = [&](int e) { return __uint_as_float(__byte_perm(w, 0x4B000000u, 0x7440 + e)); };
+    const float2 off = dup2(-8388736.f);
+    a = add2(make_float2(at(0), at(1)), off), b = add2(make_float2(at(2), at(3)), off);
   } else {
-    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(u) : "h"(lo));
-    asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(v) : "h"(hi));
+    uint32_t u, v;
+    const uint16_t lo = static_cast<uint16_t>(w), hi = static_cast<uint16_t>(w >> 16);
+    if constexpr (FMT == ADDLN_Q_E4M3) {
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(u) : "h"(lo));
+      asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(v) : "h"(hi));
+    } else {
+      asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(u) : "h"(lo));
+      asm("cvt.rn.f16x2.e5m2x2 %0, %1;" : "=r"(v) : "h"(hi));
+    }
+    a = Io<kF16>::w2f(u), b = Io<kF16>::w2f(v);
   }
-  a = Io<kF16>::w2f(u), b = Io<kF16>::w2f(v);
 }
 
 template <typename W>

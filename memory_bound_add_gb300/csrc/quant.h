@@ -37,12 +37,18 @@ struct QuantArgs {
   Walk w;
 };
 
+// Arguments of one dequant_rows launch.  scale_row, scale_group: scales between a
+// group's and the next row's, and the next group's; scales: all of them; pieces: of
+// a row, 32 16-byte vectors of out each; reciprocal: 2^32 over the 32-byte vectors
+// of out a row, rounded up.
 struct DequantArgs {
   const void* q;
   void* out;
   ScaleSpec s;
   int64_t rows;
-  int H;
+  int H, pieces;
+  uint32_t reciprocal;
+  int64_t scale_row, scale_group, scales;
 };
 
 // aligned: every row of every tensor in the I/O dtype, and every vector, begins

@@ -196,6 +196,18 @@ def test_rows_and_groups_of_zeros(dtype, fmt):
 
 @DTYPES
 @FORMATS
+@pytest.mark.parametrize("scaling,group", [("group", 64), ("pow2", 32), ("row", None)])
+def test_groups_of_zeros_in_small_rows(dtype, fmt, scaling, group):
+    # 1 / scale of the zeros times the row's 1 / rms is beyond fp32
+    x = torch.zeros(3, 264, dtype=dtype)
+    x[0, 128:] = randn((136,), dtype, 1, 1e-3)
+    x[1, :7] = randn((7,), dtype, 2, 1e-3)
+    v = {"x": x, "residual": None, "gamma": randn((264,), seed=3, sc=0.1, loc=1.0), "beta": None}
+    check_fwd(v, "rms", fmt, scaling, group, eps=1e-8)
+
+
+@DTYPES
+@FORMATS
 def test_infinities_and_nan(dtype, fmt):
     H = 264
     x = randn((4, H), dtype, 1)
