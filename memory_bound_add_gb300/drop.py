@@ -30,10 +30,10 @@ from typing import NamedTuple, Optional
 import torch
 from torch.autograd.function import once_differentiable
 
-from . import binding
+from . import binding, fast
 from .binding import DTYPE_CODE, AddLNError
-from .block import (_F32, _F, _I, _I64, _P, _addresses, _beside, _norm_kind, _rows_tensor, _tensor,
-                    changed, on_stream)
+from .block import (_F32, _F, _I, _I64, _NORMS, _P, _addresses, _beside, _current_device, _current_stream, _norm_kind,
+                    _rows_tensor, _tensor, changed, on_stream)
 
 _D, _U64 = ctypes.c_double, ctypes.c_uint64
 # Every symbol include/addln_dropout.h declares, with its ctypes signature.
@@ -45,7 +45,10 @@ SIGNATURES = {
     "dropout_add_norm_bwd_workspace_size": (_I64, [_I64, _I64, _I]),
 }
 
+_MOST = (1 << 64) - 1
+
 _lib = None
+_fast = None  # fast.py's extension, from the first call on
 _NONE = (None, None)
 
 
@@ -58,9 +61,10 @@ def bind(handle):
 
 
 def lib():
-    global _lib
+    global _lib, _fast
     if _lib is None:
         _lib = bind(binding.lib())
+        _fast = fast.module()
     return _lib
 
 
@@ -68,6 +72,10 @@ def _rng_args(rng, index):
     """(address or None, seed, offset) of an rng for device number `index`."""
     if isinstance(rng, torch.Tensor):
         return _tensor(rng, "rng", torch.int64, 2, index), 0, 0
+    if type(rng) is tuple and len(rng) == 2:
+        seed, offset = rng
+        if type(seed) is int and type(offset) is int and 0 <= seed <= _MOST and 0 <= offset <= _MOST:
+            return None, seed, offset
     try:
         seed, offset = map(operator.index, rng)
     except TypeError:
@@ -79,6 +87,7 @@ def _rng_args(rng, index):
 
 
 def _activation(x, name):
+    """The dtype's code of a contiguous CUDA tensor of any shape."""
     if not isinstance(x, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if not x.is_cuda:
@@ -89,6 +98,13 @@ def _activation(x, name):
     if not x.is_contiguous():
         raise ValueError(f"{name} must be contiguous")
     return code
+
+
+def _on(x, stream, call):
+    """on_stream, without its detours in the commonest case."""
+    if stream is None and (index := x.get_device()) == _current_device():
+        return call(_current_stream(index))
+    return on_stream(x.device, stream, call)
 
 
 # ------------------------------------------------------------------ dropout
@@ -108,6 +124,10 @@ def dropout_fwd(x, y, p, rng, *, stream=None):
 
 def dropout(x, p, rng, *, stream=None):
     """Dropout of x; its backward is the same call on the gradient."""
+    if _fast is not None and stream is None:
+        y = _fast.dropout(x, p, rng)
+        if y is not None:
+            return y
     code = _activation(x, "x")
 
     def call(s):
@@ -115,7 +135,7 @@ def dropout(x, p, rng, *, stream=None):
         _dropout(s, x, y.data_ptr(), p, rng, code)
         return y
 
-    return on_stream(x.device, stream, call)
+    return _on(x, stream, call)
 
 
 # ------------------------------------------------------------------ forward
@@ -152,19 +172,31 @@ def dropout_add_norm(f, x=None, *, p, rng, bias=None, norm="layer", gamma=None, 
     Returns (h, y or None, stats or None), stats = (mean, rstd), each [rows]
     fp32 or None where the norm has none.
     """
+    if _fast is not None and stream is None:
+        out = _fast.dropout_add_norm(f, x, p, rng, bias, _NORMS.get(norm), gamma, beta, eps, want_stats)
+        if out is not None:
+            return out[0], out[1], out[2:] if want_stats else None
     rows, H = _rows_tensor(f, "f")
 
     def call(s):
         h = torch.empty_like(f)
         y = torch.empty_like(f) if norm is not None else None
         stats = None
+        mp = rp = None
         if want_stats:
-            new = lambda w: torch.empty(rows, dtype=_F32, device=f.device) if w else None  # noqa: E731
-            stats = (new(norm == "layer"), new(norm is not None))
-        _forward(s, f, x, _addresses((h, y, *(stats or _NONE))), rows, H, p, rng, bias, norm, gamma, beta, eps)
+            mean = rstd = None
+            if norm is not None:
+                rstd = torch.empty(rows, dtype=_F32, device=f.device)
+                rp = rstd.data_ptr()
+                if norm == "layer":
+                    mean = torch.empty(rows, dtype=_F32, device=f.device)
+                    mp = mean.data_ptr()
+            stats = (mean, rstd)
+        _forward(s, f, x, (h.data_ptr(), None if y is None else y.data_ptr(), mp, rp), rows, H, p, rng, bias, norm, gamma,
+                 beta, eps)
         return h, y, stats
 
-    return on_stream(f.device, stream, call)
+    return _on(f, stream, call)
 
 
 # ----------------------------------------------------------------- backward
@@ -243,6 +275,11 @@ def dropout_add_norm_backward(dy, dh, h, stats, *, p, rng, bias=None, norm="laye
                               stream=None) -> DropoutAddNormGrads:
     """Allocate the gradients with PyTorch and run dropout_add_norm_bwd: the
     gradient of every input that is given."""
+    if _fast is not None and stream is None:
+        mean, rstd = stats or _NONE
+        g = _fast.dropout_add_norm_backward(dy, dh, h, mean, rstd, p, rng, bias, _NORMS.get(norm), gamma, beta)
+        if g is not None:
+            return DropoutAddNormGrads(*g) if norm is not None else DropoutAddNormGrads(g[0], dh, *g[2:])
     some, rows, H = _given(dy, dh)
     dev = some.get_device()
     for t, name in ((bias, "bias"), (beta, "beta")):
@@ -257,7 +294,7 @@ def dropout_add_norm_backward(dy, dh, h, stats, *, p, rng, bias=None, norm="laye
         _backward(s, some, rows, H, dy, dh, h, stats, _addresses(g), p, rng, norm, gamma, None)
         return DropoutAddNormGrads(g[0], dh if dx_is_dh else g[1], *g[2:])
 
-    return on_stream(some.device, stream, call)
+    return _on(some, stream, call)
 
 
 # ----------------------------------------------------------------- training

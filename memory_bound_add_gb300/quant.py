@@ -22,14 +22,15 @@ the gradients (h: x where there is no residual).
 """
 from __future__ import annotations
 
-import ctypes
+import functools
 from typing import NamedTuple, Optional
 
 import torch
 
-from . import binding
+from . import binding, fast
 from .binding import DTYPE_CODE, AddLNError
-from .block import _F32, _F, _I, _I64, _P, _beside, _norm_kind, _rows_tensor, _same_rows, _tensor, changed, on_stream
+from .block import (NORM_LAYER, _F32, _F, _I, _I64, _P, _beside, _current_device, _current_stream, _norm_kind, _rows_tensor, _same_rows,
+                    _tensor, changed, on_stream)
 
 Q_E4M3, Q_E5M2, Q_INT8 = 0, 1, 2
 SCALE_ROW, SCALE_GROUP, SCALE_POW2, SCALE_TENSOR = 0, 1, 2, 3
@@ -46,6 +47,7 @@ SIGNATURES = {
 }
 
 _lib = None
+_fast = None  # fast.py's extension, from the first call on
 
 
 def bind(handle):
@@ -57,9 +59,10 @@ def bind(handle):
 
 
 def lib():
-    global _lib
+    global _lib, _fast
     if _lib is None:
         _lib = bind(binding.lib())
+        _fast = fast.module()
     return _lib
 
 
@@ -88,10 +91,17 @@ def _group_of(scaling, group):
 
 def scale_layout(scale, shape):
     """(scaling, group, group_major) of the scales of a q of this shape;
-    ValueError where they do not fit.  A row's groups are told from how many
+    ValueError where they do not fit."""
+    return _layout(scale.dtype, scale.shape, scale.stride(), shape)
+
+
+@functools.lru_cache(maxsize=256)
+def _layout(dtype, scale_shape, scale_stride, shape):
+    """scale_layout of a tensor of these sizes and strides.  A row's groups are told from how many
     there are: no two of 32, 64 and 128 columns cut a row into the same number,
     but for one."""
     H = shape[-1]
+    scale = torch.empty_strided(scale_shape, scale_stride, dtype=dtype, device="meta")
     if scale.dtype not in (_F32, _E8):
         raise ValueError(f"scale must be {_F32} or {_E8}, got {scale.dtype}")
     if scale.numel() == 1 and scale.dim() <= 1:
@@ -191,43 +201,67 @@ def norm_quant(x, residual=None, *, norm="rms", gamma=None, beta=None, eps: floa
     default, 32 for "pow2".  scale: the given one, for scaling "tensor" alone.
     group_major: the scales of groups lie as [groups, rows] in memory (the
     tensor returned has the same shape and other strides)."""
+    spec = _spec(norm, format, scaling, group, bool(group_major))
+    if _fast is not None and stream is None and scale is None and not spec[5]:
+        out = _fast.norm_quant(x, residual, gamma, beta, eps, spec[0], spec[1], spec[3], spec[4], want_stats)
+        if out is not None:
+            return NormQuant(*out)
     rows, H = _rows_tensor(x, "x")
-    fmt, qt = _format(format)
-    code, g = _group_of(scaling, group)
-    dev = x.get_device()
-    if code == SCALE_TENSOR:
+    if spec[3] == SCALE_TENSOR:
         if not isinstance(scale, torch.Tensor):
             raise TypeError('scaling "tensor" needs a scale: an fp32 tensor of one element')
-        _tensor(scale, "scale", _F32, 1, dev)
+        _tensor(scale, "scale", _F32, 1, x.get_device())
     elif scale is not None:
         raise ValueError(f'a scale beside scaling "{scaling}"')
-    major = bool(group_major) and g != 0
+    # the commonest call without on_stream's detour
+    if stream is None and (index := x.get_device()) == _current_device():
+        return _norm_quant(_current_stream(index), x, residual, rows, H, gamma, beta, eps, spec, scale, want_stats)
+    return on_stream(x.device, stream, lambda s: _norm_quant(s, x, residual, rows, H, gamma, beta, eps, spec, scale,
+                                                             want_stats))
 
-    def call(s):
-        q = torch.empty_like(x, dtype=qt)
-        sc = scale
-        if code != SCALE_TENSOR:
-            G = -(-H // g) if g else 1
-            dt = _E8 if code == SCALE_POW2 else _F32
-            if major:
-                sc = torch.empty((G, *x.shape[:-1]), dtype=dt, device=x.device).movedim(0, -1)
-            else:
-                sc = torch.empty((*x.shape[:-1], G), dtype=dt, device=x.device)
-        h = torch.empty_like(x) if residual is not None else None
-        new = lambda w: torch.empty(rows, dtype=_F32, device=x.device) if w else None  # noqa: E731
-        mean, rstd = new(want_stats and norm == "layer"), new(want_stats and norm is not None)
-        at = lambda t: None if t is None else t.data_ptr()  # noqa: E731
-        _forward(s, x, residual, q.data_ptr(), sc.data_ptr(), at(h), at(mean), at(rstd), rows, H, norm, gamma, beta, eps,
-                 fmt, code, g, major)
-        return NormQuant(q, sc, h, mean, rstd)
 
-    return on_stream(x.device, stream, call)
+@functools.lru_cache(maxsize=256)
+def _spec(norm, format, scaling, group, group_major):
+    """(norm's code, format's code, q's dtype, scaling's code, group, whether
+    the groups come first, the scales' dtype) of a call's choices."""
+    code, g = _group_of(scaling, group)
+    return (_norm_kind(norm, "norm"), *_format(format), code, g, group_major and g != 0,
+            _E8 if code == SCALE_POW2 else _F32)
+
+
+def _norm_quant(s, x, residual, rows, H, gamma, beta, eps, spec, scale, want_stats):
+    norm, fmt, qt, code, g, major, st = spec
+    dev = x.get_device()
+    new = torch.empty
+    q = torch.empty_like(x, dtype=qt)
+    if code != SCALE_TENSOR:
+        G = -(-H // g) if g else 1
+        lead = x.shape[:-1]
+        scale = new((G, *lead), dtype=st, device=x.device).movedim(0, -1) if major else \
+            new((*lead, G), dtype=st, device=x.device)
+    h = mean = rstd = rp = hp = None
+    if residual is not None:
+        rp = _beside(residual, "residual", x, dev)
+        h = torch.empty_like(x)
+        hp = h.data_ptr()
+    if want_stats and norm:
+        rstd = new(rows, dtype=_F32, device=x.device)
+        if norm == NORM_LAYER:
+            mean = new(rows, dtype=_F32, device=x.device)
+    rc = (_lib or lib()).norm_quant_fwd(
+        x.data_ptr(), rp, norm, None if gamma is None else _tensor(gamma, "gamma", _F32, H, dev),
+        None if beta is None else _tensor(beta, "beta", _F32, H, dev), q.data_ptr(), fmt, code, g, major,
+        scale.data_ptr(), hp, None if mean is None else mean.data_ptr(), None if rstd is None else rstd.data_ptr(), rows,
+        H, eps, DTYPE_CODE[x.dtype], s)
+    if rc:
+        raise AddLNError(rc, "norm_quant_fwd")
+    return NormQuant(q, scale, h, mean, rstd)
 
 
 # ------------------------------------------------------------------ read back
-def _dequant(s, q, scale, out, layout, dtype, index):
-    rows, H = q.numel() // q.shape[-1], q.shape[-1]
-    rc = (_lib or lib()).dequant_rows(q.data_ptr(), _CODES[q.dtype], *layout, scale.data_ptr(), out, rows, H,
+def _dequant(s, q, scale, out, layout, dtype):
+    H = q.shape[-1]
+    rc = (_lib or lib()).dequant_rows(q.data_ptr(), _CODES[q.dtype], *layout, scale.data_ptr(), out, q.numel() // H, H,
                                       DTYPE_CODE[dtype], s)
     if rc:
         raise AddLNError(rc, "dequant_rows")
@@ -236,14 +270,15 @@ def _dequant(s, q, scale, out, layout, dtype, index):
 def _check_pair(q, scale):
     if not isinstance(q, torch.Tensor) or not isinstance(scale, torch.Tensor):
         raise TypeError("q and scale must be torch.Tensors")
+    index = q.get_device()
+    if index >= 0 and q.dtype in _CODES and q.is_contiguous() and scale.get_device() == index and q.dim() and q.shape[-1]:
+        return scale_layout(scale, q.shape)
     if not q.is_cuda:
         raise ValueError("q must be a CUDA tensor")
     if not q.dim() or q.shape[-1] < 1:
         raise ValueError("q must have a last dimension of at least 1")
     _q_tensor(q, "q", q.shape, q.get_device())
-    if scale.get_device() != q.get_device():
-        raise ValueError(f"scale must be on {q.device}, got {scale.device}")
-    return scale_layout(scale, q.shape)
+    raise ValueError(f"scale must be on {q.device}, got {scale.device}")
 
 
 def dequant_rows(q, scale, out, *, stream=None):
@@ -253,7 +288,7 @@ def dequant_rows(q, scale, out, *, stream=None):
     at = _tensor(out, "out", out.dtype, q.numel(), q.get_device())
     if not _same_rows(out.shape, q.shape):
         raise ValueError(f"out of shape {tuple(out.shape)} beside {tuple(q.shape)}")
-    on_stream(q.device, stream, lambda s: _dequant(s, q, scale, at, layout, out.dtype, q.get_device()))
+    on_stream(q.device, stream, lambda s: _dequant(s, q, scale, at, layout, out.dtype))
     changed([out])
 
 
@@ -261,13 +296,19 @@ def dequantise(q, scale, *, dtype=torch.bfloat16, stream=None):
     """What q stands for, q * scale, as a tensor of this dtype.  The scaling is
     told from scale, as norm_quant returns it (fp32 of one element and at most
     one dimension: a scale for the whole tensor)."""
+    if _fast is not None and stream is None:
+        out = _fast.dequantise(q, scale, DTYPE_CODE.get(dtype))
+        if out is not None:
+            return out
     layout = _check_pair(q, scale)
     if dtype not in DTYPE_CODE:
         raise ValueError(f"unsupported dtype {dtype}")
 
     def call(s):
         out = torch.empty_like(q, dtype=dtype)
-        _dequant(s, q, scale, out.data_ptr(), layout, dtype, q.get_device())
+        _dequant(s, q, scale, out.data_ptr(), layout, dtype)
         return out
 
+    if stream is None and (index := q.get_device()) == _current_device():
+        return call(_current_stream(index))
     return on_stream(q.device, stream, call)
