@@ -15,6 +15,11 @@
 // of its neighbour's, which it gets by shuffle.  Accesses of single elements
 // (2 bytes each) took twice as long: 8192x5001 bf16 rms/rms forward 204 us,
 // with granules 99; backward 404 and 177.
+//
+// Such rows of tensors that all begin on borders themselves need no shifts where a
+// walker's rows lie all the same way (kEdged: every 8th row does): a walker's groups
+// then are the granules as they lie in memory, its first column up to VE - 1 before
+// the row's, and only a row's first and last granule are taken apart.
 #pragma once
 
 #include <cooperative_groups.h>
@@ -31,17 +36,18 @@ constexpr int kMaxCluster = 8;    // the portable cluster size
 constexpr int kMaxSmem = 227 * 1024;  // dynamic shared memory of a CTA
 
 // VE fp32 parameters from column c on, of H; `fill` for a missing vector and
-// past the end.  SH: any address, and the end may lie within the group.
-template <int VE, bool SH>
+// before the first or past the end.  Shifted or edged: any address, and an end may
+// lie within the group.
+template <int VE, int MODE>
 __device__ __forceinline__ void load_params(const float* p, int c, int H, float fill, float (&v)[VE], int site) {
 #pragma unroll
   for (int e = 0; e < VE; ++e) v[e] = fill;
   if (p == nullptr) return;
   p += c;
-  if constexpr (SH) {
+  if constexpr (MODE != kAligned) {
 #pragma unroll
     for (int e = 0; e < VE; ++e)
-      if (c + e < H && ADDLN_IN(site, 4 * (c + e), 4, 4 * static_cast<int64_t>(H))) v[e] = __ldg(p + e);
+      if ((MODE == kShifted || c + e >= 0) && c + e < H && ADDLN_IN(site, 4 * (c + e), 4, 4 * static_cast<int64_t>(H))) v[e] = __ldg(p + e);
   } else {
     if (c >= H || !ADDLN_IN(site, 4 * c, 4 * VE, 4 * static_cast<int64_t>(H))) return;
 #pragma unroll
@@ -66,8 +72,10 @@ struct Cols {
   static constexpr int P = NV * VE / 2;
   int c0;           // first column of group 0
   int left;         // columns of the slice from c0 on (may be 0 or less)
-  int whole;        // groups k below this are whole in every lane of the warp
+  int whole;        // groups k below this are whole at their ends in every lane of the warp
   float n, inv_n;   // columns of the warp, 1 / n (0 for none)
+  int low;          // edged rows: columns of group 0 that lie before the row
+  bool cut;         // some lane of the warp has such
 
   __device__ __forceinline__ void init(int warp, int col0, int cols) {
     const int at0 = warp * NV * kStep + (threadIdx.x & 31) * VE;
@@ -77,13 +85,37 @@ struct Cols {
     n = static_cast<float>(own);
     inv_n = own ? __frcp_rn(n) : 0.f;
     whole = own / kStep;
+    low = 0, cut = false;
+  }
+  // Edged rows, `past` columns past the borders: the slice begins that much
+  // before col0.
+  __device__ __forceinline__ void init_edged(int warp, int col0, int slice, int H, int past) {
+    const int first = col0 - past, cols = min(slice, H - first);
+    init(warp, first, cols);
+    cut = warp == 0 && first < 0;
+    if (cut) {
+      low = (threadIdx.x & 31) == 0 ? -first : 0;
+      const int own = min(cols, NV * kStep) + first;
+      n = static_cast<float>(max(own, 0));
+      inv_n = own > 0 ? __frcp_rn(n) : 0.f;
+    }
   }
   __device__ __forceinline__ int col(int k) const { return c0 + k * kStep; }
   __device__ __forceinline__ bool ok(int k) const { return left > k * kStep; }
   // columns of group k that exist
   __device__ __forceinline__ int valid(int k) const { return min(max(left - k * kStep, 0), VE); }
+  // zeros in the slots of columns before the row, of group 0
+  __device__ __forceinline__ void clear_low(float2* v) const {
+    if (!cut) return;
+#pragma unroll
+    for (int e = 0; e < VE - 1; ++e) {
+      float& u = (e & 1) ? v[e >> 1].y : v[e >> 1].x;
+      u = e >= low ? u : 0.f;
+    }
+  }
   // zeros in the slots of columns that do not exist
   __device__ __forceinline__ void clear(float2 (&v)[P]) const {
+    clear_low(v);
     if (whole == NV) return;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
@@ -130,7 +162,7 @@ __device__ __forceinline__ void store_element(char* p, const uint4& v, int e) {
 
 // Writes a row's groups in the order of k, 0 to NV - 1, to `base + off` of a
 // tensor of `extent` bytes.
-template <int DT, int NV, bool SH>
+template <int DT, int NV, int MODE>
 struct Writer {
   static constexpr int S = Io<DT>::kBytes, VE = Io<DT>::kVec;
   uint4 prev;  // the last group, of lane 31
@@ -139,9 +171,18 @@ struct Writer {
                                       int64_t extent) {
     off += k * (cs.kStep * S);
     char* p = static_cast<char*>(base) + off;
-    if constexpr (!SH) {
+    if constexpr (MODE == kAligned) {
       if (cs.ok(k) && ADDLN_IN(site, off, 16, extent)) st_stream_v4(p, v);
       return;
+    } else if constexpr (MODE == kEdged) {
+      const int lo = k == 0 ? cs.low : 0, hi = cs.valid(k);
+      if (lo == 0 && hi == VE) {
+        if (ADDLN_IN(site, off, 16, extent)) st_stream_v4(p, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (e >= lo && e < hi && ADDLN_IN(site, off + e * S, S, extent)) store_element<S>(p + e * S, v, e);
+      }
     } else {
       constexpr unsigned kAll = 0xffffffffu;
       const int lane = threadIdx.x & 31;
@@ -194,8 +235,9 @@ struct Writer {
 // piece, [slot][tensor][group][lane], with SH one granule more a tensor.
 constexpr int kMaxSlots = 2;
 
-template <int DT, int NV, int NT, bool SH>
+template <int DT, int NV, int NT, int MODE>
 struct Ring {
+  static constexpr bool SH = MODE == kShifted;
   static constexpr int S = Io<DT>::kBytes, VE = Io<DT>::kVec;
   static constexpr uint32_t kTensor = (NV * 32 + (SH ? 1 : 0)) * 16;
   static constexpr uint32_t kSlot = NT * kTensor;  // bytes of a warp's slot
@@ -213,7 +255,14 @@ struct Ring {
   __device__ __forceinline__ void fetch(const Cols<VE, NV>& cs, int slot, const void* t, int64_t off, int site,
                                         int64_t extent) {
     const char* p = static_cast<const char*>(t) + off;
-    if constexpr (!SH) {
+    if constexpr (MODE == kEdged) {
+      // (a row's first granule has the end of the row before it read along)
+#pragma unroll
+      for (int k = 0; k < NV; ++k) {
+        const int n = min(max(cs.left * S - k * (cs.kStep * S), 0), 16);
+        copy(at(slot, I, k), p + k * (cs.kStep * S), n > 0 && ADDLN_IN(site, off + k * (cs.kStep * S), n, extent) ? n : 0);
+      }
+    } else if constexpr (!SH) {
 #pragma unroll
       for (int k = 0; k < NV; ++k) {
         const bool in = cs.ok(k) && ADDLN_IN(site, off + k * (cs.kStep * S), 16, extent);
@@ -312,6 +361,14 @@ struct Kept {
     }
   }
 };
+
+// First row of a CTA's (or cluster's) walker number `side`.  Edged rows: all rows of a
+// unit are the same modulo 8.
+template <int MODE>
+__device__ __forceinline__ int64_t first_row(int64_t unit, int sides, int side) {
+  if constexpr (MODE != kEdged) return unit * sides + side;
+  return (unit & 7) + 8 * ((unit >> 3) * sides + side);
+}
 
 // A CTA of a cluster may write into a peer's shared memory only once the peer
 // has started: every thread arrives when it begins, and waits before its first
@@ -469,9 +526,18 @@ __device__ __forceinline__ RowStat row_norm(Exchange<SIDES>& ex, float2 (&v)[NV 
 
 // ------------------------------------------------------------ column sums
 // Stores slots as fp32 columns of an [Hp] vector (16-byte aligned).
-template <int VE, int NV>
+template <int VE, int NV, int MODE = kAligned>
 __device__ __forceinline__ void store_cols(float* t, const Cols<VE, NV>& cs, int site, int Hp,
                                            const float2 (&v)[NV * VE / 2]) {
+  if constexpr (MODE == kEdged) {
+#pragma unroll
+    for (int e = 0; e < NV * VE; ++e) {
+      const int k = e / VE, c = cs.col(k) + e % VE;
+      if (e % VE < cs.valid(k) && (k > 0 || e >= cs.low) && ADDLN_IN(site, 4 * c, 4, 4 * static_cast<int64_t>(Hp)))
+        t[c] = (e & 1) ? v[e >> 1].y : v[e >> 1].x;
+    }
+    return;
+  }
 #pragma unroll
   for (int k = 0; k < NV; ++k)
 #pragma unroll
@@ -621,6 +687,15 @@ inline Spread spread(int H, int VE, int NV, int64_t rows, int sms, int slot_byte
 // (as in block_fwd.cu).
 inline int slots_ahead(int64_t rows, int fit, const Spread& s) {
   return rows > 8 * static_cast<int64_t>(fit) * s.sh.rows ? 1 : s.ring_slots;
+}
+
+// Units for `need` of them where `fit` are resident.  Edged rows: a multiple of 8, so
+// that a walker's rows, a stride of all walkers apart, lie the same way (rows of
+// 16-bit types do after 8 rows at the latest).
+inline int64_t units_for(int64_t need, int64_t fit, bool edged) {
+  if (!edged) return need < fit ? need : fit;
+  const int64_t up = (need + 7) / 8 * 8, down = fit / 8 * 8;
+  return up < down ? up : down;
 }
 
 // Launches kernel(args...) as units * C CTAs.

@@ -8,6 +8,10 @@
 
 namespace addln {
 
+// How rows lie: on 16-byte borders; anywhere; anywhere, but all of a walker's rows
+// of all tensors the same distance past the borders (block.cuh).
+constexpr int kAligned = 0, kShifted = 1, kEdged = 2;
+
 // How walkers (a warp, a CTA or a cluster for each row) cover the rows.
 struct Walk {
   int C;             // CTAs of a row

@@ -5,18 +5,16 @@ namespace addln {
 namespace blk {
 
 constexpr int kThreads = 256;
-constexpr int kBlocks = 4;  // blocks of 8 elements a thread, all in flight
 
 // VEC: x and y lie on 16-byte borders.  A thread has kBlocks blocks of 8
-// elements, a CTA's threads apart; the tensor's last block may be shorter.
-template <int DT, bool VEC>
+// elements, a CTA's threads apart and all in flight; the tensor's last block may be
+// shorter.
+template <int DT, bool VEC, int kBlocks>
 __global__ void __launch_bounds__(kThreads) k_dropout(const void* x, void* y, int64_t n, const DropSpec d) {
   using IO = Io<DT>;
   constexpr int S = IO::kBytes, U = S / 2;  // 16-byte vectors a block
   pdl_trigger();
   pdl_wait();
-  Philox rng;
-  rng.init(d);
   const float2 scale = dup2(d.scale);
   const int64_t b0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kBlocks) + threadIdx.x;
   const int64_t whole = VEC ? n / 8 : 0, extent = n * S;
@@ -33,6 +31,8 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const void* x, void* y, in
       if (ADDLN_IN(761, at, 16, extent)) v[j][u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(x) + at));
     }
   }
+  Philox rng;
+  rng.init(d);
 #pragma unroll
   for (int j = 0; j < kBlocks; ++j) {
     const int64_t b = b0 + j * kThreads;
@@ -81,16 +81,24 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const void* x, void* y, in
   }
 }
 
+namespace {
+using DropKernel = void (*)(const void*, void*, int64_t, const DropSpec);
+template <int DT>
+DropKernel pick(bool vec, bool many) {
+  if (vec) return many ? &k_dropout<DT, true, 4> : &k_dropout<DT, true, 1>;
+  return many ? &k_dropout<DT, false, 4> : &k_dropout<DT, false, 1>;
+}
+}  // namespace
 }  // namespace blk
 
 int launch_dropout(int dtype, const void* x, void* y, int64_t n, const DropSpec& drop, const LaunchCtx& c) {
   using namespace blk;
   const bool vec = ((reinterpret_cast<uintptr_t>(x) | reinterpret_cast<uintptr_t>(y)) & 15) == 0;
-  void (*k)(const void*, void*, int64_t, const DropSpec) =
-      dtype == kF32 ? (vec ? &k_dropout<kF32, true> : &k_dropout<kF32, false>)
-      : dtype == kF16 ? (vec ? &k_dropout<kF16, true> : &k_dropout<kF16, false>)
-                      : (vec ? &k_dropout<kBF16, true> : &k_dropout<kBF16, false>);
-  const int64_t per = 8 * kThreads * kBlocks, ctas = (n + per - 1) / per;
+  // One block a thread while all of them are on the GPU at once, else four.
+  const int64_t blocks = n / 8 + (n % 8 != 0);
+  const bool many = blocks > int64_t{2048} * c.dev.sms;
+  const DropKernel k = dtype == kF32 ? pick<kF32>(vec, many) : dtype == kF16 ? pick<kF16>(vec, many) : pick<kBF16>(vec, many);
+  const int64_t per = kThreads * (many ? 4 : 1), ctas = (blocks + per - 1) / per;
   if (ctas > 0x7fffffff) return ADDLN_ERR_SHAPE;
   const cudaError_t e = launch_kernel(k, dim3(static_cast<unsigned>(ctas)), dim3(kThreads), 0, c.stream, c.pdl, x, y, n, drop);
   if (e != cudaSuccess) {

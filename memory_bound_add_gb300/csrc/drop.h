@@ -66,12 +66,11 @@ struct DropBwdArgs {
 };
 
 int launch_dropout(int dtype, const void* x, void* y, int64_t n, const DropSpec& drop, const LaunchCtx& c);
-// aligned: every row of every tensor in the I/O dtype, and every vector, begins
-// and ends on 16-byte borders.
-int launch_drop_fwd(int dtype, bool aligned, const DropFwdArgs& p, const LaunchCtx& c);
-int64_t drop_bwd_workspace_bytes(int dtype, bool aligned, bool full, bool bias, int64_t rows, int H,
-                                 const DeviceInfo& dev);
-int launch_drop_bwd(int dtype, bool aligned, const DropBwdArgs& p, void* ws, int64_t ws_bytes, const LaunchCtx& c);
+// mode: kAligned where every row of every tensor in the I/O dtype, and every vector,
+// begins and ends on 16-byte borders, kEdged where every such tensor begins on one.
+int launch_drop_fwd(int dtype, int mode, const DropFwdArgs& p, const LaunchCtx& c);
+int64_t drop_bwd_workspace_bytes(int dtype, int mode, bool full, bool bias, int64_t rows, int H, const DeviceInfo& dev);
+int launch_drop_bwd(int dtype, int mode, const DropBwdArgs& p, void* ws, int64_t ws_bytes, const LaunchCtx& c);
 
 int read_bounds_drop(unsigned long long* word);
 int read_bounds_drop_fwd(unsigned long long* word);

@@ -48,6 +48,13 @@ int check_alias(const Range* outs, int n_out, int in_place, const Range* ins, in
   return ADDLN_OK;
 }
 
+// How the rows of tensors at these addresses, and the vectors beside them (each
+// ored), lie.
+int mode_of(uintptr_t data, uintptr_t params, int64_t row_bytes) {
+  if (data & 15) return addln::kShifted;
+  return (params | static_cast<uintptr_t>(row_bytes)) & 15 ? addln::kEdged : addln::kAligned;
+}
+
 bool valid_norm(int k) { return k >= ADDLN_NORM_NONE && k <= ADDLN_NORM_LAYER; }
 
 }  // namespace
@@ -93,7 +100,7 @@ int dropout_add_norm_fwd(const void* f, const void* x, const float* bias, double
   const int es = elem_bytes(dtype);
   const uintptr_t data = bits(f) | bits(x) | bits(h) | bits(y), params = bits(bias) | bits(gamma) | bits(beta);
   if ((data & (es - 1)) || ((params | bits(mean) | bits(rstd)) & 3)) return ADDLN_ERR_ALIGN;
-  const bool aligned = ((data | params | static_cast<uintptr_t>(H * es)) & 15) == 0;
+  const int mode = mode_of(data, params, H * es);
   const int64_t tb = rows * H * es;
   const Range outs[4] = {range_of(h, tb), range_of(y, tb), range_of(mean, rows * 4), range_of(rstd, rows * 4)};
   const Range ins[6] = {range_of(f, tb), range_of(x, tb), range_of(bias, H * 4), range_of(gamma, H * 4),
@@ -105,7 +112,7 @@ int dropout_add_norm_fwd(const void* f, const void* x, const float* bias, double
   if (rc != ADDLN_OK) return rc;
   addln::DropFwdArgs a{f, x, bias, gamma, beta, h, y, mean, rstd, d, rows, static_cast<int>(H), norm, eps,
                        static_cast<float>(1.0 / static_cast<double>(H))};
-  return addln::launch_drop_fwd(dtype, aligned, a, c);
+  return addln::launch_drop_fwd(dtype, mode, a, c);
 } catch (...) {
   return ADDLN_ERR_HOST_MEMORY;
 }
@@ -119,10 +126,10 @@ int64_t dropout_add_norm_bwd_workspace_size(int64_t rows, int64_t H, int dtype) 
   if (rc != ADDLN_OK) return rc;
   // the most over the kernels that the call may turn out to take
   int64_t most = 0;
-  for (int kind = 0; kind < 8; ++kind) {
-    const bool aligned = kind & 1;
-    if (aligned && H * elem_bytes(dtype) % 16 != 0) continue;
-    const int64_t n = addln::drop_bwd_workspace_bytes(dtype, aligned, kind & 2, kind & 4, rows, static_cast<int>(H), c.dev);
+  for (int kind = 0; kind < 12; ++kind) {
+    const int mode = kind / 4;
+    if (mode == addln::kAligned && H * elem_bytes(dtype) % 16 != 0) continue;
+    const int64_t n = addln::drop_bwd_workspace_bytes(dtype, mode, kind & 1, kind & 2, rows, static_cast<int>(H), c.dev);
     if (n < 0) return n;
     if (n > most) most = n;
   }
@@ -157,7 +164,7 @@ int dropout_add_norm_bwd(const void* dy, const void* dh, const void* h, double p
   const int es = elem_bytes(dtype);
   const uintptr_t data = bits(dy) | bits(dh) | bits(h) | bits(df) | bits(dx);
   if ((data & (es - 1)) || ((bits(gamma) | bits(mean) | bits(rstd)) & 3)) return ADDLN_ERR_ALIGN;
-  const bool aligned = ((data | bits(gamma) | static_cast<uintptr_t>(H * es)) & 15) == 0;
+  const int mode = mode_of(data, bits(gamma), H * es);
   const int64_t tb = rows * H * es;
   const bool cols = dbias || dgamma || dbeta;
   const Range ins[7] = {range_of(dy, tb), range_of(dh, tb), range_of(h, tb), range_of(gamma, H * 4),
@@ -171,7 +178,7 @@ int dropout_add_norm_bwd(const void* dy, const void* dh, const void* h, double p
   if (rc != ADDLN_OK) return rc;
   addln::DropBwdArgs a{dy, dh, h, gamma, mean, rstd, df, dx, dbias, dgamma, dbeta, nullptr, d, rows, 0,
                        static_cast<int>(H), 0, norm, static_cast<float>(1.0 / static_cast<double>(H))};
-  return addln::launch_drop_bwd(dtype, aligned, a, workspace, workspace_bytes, c);
+  return addln::launch_drop_bwd(dtype, mode, a, workspace, workspace_bytes, c);
 } catch (...) {
   return ADDLN_ERR_HOST_MEMORY;
 }

@@ -32,16 +32,17 @@ __device__ __forceinline__ float2 walker_sum2(Exchange<true>& ex, float2 v) {
 // Column sums of a kernel: dgamma, with FULL dbeta, with BIAS dbias.
 __host__ __device__ constexpr int drop_sums(bool full, bool bias) { return 1 + full + bias; }
 
-// FULL: a layer norm, or dbeta is wanted.  BIAS: dbias is wanted.  SH: some
-// rows do not begin on 16-byte borders.
-template <int DT, int NV, bool FULL, bool BIAS, bool SH>
+// FULL: a layer norm, or dbeta is wanted.  BIAS: dbias is wanted.  MODE: how
+// rows lie.
+template <int DT, int NV, bool FULL, bool BIAS, int MODE>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     k_drop_bwd(const __grid_constant__ DropBwdArgs p) {
   using IO = Io<DT>;
+  constexpr bool SH = MODE == kShifted;
   constexpr int S = IO::kBytes, VE = IO::kVec, N = VE / 2;
   constexpr int A = drop_sums(FULL, BIAS), NT = 3;
   constexpr int P = NV * N;
-  using R = Ring<DT, NV, NT, SH>;
+  using R = Ring<DT, NV, NT, MODE>;
   extern __shared__ __align__(128) unsigned char smem[];
   if (p.w.C > 1) cluster_started();
   const int T = p.w.cta_warps * 32;
@@ -49,7 +50,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
   const int rank = p.w.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.w.C);
   const int64_t cta = blockIdx.x / p.w.C;
   const int64_t stride = static_cast<int64_t>(gridDim.x / p.w.C) * p.w.rows_per_cta;
-  int64_t row = cta * p.w.rows_per_cta + side;
+  int64_t row = first_row<MODE>(cta, p.w.rows_per_cta, side);
   const int col0 = rank * p.w.slice;
   constexpr int slots = kMaxSlots;
   const int64_t extent = p.rows * static_cast<int64_t>(p.H) * S;
@@ -60,7 +61,10 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
   kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<1>() + lane * 16;
   Exchange<true> ex{p.w, p.sums_at + side * 2 * p.w.warps * 16, 0};
   Cols<VE, NV> cs;
-  cs.init(tid >> 5, col0, min(p.w.slice, p.H - col0));
+  if constexpr (MODE == kEdged)
+    cs.init_edged(tid >> 5, col0, p.w.slice, p.H, static_cast<int>(row * p.H & (VE - 1)));
+  else
+    cs.init(tid >> 5, col0, min(p.w.slice, p.H - col0));
   const bool has_dy = p.dy != nullptr, has_dh = p.dh != nullptr;
 
   auto offset = [&](int64_t r) { return (r * p.H + cs.c0) * S; };
@@ -95,7 +99,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
     float g[VE];
-    load_params<VE, SH>(has_dy ? p.gamma : nullptr, cs.col(k), p.H, 0.f, g, 784);
+    load_params<VE, MODE>(has_dy ? p.gamma : nullptr, cs.col(k), p.H, 0.f, g, 784);
     kept.put(0, k, g);
   }
   stats(row);
@@ -111,8 +115,8 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
   const float2 scale = dup2(p.drop.scale);
   for (int slot = 0; row < p.rows; row += stride, slot = slot + 1 == slots ? 0 : slot + 1) {
     const int64_t off = offset(row);
-    const uint64_t at = static_cast<uint64_t>(row) * static_cast<uint32_t>(p.H) + static_cast<uint32_t>(cs.c0);
-    Mask<VE, NV, SH> mask;
+    const uint64_t at = static_cast<uint64_t>(row * p.H + cs.c0);
+    Mask<VE, NV, MODE> mask;
     if (p.drop.on) mask.row(rng, at, p.drop.above, p.drop.wide);
     ring.template wait<1>();
     ring.meet();
@@ -123,6 +127,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     auto take = [&](int i, int k, float2 (&v)[N]) { IO::to_pairs(ring.take(slot, i, k, sh[i]), v); };
     auto hat = [&](int k, float2 (&v)[N]) {
       take(1, k, v);
+      if (MODE == kEdged && k == 0) cs.clear_low(v);
 #pragma unroll
       for (int j = 0; j < N; ++j) v[j] = mul2(FULL ? add2(v[j], nm) : v[j], rs);
     };
@@ -135,6 +140,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
       hat(k, hh);
       take(0, k, dy);
       take(2, k, d);
+      if (MODE == kEdged && k == 0) cs.clear_low(dy), cs.clear_low(d);
       kept.get(0, k, u);
 #pragma unroll
       for (int i = 0; i < N; ++i) {
@@ -153,7 +159,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     // rstd mean(u hhat), rstd mean(u)
     const float2 na2 = dup2(-rs.x * (m.x * p.inv_h));
     const float2 na1 = dup2(FULL && p.norm == ADDLN_NORM_LAYER ? -rs.x * (m.y * p.inv_h) : 0.f);
-    Writer<DT, NV, SH> dx, df;
+    Writer<DT, NV, MODE> dx, df;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float2 hh[N], o[N];
@@ -214,9 +220,9 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     }
     if (side == 0) {
       float* out = p.part + cta * A * p.Hp;
-      store_cols<VE, NV>(out, cs, 787, p.Hp, sg);
-      if constexpr (FULL) store_cols<VE, NV>(out + p.Hp, cs, 788, p.Hp, sb);
-      if constexpr (BIAS) store_cols<VE, NV>(out + (A - 1) * p.Hp, cs, 789, p.Hp, sf);
+      store_cols<VE, NV, MODE>(out, cs, 787, p.Hp, sg);
+      if constexpr (FULL) store_cols<VE, NV, MODE>(out + p.Hp, cs, 788, p.Hp, sb);
+      if constexpr (BIAS) store_cols<VE, NV, MODE>(out + (A - 1) * p.Hp, cs, 789, p.Hp, sf);
     }
   }
   if (p.w.C > 1) cooperative_groups::this_cluster().sync();
@@ -261,11 +267,12 @@ struct Choice {
 // many rows side by side as fit it, else one CTA for a row, else a cluster of
 // as few CTAs as hold it.  Shared memory: the ring (at least what the walkers
 // need to join their sums), gamma, the row sums.
-template <int DT, int NV, bool FULL, bool BIAS, bool SH>
+template <int DT, int NV, bool FULL, bool BIAS, int MODE>
 Choice make(int H, int64_t rows, int sms) {
   constexpr int VE = Io<DT>::kVec;
   Choice c;
-  c.k = &k_drop_bwd<DT, NV, FULL, BIAS, SH>;
+  c.k = &k_drop_bwd<DT, NV, FULL, BIAS, MODE>;
+  if (MODE == kEdged) H += VE - 1;
   const int groups = (H + VE - 1) / VE;
   c.sh.C = (groups + NV * kMaxThreads - 1) / (NV * kMaxThreads);
   c.sh.slice = c.sh.C == 1 ? H : ((H + c.sh.C - 1) / c.sh.C + 15) / 16 * 16;
@@ -273,7 +280,7 @@ Choice make(int H, int64_t rows, int sms) {
   c.sh.rows = c.sh.C > 1 ? 1 : rows_side_by_side(kMaxThreads / threads, rows, sms);
   c.sh.threads = threads * c.sh.rows;
   const int warps = c.sh.threads / 32;
-  int ring = warps * kMaxSlots * static_cast<int>(Ring<DT, NV, 3, SH>::kSlot);
+  int ring = warps * kMaxSlots * static_cast<int>(Ring<DT, NV, 3, MODE>::kSlot);
   int half = 0;  // walkers that give their sums to another at once
   for (int top = 1; top < c.sh.rows; top *= 2) half = top;
   const int join = half * drop_sums(FULL, BIAS) * NV * VE * threads * 4;
@@ -286,38 +293,35 @@ Choice make(int H, int64_t rows, int sms) {
 
 // 16 columns of a 16-bit type a thread where a row is longer than a warp's 8;
 // else 8 (fp32: 8 and 4).  Three column sums of shifted rows spill with 16.
-template <int DT, bool FULL, bool BIAS, bool SH>
+template <int DT, bool FULL, bool BIAS, int MODE>
 Choice choose(int H, int64_t rows, int sms) {
-  if constexpr (!(FULL && BIAS && SH && DT != kF32)) {
-    if (H > 32 * Io<DT>::kVec) return make<DT, 2, FULL, BIAS, SH>(H, rows, sms);
+  if constexpr (!(FULL && BIAS && MODE == kShifted && DT != kF32)) {
+    if (H > 32 * Io<DT>::kVec) return make<DT, 2, FULL, BIAS, MODE>(H, rows, sms);
   }
-  return make<DT, 1, FULL, BIAS, SH>(H, rows, sms);
+  return make<DT, 1, FULL, BIAS, MODE>(H, rows, sms);
 }
 
-template <int DT, bool SH>
+template <int DT, int MODE>
 Choice choose(int H, bool full, bool bias, int64_t rows, int sms) {
-  if (full) return bias ? choose<DT, true, true, SH>(H, rows, sms) : choose<DT, true, false, SH>(H, rows, sms);
-  return bias ? choose<DT, false, true, SH>(H, rows, sms) : choose<DT, false, false, SH>(H, rows, sms);
+  if (full) return bias ? choose<DT, true, true, MODE>(H, rows, sms) : choose<DT, true, false, MODE>(H, rows, sms);
+  return bias ? choose<DT, false, true, MODE>(H, rows, sms) : choose<DT, false, false, MODE>(H, rows, sms);
 }
 
 template <int DT>
-Choice choose(int H, bool aligned, bool full, bool bias, int64_t rows, int sms) {
-  return aligned ? choose<DT, false>(H, full, bias, rows, sms) : choose<DT, true>(H, full, bias, rows, sms);
+Choice choose(int H, int mode, bool full, bool bias, int64_t rows, int sms) {
+  return mode == kAligned ? choose<DT, kAligned>(H, full, bias, rows, sms)
+         : mode == kEdged ? choose<DT, kEdged>(H, full, bias, rows, sms)
+                          : choose<DT, kShifted>(H, full, bias, rows, sms);
 }
 
-Choice choose(int dtype, int H, bool aligned, bool full, bool bias, int64_t rows, int sms) {
-  return dtype == kF32   ? choose<kF32>(H, aligned, full, bias, rows, sms)
-         : dtype == kF16 ? choose<kF16>(H, aligned, full, bias, rows, sms)
-                         : choose<kBF16>(H, aligned, full, bias, rows, sms);
+Choice choose(int dtype, int H, int mode, bool full, bool bias, int64_t rows, int sms) {
+  return dtype == kF32   ? choose<kF32>(H, mode, full, bias, rows, sms)
+         : dtype == kF16 ? choose<kF16>(H, mode, full, bias, rows, sms)
+                         : choose<kBF16>(H, mode, full, bias, rows, sms);
 }
 
-// Units (CTAs or clusters) of a launch: those that fit the device at once, no
-// more than the rows need.
-int64_t units_of(const Choice& c, int64_t rows, const DeviceInfo& dev) {
-  const int fit = resident_units(reinterpret_cast<const void*>(c.k), c.sh, c.smem, dev);
-  if (fit < 0) return fit;
-  const int64_t need = (rows + c.sh.rows - 1) / c.sh.rows;
-  return need < fit ? need : fit;
+int fit_of(const Choice& c, const DeviceInfo& dev) {
+  return resident_units(reinterpret_cast<const void*>(c.k), c.sh, c.smem, dev);
 }
 
 int64_t part_bytes(int64_t parts, int sums, int64_t Hp) { return parts * sums * Hp * 4; }
@@ -339,26 +343,28 @@ BwdKernel pick_sums(int quads) {
 
 // What any number of rows up to this one needs: their CTAs are no more than
 // SMs, or than those that fit with as many rows side by side as there is room
-// for.
-int64_t drop_bwd_workspace_bytes(int dtype, bool aligned, bool full, bool bias, int64_t rows, int H,
-                                 const DeviceInfo& dev) {
+// for, and for edged rows as many again as make it a multiple of 8.
+int64_t drop_bwd_workspace_bytes(int dtype, int mode, bool full, bool bias, int64_t rows, int H, const DeviceInfo& dev) {
   using namespace blk;
-  const Choice ch = choose(dtype, H, aligned, full, bias, INT64_MAX / 2, dev.sms);
-  const int64_t fit = units_of(ch, INT64_MAX / 2, dev);
+  const Choice ch = choose(dtype, H, mode, full, bias, INT64_MAX / 2, dev.sms);
+  const int fit = fit_of(ch, dev);
   if (fit < 0) return fit;
   int64_t units = fit > dev.sms ? fit : dev.sms;
   if (units > rows) units = rows;
+  if (mode == kEdged) units = (units + 7) / 8 * 8;
   return part_bytes(units, drop_sums(full, bias), (H + 3) / 4 * 4);
 }
 
-int launch_drop_bwd(int dtype, bool aligned, const DropBwdArgs& args, void* ws, int64_t ws_bytes, const LaunchCtx& c) {
+int launch_drop_bwd(int dtype, int mode, const DropBwdArgs& args, void* ws, int64_t ws_bytes, const LaunchCtx& c) {
   using namespace blk;
   DropBwdArgs p = args;
   const bool full = p.norm == ADDLN_NORM_LAYER || p.dbeta, bias = p.dbias != nullptr;
-  const Choice ch = choose(dtype, p.H, aligned, full, bias, p.rows, c.dev.sms);
+  const Choice ch = choose(dtype, p.H, mode, full, bias, p.rows, c.dev.sms);
   p.w = walk_of(ch.sh);
-  p.parts = units_of(ch, p.rows, c.dev);
-  if (p.parts < 0) return static_cast<int>(p.parts);
+  const int fit = fit_of(ch, c.dev);
+  if (fit < 0) return fit;
+  if (mode == kEdged && fit < 8) return launch_drop_bwd(dtype, kShifted, args, ws, ws_bytes, c);
+  p.parts = units_for((p.rows + ch.sh.rows - 1) / ch.sh.rows, fit, mode == kEdged);
   p.kept_at = ch.kept_at;
   p.sums_at = ch.sums_at;
   p.Hp = (p.H + 3) / 4 * 4;

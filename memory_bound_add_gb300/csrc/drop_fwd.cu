@@ -10,11 +10,13 @@ namespace blk {
 // The vectors: gamma, and with FULL bias and beta.  Few columns a thread: in
 // registers; else in shared memory, one copy for all rows that a CTA has side
 // by side (as in block_fwd.cu).
-__host__ __device__ constexpr bool drop_in_registers(int columns, bool full, bool sh) { return columns <= 8 || !(full || sh); }
+__host__ __device__ constexpr bool drop_in_registers(int columns, bool full, int mode) {
+  return columns <= 8 || !(full || mode == kShifted);
+}
 
-template <int VE, int NV, bool FULL, bool SH>
+template <int VE, int NV, bool FULL, int MODE>
 struct DropParams {
-  static constexpr bool kRegs = drop_in_registers(NV * VE, FULL, SH);
+  static constexpr bool kRegs = drop_in_registers(NV * VE, FULL, MODE);
   static constexpr int P = kRegs ? NV * VE / 2 : 1, N = FULL ? 3 : 1;
   float2 r[N][P];
   Kept<VE, NV> kept;
@@ -32,7 +34,7 @@ struct DropParams {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float v[VE];
-      load_params<VE, SH>(from[i], c, p.H, 0.f, v, 770 + i);
+      load_params<VE, MODE>(from[i], c, p.H, 0.f, v, 770 + i);
       if constexpr (kRegs) {
 #pragma unroll
         for (int e = 0; e < VE / 2; ++e) r[i][k * VE / 2 + e] = make_float2(v[2 * e], v[2 * e + 1]);
@@ -43,15 +45,16 @@ struct DropParams {
   }
 };
 
-// FULL: a layer norm, or a bias or a beta.  SH: some rows do not begin on
-// 16-byte borders.
-template <int DT, int NV, bool FULL, bool SH>
+// FULL: a layer norm, or a bias or a beta.  MODE: how rows
+// lie.
+template <int DT, int NV, bool FULL, int MODE>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     k_drop_fwd(const __grid_constant__ DropFwdArgs p) {
   using IO = Io<DT>;
+  constexpr bool SH = MODE == kShifted;
   constexpr int S = IO::kBytes, VE = IO::kVec, Q = VE / 2;
   constexpr int P = NV * Q;
-  using R = Ring<DT, NV, 2, SH>;
+  using R = Ring<DT, NV, 2, MODE>;
   extern __shared__ __align__(128) unsigned char smem[];
   if (p.w.C > 1) cluster_started();
   const int slots = p.slots;
@@ -59,16 +62,19 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
   const int side = (threadIdx.x >> 5) / p.w.cta_warps, warp = (threadIdx.x >> 5) - side * p.w.cta_warps;
   const int rank = p.w.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.w.C);
   const int64_t stride = static_cast<int64_t>(gridDim.x / p.w.C) * p.w.rows_per_cta;
-  int64_t row = static_cast<int64_t>(blockIdx.x / p.w.C) * p.w.rows_per_cta + side;
+  int64_t row = first_row<MODE>(blockIdx.x / p.w.C, p.w.rows_per_cta, side);
   const int col0 = rank * p.w.slice;
   const int64_t extent = p.rows * static_cast<int64_t>(p.H) * S;
-  Exchange<!drop_in_registers(NV * VE, FULL, SH)> ex{p.w, p.sums_at + side * 2 * p.w.warps * 16, 0};
+  Exchange<!drop_in_registers(NV * VE, FULL, MODE)> ex{p.w, p.sums_at + side * 2 * p.w.warps * 16, 0};
   const bool leader = rank == 0 && lane == 0 && warp == 0;
   const bool has_x = p.x != nullptr;
   R ring;
   ring.base = smem_addr(smem) + (threadIdx.x >> 5) * p.ring_slots * R::kSlot + lane * 16;
   Cols<VE, NV> cs;
-  cs.init(warp, col0, min(p.w.slice, p.H - col0));
+  if constexpr (MODE == kEdged)
+    cs.init_edged(warp, col0, p.w.slice, p.H, static_cast<int>(row * p.H & (VE - 1)));
+  else
+    cs.init(warp, col0, min(p.w.slice, p.H - col0));
   auto offset = [&](int64_t r) { return (r * p.H + cs.c0) * S; };
   auto fetch = [&](int slot, int64_t r) {
     if (r < p.rows) {
@@ -83,8 +89,8 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
   for (int s = 0; s < slots; ++s) fetch(s, row + s * stride);
   Philox rng;
   rng.init(p.drop);
-  DropParams<VE, NV, FULL, SH> par;
-  constexpr bool kRegs = DropParams<VE, NV, FULL, SH>::kRegs;
+  DropParams<VE, NV, FULL, MODE> par;
+  constexpr bool kRegs = DropParams<VE, NV, FULL, MODE>::kRegs;
   if constexpr (!kRegs)
     par.kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<FULL ? 3 : 1>() + lane * 16;
   if (kRegs || side == 0) {
@@ -97,8 +103,8 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
 
   for (int slot = 0; row < p.rows; row += stride, slot = slot + 1 == slots ? 0 : slot + 1) {
     const int64_t off = offset(row);
-    const uint64_t at = static_cast<uint64_t>(row) * static_cast<uint32_t>(p.H) + static_cast<uint32_t>(cs.c0);
-    Mask<VE, NV, SH> mask;
+    const uint64_t at = static_cast<uint64_t>(row * p.H + cs.c0);
+    Mask<VE, NV, MODE> mask;
     if (p.drop.on) mask.row(rng, at, p.drop.above, p.drop.wide);
     if (slots == 1) ring.template wait<0>(); else ring.template wait<1>();
     ring.meet();
@@ -126,7 +132,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     ring.meet();
     fetch(slot, row + slots * stride);  // the slot has been read
     if (p.h != nullptr) {
-      Writer<DT, NV, SH> out;
+      Writer<DT, NV, MODE> out;
 #pragma unroll
       for (int k = 0; k < NV; ++k) out.put(cs, p.h, off, k, IO::from_pairs(v + k * Q), 775, extent);
     }
@@ -137,7 +143,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
       if (FULL && p.mean) p.mean[row] = st.mean;
     }
     const float2 negm = dup2(-st.m), r2 = dup2(st.M2);
-    Writer<DT, NV, SH> out;
+    Writer<DT, NV, MODE> out;
 #pragma unroll
     for (int k = 0; k < NV; ++k) {
       float2 g[Q], e[Q];
@@ -166,42 +172,44 @@ struct Choice {
   Spread s;
 };
 
-template <int DT, int NV, bool SH>
+template <int DT, int NV, int MODE>
 Choice make(const DropFwdArgs& p, bool full, int sms) {
   constexpr int VE = Io<DT>::kVec;
   Choice c;
-  c.k = full ? &k_drop_fwd<DT, NV, true, SH> : &k_drop_fwd<DT, NV, false, SH>;
-  const bool shared = !drop_in_registers(NV * VE, full, SH);
-  c.s = spread(p.H, VE, NV, p.rows, sms, Ring<DT, NV, 2, SH>::kSlot,
+  c.k = full ? &k_drop_fwd<DT, NV, true, MODE> : &k_drop_fwd<DT, NV, false, MODE>;
+  const bool shared = !drop_in_registers(NV * VE, full, MODE);
+  c.s = spread(MODE == kEdged ? p.H + VE - 1 : p.H, VE, NV, p.rows, sms, Ring<DT, NV, 2, MODE>::kSlot,
                !shared ? 0 : full ? Kept<VE, NV>::template bytes<3>() : Kept<VE, NV>::template bytes<1>(), 16);
   return c;
 }
 
-template <int DT, bool SH>
+template <int DT, int MODE>
 Choice choose(const DropFwdArgs& p, bool full, int sms) {
   constexpr int VE = Io<DT>::kVec;
-  switch (groups_a_thread((p.H + VE - 1) / VE)) {
-    case 1: return make<DT, 1, SH>(p, full, sms);
-    case 2: return make<DT, 2, SH>(p, full, sms);
-    case 3: return make<DT, 3, SH>(p, full, sms);
-    default: return make<DT, 4, SH>(p, full, sms);
+  switch (groups_a_thread(((MODE == kEdged ? p.H + VE - 1 : p.H) + VE - 1) / VE)) {
+    case 1: return make<DT, 1, MODE>(p, full, sms);
+    case 2: return make<DT, 2, MODE>(p, full, sms);
+    case 3: return make<DT, 3, MODE>(p, full, sms);
+    default: return make<DT, 4, MODE>(p, full, sms);
   }
 }
 
 template <int DT>
-Choice choose(const DropFwdArgs& p, bool aligned, bool full, int sms) {
-  return aligned ? choose<DT, false>(p, full, sms) : choose<DT, true>(p, full, sms);
+Choice choose(const DropFwdArgs& p, int mode, bool full, int sms) {
+  return mode == kAligned ? choose<DT, kAligned>(p, full, sms)
+         : mode == kEdged ? choose<DT, kEdged>(p, full, sms)
+                          : choose<DT, kShifted>(p, full, sms);
 }
 
 }  // namespace
 }  // namespace blk
 
-int launch_drop_fwd(int dtype, bool aligned, const DropFwdArgs& args, const LaunchCtx& c) {
+int launch_drop_fwd(int dtype, int mode, const DropFwdArgs& args, const LaunchCtx& c) {
   using namespace blk;
   const bool full = args.norm == ADDLN_NORM_LAYER || args.bias || args.beta;
-  const Choice ch = dtype == kF32 ? choose<kF32>(args, aligned, full, c.dev.sms)
-                    : dtype == kF16 ? choose<kF16>(args, aligned, full, c.dev.sms)
-                                    : choose<kBF16>(args, aligned, full, c.dev.sms);
+  const Choice ch = dtype == kF32 ? choose<kF32>(args, mode, full, c.dev.sms)
+                    : dtype == kF16 ? choose<kF16>(args, mode, full, c.dev.sms)
+                                    : choose<kBF16>(args, mode, full, c.dev.sms);
   DropFwdArgs p = args;
   p.w = walk_of(ch.s.sh);
   p.kept_at = ch.s.kept_at;
@@ -209,9 +217,10 @@ int launch_drop_fwd(int dtype, bool aligned, const DropFwdArgs& args, const Laun
   p.ring_slots = ch.s.ring_slots;
   const int fit = resident_units(reinterpret_cast<const void*>(ch.k), ch.s.sh, ch.s.smem, c.dev);
   if (fit < 0) return fit;
+  if (mode == kEdged && fit < 8) return launch_drop_fwd(dtype, kShifted, args, c);
   p.slots = slots_ahead(p.rows, fit, ch.s);
   const int64_t need = (p.rows + ch.s.sh.rows - 1) / ch.s.sh.rows;
-  const cudaError_t e = launch_units(ch.k, need < fit ? need : fit, ch.s.sh, ch.s.smem, c, p);
+  const cudaError_t e = launch_units(ch.k, units_for(need, fit, mode == kEdged), ch.s.sh, ch.s.smem, c, p);
   if (e != cudaSuccess) {
     note_cuda_error(static_cast<int>(e));
     return ADDLN_ERR_LAUNCH;

@@ -93,13 +93,15 @@ __device__ __forceinline__ uint32_t keep_bits(const uint4& w, uint32_t above) {
   return m;
 }
 
-// The mask of a thread's groups of one row.  Rows on 16-byte borders: a group
-// of 8 is a block of bits, one of 4 (fp32) a half of one.  Other rows (SH): a
+// The mask of a thread's groups of one row.  Rows on 16-byte borders, and edged
+// ones: a group of 8 is a block of bits, one of 4 (fp32) a half of one.  Shifted
+// rows: a
 // group may lie in two blocks, its own and the next one, which is the next
 // lane's, or lane 0's of the next k, or behind the warp's last group a block of
 // its own; so all groups' bits are made first, 8 a group, and exchanged.
-template <int VE, int NV, bool SH>
+template <int VE, int NV, int MODE>
 struct Mask {
+  static constexpr bool SH = MODE == kShifted;
   uint32_t bits;  // SH: of group k from bit 8 k on
 
   // at: index in the tensor of this thread's first column of group 0

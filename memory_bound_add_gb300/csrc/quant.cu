@@ -78,11 +78,13 @@ __device__ __forceinline__ Scale pow2_of(float largest, int format) {
 
 // gamma and, with FULL, beta: in registers or in shared memory, as in
 // block_fwd.cu.
-__host__ __device__ constexpr bool quant_in_registers(int columns, bool full, bool sh) { return columns <= 8 || !(full || sh); }
+__host__ __device__ constexpr bool quant_in_registers(int columns, bool full, int mode) {
+  return columns <= 8 || !(full || mode == kShifted);
+}
 
-template <int VE, int NV, bool FULL, bool SH>
+template <int VE, int NV, bool FULL, int MODE>
 struct QuantParams {
-  static constexpr bool kRegs = quant_in_registers(NV * VE, FULL, SH);
+  static constexpr bool kRegs = quant_in_registers(NV * VE, FULL, MODE);
   static constexpr int P = kRegs ? NV * VE / 2 : 1, N = FULL ? 2 : 1;
   float2 r[N][P];
   Kept<VE, NV> kept;
@@ -100,7 +102,7 @@ struct QuantParams {
 #pragma unroll
     for (int i = 0; i < N; ++i) {
       float v[VE];
-      load_params<VE, SH>(from[i], c, p.H, 0.f, v, 800 + i);
+      load_params<VE, MODE>(from[i], c, p.H, 0.f, v, 800 + i);
       if constexpr (kRegs) {
 #pragma unroll
         for (int e = 0; e < VE / 2; ++e) r[i][k * VE / 2 + e] = make_float2(v[2 * e], v[2 * e + 1]);
@@ -111,14 +113,15 @@ struct QuantParams {
   }
 };
 
-// FULL: a layer norm or a beta.  SH: some rows do not begin on borders.
-template <int DT, int NV, bool FULL, bool SH>
+// FULL: a layer norm or a beta.  MODE: how rows lie.
+template <int DT, int NV, bool FULL, int MODE>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     k_norm_quant(const __grid_constant__ QuantArgs p) {
   using IO = Io<DT>;
+  constexpr bool SH = MODE == kShifted;
   constexpr int S = IO::kBytes, VE = IO::kVec, Q = VE / 2;
   constexpr int P = NV * Q;
-  using R = Ring<DT, NV, 2, SH>;
+  using R = Ring<DT, NV, 2, MODE>;
   using W = typename Bytes<VE>::W;
   extern __shared__ __align__(128) unsigned char smem[];
   if (p.w.C > 1) cluster_started();
@@ -127,16 +130,19 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
   const int side = (threadIdx.x >> 5) / p.w.cta_warps, warp = (threadIdx.x >> 5) - side * p.w.cta_warps;
   const int rank = p.w.C == 1 ? 0 : static_cast<int>(blockIdx.x % p.w.C);
   const int64_t stride = static_cast<int64_t>(gridDim.x / p.w.C) * p.w.rows_per_cta;
-  int64_t row = static_cast<int64_t>(blockIdx.x / p.w.C) * p.w.rows_per_cta + side;
+  int64_t row = first_row<MODE>(blockIdx.x / p.w.C, p.w.rows_per_cta, side);
   const int col0 = rank * p.w.slice;
   const int64_t elements = p.rows * static_cast<int64_t>(p.H), extent = elements * S;
-  Exchange<!quant_in_registers(NV * VE, FULL, SH)> ex{p.w, p.sums_at + side * 2 * p.w.warps * 16, 0};
+  Exchange<!quant_in_registers(NV * VE, FULL, MODE)> ex{p.w, p.sums_at + side * 2 * p.w.warps * 16, 0};
   const bool leader = rank == 0 && lane == 0 && warp == 0;
   const bool has_r = p.r != nullptr, has_norm = p.norm != ADDLN_NORM_NONE;
   R ring;
   ring.base = smem_addr(smem) + (threadIdx.x >> 5) * p.ring_slots * R::kSlot + lane * 16;
   Cols<VE, NV> cs;
-  cs.init(warp, col0, min(p.w.slice, p.H - col0));
+  if constexpr (MODE == kEdged)
+    cs.init_edged(warp, col0, p.w.slice, p.H, static_cast<int>(row * p.H & (VE - 1)));
+  else
+    cs.init(warp, col0, min(p.w.slice, p.H - col0));
   auto fetch = [&](int slot, int64_t r) {
     if (r < p.rows) {
       const int64_t at = (r * p.H + cs.c0) * S;
@@ -148,8 +154,8 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
   pdl_trigger();
   pdl_wait();
   for (int s = 0; s < slots; ++s) fetch(s, row + s * stride);
-  QuantParams<VE, NV, FULL, SH> par;
-  constexpr bool kRegs = QuantParams<VE, NV, FULL, SH>::kRegs;
+  QuantParams<VE, NV, FULL, MODE> par;
+  constexpr bool kRegs = QuantParams<VE, NV, FULL, MODE>::kRegs;
   if constexpr (!kRegs)
     par.kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<FULL ? 2 : 1>() + lane * 16;
   if (kRegs || side == 0) {
@@ -179,11 +185,11 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
         for (int i = 0; i < Q; ++i) v[k * Q + i] = add2(v[k * Q + i], r[i]);
       }
     }
-    if constexpr (SH) cs.clear(v);
+    if constexpr (MODE != kAligned) cs.clear(v);
     ring.meet();
     fetch(slot, row + slots * stride);  // the slot has been read
     if (p.h != nullptr) {
-      Writer<DT, NV, SH> out;
+      Writer<DT, NV, MODE> out;
 #pragma unroll
       for (int k = 0; k < NV; ++k) out.put(cs, p.h, off, k, IO::from_pairs(v + k * Q), 805, extent);
     }
@@ -328,7 +334,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
       round(std::integral_constant<int, ADDLN_Q_E5M2>());
     else
       round(std::integral_constant<int, ADDLN_Q_INT8>());
-    ByteWriter<VE, NV, SH> out;
+    ByteWriter<VE, NV, MODE> out;
 #pragma unroll
     for (int k = 0; k < NV; ++k) out.put(cs, p.q, at, k, w[k], 809, elements);
   }
@@ -344,43 +350,48 @@ struct Choice {
   Spread s;
 };
 
-template <int DT, int NV, bool SH>
+template <int DT, int NV, int MODE>
 Choice make(const QuantArgs& p, bool full, int sms) {
   constexpr int VE = Io<DT>::kVec;
   Choice c;
-  c.k = full ? &k_norm_quant<DT, NV, true, SH> : &k_norm_quant<DT, NV, false, SH>;
-  const bool shared = !quant_in_registers(NV * VE, full, SH);
+  c.k = full ? &k_norm_quant<DT, NV, true, MODE> : &k_norm_quant<DT, NV, false, MODE>;
+  const bool shared = !quant_in_registers(NV * VE, full, MODE);
   // a CTA's slice of a row holds whole groups
-  c.s = spread(p.H, VE, NV, p.rows, sms, Ring<DT, NV, 2, SH>::kSlot,
+  c.s = spread(MODE == kEdged ? p.H + VE - 1 : p.H, VE, NV, p.rows, sms, Ring<DT, NV, 2, MODE>::kSlot,
                !shared ? 0 : full ? Kept<VE, NV>::template bytes<2>() : Kept<VE, NV>::template bytes<1>(), 128);
   return c;
 }
 
-template <int DT, bool SH>
+template <int DT, int MODE>
 Choice choose(const QuantArgs& p, bool full, int sms) {
   constexpr int VE = Io<DT>::kVec;
-  switch (groups_a_thread((p.H + VE - 1) / VE)) {
-    case 1: return make<DT, 1, SH>(p, full, sms);
-    case 2: return make<DT, 2, SH>(p, full, sms);
-    case 3: return make<DT, 3, SH>(p, full, sms);
-    default: return make<DT, 4, SH>(p, full, sms);
+  switch (groups_a_thread(((MODE == kEdged ? p.H + VE - 1 : p.H) + VE - 1) / VE)) {
+    case 1: return make<DT, 1, MODE>(p, full, sms);
+    case 2: return make<DT, 2, MODE>(p, full, sms);
+    case 3: return make<DT, 3, MODE>(p, full, sms);
+    default: return make<DT, 4, MODE>(p, full, sms);
   }
 }
 
 template <int DT>
-Choice choose(const QuantArgs& p, bool aligned, bool full, int sms) {
-  return aligned ? choose<DT, false>(p, full, sms) : choose<DT, true>(p, full, sms);
+Choice choose(const QuantArgs& p, int mode, bool full, int sms) {
+  return mode == kAligned ? choose<DT, kAligned>(p, full, sms)
+         : mode == kEdged ? choose<DT, kEdged>(p, full, sms)
+                          : choose<DT, kShifted>(p, full, sms);
 }
 
 }  // namespace
 }  // namespace blk
 
-int launch_norm_quant(int dtype, bool aligned, const QuantArgs& args, const LaunchCtx& c) {
+int launch_norm_quant(int dtype, int mode, const QuantArgs& args, const LaunchCtx& c) {
   using namespace blk;
   const bool full = args.norm == ADDLN_NORM_LAYER || args.beta;
-  const Choice ch = dtype == kF32 ? choose<kF32>(args, aligned, full, c.dev.sms)
-                    : dtype == kF16 ? choose<kF16>(args, aligned, full, c.dev.sms)
-                                    : choose<kBF16>(args, aligned, full, c.dev.sms);
+  const bool groups = args.s.scaling == ADDLN_SCALE_GROUP || args.s.scaling == ADDLN_SCALE_POW2;
+  // a granule of an edged row may lie in two groups
+  if (mode == kEdged && groups) mode = kShifted;
+  const Choice ch = dtype == kF32 ? choose<kF32>(args, mode, full, c.dev.sms)
+                    : dtype == kF16 ? choose<kF16>(args, mode, full, c.dev.sms)
+                                    : choose<kBF16>(args, mode, full, c.dev.sms);
   QuantArgs p = args;
   p.w = walk_of(ch.s.sh);
   p.kept_at = ch.s.kept_at;
@@ -388,9 +399,10 @@ int launch_norm_quant(int dtype, bool aligned, const QuantArgs& args, const Laun
   p.ring_slots = ch.s.ring_slots;
   const int fit = resident_units(reinterpret_cast<const void*>(ch.k), ch.s.sh, ch.s.smem, c.dev);
   if (fit < 0) return fit;
+  if (mode == kEdged && fit < 8) return launch_norm_quant(dtype, kShifted, args, c);
   p.slots = slots_ahead(p.rows, fit, ch.s);
   const int64_t need = (p.rows + ch.s.sh.rows - 1) / ch.s.sh.rows;
-  const cudaError_t e = launch_units(ch.k, need < fit ? need : fit, ch.s.sh, ch.s.smem, c, p);
+  const cudaError_t e = launch_units(ch.k, units_for(need, fit, mode == kEdged), ch.s.sh, ch.s.smem, c, p);
   if (e != cudaSuccess) {
     note_cuda_error(static_cast<int>(e));
     return ADDLN_ERR_LAUNCH;

@@ -78,9 +78,9 @@ __device__ __forceinline__ void st_stream_word(char* p, W v) {
 }
 
 // Writer (block.cuh) for rows of bytes: a row's groups of VE bytes in the order
-// of k.  Rows that begin off the words' borders (SH) are written in whole words
+// of k.  Rows that begin off the words' borders (shifted) are written in whole words
 // too, each of a group's begin and its neighbour's end.
-template <int VE, int NV, bool SH>
+template <int VE, int NV, int MODE>
 struct ByteWriter {
   using W = typename Bytes<VE>::W;
   W prev;  // the last group, of lane 31
@@ -88,8 +88,17 @@ struct ByteWriter {
   __device__ __forceinline__ void put(const Cols<VE, NV>& cs, void* base, int64_t off, int k, W v, int site, int64_t extent) {
     off += k * cs.kStep;
     char* p = static_cast<char*>(base) + off;
-    if constexpr (!SH) {
+    if constexpr (MODE == kAligned) {
       if (cs.ok(k) && ADDLN_IN(site, off, VE, extent)) st_stream_word<W>(p, v);
+    } else if constexpr (MODE == kEdged) {
+      const int lo = k == 0 ? cs.low : 0, hi = cs.valid(k);
+      if (lo == 0 && hi == VE) {
+        if (ADDLN_IN(site, off, VE, extent)) st_stream_word<W>(p, v);
+      } else {
+#pragma unroll
+        for (int e = 0; e < VE; ++e)
+          if (e >= lo && e < hi && ADDLN_IN(site, off + e, 1, extent)) p[e] = static_cast<char>(v >> (8 * e));
+      }
     } else {
       const int lane = threadIdx.x & 31;
       const int s = static_cast<int>(reinterpret_cast<uintptr_t>(p) & (VE - 1));  // the same for the warp

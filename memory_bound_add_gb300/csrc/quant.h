@@ -39,8 +39,7 @@ struct QuantArgs {
 
 // Arguments of one dequant_rows launch.  scale_row, scale_group: scales between a
 // group's and the next row's, and the next group's; scales: all of them; pieces: of
-// a row, 32 16-byte vectors of out each; reciprocal: 2^32 over the 32-byte vectors
-// of out a row, rounded up.
+// a row, 32 16-byte vectors of out each; reciprocal: 2^32 / H, rounded up.
 struct DequantArgs {
   const void* q;
   void* out;
@@ -51,10 +50,11 @@ struct DequantArgs {
   int64_t scale_row, scale_group, scales;
 };
 
-// aligned: every row of every tensor in the I/O dtype, and every vector, begins
-// and ends on 16-byte borders, and every row of q on borders of 16 bytes over
-// the I/O type's size.
-int launch_norm_quant(int dtype, bool aligned, const QuantArgs& p, const LaunchCtx& c);
+// mode: kAligned where every row of every tensor in the I/O dtype, and every vector,
+// begins and ends on 16-byte borders, and every row of q on borders of 16 bytes over
+// the I/O type's size; kEdged where all these tensors begin on such.
+int launch_norm_quant(int dtype, int mode, const QuantArgs& p, const LaunchCtx& c);
+// aligned: as kAligned, of out and q.
 int launch_dequant(int dtype, bool aligned, const DequantArgs& p, const LaunchCtx& c);
 
 int read_bounds_quant(unsigned long long* word);

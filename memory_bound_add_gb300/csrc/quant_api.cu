@@ -59,7 +59,9 @@ int norm_quant_fwd(const void* x, const void* residual, int norm, const float* g
   if ((data & (es - 1)) || ((params | bits(mean) | bits(rstd)) & 3) || (scaling != ADDLN_SCALE_POW2 && (bits(scale) & 3)))
     return ADDLN_ERR_ALIGN;
   // a 16-byte vector of the I/O type becomes 16 / es bytes of q
-  const bool aligned = ((data | params | static_cast<uintptr_t>(H * es)) & 15) == 0 && (bits(q) & (16 / es - 1)) == 0;
+  const bool begins = (data & 15) == 0 && (bits(q) & (16 / es - 1)) == 0;
+  const bool rest = ((params | static_cast<uintptr_t>(H * es)) & 15) == 0;
+  const int mode = !begins ? addln::kShifted : rest ? addln::kAligned : addln::kEdged;
   const int64_t tb = rows * H * es;
   const bool given = scaling == ADDLN_SCALE_TENSOR;
   const Range sr = range_of(scale, scale_bytes), none = range_of(nullptr, 0);
@@ -78,7 +80,7 @@ int norm_quant_fwd(const void* x, const void* residual, int norm, const float* g
   if (rc != ADDLN_OK) return rc;
   addln::QuantArgs a{x, residual, gamma, beta, q, h, mean, rstd, s, rows, static_cast<int>(H), norm, eps,
                      static_cast<float>(1.0 / static_cast<double>(H))};
-  return addln::launch_norm_quant(dtype, aligned, a, c);
+  return addln::launch_norm_quant(dtype, mode, a, c);
 } catch (...) {
   return ADDLN_ERR_HOST_MEMORY;
 }
