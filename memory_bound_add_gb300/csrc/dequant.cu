@@ -45,108 +45,96 @@ __device__ __forceinline__ uint32_t load_scale(const DequantArgs& p, int64_t i, 
   return pow2 ? __ldg(static_cast<const uint8_t*>(p.s.scale) + i) : __ldg(static_cast<const uint32_t*>(p.s.scale) + i);
 }
 
-// Tensors that begin on such borders are one run of vectors of 32 bytes of out, of
-// which a thread takes U, a CTA's threads apart: 32-byte stores, and 16 bytes of q a
-// load (8 for fp32).  32768x8192 from e4m3 to bf16 110 us (7.3 TB/s) where warps of
-// rows, 8 bytes a load, take 183.
+// Tensors that begin on such borders are one run of vectors of 32 bytes of out, one
+// a thread: 32-byte stores, and 16 bytes of q a load (8 for fp32).  32768x8192 from
+// e4m3 to bf16 110 us (7.3 TB/s) where warps of rows, 8 bytes a load, take 183; four
+// vectors a thread are no faster there and slower below (4096x768 3.9 us, one 2.9).
 //
 // RAGGED: rows are not whole vectors, so that a row's or a group's end may lie in
 // one.  Its elements then have up to three scales (the rest of a group, a row's
 // short last one, the next row's first): those before b1, those before b2, the
 // others.
-template <int DT, int FMT, int U, bool RAGGED>
+template <int DT, int FMT, bool RAGGED>
 __global__ void __launch_bounds__(kDequantThreads) k_dequant_run(const __grid_constant__ DequantArgs p) {
   using IO = Io<DT>;
   constexpr int S = IO::kBytes, VW = 32 / S, N = VW / 4;  // columns and words of q a vector
   pdl_trigger();
   pdl_wait();
-  const uint64_t e0 = static_cast<uint64_t>(blockIdx.x) * (kDequantThreads * U * VW);
+  const uint64_t e0 = static_cast<uint64_t>(blockIdx.x) * (kDequantThreads * VW);
   const uint64_t elements = static_cast<uint64_t>(p.rows) * p.H;
   const uint64_t row0 = (e0 >> 32) ? e0 / static_cast<uint32_t>(p.H) : static_cast<uint32_t>(e0) / static_cast<uint32_t>(p.H);
-  const uint32_t in_row = static_cast<uint32_t>(e0 - row0 * p.H);
+  const uint64_t at = e0 + threadIdx.x * VW;
+  if (at >= elements) return;
+  // l is below 2^16: the product's upper half with 2^32 / H rounded up is the
+  // exact quotient
+  const uint32_t l = static_cast<uint32_t>(e0 - row0 * p.H) + threadIdx.x * VW;
+  const uint32_t r = __umulhi(l, p.reciprocal);
+  int c = static_cast<int>(l - r * p.H);
+  int64_t row = static_cast<int64_t>(row0 + r);
   const bool pow2 = p.s.scaling == ADDLN_SCALE_POW2;
   const int shift = p.s.lanes_shift;
-  auto scale_at = [&](int64_t row, int c) {
+  auto scale = [&] {
     return row < p.rows ? load_scale(p, row * p.scale_row + (c >> shift) * p.scale_group, pow2) : 0;
   };
-  uint32_t w[U][N], s[U], s1[RAGGED ? U : 1], s2[RAGGED ? U : 1];
-  int b1[RAGGED ? U : 1], b2[RAGGED ? U : 1];
+  const bool tail = RAGGED && at + VW > elements;
+  const uint8_t* q = static_cast<const uint8_t*>(p.q) + at;
+  uint32_t w[N] = {};
+  if (tail) {
 #pragma unroll
-  for (int j = 0; j < U; ++j) {
-    const uint32_t l = in_row + (j * kDequantThreads + threadIdx.x) * VW;
-    const uint64_t at = e0 + (j * kDequantThreads + threadIdx.x) * VW;
-    s[j] = 0;
-    if constexpr (RAGGED) s1[j] = s2[j] = 0, b1[j] = b2[j] = VW;
-#pragma unroll
-    for (int i = 0; i < N; ++i) w[j][i] = 0;
-    if (at >= elements) continue;
-    // l is below 2^16: the product's upper half with 2^32 / H rounded up is the
-    // exact quotient
-    const uint32_t r = __umulhi(l, p.reciprocal);
-    int c = static_cast<int>(l - r * p.H);
-    int64_t row = static_cast<int64_t>(row0 + r);
-    const uint8_t* q = static_cast<const uint8_t*>(p.q) + at;
-    if (RAGGED && at + VW > elements) {
-#pragma unroll
-      for (int e = 0; e < VW; ++e)
-        if (at + e < elements && ADDLN_IN(825, at + e, 1, elements)) w[j][e / 4] |= static_cast<uint32_t>(__ldg(q + e)) << (8 * (e % 4));
-    } else if (ADDLN_IN(825, at, VW, elements)) {
-      if constexpr (N == 4) {
-        const uint4 u = __ldcs(reinterpret_cast<const uint4*>(q));
-        w[j][0] = u.x, w[j][1] = u.y, w[j][2] = u.z, w[j][3] = u.w;
-      } else {
-        const uint2 u = __ldcs(reinterpret_cast<const uint2*>(q));
-        w[j][0] = u.x, w[j][1] = u.y;
-      }
+    for (int e = 0; e < VW; ++e)
+      if (at + e < elements && ADDLN_IN(825, at + e, 1, elements)) w[e / 4] |= static_cast<uint32_t>(__ldg(q + e)) << (8 * (e % 4));
+  } else if (ADDLN_IN(825, at, VW, elements)) {
+    if constexpr (N == 4) {
+      const uint4 u = __ldcs(reinterpret_cast<const uint4*>(q));
+      w[0] = u.x, w[1] = u.y, w[2] = u.z, w[3] = u.w;
+    } else {
+      const uint2 u = __ldcs(reinterpret_cast<const uint2*>(q));
+      w[0] = u.x, w[1] = u.y;
     }
-    s[j] = scale_at(row, c);
-    if constexpr (RAGGED) {
-      auto left = [&] { return min(p.H - c, (((c >> shift) + 1) << shift) - c); };  // of the group
-      auto next = [&](int n) {
-        c += n;
-        if (c == p.H) c = 0, ++row;
-      };
-      int n = left();
-      if (n < VW) {
-        b1[j] = n;
+  }
+  const uint32_t s0 = scale();
+  uint32_t s1 = 0, s2 = 0;
+  int b1 = VW, b2 = VW;
+  if constexpr (RAGGED) {
+    auto left = [&] { return min(p.H - c, (((c >> shift) + 1) << shift) - c); };  // of the group
+    auto next = [&](int n) {
+      c += n;
+      if (c == p.H) c = 0, ++row;
+    };
+    int n = left();
+    if (n < VW) {
+      b1 = n;
+      next(n);
+      s1 = scale();
+      n = left();
+      if (b1 + n < VW) {
+        b2 = b1 + n;
         next(n);
-        s1[j] = scale_at(row, c);
-        n = left();
-        if (b1[j] + n < VW) {
-          b2[j] = b1[j] + n;
-          next(n);
-          s2[j] = scale_at(row, c);
-        }
+        s2 = scale();
       }
     }
   }
+  const float a = scale_from(s0, pow2);
+  float2 f[VW / 2];
 #pragma unroll
-  for (int j = 0; j < U; ++j) {
-    const uint64_t at = e0 + (j * kDequantThreads + threadIdx.x) * VW;
-    if (at >= elements) break;
-    const float a = scale_from(s[j], pow2);
-    float2 f[VW / 2];
+  for (int i = 0; i < N; ++i) from_q<FMT>(w[i], f[2 * i], f[2 * i + 1]);
+  if (!RAGGED || b1 == VW) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) from_q<FMT>(w[j][i], f[2 * i], f[2 * i + 1]);
-    if (!RAGGED || b1[RAGGED ? j : 0] == VW) {
+    for (int i = 0; i < VW / 2; ++i) f[i] = mul2(f[i], dup2(a));
+  } else {
+    const float b = scale_from(s1, pow2), d = scale_from(s2, pow2);
+    auto of = [&](int e) { return e < b1 ? a : e < b2 ? b : d; };
 #pragma unroll
-      for (int i = 0; i < VW / 2; ++i) f[i] = mul2(f[i], dup2(a));
-    } else if constexpr (RAGGED) {
-      const float b = scale_from(s1[j], pow2), d = scale_from(s2[j], pow2);
-      auto of = [&](int e) { return e < b1[j] ? a : e < b2[j] ? b : d; };
+    for (int i = 0; i < VW / 2; ++i) f[i] = mul2(f[i], make_float2(of(2 * i), of(2 * i + 1)));
+  }
+  const uint4 lo = IO::from_pairs(f), hi = IO::from_pairs(f + VW / 4);
+  char* out = static_cast<char*>(p.out) + at * S;
+  if (tail) {
 #pragma unroll
-      for (int i = 0; i < VW / 2; ++i) f[i] = mul2(f[i], make_float2(of(2 * i), of(2 * i + 1)));
-    }
-    const uint4 lo = IO::from_pairs(f), hi = IO::from_pairs(f + VW / 4);
-    char* out = static_cast<char*>(p.out) + at * S;
-    if (RAGGED && at + VW > elements) {
-#pragma unroll
-      for (int e = 0; e < VW; ++e)
-        if (at + e < elements && ADDLN_IN(826, (at + e) * S, S, elements * S))
-          store_element<S>(out + e * S, e < VW / 2 ? lo : hi, e % (VW / 2));
-      continue;
-    }
-    if (!ADDLN_IN(826, at * S, 32, elements * S)) continue;
+    for (int e = 0; e < VW; ++e)
+      if (at + e < elements && ADDLN_IN(826, (at + e) * S, S, elements * S))
+        store_element<S>(out + e * S, e < VW / 2 ? lo : hi, e % (VW / 2));
+  } else if (ADDLN_IN(826, at * S, 32, elements * S)) {
     asm volatile("st.global.cs.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(out), "r"(lo.x), "r"(lo.y), "r"(lo.z),
                  "r"(lo.w), "r"(hi.x), "r"(hi.y), "r"(hi.z), "r"(hi.w)
                  : "memory");
@@ -202,19 +190,19 @@ __global__ void __launch_bounds__(kDequantThreads) k_dequant(const __grid_consta
 
 namespace {
 using DequantKernel = void (*)(DequantArgs);
-// run: 0 where the tensors are no runs of vectors, else 1, and 2 more for ragged
-// ones.
+enum Run { kNone, kWhole, kRagged };  // of vectors
 template <int DT, int FMT>
-DequantKernel pick(int run, bool many, bool aligned) {
-  if (run == 3) return many ? &k_dequant_run<DT, FMT, 4, true> : &k_dequant_run<DT, FMT, 1, true>;
-  if (run == 1) return many ? &k_dequant_run<DT, FMT, 4, false> : &k_dequant_run<DT, FMT, 1, false>;
-  return aligned ? &k_dequant<DT, FMT, false> : &k_dequant<DT, FMT, true>;
+DequantKernel pick(Run run, bool aligned) {
+  return run == kWhole    ? &k_dequant_run<DT, FMT, false>
+         : run == kRagged ? &k_dequant_run<DT, FMT, true>
+         : aligned        ? &k_dequant<DT, FMT, false>
+                          : &k_dequant<DT, FMT, true>;
 }
 template <int DT>
-DequantKernel pick(int format, int run, bool many, bool aligned) {
-  return format == ADDLN_Q_E4M3   ? pick<DT, ADDLN_Q_E4M3>(run, many, aligned)
-         : format == ADDLN_Q_E5M2 ? pick<DT, ADDLN_Q_E5M2>(run, many, aligned)
-                                  : pick<DT, ADDLN_Q_INT8>(run, many, aligned);
+DequantKernel pick(int format, Run run, bool aligned) {
+  return format == ADDLN_Q_E4M3   ? pick<DT, ADDLN_Q_E4M3>(run, aligned)
+         : format == ADDLN_Q_E5M2 ? pick<DT, ADDLN_Q_E5M2>(run, aligned)
+                                  : pick<DT, ADDLN_Q_INT8>(run, aligned);
 }
 }  // namespace
 }  // namespace blk
@@ -231,20 +219,17 @@ int launch_dequant(int dtype, bool aligned, const DequantArgs& args, const Launc
   if (!group) p.s.lanes_shift = 24;  // one group, longer than any row
   const bool begins = (reinterpret_cast<uintptr_t>(p.out) & 31) == 0 && (reinterpret_cast<uintptr_t>(p.q) & (VW - 1)) == 0;
   // (rows shorter than a group's 32 columns: more than three scales a vector)
-  const int run = !begins || p.H < 32 ? 0 : p.H % VW == 0 ? 1 : 3;
-  // One vector a thread while all of them are on the GPU at once, else four.
-  const int64_t vectors = (p.rows * p.H + VW - 1) / VW;
-  const bool many = vectors > int64_t{2048} * c.dev.sms;
-  const DequantKernel k = dtype == kF32   ? pick<kF32>(p.s.format, run, many, aligned)
-                          : dtype == kF16 ? pick<kF16>(p.s.format, run, many, aligned)
-                                          : pick<kBF16>(p.s.format, run, many, aligned);
+  const Run run = !begins || p.H < 32 ? kNone : p.H % VW == 0 ? kWhole : kRagged;
+  const DequantKernel k = dtype == kF32   ? pick<kF32>(p.s.format, run, aligned)
+                          : dtype == kF16 ? pick<kF16>(p.s.format, run, aligned)
+                                          : pick<kBF16>(p.s.format, run, aligned);
   int64_t units = (p.rows + R - 1) / R * p.pieces, per = kDequantThreads / 32;  // warps
-  if (run) {
+  if (run != kNone) {
     p.reciprocal = static_cast<uint32_t>(((uint64_t{1} << 32) + p.H - 1) / p.H);
-    units = vectors, per = kDequantThreads * (many ? 4 : 1);
+    units = (p.rows * p.H + VW - 1) / VW, per = kDequantThreads;
   }
   const int64_t ctas = (units + per - 1) / per;
-  if (ctas > (int64_t{1} << 28)) return ADDLN_ERR_SHAPE;  // a warp's number has 32 bits
+  if (ctas > (run != kNone ? 0x7fffffff : 1 << 28)) return ADDLN_ERR_SHAPE;  // (a warp's number has 32 bits)
   const cudaError_t e = launch_kernel(k, dim3(static_cast<unsigned>(ctas)), dim3(kDequantThreads), 0, c.stream, c.pdl, p);
   if (e != cudaSuccess) {
     note_cuda_error(static_cast<int>(e));

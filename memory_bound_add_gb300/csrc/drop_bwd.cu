@@ -32,10 +32,21 @@ __device__ __forceinline__ float2 walker_sum2(Exchange<true>& ex, float2 v) {
 // Column sums of a kernel: dgamma, with FULL dbeta, with BIAS dbias.
 __host__ __device__ constexpr int drop_sums(bool full, bool bias) { return 1 + full + bias; }
 
+// Threads a CTA and registers a thread: 8 columns of a 16-bit type a thread fit 96
+// registers, so that more rows are on an SM at once (us, 4096x768 fp16 layer with all
+// gradients: 16 columns and 128 registers 15.2, 8 and 128 14.1, 8 and 96 13.3, 8 and
+// 80 14.6); shifted rows need more.
+__host__ __device__ constexpr bool bwd_lean(int dt, int nv, int mode) { return dt != kF32 && nv == 1 && mode != kShifted; }
+__host__ __device__ constexpr int bwd_threads(int dt, int nv, int mode) { return bwd_lean(dt, nv, mode) ? 640 : kMaxThreads; }
+template <int DT, int NV, int MODE>
+constexpr int bwd_regs() {
+  return bwd_lean(DT, NV, MODE) ? 96 : 128;
+}
+
 // FULL: a layer norm, or dbeta is wanted.  BIAS: dbias is wanted.  MODE: how
 // rows lie.
 template <int DT, int NV, bool FULL, bool BIAS, int MODE>
-__global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
+__global__ void __launch_bounds__(bwd_threads(DT, NV, MODE)) __maxnreg__((bwd_regs<DT, NV, MODE>()))
     k_drop_bwd(const __grid_constant__ DropBwdArgs p) {
   using IO = Io<DT>;
   constexpr bool SH = MODE == kShifted;
@@ -263,21 +274,21 @@ struct Choice {
   int smem = 0, kept_at = 0, sums_at = 0;
 };
 
-// NV groups of VE columns a thread; a CTA of up to kMaxThreads threads for as
+// NV groups of VE columns a thread; a CTA of up to bwd_threads threads for as
 // many rows side by side as fit it, else one CTA for a row, else a cluster of
 // as few CTAs as hold it.  Shared memory: the ring (at least what the walkers
 // need to join their sums), gamma, the row sums.
 template <int DT, int NV, bool FULL, bool BIAS, int MODE>
 Choice make(int H, int64_t rows, int sms) {
-  constexpr int VE = Io<DT>::kVec;
+  constexpr int VE = Io<DT>::kVec, kMost = bwd_threads(DT, NV, MODE);
   Choice c;
   c.k = &k_drop_bwd<DT, NV, FULL, BIAS, MODE>;
   if (MODE == kEdged) H += VE - 1;
   const int groups = (H + VE - 1) / VE;
-  c.sh.C = (groups + NV * kMaxThreads - 1) / (NV * kMaxThreads);
+  c.sh.C = (groups + NV * kMost - 1) / (NV * kMost);
   c.sh.slice = c.sh.C == 1 ? H : ((H + c.sh.C - 1) / c.sh.C + 15) / 16 * 16;
   const int threads = ((c.sh.slice + VE - 1) / VE + 32 * NV - 1) / (32 * NV) * 32;
-  c.sh.rows = c.sh.C > 1 ? 1 : rows_side_by_side(kMaxThreads / threads, rows, sms);
+  c.sh.rows = c.sh.C > 1 ? 1 : rows_side_by_side(kMost / threads, rows, sms);
   c.sh.threads = threads * c.sh.rows;
   const int warps = c.sh.threads / 32;
   int ring = warps * kMaxSlots * static_cast<int>(Ring<DT, NV, 3, MODE>::kSlot);
@@ -291,12 +302,22 @@ Choice make(int H, int64_t rows, int sms) {
   return c;
 }
 
-// 16 columns of a 16-bit type a thread where a row is longer than a warp's 8;
-// else 8 (fp32: 8 and 4).  Three column sums of shifted rows spill with 16.
+// The rows that walkers of 8 columns of a 16-bit type a thread have eight each of.
+inline int64_t few_rows(int H, int sms) {
+  const int t = (H + 255) / 256 * 32;
+  return t > 640 ? 0 : 8 * static_cast<int64_t>(sms) * (640 / t);
+}
+
+// 16 columns of a 16-bit type a thread (8 of fp32) where a row is longer than a
+// warp's 8 and a walker has more than eight rows (or none would fit one CTA); else 8
+// (fp32: 4 for short rows).  us with 8 / 16: 4096x768 layer (6 rows to a walker)
+// 13.3 / 15.2, 65536x768 124 / 111, 8192x2048 rms 44 / 33, 8192x4096 83 / 59.  Three
+// column sums of shifted rows spill with 16.
 template <int DT, bool FULL, bool BIAS, int MODE>
 Choice choose(int H, int64_t rows, int sms) {
   if constexpr (!(FULL && BIAS && MODE == kShifted && DT != kF32)) {
-    if (H > 32 * Io<DT>::kVec) return make<DT, 2, FULL, BIAS, MODE>(H, rows, sms);
+    if (H > 32 * Io<DT>::kVec && (DT == kF32 || rows > few_rows(H, sms)))
+      return make<DT, 2, FULL, BIAS, MODE>(H, rows, sms);
   }
   return make<DT, 1, FULL, BIAS, MODE>(H, rows, sms);
 }
@@ -342,14 +363,16 @@ BwdKernel pick_sums(int quads) {
 }  // namespace blk
 
 // What any number of rows up to this one needs: their CTAs are no more than
-// SMs, or than those that fit with as many rows side by side as there is room
-// for, and for edged rows as many again as make it a multiple of 8.
+// SMs, or than those of either kernel that fit with as many rows side by side as
+// there is room for, and for edged rows as many again as make it a multiple of 8.
 int64_t drop_bwd_workspace_bytes(int dtype, int mode, bool full, bool bias, int64_t rows, int H, const DeviceInfo& dev) {
   using namespace blk;
-  const Choice ch = choose(dtype, H, mode, full, bias, INT64_MAX / 2, dev.sms);
-  const int fit = fit_of(ch, dev);
-  if (fit < 0) return fit;
-  int64_t units = fit > dev.sms ? fit : dev.sms;
+  int64_t units = dev.sms;
+  for (const int64_t r : {few_rows(H, dev.sms), INT64_MAX / 2}) {
+    const int fit = fit_of(choose(dtype, H, mode, full, bias, r, dev.sms), dev);
+    if (fit < 0) return fit;
+    if (fit > units) units = fit;
+  }
   if (units > rows) units = rows;
   if (mode == kEdged) units = (units + 7) / 8 * 8;
   return part_bytes(units, drop_sums(full, bias), (H + 3) / 4 * 4);
