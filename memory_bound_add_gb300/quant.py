@@ -104,7 +104,7 @@ def _layout(dtype, scale_shape, scale_stride, shape):
     scale = torch.empty_strided(scale_shape, scale_stride, dtype=dtype, device="meta")
     if scale.dtype not in (_F32, _E8):
         raise ValueError(f"scale must be {_F32} or {_E8}, got {scale.dtype}")
-    if scale.numel() == 1 and scale.dim() <= 1:
+    if scale.numel() == 1 and scale.dim() <= 1 and not (scale.dtype is _E8 and len(shape) == scale.dim() == 1):
         if scale.dtype is not _F32:
             raise ValueError(f"a scale for the whole tensor must be {_F32}")
         return SCALE_TENSOR, 0, 0

@@ -278,6 +278,19 @@ def test_read_back_of_the_least_scales():
     assert got[:3].tolist() == [2.0 ** -127, 2.0 ** -126, 1.0] and got[3].isnan()
 
 
+@DTYPES
+def test_one_dimension(dtype):
+    # a single row without leading sizes
+    for H in (20, 264):
+        x = randn((H,), dtype, 1)
+        for scaling, group in SCALINGS:
+            r = mba.norm_quant(x.cuda(), norm=None, scaling=scaling, group=group)
+            two = mba.norm_quant(x.cuda().view(1, H), norm=None, scaling=scaling, group=group)
+            assert r.q.shape == (H,) and r.scale.shape == two.scale.shape[1:]
+            a, b = mba.dequantise(r.q, r.scale), mba.dequantise(two.q, two.scale)
+            assert torch.equal(a, b[0])
+
+
 def test_no_rows_and_one_column():
     e = torch.empty(0, 64, device="cuda", dtype=BF16)
     r = mba.norm_quant(e, e, gamma=torch.ones(64, device="cuda"), scaling="group")
