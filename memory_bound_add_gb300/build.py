@@ -77,7 +77,8 @@ def build_fast(force: bool = False) -> str | None:
     tmp = FAST_LIB + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{i}" for i in include), FAST_SRC,
-           "-o", tmp, "-L" + os.path.join(base, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda"]
+           "-o", tmp, "-L" + os.path.join(base, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda",
+           "-ltorch_cuda"]
     try:
         res = subprocess.run(cmd, capture_output=True, text=True)
         failed = res.stderr[-2000:] if res.returncode else ""

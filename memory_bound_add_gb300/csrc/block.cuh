@@ -129,6 +129,18 @@ struct Cols {
   }
 };
 
+// Asks L2 for a warp's part of a row of t, whose first byte of group 0 in this thread
+// is at `off` (a hint, before the kernel that wrote it may be done: nothing is read,
+// and every SM's writes land in L2).
+template <int S, int VE, int NV>
+__device__ __forceinline__ void prefetch_row(const void* t, int64_t off, const Cols<VE, NV>& cs, int site, int64_t extent) {
+  const int lane = threadIdx.x & 31;
+  // lane l asks for the warp's l-th line
+  const int64_t at = off + lane * (128 - 16);
+  if (t != nullptr && lane * 128 < (cs.left + lane * VE) * S && lane * 128 < NV * cs.kStep * S && ADDLN_IN(site, at, 1, extent))
+    prefetch_line(static_cast<const char*>(t) + at);
+}
+
 // ------------------------------------------------------- shifted granules
 // Bytes [sh, sh + 16) of the 32 bytes lo, hi; sh < 16, a multiple of 2.
 __device__ __forceinline__ uint4 window(const uint4& lo, const uint4& hi, int sh) {

@@ -13,10 +13,13 @@ template <int DT, bool VEC, int kBlocks>
 __global__ void __launch_bounds__(kThreads) k_dropout(const void* x, void* y, int64_t n, const DropSpec d) {
   using IO = Io<DT>;
   constexpr int S = IO::kBytes, U = S / 2;  // 16-byte vectors a block
+  const int64_t b0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kBlocks) + threadIdx.x;
+  // a short tensor's lines asked of L2 while the kernel before may be finishing
+  if (kBlocks == 1 && (threadIdx.x & (16 / S - 1)) == 0 && b0 * 8 < n && ADDLN_IN(764, b0 * 8 * S, 1, n * S))
+    prefetch_line(static_cast<const char*>(x) + b0 * 8 * S);
   pdl_trigger();
   pdl_wait();
   const float2 scale = dup2(d.scale);
-  const int64_t b0 = static_cast<int64_t>(blockIdx.x) * (kThreads * kBlocks) + threadIdx.x;
   const int64_t whole = VEC ? n / 8 : 0, extent = n * S;
   uint4 v[kBlocks][U];
 #pragma unroll

@@ -97,6 +97,14 @@ __global__ void __launch_bounds__(bwd_threads(DT, NV, MODE)) __maxnreg__((bwd_re
     if constexpr (FULL)
       if (p.mean) mean_n = __ldg(p.mean + r);
   };
+  // where a walker has few rows
+  if (p.rows <= 8 * stride)
+    for (int s = 0; s < slots && row + s * stride < p.rows; ++s) {
+      const int64_t at = offset(row + s * stride);
+      prefetch_row<S>(p.dy, at, cs, 779, extent);
+      prefetch_row<S>(p.dy ? p.h : nullptr, at, cs, 779, extent);
+      prefetch_row<S>(p.dh, at, cs, 779, extent);
+    }
   pdl_trigger();
   pdl_wait();
   // a tensor that the call does not have is zeros, written once

@@ -97,18 +97,16 @@ struct QuantParams {
       kept.get(i, k, v);
     }
   }
-  __device__ __forceinline__ void load(const QuantArgs& p, int c, int k) {
-    const float* from[2] = {p.gamma, p.beta};
+  // vector i, group k, at column c
+  __device__ __forceinline__ void load(const QuantArgs& p, int i, int c, int k) {
+    const float* from = i == 0 ? p.gamma : p.beta;
+    float v[VE];
+    load_params<VE, MODE>(from, c, p.H, 0.f, v, 800);
+    if constexpr (kRegs) {
 #pragma unroll
-    for (int i = 0; i < N; ++i) {
-      float v[VE];
-      load_params<VE, MODE>(from[i], c, p.H, 0.f, v, 800 + i);
-      if constexpr (kRegs) {
-#pragma unroll
-        for (int e = 0; e < VE / 2; ++e) r[i][k * VE / 2 + e] = make_float2(v[2 * e], v[2 * e + 1]);
-      } else {
-        kept.put(i, k, v);
-      }
+      for (int e = 0; e < VE / 2; ++e) r[i][k * VE / 2 + e] = make_float2(v[2 * e], v[2 * e + 1]);
+    } else {
+      kept.put(i, k, v);
     }
   }
 };
@@ -151,6 +149,13 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     }
     ring.commit();
   };
+  // where a walker has few rows
+  if (p.rows <= 8 * stride)
+    for (int s = 0; s < slots && row + s * stride < p.rows; ++s) {
+      const int64_t at = ((row + s * stride) * p.H + cs.c0) * S;
+      prefetch_row<S>(p.x, at, cs, 810, extent);
+      prefetch_row<S>(p.r, at, cs, 810, extent);
+    }
   pdl_trigger();
   pdl_wait();
   for (int s = 0; s < slots; ++s) fetch(s, row + s * stride);
@@ -158,11 +163,16 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
   constexpr bool kRegs = QuantParams<VE, NV, FULL, MODE>::kRegs;
   if constexpr (!kRegs)
     par.kept.base = smem_addr(smem) + p.kept_at + warp * Kept<VE, NV>::template bytes<FULL ? 2 : 1>() + lane * 16;
-  if (kRegs || side == 0) {
+  if constexpr (kRegs) {
 #pragma unroll
-    for (int k = 0; k < NV; ++k) par.load(p, cs.col(k), k);
+    for (int i = 0; i < par.N; ++i)
+#pragma unroll
+      for (int k = 0; k < NV; ++k) par.load(p, i, cs.col(k), k);
+  } else {
+    // the rows side by side share the work
+    for (int t = side; t < par.N * NV; t += p.w.rows_per_cta) par.load(p, t / NV, cs.col(t % NV), t % NV);
+    __syncthreads();
   }
-  if constexpr (!kRegs) __syncthreads();
   const int format = p.s.format, scaling = p.s.scaling;
   const float inv_top = 1.f / static_cast<float>(q_top(format));
   float given = 0.f;
