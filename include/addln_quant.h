@@ -17,7 +17,7 @@
  *                         (32, 64 or 128; the row's last group may be shorter)
  *     ADDLN_SCALE_POW2    the same groups, each with the least power of two 2^e
  *                         by which no value is cut, one byte e + 127
- *     ADDLN_SCALE_TENSOR  fp32 [1], given, > 0: values beyond are cut
+ *     ADDLN_SCALE_TENSOR  fp32 [1], given, at least 2^-126: values beyond are cut
  * and the scales of groups lie as [rows, groups], or with group_major as
  * [groups, rows].  No scale that is made here is below 2^-126 (rows of zeros).
  * Where the largest |y| is NaN or infinite the scale is NaN (byte 255), and

@@ -34,7 +34,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const void* x, void* y, in
       if (ADDLN_IN(761, at, 16, extent)) v[j][u] = __ldcs(reinterpret_cast<const uint4*>(static_cast<const char*>(x) + at));
     }
   }
-  Philox rng;
+  Philox<false> rng;
   rng.init(d);
 #pragma unroll
   for (int j = 0; j < kBlocks; ++j) {
@@ -42,7 +42,7 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const void* x, void* y, in
     if (b * 8 >= n) break;
     uint4 w = make_uint4(0, 0, 0, 0);
     uint32_t above = d.above;
-    if (d.on) w = rng(b, d.wide);
+    if (d.on) w = rng(b, 0, d.wide);
     const uint32_t t[4] = {w.x, w.y, w.z, w.w};
     if (b < whole) {
 #pragma unroll

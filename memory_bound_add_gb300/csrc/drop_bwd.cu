@@ -35,18 +35,24 @@ __host__ __device__ constexpr int drop_sums(bool full, bool bias) { return 1 + f
 // Threads a CTA and registers a thread: 8 columns of a 16-bit type a thread fit 96
 // registers, so that more rows are on an SM at once (us, 4096x768 fp16 layer with all
 // gradients: 16 columns and 128 registers 15.2, 8 and 128 14.1, 8 and 96 13.3, 8 and
-// 80 14.6); shifted rows need more.
-__host__ __device__ constexpr bool bwd_lean(int dt, int nv, int mode) { return dt != kF32 && nv == 1 && mode != kShifted; }
-__host__ __device__ constexpr int bwd_threads(int dt, int nv, int mode) { return bwd_lean(dt, nv, mode) ? 640 : kMaxThreads; }
-template <int DT, int NV, int MODE>
+// 80 14.6); shifted rows, and three sums of edged ones, need more.
+// (sums: column sums)
+__host__ __device__ constexpr bool bwd_lean(int dt, int nv, int sums, int mode) {
+  return dt != kF32 && nv == 1 && (mode == kAligned || (mode == kEdged && sums < 3));
+}
+__host__ __device__ constexpr int bwd_threads(int dt, int nv, int sums, int mode) {
+  return bwd_lean(dt, nv, sums, mode) ? 640 : kMaxThreads;
+}
+template <int DT, int NV, int A, int MODE>
 constexpr int bwd_regs() {
-  return bwd_lean(DT, NV, MODE) ? 96 : 128;
+  return bwd_lean(DT, NV, A, MODE) ? 96 : 128;
 }
 
 // FULL: a layer norm, or dbeta is wanted.  BIAS: dbias is wanted.  MODE: how
 // rows lie.
 template <int DT, int NV, bool FULL, bool BIAS, int MODE>
-__global__ void __launch_bounds__(bwd_threads(DT, NV, MODE)) __maxnreg__((bwd_regs<DT, NV, MODE>()))
+__global__ void __launch_bounds__(bwd_threads(DT, NV, drop_sums(FULL, BIAS), MODE))
+    __maxnreg__((bwd_regs<DT, NV, drop_sums(FULL, BIAS), MODE>()))
     k_drop_bwd(const __grid_constant__ DropBwdArgs p) {
   using IO = Io<DT>;
   constexpr bool SH = MODE == kShifted;
@@ -113,7 +119,7 @@ __global__ void __launch_bounds__(bwd_threads(DT, NV, MODE)) __maxnreg__((bwd_re
     if (!has_dh) ring.template clear<2>(s);
   }
   for (int s = 0; s < slots; ++s) fetch(s, row + s * stride);
-  Philox rng;
+  Philox<(A < 3 && !bwd_lean(DT, NV, A, MODE))> rng;
   rng.init(p.drop);
 #pragma unroll
   for (int k = 0; k < NV; ++k) {
@@ -288,7 +294,7 @@ struct Choice {
 // need to join their sums), gamma, the row sums.
 template <int DT, int NV, bool FULL, bool BIAS, int MODE>
 Choice make(int H, int64_t rows, int sms) {
-  constexpr int VE = Io<DT>::kVec, kMost = bwd_threads(DT, NV, MODE);
+  constexpr int VE = Io<DT>::kVec, kMost = bwd_threads(DT, NV, drop_sums(FULL, BIAS), MODE);
   Choice c;
   c.k = &k_drop_bwd<DT, NV, FULL, BIAS, MODE>;
   if (MODE == kEdged) H += VE - 1;
@@ -310,10 +316,11 @@ Choice make(int H, int64_t rows, int sms) {
   return c;
 }
 
-// The rows that walkers of 8 columns of a 16-bit type a thread have eight each of.
-inline int64_t few_rows(int H, int sms) {
+// The rows that walkers of 8 columns of a 16-bit type a thread have eight each of, in
+// CTAs of up to `most` threads.
+inline int64_t few_rows(int H, int sms, int most) {
   const int t = (H + 255) / 256 * 32;
-  return t > 640 ? 0 : 8 * static_cast<int64_t>(sms) * (640 / t);
+  return t > most ? 0 : 8 * static_cast<int64_t>(sms) * (most / t);
 }
 
 // 16 columns of a 16-bit type a thread (8 of fp32) where a row is longer than a
@@ -324,7 +331,7 @@ inline int64_t few_rows(int H, int sms) {
 template <int DT, bool FULL, bool BIAS, int MODE>
 Choice choose(int H, int64_t rows, int sms) {
   if constexpr (!(FULL && BIAS && MODE == kShifted && DT != kF32)) {
-    if (H > 32 * Io<DT>::kVec && (DT == kF32 || rows > few_rows(H, sms)))
+    if (H > 32 * Io<DT>::kVec && (DT == kF32 || rows > few_rows(H, sms, bwd_threads(DT, 1, drop_sums(FULL, BIAS), MODE))))
       return make<DT, 2, FULL, BIAS, MODE>(H, rows, sms);
   }
   return make<DT, 1, FULL, BIAS, MODE>(H, rows, sms);
@@ -376,7 +383,8 @@ BwdKernel pick_sums(int quads) {
 int64_t drop_bwd_workspace_bytes(int dtype, int mode, bool full, bool bias, int64_t rows, int H, const DeviceInfo& dev) {
   using namespace blk;
   int64_t units = dev.sms;
-  for (const int64_t r : {few_rows(H, dev.sms), INT64_MAX / 2}) {
+  for (const int64_t r : {few_rows(H, dev.sms, 640), few_rows(H, dev.sms, kMaxThreads), INT64_MAX / 2}) {
+    if (r == 0) continue;  // wider than a CTA
     const int fit = fit_of(choose(dtype, H, mode, full, bias, r, dev.sms), dev);
     if (fit < 0) return fit;
     if (fit > units) units = fit;

@@ -92,7 +92,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
   pdl_trigger();
   pdl_wait();
   for (int s = 0; s < slots; ++s) fetch(s, row + s * stride);
-  Philox rng;
+  Philox<true> rng;
   rng.init(p.drop);
   DropParams<VE, NV, FULL, MODE> par;
   constexpr bool kRegs = DropParams<VE, NV, FULL, MODE>::kRegs;

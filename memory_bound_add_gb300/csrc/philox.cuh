@@ -21,13 +21,20 @@ namespace blk {
 // (the upper half of the block's number) and of the key is the same for all
 // blocks that share that word: two of the 20 products, and the xors beside them,
 // are made once, which leaves 18 products a block.  The keys are the same for the
-// whole grid: a warp reduction says so to the compiler, which then keeps the ten
-// rounds' keys in uniform registers instead of adding them up for every block.
-// Both together: 32768x8192 bf16 dropout 187 us to 159, the boundary forward 347 to
-// 320.
+// whole grid: a warp reduction says so to the compiler, which then keeps them in
+// uniform registers.  Both together: 32768x8192 bf16 dropout 187 us to 159, the
+// boundary forward 347 to 320.
+//
+// KEYS: the other rounds' keys are reduced too, or the compiler adds them up anew for
+// every block (85 instructions a block with all, so 69): worth 16 reductions where a
+// thread makes many blocks and registers are left (boundary forward 8192x4096 bf16
+// 43.8 us to 42.9, backward 32768x8192 427 to 418; dropout with its four blocks a
+// thread 159 to 170).
+template <bool KEYS>
 struct Philox {
   uint32_t k0, k1, o0, o1;      // key, upper half of the counter
   uint32_t hi, a0, a2, b0, b3;  // second word, and what it gives
+  uint32_t ka[KEYS ? 8 : 1], kb[KEYS ? 8 : 1];
 
   __device__ __forceinline__ static void mul(uint32_t a, uint32_t m, uint32_t& h, uint32_t& l) {
     const uint64_t p = static_cast<uint64_t>(a) * m;
@@ -56,12 +63,19 @@ struct Philox {
     k0 = same(seed), k1 = same(seed >> 32);
     o0 = same(offset), o1 = same(offset >> 32);
     head(0);
+    if constexpr (KEYS) {
+#pragma unroll
+      for (uint32_t r = 2; r < 10; ++r) ka[r - 2] = same(k0 + r * kW0), kb[r - 2] = same(k1 + r * kW1);
+    }
   }
-  // the four words of block `at`; wide: its number may have an upper half
-  __device__ __forceinline__ uint4 operator()(uint64_t at, bool wide) {
-    if (wide && static_cast<uint32_t>(at >> 32) != hi) head(static_cast<uint32_t>(at >> 32));
+  // the four words of block `at` + `more`; wide: its number may have an upper half
+  __device__ __forceinline__ uint4 operator()(uint64_t at, uint32_t more, bool wide) {
+    if (wide) {
+      const uint32_t second = static_cast<uint32_t>((at + more) >> 32);
+      if (second != hi) head(second);
+    }
     uint32_t h, l, c0, c1, c2, c3;
-    mul(static_cast<uint32_t>(at), kM0, h, l);
+    mul(static_cast<uint32_t>(at) + more, kM0, h, l);
     c2 = h ^ a2;
     mul(c2, kM1, h, c1);
     c0 = h ^ a0, c2 = l ^ b0, c3 = b3;
@@ -70,8 +84,8 @@ struct Philox {
       uint32_t h0, l0, h1, l1;
       mul(c0, kM0, h0, l0);
       mul(c2, kM1, h1, l1);
-      c0 = h1 ^ c1 ^ (k0 + r * kW0);
-      c2 = h0 ^ c3 ^ (k1 + r * kW1);
+      c0 = h1 ^ c1 ^ (KEYS ? ka[KEYS ? r - 2 : 0] : k0 + r * kW0);
+      c2 = h0 ^ c3 ^ (KEYS ? kb[KEYS ? r - 2 : 0] : k1 + r * kW1);
       c1 = l1, c3 = l0;
     }
     return make_uint4(c0, c1, c2, c3);
@@ -107,14 +121,15 @@ struct Mask {
   uint32_t bits;  // SH: of group k from bit 8 k on
 
   // at: index in the tensor of this thread's first column of group 0
-  __device__ __forceinline__ void row(Philox& rng, uint64_t at, uint32_t above, bool wide) {
+  template <typename P>
+  __device__ __forceinline__ void row(P& rng, uint64_t at, uint32_t above, bool wide) {
     if constexpr (SH) {
       constexpr unsigned kAll = 0xffffffffu;
       const int lane = threadIdx.x & 31;
       uint32_t own = 0;
 #pragma unroll
-      for (int k = 0; k < NV; ++k) own |= keep_bits(rng((at + k * 32 * VE) >> 3, wide), above) << (8 * k);
-      const uint32_t end = keep_bits(rng((at + ((NV - 1) * 32 + 1) * VE) >> 3, wide), above);
+      for (int k = 0; k < NV; ++k) own |= keep_bits(rng(at >> 3, k * 4 * VE, wide), above) << (8 * k);
+      const uint32_t end = keep_bits(rng((at + VE) >> 3, (NV - 1) * 4 * VE, wide), above);
       uint32_t next = __shfl_sync(kAll, own, (lane + 1) & 31);
       if (lane == 31) next = (NV > 1 ? next >> 8 : 0u) | end << (8 * (NV - 1));
       const int s = static_cast<int>(at & 7);
@@ -127,7 +142,8 @@ struct Mask {
     }
   }
   // v[i] of group k: kept ones times `scale`, dropped ones 0
-  __device__ __forceinline__ void apply(Philox& rng, uint64_t at, int k, uint32_t above, bool wide, float2 scale,
+  template <typename P>
+  __device__ __forceinline__ void apply(P& rng, uint64_t at, int k, uint32_t above, bool wide, float2 scale,
                                         float2 (&v)[VE / 2]) const {
     if constexpr (SH) {
 #pragma unroll
@@ -137,7 +153,7 @@ struct Mask {
         v[i].y = (bits >> (8 * k + 2 * i)) & 2u ? u.y : 0.f;
       }
     } else {
-      const uint4 w = rng((at + k * 32 * VE) >> 3, wide);
+      const uint4 w = rng(at >> 3, k * 4 * VE, wide);
       uint32_t t[4] = {w.x, w.y, w.z, w.w};
       if constexpr (VE == 4) {
         const bool up = ((at >> 2) & 1) != 0;

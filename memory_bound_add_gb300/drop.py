@@ -123,7 +123,8 @@ def dropout_fwd(x, y, p, rng, *, stream=None):
 
 
 def dropout(x, p, rng, *, stream=None):
-    """Dropout of x; its backward is the same call on the gradient."""
+    """Dropout of x; its backward is the same call on the gradient (no graph is
+    made here: dropout_train makes one)."""
     if _fast is not None and stream is None:
         y = _fast.dropout(x, p, rng)
         if y is not None:
@@ -167,7 +168,8 @@ def dropout_add_norm_fwd(f, x, h, y=None, stats=None, *, p, rng, bias=None, norm
 
 def dropout_add_norm(f, x=None, *, p, rng, bias=None, norm="layer", gamma=None, beta=None, eps: float = 1e-5,
                      want_stats: bool = False, stream=None):
-    """Allocate the outputs with PyTorch and run dropout_add_norm_fwd.
+    """Allocate the outputs with PyTorch and run dropout_add_norm_fwd (no graph
+    is made here: dropout_add_norm_train makes one).
 
     Returns (h, y or None, stats or None), stats = (mean, rstd), each [rows]
     fp32 or None where the norm has none.

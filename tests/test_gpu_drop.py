@@ -157,6 +157,22 @@ def test_dropout_past_32_bits():
         assert torch.equal(x[start:start + m].cpu() != 0, keep(m, 0.5, (3, 4), start))
 
 
+@pytest.mark.slow
+def test_blocks_past_32_bits():
+    # more than 2^32 blocks of 8 elements, alone and at the boundary
+    rows, H = (1 << 20) + 8, 32768
+    n = rows * H
+    if torch.cuda.mem_get_info()[0] < 3 * n:
+        pytest.skip("not enough device memory")
+    x = torch.empty(rows, H, dtype=BF16, device="cuda")
+    for f in (lambda: mba.dropout_fwd(x, x, 0.5, (3, 4)),
+              lambda: mba.dropout_add_norm_fwd(x, None, x, p=0.5, rng=(3, 4), norm=None)):
+        x.fill_(1)
+        f()
+        for start in (0, (1 << 35) - 40, (1 << 35) + 3 * H, n - 100):
+            assert torch.equal(x.view(-1)[start:start + 100].cpu() != 0, keep(100, 0.5, (3, 4), start))
+
+
 # ------------------------------------------------------------- the boundary
 WIDTHS = [1, 2, 7, 8, 12, 31, 33, 64, 100, 250, 256, 264, 516, 768, 1000, 1001, 2050, 4096, 4097, 4104, 8192]
 KINDS = [("layer", True, True), ("rms", False, False), (None, True, False), ("rms", True, True), ("layer", False, False),
