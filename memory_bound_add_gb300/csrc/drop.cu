@@ -1,4 +1,8 @@
-// y = dropout(x), element by element.  Bound by memory: 2 S bytes an element.
+// y = dropout(x), element by element: 2 S bytes and an eighth of a block of random
+// bits an element.  Bound by memory where the tensor is large: 32768x8192 bf16 158 us
+// (6.8 TB/s, 1.02 of a copy), 8192x4096 fp32 41 us (0.98); 4096x768 fp16 3.3 us, a
+// launch and 13 MB.  17.5 instructions an element of bf16 leave a quarter of the issue
+// slots empty.
 #include "philox.cuh"
 
 namespace addln {

@@ -43,8 +43,16 @@ struct DropParams {
   }
 };
 
-// FULL: a layer norm, or a bias or a beta.  MODE: how rows
-// lie.
+// FULL: a layer norm, or a bias or a beta.  MODE: how rows lie.
+//
+// The call moves 4 rows H elements (3 without a norm) and is bound by memory where
+// rows are many: 32768x8192 bf16 rms 316 us (6.8 TB/s, 1.02 of a copy), 8192x4096 42.9
+// (0.94), 65536x768 layer 67.9 (0.89), odd widths too: 8192x5001 56.7 (0.86).  The
+// tile (up to 32 columns a thread, 128 registers, two rows ahead) is block_fwd.cu's.
+// A mask costs 8.6 instructions an element of 23: half of the issue slots are used, so
+// that layer norms and few rows a walker are bound by instructions and a row's
+// latency: 8192x4096 layer with bias 53.9 us (0.75), 4097x1001 rms 9.3 (0.53),
+// 4096x768 fp16 layer 7.9 (0.48).
 template <int DT, int NV, bool FULL, int MODE>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     k_drop_fwd(const __grid_constant__ DropFwdArgs p) {

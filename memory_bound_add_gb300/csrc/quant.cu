@@ -112,6 +112,14 @@ struct QuantParams {
 };
 
 // FULL: a layer norm or a beta.  MODE: how rows lie.
+//
+// The call moves 3 S + 1 bytes an element.  32768x8192 bf16 rms to e4m3, groups of 128:
+// 293 us (6.45 TB/s, 0.96 of a copy); 8192x4096 a scale a row 38.3 (0.91), 65536x768
+// powers of two 54.9 (0.96); 2048x4096 fp16 10.7 (0.82: 3.4 rows a walker).  19 to 21
+// instructions an element use half of the issue slots; 96 registers (five CTAs an SM)
+// and half the columns a thread measured the same or slower.  Layer norms are bound by
+// instructions: 8192x4096 to int8 52 us (0.67), 4097x1001 11.1 (0.39).  Groups of odd
+// widths take shifted rows: 8192x5001 90 us (0.48).
 template <int DT, int NV, bool FULL, int MODE>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     k_norm_quant(const __grid_constant__ QuantArgs p) {

@@ -281,7 +281,7 @@ def dropout_add_norm_backward(dy, dh, h, stats, *, p, rng, bias=None, norm="laye
         mean, rstd = stats or _NONE
         g = _fast.dropout_add_norm_backward(dy, dh, h, mean, rstd, p, rng, bias, _NORMS.get(norm), gamma, beta)
         if g is not None:
-            return DropoutAddNormGrads(*g) if norm is not None else DropoutAddNormGrads(g[0], dh, *g[2:])
+            return tuple.__new__(DropoutAddNormGrads, g if norm is not None else (g[0], dh, *g[2:]))
     some, rows, H = _given(dy, dh)
     dev = some.get_device()
     for t, name in ((bias, "bias"), (beta, "beta")):

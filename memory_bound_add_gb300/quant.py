@@ -205,7 +205,7 @@ def norm_quant(x, residual=None, *, norm="rms", gamma=None, beta=None, eps: floa
     if _fast is not None and stream is None and scale is None and not spec[5]:
         out = _fast.norm_quant(x, residual, gamma, beta, eps, spec[0], spec[1], spec[3], spec[4], want_stats)
         if out is not None:
-            return NormQuant(*out)
+            return tuple.__new__(NormQuant, out)
     rows, H = _rows_tensor(x, "x")
     if spec[3] == SCALE_TENSOR:
         if not isinstance(scale, torch.Tensor):
