@@ -378,8 +378,10 @@ struct Kept {
 // unit are the same modulo 8.
 template <int MODE>
 __device__ __forceinline__ int64_t first_row(int64_t unit, int sides, int side) {
-  if constexpr (MODE != kEdged) return unit * sides + side;
-  return (unit & 7) + 8 * ((unit >> 3) * sides + side);
+  if constexpr (MODE != kEdged)
+    return unit * sides + side;
+  else
+    return (unit & 7) + 8 * ((unit >> 3) * sides + side);
 }
 
 // A CTA of a cluster may write into a peer's shared memory only once the peer
@@ -548,17 +550,17 @@ __device__ __forceinline__ void store_cols(float* t, const Cols<VE, NV>& cs, int
       if (e % VE < cs.valid(k) && (k > 0 || e >= cs.low) && ADDLN_IN(site, 4 * c, 4, 4 * static_cast<int64_t>(Hp)))
         t[c] = (e & 1) ? v[e >> 1].y : v[e >> 1].x;
     }
-    return;
+  } else {
+#pragma unroll
+    for (int k = 0; k < NV; ++k)
+#pragma unroll
+      for (int i = 0; i < VE / 4; ++i) {
+        // Hp is a multiple of 4: four columns of which one exists fit
+        if (cs.valid(k) <= 4 * i || !ADDLN_IN(site, 4 * (cs.col(k) + 4 * i), 16, 4 * static_cast<int64_t>(Hp))) continue;
+        const float2 a = v[k * VE / 2 + 2 * i], b = v[k * VE / 2 + 2 * i + 1];
+        *reinterpret_cast<float4*>(t + cs.col(k) + 4 * i) = make_float4(a.x, a.y, b.x, b.y);
+      }
   }
-#pragma unroll
-  for (int k = 0; k < NV; ++k)
-#pragma unroll
-    for (int i = 0; i < VE / 4; ++i) {
-      // Hp is a multiple of 4: four columns of which one exists fit
-      if (cs.valid(k) <= 4 * i || !ADDLN_IN(site, 4 * (cs.col(k) + 4 * i), 16, 4 * static_cast<int64_t>(Hp))) continue;
-      const float2 a = v[k * VE / 2 + 2 * i], b = v[k * VE / 2 + 2 * i + 1];
-      *reinterpret_cast<float4*>(t + cs.col(k) + 4 * i) = make_float4(a.x, a.y, b.x, b.y);
-    }
 }
 
 constexpr int kSumThreads = 256;
@@ -570,11 +572,11 @@ __device__ __forceinline__ float4 add4(float4 a, float4 b) {
 // r[a] = sum over i < n of the quad at src + i * ld + a * la (in floats);
 // every thread of the block takes part, the result is in the threads below
 // QUADS.
-template <int A, int QUADS>
+template <int A, int QUADS, int THREADS = kSumThreads>
 __device__ __forceinline__ void block_quad_sums(const float* src, int64_t n, int64_t ld, int64_t la, bool in,
                                                 int64_t extent, float4 (*wsum)[A][QUADS], float4 (&r)[A]) {
   constexpr int kU = 8 / A;  // partials a thread has in flight
-  constexpr int kStep = kSumThreads / QUADS;
+  constexpr int kStep = THREADS / QUADS;
   const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
 #pragma unroll
   for (int a = 0; a < A; ++a) r[a] = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -612,7 +614,7 @@ __device__ __forceinline__ void block_quad_sums(const float* src, int64_t n, int
     for (int a = 0; a < A; ++a) {
       r[a] = wsum[0][a][t];
 #pragma unroll
-      for (int w = 1; w < kSumThreads / 32; ++w) r[a] = add4(r[a], wsum[w][a][t]);
+      for (int w = 1; w < THREADS / 32; ++w) r[a] = add4(r[a], wsum[w][a][t]);
     }
 }
 

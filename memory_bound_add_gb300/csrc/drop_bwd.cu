@@ -262,17 +262,18 @@ __global__ void __launch_bounds__(bwd_threads(DT, NV, drop_sums(FULL, BIAS), MOD
   if (p.w.C > 1) cooperative_groups::this_cluster().sync();
 }
 
-// The CTAs' column sums of QUADS column quads, added in a fixed order.
-template <bool FULL, bool BIAS, int QUADS>
-__global__ void __launch_bounds__(kSumThreads) k_drop_sums(const __grid_constant__ DropBwdArgs p) {
+// The CTAs' column sums of QUADS column quads, added in a fixed order.  Its time is a
+// launch and its loads' latency.
+template <bool FULL, bool BIAS, int QUADS, int THREADS>
+__global__ void __launch_bounds__(THREADS) k_drop_sums(const __grid_constant__ DropBwdArgs p) {
   constexpr int A = drop_sums(FULL, BIAS);
-  __shared__ float4 wsum[kSumThreads / 32][A][QUADS];
+  __shared__ float4 wsum[THREADS / 32][A][QUADS];
   pdl_trigger();
   pdl_wait();
   const int t = threadIdx.x;
   const int j = (blockIdx.x * QUADS + t % QUADS) * 4;  // the thread's first column
   float4 r[A];
-  block_quad_sums<A, QUADS>(p.part + j, p.parts, static_cast<int64_t>(A) * p.Hp, p.Hp, j < p.H,
+  block_quad_sums<A, QUADS, THREADS>(p.part + j, p.parts, static_cast<int64_t>(A) * p.Hp, p.Hp, j < p.H,
                             (p.parts * A * p.Hp - j) * 4, wsum, r);
   if (t >= QUADS) return;
 #pragma unroll
@@ -371,16 +372,10 @@ int fit_of(const Choice& c, const DeviceInfo& dev) {
 
 int64_t part_bytes(int64_t parts, int sums, int64_t Hp) { return parts * sums * Hp * 4; }
 
-// Quads a block: the most (of 2, 4, 8) whose partials a thread still loads in
-// one round.
-inline int sums_quads(int64_t parts, int sums) {
-  const int64_t one_round = kSumThreads * (8 / sums);
-  return 8 * parts <= one_round ? 8 : 4 * parts <= one_round ? 4 : 2;
-}
-
 template <bool FULL, bool BIAS>
-BwdKernel pick_sums(int quads) {
-  return quads == 8 ? &k_drop_sums<FULL, BIAS, 8> : quads == 4 ? &k_drop_sums<FULL, BIAS, 4> : &k_drop_sums<FULL, BIAS, 2>;
+BwdKernel pick_sums(int quads, int threads) {
+  if (threads == 512) return quads == 8 ? &k_drop_sums<FULL, BIAS, 8, 512> : &k_drop_sums<FULL, BIAS, 4, 512>;
+  return quads == 8 ? &k_drop_sums<FULL, BIAS, 8, 256> : &k_drop_sums<FULL, BIAS, 4, 256>;
 }
 
 }  // namespace
@@ -425,10 +420,16 @@ int launch_drop_bwd(int dtype, int mode, const DropBwdArgs& args, void* ws, int6
   }
   cudaError_t e = launch_units(ch.k, p.parts, ch.sh, ch.smem, c, p);
   if (e == cudaSuccess && cols) {
-    const int quads = sums_quads(p.parts, drop_sums(full, bias));
-    const BwdKernel ks = full ? (bias ? pick_sums<true, true>(quads) : pick_sums<true, false>(quads))
-                              : (bias ? pick_sums<false, true>(quads) : pick_sums<false, false>(quads));
-    e = launch_kernel(ks, dim3(static_cast<unsigned>((p.Hp / 4 + quads - 1) / quads)), dim3(kSumThreads), 0, c.stream, c.pdl, p);
+    // 512 threads where each of 256 would have several partials; four quads a block
+    // unless that makes more than two blocks an SM (us of a call with 256 and two quads,
+    // 512 and four, 512 and eight: 4096x768 fp16 rms 13.2, 12.4, 12.6; 2048x4096 layer
+    // 23.7, 23.0, 23.6; 4096x8192 rms 63.0, 62.1, 60.2; 64x768 fp32, 64 partials, with 256
+    // / 512 and four 4.0 / 4.7).
+    const int threads = p.parts > 128 ? 512 : 256, quads = p.Hp / 16 > 2 * c.dev.sms ? 8 : 4;
+    const BwdKernel ks = full ? (bias ? pick_sums<true, true>(quads, threads) : pick_sums<true, false>(quads, threads))
+                              : (bias ? pick_sums<false, true>(quads, threads) : pick_sums<false, false>(quads, threads));
+    e = launch_kernel(ks, dim3(static_cast<unsigned>((p.Hp / 4 + quads - 1) / quads)), dim3(static_cast<unsigned>(threads)), 0,
+                      c.stream, c.pdl, p);
   }
   if (e != cudaSuccess) {
     note_cuda_error(static_cast<int>(e));
