@@ -24,7 +24,8 @@ __global__ void __launch_bounds__(kThreads) k_dropout(const void* x, void* y, in
   pdl_trigger();
   pdl_wait();
   const float2 scale = dup2(d.scale);
-  const int64_t whole = VEC ? n / 8 : 0, extent = n * S;
+  const int64_t whole = VEC ? n / 8 : 0;
+  [[maybe_unused]] const int64_t extent = n * S;
   uint4 v[kBlocks][U];
 #pragma unroll
   for (int j = 0; j < kBlocks; ++j) {

@@ -55,10 +55,10 @@ constexpr int bwd_regs() {
 // registers that a second row a thread would need; an SM has one or two rows at a
 // time.  With rms norms and many rows it is bound by memory: 32768x8192 bf16 419 us
 // (6.4 TB/s, 0.96 of a copy), 8192x4096 58.0 (0.87), fp32 103 (0.98); layer norms with
-// all gradients by instructions: 65.7 us (0.76), 65536x768 107 (0.56); rows of more
+// all gradients by instructions: 65.1 us (0.77), 65536x768 107 (0.56); rows of more
 // than 4096 columns leave 10 to 16 warps an SM: 8192x5001 105 us (0.58; 8 columns a
-// thread, 20 warps, 110).  Few rows pay for the sums: 4096x768 fp16 layer 14.7 us, of
-// which joining them in a CTA and the second kernel take 4.9.
+// thread, 20 warps, 110).  Few rows pay for the sums: 4096x768 fp16 layer 14.2 us, of
+// which joining them in a CTA and the second kernel take 4.3.
 template <int DT, int NV, bool FULL, bool BIAS, int MODE>
 __global__ void __launch_bounds__(bwd_threads(DT, NV, drop_sums(FULL, BIAS), MODE))
     __maxnreg__((bwd_regs<DT, NV, drop_sums(FULL, BIAS), MODE>()))

@@ -51,7 +51,7 @@ struct DropParams {
 // tile (up to 32 columns a thread, 128 registers, two rows ahead) is block_fwd.cu's.
 // A mask costs 8.6 instructions an element of 23: half of the issue slots are used, so
 // that layer norms and few rows a walker are bound by instructions and a row's
-// latency: 8192x4096 layer with bias 53.9 us (0.75), 4097x1001 rms 9.3 (0.53),
+// latency: 8192x4096 layer with bias 53.9 us (0.75), 4097x1001 rms 9.1 (0.54),
 // 4096x768 fp16 layer 7.9 (0.48).
 template <int DT, int NV, bool FULL, int MODE>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
 #pragma unroll
       for (int i = 0; i < Q; ++i) v[k * Q + i] = z[i];
     }
-    cs.clear(v);
+    // columns before the row have the end of another; those past it are zeros
+    if constexpr (MODE == kEdged) cs.clear_low(v);
     ring.meet();
     fetch(slot, row + slots * stride);  // the slot has been read
     if (p.h != nullptr) {

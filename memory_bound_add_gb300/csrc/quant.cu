@@ -118,7 +118,7 @@ struct QuantParams {
 // powers of two 54.9 (0.96); 2048x4096 fp16 10.7 (0.82: 3.4 rows a walker).  19 to 21
 // instructions an element use half of the issue slots; 96 registers (five CTAs an SM)
 // and half the columns a thread measured the same or slower.  Layer norms are bound by
-// instructions: 8192x4096 to int8 52 us (0.67), 4097x1001 11.1 (0.39).  Groups of odd
+// instructions: 8192x4096 to int8 49 us (0.72), 4097x1001 10.2 (0.42).  Groups of odd
 // widths take shifted rows: 8192x5001 90 us (0.48).
 template <int DT, int NV, bool FULL, int MODE>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
@@ -203,7 +203,8 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
         for (int i = 0; i < Q; ++i) v[k * Q + i] = add2(v[k * Q + i], r[i]);
       }
     }
-    if constexpr (MODE != kAligned) cs.clear(v);
+    // columns before the row have the end of another; those past it are zeros
+    if constexpr (MODE == kEdged) cs.clear_low(v);
     ring.meet();
     fetch(slot, row + slots * stride);  // the slot has been read
     if (p.h != nullptr) {
@@ -344,12 +345,16 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
         w[k] = to_q<decltype(fmt)::value>(mul2(v[k * Q], i2), mul2(v[k * Q + 1], i2));
         if constexpr (VE == 8)
           w[k] |= static_cast<W>(to_q<decltype(fmt)::value>(mul2(v[k * Q + 2], i2), mul2(v[k * Q + 3], i2))) << 32;
+        // a NaN scale's integers
+        if (decltype(fmt)::value == kQWhole && isnan(inv[k])) w[k] = 0;
       }
     };
     if (format == ADDLN_Q_E4M3)
       round(std::integral_constant<int, ADDLN_Q_E4M3>());
     else if (format == ADDLN_Q_E5M2)
       round(std::integral_constant<int, ADDLN_Q_E5M2>());
+    else if (scaling != ADDLN_SCALE_TENSOR)
+      round(std::integral_constant<int, kQWhole>());
     else
       round(std::integral_constant<int, ADDLN_Q_INT8>());
     ByteWriter<VE, NV, MODE> out;

@@ -27,22 +27,34 @@ __device__ __forceinline__ int q_top(int format) {
 
 // Four values to the four bytes of a word.  The fp8 conversions and the integer
 // one round to nearest, ties to even, and cut; a NaN becomes the format's NaN,
-// as an integer 0.
+// as an integer 0.  kQWhole: integers of values that are at most 127 by their
+// scale; a sum with 1.5 2^23 leaves them rounded in its low byte (2.5 instructions
+// an element less).
+constexpr int kQWhole = 8;
 template <int FMT>
 __device__ __forceinline__ uint32_t to_q(float2 a, float2 b) {
-  uint16_t lo, hi;
-  if constexpr (FMT == ADDLN_Q_E4M3) {
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
-    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
-  } else if constexpr (FMT == ADDLN_Q_E5M2) {
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
-    asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
+  // the low bytes of four words
+  auto bytes = [](uint32_t p, uint32_t q, uint32_t r, uint32_t s) {
+    return __byte_perm(__byte_perm(p, q, 0x0040), __byte_perm(r, s, 0x0040), 0x5410);
+  };
+  if constexpr (FMT == ADDLN_Q_E4M3 || FMT == ADDLN_Q_E5M2) {
+    uint16_t lo, hi;
+    if constexpr (FMT == ADDLN_Q_E4M3) {
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
+      asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
+    } else {
+      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(lo) : "f"(a.y), "f"(a.x));
+      asm("cvt.rn.satfinite.e5m2x2.f32 %0, %1, %2;" : "=h"(hi) : "f"(b.y), "f"(b.x));
+    }
+    return lo | static_cast<uint32_t>(hi) << 16;
+  } else if constexpr (FMT == kQWhole) {
+    const float2 big = dup2(12582912.f);
+    a = add2(a, big), b = add2(b, big);
+    return bytes(__float_as_uint(a.x), __float_as_uint(a.y), __float_as_uint(b.x), __float_as_uint(b.y));
   } else {
     auto whole = [](float v) { return static_cast<uint32_t>(min(max(__float2int_rn(v), -127), 127)); };
-    // the low bytes of four words
-    return __byte_perm(__byte_perm(whole(a.x), whole(a.y), 0x0040), __byte_perm(whole(b.x), whole(b.y), 0x0040), 0x5410);
+    return bytes(whole(a.x), whole(a.y), whole(b.x), whole(b.y));
   }
-  return lo | static_cast<uint32_t>(hi) << 16;
 }
 
 // Four bytes of a word to what they are without their scale.  Integers: a byte
