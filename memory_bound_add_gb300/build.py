@@ -4,7 +4,7 @@ Compiles every ``csrc/*.cu`` translation unit in parallel with nvcc
 (``-gencode arch=compute_103a,code=sm_103a``, no fast-math) and links them
 into ``_build/libaddln.so`` with the CUDA runtime linked statically, so the
 library needs nothing from PyTorch at load time.  Rebuilds only when a
-source or header is newer than the library.  Beside it ``_build/addln_fast.so``,
+source or header is newer than the library.  Beside it ``_build/addln_fast-*.so``,
 a Python extension (g++, against the installed PyTorch) that makes the commonest
 calls of some operators without their Python; where it is missing, those calls
 take the Python path.
@@ -30,7 +30,6 @@ CHECKED_DIR = os.path.join(OUT_DIR, "checked")
 CHECKED_LIB = os.path.join(CHECKED_DIR, "libaddln_checked.so")
 
 FAST_SRC = os.path.join(CSRC, "fast.cpp")
-FAST_LIB = os.path.join(OUT_DIR, "addln_fast.so")
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE]
@@ -59,6 +58,12 @@ def up_to_date(lib: str = LIB) -> bool:
     return all(os.path.getmtime(f) <= t for f in _inputs())
 
 
+def fast_lib() -> str:
+    """The extension's path; its name has the PyTorch that it is built against."""
+    import torch
+    return os.path.join(OUT_DIR, f"addln_fast-{torch.__version__}.so")
+
+
 def build_fast(force: bool = False) -> str | None:
     """Build the Python extension if needed and return its path, or None, with
     a warning, where it does not compile."""
@@ -67,14 +72,15 @@ def build_fast(force: bool = False) -> str | None:
 
     import torch
     newest = max(map(os.path.getmtime, [FAST_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))]))
-    if not force and os.path.exists(FAST_LIB) and os.path.getmtime(FAST_LIB) >= newest:
-        return FAST_LIB
+    lib = fast_lib()
+    if not force and os.path.exists(lib) and os.path.getmtime(lib) >= newest:
+        return lib
     os.makedirs(OUT_DIR, exist_ok=True)
     base = os.path.dirname(torch.__file__)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
     include = [os.path.join(base, "include"), os.path.join(base, "include", "torch", "csrc", "api", "include"),
                os.path.join(cuda, "include"), sysconfig.get_paths()["include"]]
-    tmp = FAST_LIB + f".tmp{os.getpid()}"
+    tmp = lib + f".tmp{os.getpid()}"
     cmd = ["g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-fvisibility=hidden",
            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", *(f"-I{i}" for i in include), FAST_SRC,
            "-o", tmp, "-L" + os.path.join(base, "lib"), "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_cuda",
@@ -85,10 +91,10 @@ def build_fast(force: bool = False) -> str | None:
     except OSError as e:
         failed = str(e)
     if failed:
-        warnings.warn(f"addln_fast.so was not built; calls take the Python path:\n{failed}")
+        warnings.warn(f"the extension was not built; calls take the Python path:\n{failed}")
         return None
-    os.replace(tmp, FAST_LIB)
-    return FAST_LIB
+    os.replace(tmp, lib)
+    return lib
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list | None = None,

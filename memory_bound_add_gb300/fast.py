@@ -9,11 +9,10 @@ from __future__ import annotations
 
 import ctypes
 import importlib.util
-import os
 
 from . import binding
+from .build import fast_lib
 
-PATH = os.path.join(os.path.dirname(binding.LIB_PATH), "addln_fast.so")
 _ENTRIES = ("dropout_fwd", "dropout_add_norm_fwd", "dropout_add_norm_bwd", "dropout_add_norm_bwd_workspace_size",
             "norm_quant_fwd", "dequant_rows")
 _module = False  # not looked for yet
@@ -25,7 +24,7 @@ def module():
     if _module is False:
         handle = binding.lib()
         try:
-            spec = importlib.util.spec_from_file_location("addln_fast", PATH)
+            spec = importlib.util.spec_from_file_location("addln_fast", fast_lib())
             found = importlib.util.module_from_spec(spec)
             spec.loader.exec_module(found)
             found.init(*(ctypes.cast(getattr(handle, n), ctypes.c_void_p).value for n in _ENTRIES))
