@@ -76,6 +76,10 @@ __device__ __forceinline__ Scale pow2_of(float largest, int format) {
   return {__uint_as_float(static_cast<uint32_t>(e) << 23), __uint_as_float(static_cast<uint32_t>(254 - e) << 23)};
 }
 
+// Without FULL gamma is kept times this, which goes back with 1 / rms: values next to
+// the type's lowest, whose 1 / rms is 0, then stay finite (and so become 0).
+constexpr float kGammaScale = 0x1p-16f;
+
 // gamma and, with FULL, beta: in registers or in shared memory, as in
 // block_fwd.cu.
 __host__ __device__ constexpr bool quant_in_registers(int columns, bool full, int mode) {
@@ -102,6 +106,10 @@ struct QuantParams {
     const float* from = i == 0 ? p.gamma : p.beta;
     float v[VE];
     load_params<VE, MODE>(from, c, p.H, 0.f, v, 800);
+    if constexpr (!FULL) {
+#pragma unroll
+      for (int e = 0; e < VE; ++e) v[e] *= kGammaScale;
+    }
     if constexpr (kRegs) {
 #pragma unroll
       for (int e = 0; e < VE / 2; ++e) r[i][k * VE / 2 + e] = make_float2(v[2 * e], v[2 * e + 1]);
@@ -248,7 +256,8 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
         } else {
           sum = walker_sum(ex, sum);
         }
-        st.M2 = f = row_rstd(sum, p.inv_h, p.eps);
+        st.M2 = row_rstd(sum, p.inv_h, p.eps);
+        f = st.M2 * (1.f / kGammaScale);
       }
       if (leader && ADDLN_IN(806, 4 * row, 4, 4 * p.rows)) {
         if (p.rstd) p.rstd[row] = st.M2;

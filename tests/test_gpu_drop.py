@@ -240,6 +240,23 @@ def test_dropped_values_do_not_reach_the_row(dtype):
 
 
 @DTYPES
+def test_lowest_values(dtype):
+    # a mask's lowest values in the stream: where the sum of squares passes fp32,
+    # 1 / rms is 0 and so is the row
+    low = torch.finfo(dtype).min
+    x = randn((3, 264), dtype, 1)
+    x[1, 40:200] = low
+    f, w = torch.zeros(3, 264, dtype=dtype), torch.ones(264)
+    h, y, st = mba.dropout_add_norm(f.cuda(), x.cuda(), p=0.5, rng=(1, 2), norm="rms", gamma=w.cuda(), want_stats=True)
+    assert torch.equal(h.cpu(), x)
+    if dtype is F16:
+        wh, wy, _, eh, ey = drop_forward(f, x, None, 0.5, (1, 2), "rms", w, None, 1e-5)
+        assert_within(y, wy, ey, "y")
+    else:
+        assert st[1][1] == 0 and not y[1].any() and y[0].any()
+
+
+@DTYPES
 @pytest.mark.parametrize("H", [5, 520, 768, 4099])
 def test_off_the_borders_and_given_outputs(dtype, H):
     v = make((6, H), dtype, "layer", True, True, seed=H)

@@ -238,6 +238,34 @@ def test_infinities_and_nan(dtype, fmt):
     assert q[1, 40] == 0 if fmt == "int8" else q[1, 40].isnan()
 
 
+@DTYPES
+@FORMATS
+@pytest.mark.parametrize("scaling,group", [("row", None), ("group", 32), ("pow2", 64)])
+def test_lowest_values(dtype, fmt, scaling, group):
+    # a mask's lowest values: where the sum of squares passes fp32, 1 / rms is 0 and
+    # so is the row; fp16's lowest is an ordinary number
+    low = torch.finfo(dtype).min
+    x = randn((3, 264), dtype, 1)
+    x[1, 40:200], x[2, 7] = low, -low
+    gamma = randn((264,), seed=2, sc=0.1, loc=1.5)
+    v = {"x": x, "residual": None, "gamma": gamma, "beta": None}
+    r = mba.norm_quant(x.cuda(), gamma=gamma.cuda(), format=fmt, scaling=scaling, group=group, want_stats=True)
+    if dtype is F16:
+        check_fwd(v, "rms", fmt, scaling, group)
+    else:
+        assert not r.q[1:].cpu().float().any() and (r.scale[1:].cpu().float() == LEAST).all()
+        assert r.rstd[1:].tolist() == [0.0, 0.0] and r.q[0].cpu().float().any()
+
+
+@DTYPES
+def test_wide_gammas(dtype):
+    x = randn((5, 264), dtype, 1)
+    for g in (1e-6, 1e-3, 1e3, 1e6):
+        v = {"x": x, "residual": None, "gamma": randn((264,), seed=2, sc=g), "beta": None}
+        for scaling, group in (("row", None), ("group", 32), ("pow2", 32)):
+            check_fwd(v, "rms", "e4m3", scaling, group, read=False)
+
+
 @FORMATS
 def test_powers_of_two_at_their_borders(fmt):
     # a row's largest value at the format's largest times a power of two, and
