@@ -466,8 +466,8 @@ template <int VE, int NV, bool SIDES>
 __device__ __forceinline__ RowStat walker_stats(Exchange<SIDES>& ex, float2 (&v)[NV * VE / 2], const Cols<VE, NV>& cs) {
   constexpr int P = NV * VE / 2;
   constexpr unsigned kAll = 0xffffffffu;
+  // the slots of columns that do not exist hold zeros
   float2 s[2] = {dup2(0.f), dup2(0.f)}, q[2] = {dup2(0.f), dup2(0.f)};
-  cs.clear(v);
 #pragma unroll
   for (int j = 0; j < P; ++j) s[j & 1] = add2(s[j & 1], v[j]);
   s[0] = add2(s[0], s[1]);
