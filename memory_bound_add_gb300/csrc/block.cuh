@@ -37,7 +37,8 @@ constexpr int kMaxSmem = 227 * 1024;  // dynamic shared memory of a CTA
 
 // VE fp32 parameters from column c on, of H; `fill` for a missing vector and
 // before the first or past the end.  Shifted or edged: any address, and an end may
-// lie within the group.
+// lie within the group.  H may be the end of a CTA's slice (Cols::end) where what
+// stands in slots past it has to stay zero.
 template <int VE, int MODE>
 __device__ __forceinline__ void load_params(const float* p, int c, int H, float fill, float (&v)[VE], int site) {
 #pragma unroll
@@ -101,6 +102,9 @@ struct Cols {
     }
   }
   __device__ __forceinline__ int col(int k) const { return c0 + k * kStep; }
+  // The column behind the slice's last.  A CTA has whole warps, so slots may lie past
+  // it whose columns the cluster's next CTA has.
+  __device__ __forceinline__ int end() const { return c0 + left; }
   __device__ __forceinline__ bool ok(int k) const { return left > k * kStep; }
   // columns of group k that exist
   __device__ __forceinline__ int valid(int k) const { return min(max(left - k * kStep, 0), VE); }
