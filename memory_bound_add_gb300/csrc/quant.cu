@@ -101,11 +101,12 @@ struct QuantParams {
       kept.get(i, k, v);
     }
   }
-  // vector i, group k, at column c
-  __device__ __forceinline__ void load(const QuantArgs& p, int i, int c, int k) {
+  // vector i, group k; zeros past the slice, whose slots would reach the row's
+  // largest value by way of the beta
+  __device__ __forceinline__ void load(const QuantArgs& p, int i, const Cols<VE, NV>& cs, int k) {
     const float* from = i == 0 ? p.gamma : p.beta;
     float v[VE];
-    load_params<VE, MODE>(from, c, p.H, 0.f, v, 800);
+    load_params<VE, MODE>(from, cs.col(k), cs.end(), 0.f, v, 800);
     if constexpr (!FULL) {
 #pragma unroll
       for (int e = 0; e < VE; ++e) v[e] *= kGammaScale;
@@ -183,10 +184,10 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
 #pragma unroll
     for (int i = 0; i < par.N; ++i)
 #pragma unroll
-      for (int k = 0; k < NV; ++k) par.load(p, i, cs.col(k), k);
+      for (int k = 0; k < NV; ++k) par.load(p, i, cs, k);
   } else {
     // the rows side by side share the work
-    for (int t = side; t < par.N * NV; t += p.w.rows_per_cta) par.load(p, t / NV, cs.col(t % NV), t % NV);
+    for (int t = side; t < par.N * NV; t += p.w.rows_per_cta) par.load(p, t / NV, cs, t % NV);
     __syncthreads();
   }
   const int format = p.s.format, scaling = p.s.scaling;
