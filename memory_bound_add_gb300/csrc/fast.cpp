@@ -130,6 +130,12 @@ bool number(PyObject* o, int64_t* v) {
   return false;
 }
 
+// True or False itself: what Python merely takes for one is left to its path.
+bool truth(PyObject* o, bool* v) {
+  *v = o == Py_True;
+  return *v || o == Py_False;
+}
+
 PyObject* none() { Py_RETURN_NONE; }
 PyObject* wrap(const at::Tensor& t) { return t.defined() ? THPVariable_Wrap(t) : none(); }
 void* ptr(const at::Tensor& t) { return t.defined() ? t.mutable_data_ptr() : nullptr; }
@@ -186,11 +192,12 @@ PyObject* dropout_add_norm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float *bias, *gamma, *beta;
     int64_t norm;
     double eps;
+    bool stats;
     if (n != 10 || lib.fwd == nullptr || !f.take_rows(a[0]) || !f.beside(a[1], &x) || !d.take(a[2], a[3], f) ||
         !f.vector(a[4], f.H, &bias) || !number(a[5], &norm) || !f.vector(a[6], f.H, &gamma) || !f.vector(a[7], f.H, &beta) ||
-        !number(a[8], &eps))
+        !number(a[8], &eps) || !truth(a[9], &stats))
       return none();
-    const bool stats = a[9] == Py_True && norm != ADDLN_NORM_NONE;
+    stats = stats && norm != ADDLN_NORM_NONE;
     at::Tensor y, mean, rstd;
     const at::Tensor h = f.same(f.t->scalar_type());
     if (norm != ADDLN_NORM_NONE) y = f.same(f.t->scalar_type());
@@ -255,11 +262,12 @@ PyObject* norm_quant(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const float *gamma, *beta;
     double eps;
     int64_t norm, format, scaling, group;
+    bool stats;
     if (n != 10 || lib.quant == nullptr || !x.take_rows(a[0]) || !x.beside(a[1], &r) || !x.vector(a[2], x.H, &gamma) ||
         !x.vector(a[3], x.H, &beta) || !number(a[4], &eps) || !number(a[5], &norm) || !number(a[6], &format) ||
-        !number(a[7], &scaling) || !number(a[8], &group) || scaling == ADDLN_SCALE_TENSOR)
+        !number(a[7], &scaling) || !number(a[8], &group) || !truth(a[9], &stats) || scaling == ADDLN_SCALE_TENSOR)
       return none();
-    const bool stats = a[9] == Py_True && norm != ADDLN_NORM_NONE;
+    stats = stats && norm != ADDLN_NORM_NONE;
     at::Tensor h, mean, rstd;
     const at::Tensor q = x.same(q_type(format));
     at::DimVector shape(x.t->sizes().begin(), x.t->sizes().end());

@@ -2,6 +2,7 @@
 refusals, and calls that it has to leave to the Python path."""
 from __future__ import annotations
 
+import numpy as np
 import pytest
 import torch
 
@@ -152,3 +153,14 @@ def test_refusals_stay(counted):
         with pytest.raises(error):
             call()
     assert counted.taken == 0
+
+
+@pytest.mark.parametrize("yes,no", [(1, 0), (np.bool_(True), np.bool_(False)), ("yes", "")])
+def test_truth_values_that_are_no_bools(counted, monkeypatch, yes, no):
+    f, w = randn((4, 64), seed=1).cuda(), torch.ones(64, device="cuda")
+    for v in (yes, no):
+        for call in (lambda: mba.dropout_add_norm(f, f, p=0.1, rng=(1, 2), gamma=w, want_stats=v),
+                     lambda: mba.norm_quant(f, norm="layer", gamma=w, want_stats=v)):
+            both(counted, monkeypatch, call, taken=False)
+    assert all(t is not None for t in mba.dropout_add_norm(f, f, p=0.1, rng=(1, 2), gamma=w, want_stats=yes)[2])
+    assert mba.norm_quant(f, norm="layer", gamma=w, want_stats=yes).rstd is not None
