@@ -157,6 +157,9 @@ PyObject* tuple(const T&... t) {
   return nullptr;
 }
 
+// Whether a vector's gradient, which is made with one dimension, has its shape.
+bool one_dimension(PyObject* o) { return o == Py_None || THPVariable_Unpack(o).dim() == 1; }
+
 // Runs a call's body; a C++ exception (no memory, say) becomes None.
 template <typename F>
 PyObject* guarded(F f) {
@@ -222,7 +225,7 @@ PyObject* dropout_add_norm_backward(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (n != 11 || lib.bwd == nullptr || !g.take_rows(a[0] == Py_None ? a[1] : a[0]) || !g.beside(a[0], &dy) ||
         !g.beside(a[1], &dh) || !g.beside(a[2], &h) || !g.vector(a[3], g.rows, &mean) || !g.vector(a[4], g.rows, &rstd) ||
         !d.take(a[5], a[6], g) || !g.vector(a[7], g.H, &bias) || !number(a[8], &norm) || !g.vector(a[9], g.H, &gamma) ||
-        !g.vector(a[10], g.H, &beta))
+        !g.vector(a[10], g.H, &beta) || !one_dimension(a[7]) || !one_dimension(a[9]) || !one_dimension(a[10]))
       return none();
     const at::Tensor df = g.same(g.t->scalar_type());
     at::Tensor dx, dbias, dgamma, dbeta, ws;

@@ -164,3 +164,13 @@ def test_truth_values_that_are_no_bools(counted, monkeypatch, yes, no):
             both(counted, monkeypatch, call, taken=False)
     assert all(t is not None for t in mba.dropout_add_norm(f, f, p=0.1, rng=(1, 2), gamma=w, want_stats=yes)[2])
     assert mba.norm_quant(f, norm="layer", gamma=w, want_stats=yes).rstd is not None
+
+
+def test_gradients_have_their_vectors_shapes(counted, monkeypatch):
+    # a vector of H elements may have other sizes of 1; its gradient is like it
+    f, st = randn((4, 64), seed=1).cuda(), (torch.zeros(4, device="cuda"), torch.ones(4, device="cuda"))
+    for name in ("bias", "gamma", "beta"):
+        kw = dict({k: torch.ones(64, device="cuda") for k in ("bias", "gamma", "beta")}, p=0.1, rng=(1, 2))
+        kw[name] = kw[name].view(1, 64)
+        both(counted, monkeypatch, lambda: mba.dropout_add_norm_backward(f, f, f, st, **kw), taken=False)
+        assert getattr(mba.dropout_add_norm_backward(f, f, f, st, **kw), "d" + name).shape == (1, 64)
