@@ -15,6 +15,7 @@ import glob
 import os
 import shutil
 import subprocess
+import sys
 from concurrent.futures import ThreadPoolExecutor
 
 PKG = os.path.dirname(os.path.abspath(__file__))
@@ -59,9 +60,13 @@ def up_to_date(lib: str = LIB) -> bool:
 
 
 def fast_lib() -> str:
-    """The extension's path; its name has the PyTorch that it is built against."""
+    """The extension's path; its name has the PyTorch and the Python that it is
+    built against."""
+    import sysconfig
+
     import torch
-    return os.path.join(OUT_DIR, f"addln_fast-{torch.__version__}.so")
+    abi = sysconfig.get_config_var("SOABI") or sys.implementation.cache_tag
+    return os.path.join(OUT_DIR, f"addln_fast-{torch.__version__}.{abi}.so")
 
 
 def build_fast(force: bool = False) -> str | None:
@@ -180,5 +185,4 @@ def ptxas_report(extra_flags: list | None = None) -> dict:
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force=True, verbose="-v" in sys.argv))
