@@ -71,11 +71,17 @@ def fast_lib() -> str:
 
 def build_fast(force: bool = False) -> str | None:
     """Build the Python extension if needed and return its path, or None, with
-    a warning, where it does not compile."""
+    a warning, where there is no PyTorch or it does not compile."""
     import sysconfig
     import warnings
 
-    import torch
+    def missing(why):
+        warnings.warn(f"the extension was not built; calls take the Python path:\n{why}")
+
+    try:
+        import torch
+    except ImportError as e:
+        return missing(e)
     newest = max(map(os.path.getmtime, [FAST_SRC, *glob.glob(os.path.join(INCLUDE, "*.h"))]))
     lib = fast_lib()
     if not force and os.path.exists(lib) and os.path.getmtime(lib) >= newest:
@@ -96,8 +102,7 @@ def build_fast(force: bool = False) -> str | None:
     except OSError as e:
         failed = str(e)
     if failed:
-        warnings.warn(f"the extension was not built; calls take the Python path:\n{failed}")
-        return None
+        return missing(failed)
     os.replace(tmp, lib)
     return lib
 
