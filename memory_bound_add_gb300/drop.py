@@ -302,8 +302,13 @@ def dropout_add_norm_backward(dy, dh, h, stats, *, p, rng, bias=None, norm="laye
 # ----------------------------------------------------------------- training
 def _frozen(rng):
     """rng as it is now: the backward has to make this call's mask, however
-    the tensor is advanced meanwhile."""
-    return rng.clone() if isinstance(rng, torch.Tensor) else rng
+    the tensor (or list, or array) is advanced meanwhile."""
+    if isinstance(rng, torch.Tensor):
+        return rng.clone()
+    try:
+        return tuple(map(operator.index, rng))
+    except TypeError:
+        return rng  # refused where it is used
 
 
 class DropoutFunction(torch.autograd.Function):
