@@ -383,8 +383,15 @@ class FusedDropoutAddNorm(torch.nn.Module):
     it only).  Returns (h, y).  Its seed and offset lie in the buffer `rng`,
     seeded from torch's generator; each training step takes the next offset, in
     device memory, so that a captured step draws a new mask at every replay.
-    forward's own rng replaces them (a step that is computed again for its
-    backward has to pass the first one's).  In eval() nothing is dropped."""
+    forward's own rng replaces them.  A step that is computed again during the
+    backward (activation checkpointing) would find the offset moved on, so there
+    forward refuses to draw; pass rng to such steps:
+
+        rng = m.rng.clone()
+        m.rng[1] += 1
+        h, y = checkpoint(m, f, x, rng, use_reentrant=False)
+
+    In eval() nothing is dropped."""
 
     def __init__(self, hidden: int, p: float = 0.1, norm: Optional[str] = "layer", bias: bool = True,
                  input_bias: bool = False, eps: float = 1e-5, device=None):
@@ -404,6 +411,9 @@ class FusedDropoutAddNorm(torch.nn.Module):
     def forward(self, f, x=None, rng=None):
         p = self.p if self.training else 0.0
         advance = rng is None and p > 0.0
+        if advance and torch._C._current_graph_task_id() != -1:
+            raise RuntimeError("FusedDropoutAddNorm computed during a backward (checkpointing?) would draw another mask than "
+                               "the step's first forward: pass rng")
         if rng is None:
             rng = self.rng if p > 0.0 else (0, 0)
         out = dropout_add_norm_train(f, x, p=p, rng=rng, bias=self.input_bias, norm=self.norm, gamma=self.weight,

@@ -2,9 +2,10 @@
 from __future__ import annotations
 
 import numpy as np
+import pytest
 import torch
 
-from memory_bound_add_gb300.drop import _frozen, _rng_args
+from memory_bound_add_gb300.drop import FusedDropoutAddNorm, _frozen, _rng_args
 
 
 def test_a_kept_rng_does_not_follow_what_it_was_made_of():
@@ -17,3 +18,26 @@ def test_a_kept_rng_does_not_follow_what_it_was_made_of():
         assert [int(v) for v in kept] == [3, 4]
     assert _rng_args(_frozen([3, 4]), 0) == (None, 3, 4)
     assert _frozen((3, 4)) == (3, 4) and _frozen(7) == 7
+
+
+def test_no_mask_is_drawn_during_a_backward():
+    m, x = FusedDropoutAddNorm(8, p=0.5), torch.zeros(2, 8)
+    calls = [lambda: m(x, x), lambda: m(x, x, (1, 2)), lambda: m.eval()(x, x)]
+    wants = [RuntimeError, ValueError, ValueError]  # the others are refused for not being on a GPU
+
+    class Again(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, a):
+            return a * 1
+
+        @staticmethod
+        def backward(ctx, g):
+            for call, want in zip(calls, wants):
+                with pytest.raises(want, match="rng" if want is RuntimeError else "CUDA"):
+                    call()
+            return g
+
+    with pytest.raises(ValueError, match="CUDA"):
+        m(x, x)
+    Again.apply(torch.zeros(3, requires_grad=True)).sum().backward()
+    assert m.rng[1] == 0

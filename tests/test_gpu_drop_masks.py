@@ -4,6 +4,7 @@ from __future__ import annotations
 import numpy as np
 import pytest
 import torch
+from torch.utils.checkpoint import checkpoint
 
 from test_gpu_drop import F32, _built, mba, randn  # noqa: F401
 
@@ -24,3 +25,27 @@ def test_an_rng_that_is_changed_before_the_backward(make):
     rng[0] = 9
     (h * w).sum().backward()
     assert torch.equal(x.grad, mba.dropout(w, 0.3, (1, 2)))
+
+
+def step(f, x, call):
+    leaf = f.clone().requires_grad_(True)
+    h, y = call(leaf, x)
+    (h.square() + y).sum().backward()
+    return h.detach(), leaf.grad
+
+
+@pytest.mark.parametrize("reentrant", [False, True])
+def test_a_step_that_is_computed_again(reentrant):
+    m = mba.FusedDropoutAddNorm(264, p=0.25, input_bias=True, device="cuda")
+    f, x = randn((12, 264), F32, 1).cuda(), randn((12, 264), F32, 2).cuda()
+    again = lambda *rng: lambda a, b: checkpoint(m, a, b, *rng, use_reentrant=reentrant)  # noqa: E731
+    # the module's own offset has moved on by then: another mask, so it is refused
+    with pytest.raises(RuntimeError, match="rng"):
+        step(f, x, again())
+    for rng in ((int(m.rng[0]), 7), m.rng.clone()):
+        want = step(f, x, lambda a, b: m(a, b, rng))
+        got = step(f, x, again(rng))
+        assert all(map(torch.equal, got, want))
+    # without dropout there is nothing to draw
+    m.eval()
+    assert all(map(torch.equal, step(f, x, again()), step(f, x, m)))
