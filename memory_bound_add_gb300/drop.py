@@ -22,6 +22,7 @@ Use another offset for every call.  p counts in steps of 2^-16.
 """
 from __future__ import annotations
 
+import copy
 import ctypes
 import functools
 import operator
@@ -377,6 +378,12 @@ def dropout_add_norm_train(f, x=None, *, p, rng, bias=None, norm="layer", gamma=
     return DropoutAddNormFunction.apply(f, x, bias, gamma, beta, p, rng, norm, eps)
 
 
+def _new_rng(device):
+    """A seed from torch's generator and an offset of 0."""
+    seed = int(torch.randint(0, (1 << 63) - 1, (), device="cpu"))
+    return torch.tensor([seed, 0], dtype=torch.int64, device=device)
+
+
 class FusedDropoutAddNorm(torch.nn.Module):
     """The boundary as a module: norm(x + dropout(f + input_bias)) with fp32
     parameters of size `hidden` (weight ones, bias zeros; input_bias zeros, with
@@ -391,6 +398,8 @@ class FusedDropoutAddNorm(torch.nn.Module):
         m.rng[1] += 1
         h, y = checkpoint(m, f, x, rng, use_reentrant=False)
 
+    A deepcopy draws a seed of its own, so that layers made as copies of one drop
+    different places; a loaded state has the seed and offset that were saved.
     In eval() nothing is dropped."""
 
     def __init__(self, hidden: int, p: float = 0.1, norm: Optional[str] = "layer", bias: bool = True,
@@ -405,8 +414,14 @@ class FusedDropoutAddNorm(torch.nn.Module):
         self.weight = new(1, norm is not None)
         self.bias = new(0, norm is not None and bias)
         self.input_bias = new(0, input_bias)
-        seed = int(torch.randint(0, (1 << 63) - 1, (), device="cpu"))
-        self.register_buffer("rng", torch.tensor([seed, 0], dtype=torch.int64, device=device))
+        self.register_buffer("rng", _new_rng(device))
+
+    def __deepcopy__(self, memo):
+        new = type(self).__new__(type(self))
+        memo[id(self)] = new
+        new.__dict__.update(copy.deepcopy(self.__dict__, memo))
+        new.rng = _new_rng(self.rng.device)
+        return new
 
     def forward(self, f, x=None, rng=None):
         p = self.p if self.training else 0.0

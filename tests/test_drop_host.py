@@ -1,6 +1,8 @@
 """What the dropout operators' autograd forms keep for their backward, without a GPU."""
 from __future__ import annotations
 
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -41,3 +43,19 @@ def test_no_mask_is_drawn_during_a_backward():
         m(x, x)
     Again.apply(torch.zeros(3, requires_grad=True)).sum().backward()
     assert m.rng[1] == 0
+
+
+def test_copies_have_seeds_of_their_own():
+    m = FusedDropoutAddNorm(8, p=0.5, input_bias=True)
+    m.rng[1] = 5
+    m.weight.data.fill_(3.0)
+    layers = torch.nn.ModuleList([copy.deepcopy(m) for _ in range(3)])
+    assert len({int(v.rng[0]) for v in (m, *layers)}) == 4 and all(int(v.rng[1]) == 0 for v in layers)
+    c = copy.deepcopy(layers)[0]
+    assert c.rng[0] != layers[0].rng[0] and c.weight[0] == 3.0 and c.weight is not m.weight and c.training
+    assert {n for n, _ in c.named_parameters()} == {"weight", "bias", "input_bias"}
+    # one module twice stays one module
+    assert len({id(v) for v in copy.deepcopy([m, m])}) == 1
+    # a state is continued by loading it
+    c.load_state_dict(m.state_dict())
+    assert torch.equal(c.rng, m.rng) and c.rng.data_ptr() != m.rng.data_ptr()

@@ -1,6 +1,8 @@
 """Which masks the autograd forms and the module draw."""
 from __future__ import annotations
 
+import copy
+
 import numpy as np
 import pytest
 import torch
@@ -49,3 +51,17 @@ def test_a_step_that_is_computed_again(reentrant):
     # without dropout there is nothing to draw
     m.eval()
     assert all(map(torch.equal, step(f, x, again()), step(f, x, m)))
+
+
+def test_copies_draw_their_own_masks():
+    m = mba.FusedDropoutAddNorm(264, p=0.5, device="cuda")
+    f, x = randn((12, 264), F32, 1).cuda(), randn((12, 264), F32, 2).cuda()
+    m(f, x)
+    c = copy.deepcopy(m)
+    seen = [(int(v.rng[0]), int(v.rng[1])) for v in (m, c)]
+    assert seen[0][0] != seen[1][0]
+    assert not torch.equal(m(f, x)[0], c(f, x)[0])
+    # a state is continued by loading it
+    c.load_state_dict(m.state_dict())
+    assert torch.equal(c.rng, m.rng) and c.rng.data_ptr() != m.rng.data_ptr()
+    assert torch.equal(m(f, x)[0], c(f, x)[0])
