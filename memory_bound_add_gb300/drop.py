@@ -22,6 +22,7 @@ Use another offset for every call.  p counts in steps of 2^-16.
 """
 from __future__ import annotations
 
+import contextlib
 import copy
 import ctypes
 import functools
@@ -387,9 +388,13 @@ def _new_rng(device):
 class FusedDropoutAddNorm(torch.nn.Module):
     """The boundary as a module: norm(x + dropout(f + input_bias)) with fp32
     parameters of size `hidden` (weight ones, bias zeros; input_bias zeros, with
-    it only).  Returns (h, y).  Its seed and offset lie in the buffer `rng`,
+    it only).  Returns (h, y).  Its seed and offset lie in the tensor `rng`,
     seeded from torch's generator; each training step takes the next offset, in
     device memory, so that a captured step draws a new mask at every replay.
+    rng moves, is saved and is loaded with the module, but is no buffer, or
+    DistributedDataParallel would give all ranks rank 0's masks; ranks whose masks
+    are to differ need seeds that do (another torch.manual_seed, or rng[0] += rank,
+    after loading a state too).
     forward's own rng replaces them.  A step that is computed again during the
     backward (activation checkpointing) would find the offset moved on, so there
     forward refuses to draw; pass rng to such steps:
@@ -414,7 +419,33 @@ class FusedDropoutAddNorm(torch.nn.Module):
         self.weight = new(1, norm is not None)
         self.bias = new(0, norm is not None and bias)
         self.input_bias = new(0, input_bias)
-        self.register_buffer("rng", _new_rng(device))
+        self.rng = _new_rng(device)
+
+    @contextlib.contextmanager
+    def _rng_as_buffer(self):
+        """What moves, saves and loads buffers takes rng for one inside."""
+        self._buffers["rng"] = self.__dict__.pop("rng")
+        try:
+            yield
+        finally:
+            self.__dict__["rng"] = self._buffers.pop("rng")
+
+    def _apply(self, *args, **kw):
+        with self._rng_as_buffer():
+            return super()._apply(*args, **kw)
+
+    def _save_to_state_dict(self, *args, **kw):
+        with self._rng_as_buffer():
+            super()._save_to_state_dict(*args, **kw)
+
+    def _load_from_state_dict(self, *args, **kw):
+        with self._rng_as_buffer():
+            super()._load_from_state_dict(*args, **kw)
+
+    def __setstate__(self, state):
+        super().__setstate__(state)
+        if "rng" in self._buffers:  # pickled when it was a buffer
+            self.rng = self._buffers.pop("rng")
 
     def __deepcopy__(self, memo):
         new = type(self).__new__(type(self))
