@@ -144,7 +144,7 @@ __global__ void k_params_in(const float* g, const float* b, float* gd, float* bd
   addln::pdl_wait();
   const int step = gridDim.x * blockDim.x;
   for (int i = blockIdx.x * blockDim.x + threadIdx.x; i < H; i += step) {
-    if (!ADDLN_IN(701, 4 * i, 4, 4 * static_cast<int64_t>(H))) continue;
+    if (!ADDLN_IN(791, 4 * i, 4, 4 * static_cast<int64_t>(H))) continue;
     gd[i] = g[i];
     bd[i] = b[i];
   }

@@ -161,7 +161,7 @@ __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
   auto fetch = [&](int slot, int64_t r) {
     if (r < p.rows) {
       const int64_t at = (r * p.H + cs.c0) * S;
-      ring.template fetch<0>(cs, slot, p.x, at, 802, extent);
+      ring.template fetch<0>(cs, slot, p.x, at, 811, extent);
       if (has_r) ring.template fetch<1>(cs, slot, p.r, at, 803, extent);
     }
     ring.commit();
