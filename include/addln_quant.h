@@ -19,7 +19,9 @@
  *                         by which no value is cut, one byte e + 127
  *     ADDLN_SCALE_TENSOR  fp32 [1], given, at least 2^-126: values beyond are cut
  * and the scales of groups lie as [rows, groups], or with group_major as
- * [groups, rows].  No scale that is made here is below 2^-126 (rows of zeros).
+ * [groups, rows]; a tensor-core product with block scales wants those of POW2
+ * in tiles of 128 rows by 4 groups, an order that is not made here.  No scale
+ * that is made here is below 2^-126 (rows of zeros).
  * Where the largest |y| is NaN or infinite the scale is NaN (byte 255), and
  * so is q, in integers 0.  With a given scale NaN gives NaN (integers: 0) and
  * an infinity the largest value.

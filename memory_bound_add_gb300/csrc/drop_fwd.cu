@@ -47,13 +47,19 @@ struct DropParams {
 // FULL: a layer norm, or a bias or a beta.  MODE: how rows lie.
 //
 // The call moves 4 rows H elements (3 without a norm) and is bound by memory where
-// rows are many: 32768x8192 bf16 rms 316 us (6.8 TB/s, 1.02 of a copy), 8192x4096 42.9
-// (0.94), 65536x768 layer 67.9 (0.89), odd widths too: 8192x5001 56.7 (0.86).  The
+// rows are many: 32768x8192 bf16 rms 316 us (6.8 TB/s, 1.02 of a copy), 8192x4096 43.9
+// (0.92), 65536x768 layer 67.7 (0.89), odd widths too: 8192x5001 56.0 (0.87).  The
 // tile (up to 32 columns a thread, 128 registers, two rows ahead) is block_fwd.cu's.
-// A mask costs 8.6 instructions an element of 23: half of the issue slots are used, so
-// that layer norms and few rows a walker are bound by instructions and a row's
-// latency: 8192x4096 layer with bias 53.9 us (0.75), 4097x1001 rms 9.1 (0.54),
-// 4096x768 fp16 layer 7.9 (0.48).
+// A mask costs 8.6 instructions an element of 23, and half of the issue slots are used:
+// layer norms and few rows a walker are bound by the latency of a row's chain (loads,
+// mask, exchanges, stores) at 16 warps an SM: 8192x4096 layer with bias 53.5 us (0.75),
+// 4097x1001 rms 9.1 (0.54), 4096x768 fp16 layer 7.9 (0.48).  Rows of several CTAs meet
+// through the cluster twice: 4096x11008 fp32 rms with bias 201 us (0.54), 4096x20000 bf16
+// 208 (0.47), layer 222 (0.44).  Rows of at most 128 columns leave most of a warp's lanes
+// without any: 65536x128 layer with bias 32.2 (0.31).
+//
+// (128 registers: as block_fwd.cu's kFwdRegs, which has the sweep.  nvcc takes the number
+// beside a thread count only where it depends on a template's argument.)
 template <int DT, int NV, bool FULL, int MODE>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     k_drop_fwd(const __grid_constant__ DropFwdArgs p) {

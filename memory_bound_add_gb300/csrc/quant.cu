@@ -77,7 +77,8 @@ __device__ __forceinline__ Scale pow2_of(float largest, int format) {
 }
 
 // Without FULL gamma is kept times this, which goes back with 1 / rms: values next to
-// the type's lowest, whose 1 / rms is 0, then stay finite (and so become 0).
+// the type's lowest, whose 1 / rms is 0, then stay finite (and so become 0).  In return
+// rows whose |x gamma| is below 2^-110 lose digits of their scale to fp32's least numbers.
 constexpr float kGammaScale = 0x1p-16f;
 
 // gamma and, with FULL, beta: in registers or in shared memory, as in
@@ -126,9 +127,14 @@ struct QuantParams {
 // 293 us (6.45 TB/s, 0.96 of a copy); 8192x4096 a scale a row 38.3 (0.91), 65536x768
 // powers of two 54.9 (0.96); 2048x4096 fp16 10.7 (0.82: 3.4 rows a walker).  19 to 21
 // instructions an element use half of the issue slots; 96 registers (five CTAs an SM)
-// and half the columns a thread measured the same or slower.  Layer norms are bound by
-// instructions: 8192x4096 to int8 49 us (0.72), 4097x1001 10.2 (0.42).  Groups of odd
-// widths take shifted rows: 8192x5001 90 us (0.48).
+// and half the columns a thread measured the same or slower.  Layer norms use 45% of the
+// issue slots too: they are bound by latency (two passes over the registers and two
+// exchanges a row) at 16 warps an SM: 8192x4096 to int8 48.5 us (0.72), 4097x1001 9.9
+// (0.43); with several CTAs a row 4096x20000 to e4m3, a scale a row, 230 (0.37).  Groups
+// of odd widths take shifted rows, 50 to 60 instructions an element: 8192x5001 91 us
+// (0.48).
+//
+// (128 registers: see k_drop_fwd.)
 template <int DT, int NV, bool FULL, int MODE>
 __global__ void __launch_bounds__(kMaxThreads) __maxnreg__((NV > 0 ? 128 : 0))
     k_norm_quant(const __grid_constant__ QuantArgs p) {
