@@ -67,6 +67,8 @@ extern "C" {
  *               are written for layer norms alone
  *   eps         >= 0, for both norms.  With eps = 0 a row whose mean square
  *               (layer: variance) is 0 gives NaN, the 0 * inf of the formula
+ * A row whose sum of squares (layer: of squared deviations) passes fp32 has
+ * 1 / sqrt = 0 and so y = beta; one with infinities or NaN is NaN.
  * h and y may each be exactly f or x (in place), not the same one; any other
  * overlap of an output is ADDLN_ERR_ALIAS.  rows == 0 is a no-op.
  */

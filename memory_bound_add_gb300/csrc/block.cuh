@@ -462,9 +462,37 @@ __device__ __forceinline__ float walker_sum(Exchange<SIDES>& ex, float v) {
 // Two different fp32 values of size K differ by 2^-24 K or more, so an M2
 // below a quarter of that square is the rounding of K_w in a row of equal
 // values: such a row is made exact (all deviations and M2 zero).
+//
+// Squares beyond fp32 make M2 infinite (infinities and NaN in the row: a NaN), so that
+// 1 / sqrt is 0 and y beta, whatever m is.  What merging makes of the distances between
+// the warps' shifts may have passed fp32 too then: m is 0, the mean is taken of shares,
+// and M2 is a NaN where a warp's is.
 struct RowStat {
   float mean, m, M2;
 };
+
+// The larger one; a NaN stays one.
+__device__ __forceinline__ float max_nan(float a, float b) {
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(b));
+  return a;
+}
+
+// Mean and M2 of such a row from its warps' parts, b as walker_stats exchanges them, n
+// values in all.  Out of line: within the loop it cost the layer norm to 8 bits 2 to 3%
+// (8192x4096 bf16 to int8, us: without these rows 48.5, in line 49.9, so 49.1).
+static __device__ __noinline__ float2 beyond_fp32(const float4* b, int warps, int width, float n) {
+  const float share = __frcp_rn(n);
+  float s = 0.f, q = __uint_as_float(0x7f800000u);
+  for (int i = (threadIdx.x & 31) & (width - 1); i < warps; i += width) {
+    s += (b[i].x + b[i].z) * (b[i].y * share);
+    q += b[i].w;
+  }
+  for (int off = 1; off < width; off <<= 1) {
+    s += __shfl_xor_sync(0xffffffffu, s, off);
+    q += __shfl_xor_sync(0xffffffffu, q, off);
+  }
+  return make_float2(s, q);
+}
 
 template <int VE, int NV, bool SIDES>
 __device__ __forceinline__ RowStat walker_stats(Exchange<SIDES>& ex, float2 (&v)[NV * VE / 2], const Cols<VE, NV>& cs) {
@@ -496,11 +524,12 @@ __device__ __forceinline__ RowStat walker_stats(Exchange<SIDES>& ex, float2 (&v)
   for (int off = 16; off > 0; off >>= 1)
     w = add2(w, make_float2(__shfl_xor_sync(kAll, w.x, off), __shfl_xor_sync(kAll, w.y, off)));
   const float m = w.x * cs.inv_n;
-  Part t{cs.n, m, fmaxf(fmaf(-w.x, m, w.y), 0.f) + (w.y - w.y)};  // a NaN stays
+  Part t{cs.n, m, max_nan(fmaf(-w.x, m, w.y), 0.f)};
   float K0 = K;
+  const float4* b = nullptr;
+  const int width = ex.w.width;
   if (ex.w.warps > 1) {
-    const float4* b = ex(make_float4(K, t.n, t.m, t.M2));
-    const int width = ex.w.width;
+    b = ex(make_float4(K, t.n, t.m, t.M2));
     K0 = b[0].x;
     t = Part{0.f, 0.f, 0.f};
     for (int i = (threadIdx.x & 31) & (width - 1); i < ex.w.warps; i += width) {
@@ -512,6 +541,13 @@ __device__ __forceinline__ RowStat walker_stats(Exchange<SIDES>& ex, float2 (&v)
                                __shfl_xor_sync(kAll, t.M2, off)});
   }
   RowStat st{K0 + t.m, t.m - (K - K0), t.M2};
+  if (!isfinite(t.M2)) {
+    st.m = 0.f;
+    if (ex.w.warps > 1) {
+      const float2 r = beyond_fp32(b, ex.w.warps, width, t.n);
+      st.mean = r.x, st.M2 = r.y;
+    }
+  }
   const float least = 0x1p-25f * K0;
   if (t.M2 < least * least) {
 #pragma unroll

@@ -14,10 +14,6 @@ __device__ __forceinline__ float abs_max(float m, float2 v) {
   asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(m) : "f"(m), "f"(v.x), "f"(v.y));
   return m;
 }
-__device__ __forceinline__ float max_nan(float a, float b) {
-  asm("max.NaN.f32 %0, %1, %2;" : "=f"(a) : "f"(a), "f"(b));
-  return a;
-}
 // Over a warp's lanes, of numbers that are not negative: their bits have the same
 // order, with infinity and then NaN above all.
 __device__ __forceinline__ float warp_max(float m) {
@@ -129,7 +125,7 @@ struct QuantParams {
 // instructions an element use half of the issue slots; 96 registers (five CTAs an SM)
 // and half the columns a thread measured the same or slower.  Layer norms use 45% of the
 // issue slots too: they are bound by latency (two passes over the registers and two
-// exchanges a row) at 16 warps an SM: 8192x4096 to int8 48.5 us (0.72), 4097x1001 9.9
+// exchanges a row) at 16 warps an SM: 8192x4096 to int8 49.3 us (0.71), 4097x1001 9.9
 // (0.43); with several CTAs a row 4096x20000 to e4m3, a scale a row, 230 (0.37).  Groups
 // of odd widths take shifted rows, 50 to 60 instructions an element: 8192x5001 91 us
 // (0.48).
