@@ -65,3 +65,34 @@ def test_copies_draw_their_own_masks():
     c.load_state_dict(m.state_dict())
     assert torch.equal(c.rng, m.rng) and c.rng.data_ptr() != m.rng.data_ptr()
     assert torch.equal(m(f, x)[0], c(f, x)[0])
+
+
+def test_a_captured_step_that_is_computed_again():
+    # as the module's docstring has it: every replay draws the next mask, for its backward too
+    m = mba.FusedDropoutAddNorm(768, p=0.5, norm="rms", bias=False, device="cuda")
+    f, x = randn((64, 768), seed=1).cuda().requires_grad_(True), randn((64, 768), seed=2).cuda()
+
+    def train():
+        rng = m.rng.clone()
+        m.rng[1] += 1
+        h, y = checkpoint(m, f, x, rng, use_reentrant=False, preserve_rng_state=False)
+        (h.square() + y).sum().backward()
+        return h
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        for _ in range(2):
+            train()
+    torch.cuda.current_stream().wait_stream(s)
+    f.grad = m.weight.grad = None
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        h = train()
+    seed, at = m.rng.tolist()
+    for i in range(3):
+        f.grad.zero_(), m.weight.grad.zero_()
+        g.replay()
+        want = step(f.detach(), x, lambda a, b: m(a, b, (seed, at + i)))
+        assert torch.equal(h, want[0]) and torch.equal(f.grad, want[1])
+    assert m.rng.tolist() == [seed, at + 3]
